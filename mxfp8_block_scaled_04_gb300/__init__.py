@@ -23,3 +23,13 @@ from .binding import (  # noqa: F401
     mxfp8_quantize_dgated_host, mxfp8_quantize_dgated_host_staging_bytes, quantize_dgated_host,
     QuantizeConfig, SCALES_PLAIN, SCALES_SWIZZLED, make_config, mxfp8_quantize_ex, mxfp8_scale_bytes,
 )
+from .mxfp4 import (  # noqa: F401
+    MXFP4Matrix, MXFP4Tensor, dequantize_mxfp4, matmul_mxfp4, matmul_mxfp4_grouped, mxfp4_dequantize,
+    mxfp4_grouped_scale_bytes, mxfp4_matmul, mxfp4_matmul_grouped, mxfp4_quantize, mxfp4_quantize_grouped,
+    mxfp4_row_bytes, mxfp4_scale_bytes, quantize_mxfp4, quantize_mxfp4_grouped,
+)
+from .moe import (  # noqa: F401
+    MoEPlan, MoERoute, RouteConfig, make_route_config, moe_combine, moe_combine_backward, moe_combine_backward_c,
+    moe_combine_c, moe_plan, moe_plan_c, moe_plan_workspace_bytes, moe_route, moe_route_backward,
+    moe_route_backward_c, moe_route_c,
+)

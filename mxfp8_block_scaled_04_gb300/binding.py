@@ -87,6 +87,24 @@ def lib():
                                                            vp]
             L.mxfp8_quantize_grouped_swizzled.restype = i32
             L.mxfp8_quantize_grouped_swizzled.argtypes = [vp, i64, i64, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+            sz = ctypes.c_size_t
+            for name, restype, argtypes in (
+                    ("mxfp4_row_bytes", sz, [i64]),
+                    ("mxfp4_scale_bytes", sz, [i64, i64]),
+                    ("mxfp4_grouped_scale_bytes", sz, [i64, i64, i32]),
+                    ("mxfp4_quantize", i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp]),
+                    ("mxfp4_quantize_grouped", i32, [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, vp]),
+                    ("mxfp4_dequantize", i32, [vp, vp, i64, i64, vp, i32, vp]),
+                    ("mxfp4_matmul", i32, [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]),
+                    ("mxfp4_matmul_grouped", i32, [vp, vp, i64, i32, vp, vp, vp, i64, i64, vp, i32, vp, vp]),
+                    ("moe_route", i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp]),
+                    ("moe_route_backward", i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]),
+                    ("moe_plan_workspace_bytes", sz, [i64, i64]),
+                    ("moe_plan", i32, [vp, i64, i32, i64, vp, vp, vp, vp, vp]),
+                    ("moe_combine", i32, [vp, i64, i64, vp, vp, i64, i32, vp, vp]),
+                    ("moe_combine_backward", i32, [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp])):
+                getattr(L, name).restype = restype
+                getattr(L, name).argtypes = argtypes
             L.mxfp8_grouped_swizzled_scale_bytes.restype = ctypes.c_size_t
             L.mxfp8_grouped_swizzled_scale_bytes.argtypes = [ctypes.POINTER(ctypes.c_int64), i32, i64, i32]
             L.mxfp8_quantize_gated_grouped.restype = i32

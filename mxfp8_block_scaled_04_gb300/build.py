@@ -16,12 +16,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libmxfp8.so")
-SOURCES = [os.path.join(PKG, "csrc", "api.cu")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("api.cu", "mxfp4.cu", "moe.cu")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
 def _inputs():
-    return SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + [os.path.join(ROOT, "include", "mxfp8.h")]
+    return (SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + glob.glob(os.path.join(PKG, "csrc", "*.h")) +
+            glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
 def needs_build() -> bool:
@@ -39,12 +40,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not os.path.exists(nvcc):
         nvcc = "nvcc"
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", os.path.join(ROOT, "include"), "-o", tmp] + SOURCES
+    flags = [ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+        flags.insert(0, "-Xptxas=-v")
+    objects, running = [], []
+    for src in SOURCES:  # one nvcc per translation unit, side by side
+        obj = os.path.join(BUILD_DIR, f"{os.path.splitext(os.path.basename(src))[0]}.tmp{os.getpid()}.o")
+        cmd = [nvcc] + flags + ["-c", "-o", obj, src]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        objects.append(obj)
+        running.append((cmd, subprocess.Popen(cmd)))
+    codes = [p.wait() for _, p in running]
+    try:
+        for (cmd, _), code in zip(running, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.run([nvcc, ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objects, check=True)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

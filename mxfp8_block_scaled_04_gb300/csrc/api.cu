@@ -19,6 +19,7 @@
 #include "dact.cuh"
 #include "dbias_reduce.cuh"
 #include "dgated.cuh"
+#include "host.h"
 #include "quantize.cuh"
 
 namespace {
@@ -496,6 +497,37 @@ mxfp8_status_t grouped_impl(const void *x, int64_t total_rows, int64_t N, int nu
 }
 
 }  // namespace
+
+// Helpers for the library's other translation units (host.h).
+namespace mxfp8 {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
+
+bool pointer_on_device(const void *p, int device) { return on_device(p, device); }
+
+mxfp8_status_t active_device(int *device) { return current_device(device); }
+
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
+unsigned int *fault_word_address(int device)
+{
+    static std::atomic<unsigned int *> cached[kMaxDevices];
+    if (device < 0 || device >= kMaxDevices)
+        return nullptr;
+    unsigned int *p = cached[device].load(std::memory_order_acquire);
+    if (p == nullptr) {
+        void *sym = nullptr;
+        if (cudaGetSymbolAddress(&sym, g_fault_word) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        p = static_cast<unsigned int *>(sym);
+        cached[device].store(p, std::memory_order_release);
+    }
+    return p;
+}
+
+}  // namespace mxfp8
 
 extern "C" {
 

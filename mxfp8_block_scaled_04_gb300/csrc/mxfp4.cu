@@ -1,0 +1,355 @@
+// C ABI of the MXFP4 cast and products (declarations and contract in include/mxfp4.h): host-side checks,
+// tensor maps and launches; the device code is in mxfp4_cast.cuh and mxfp4_gemm.cuh.
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/mxfp4.h"
+#include "host.h"
+#include "mxfp4_cast.cuh"
+#include "mxfp4_gemm.cuh"
+
+namespace {
+
+using namespace mxfp8;
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxDim = int64_t{1} << 31;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool type_ok(int t) { return t == MXFP4_BF16 || t == MXFP4_F32; }
+
+// SMs of the device; opts the kernel in to `smem` bytes once per device (`done` is the kernel's own).
+struct KernelSetup {
+    std::mutex mu;
+    int sms[kMaxDevices] = {};
+    int per_sm[kMaxDevices] = {};
+
+    template <typename K>
+    mxfp8_status_t operator()(K *kern, int device, int threads, int smem, int *ctas)
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (device < 0 || device >= kMaxDevices)
+            return MXFP8_ERR_DEVICE;
+        if (per_sm[device] == 0) {
+            int n = 0, s = 0;
+            if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                return MXFP8_ERR_LAUNCH;
+            }
+            sms[device] = s;
+            per_sm[device] = n;
+        }
+        *ctas = per_sm[device] * sms[device];
+        return MXFP8_OK;
+    }
+};
+
+template <bool F32, bool COL, bool GROUPED>
+mxfp8_status_t launch_cast_as(const CastParams &p, int64_t tiles, int device, cudaStream_t stream)
+{
+    static KernelSetup setup;
+    constexpr int smem = cast_smem_bytes<F32>(COL);
+    int ctas = 0;
+    const mxfp8_status_t st = setup(mxfp4_cast_kernel<F32, COL, GROUPED>, device, kCastThreads, smem, &ctas);
+    if (st != MXFP8_OK)
+        return st;
+    const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
+    return launch_serialized(mxfp4_cast_kernel<F32, COL, GROUPED>, dim3(grid), kCastThreads, smem, 1, stream, p);
+}
+
+mxfp8_status_t code_map(CUtensorMap *map, const void *codes, int64_t rows, int64_t row_bytes, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr)
+        return MXFP8_ERR_DEVICE;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? MXFP8_OK
+               : MXFP8_ERR_LAUNCH;
+}
+
+template <int QT, bool F32, bool GROUPED>
+mxfp8_status_t launch_gemm_as(const CUtensorMap &pm, const CUtensorMap &qm, const GemmParams &p, int64_t tiles, int device, cudaStream_t stream)
+{
+    static KernelSetup setup;
+    constexpr int smem = GemmShape<QT>::kSmem;
+    int ctas = 0;
+    const mxfp8_status_t st = setup(mxfp4_gemm_kernel<QT, F32, GROUPED>, device, kGemmThreads, smem, &ctas);
+    if (st != MXFP8_OK)
+        return st;
+    const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
+    return launch_serialized(mxfp4_gemm_kernel<QT, F32, GROUPED>, dim3(grid), kGemmThreads, smem, 1, stream, pm, qm, p);
+}
+
+// Checks and parameters that both products share.  Q: the tokens' rows; P: the weights' rows (per expert).
+mxfp8_status_t gemm_params(GemmParams *p, const void *q_codes, const void *q_scale, int64_t Q, const void *p_codes, const void *p_scale, int64_t P,
+                           int64_t K, void *out, int out_type, int64_t ldo)
+{
+    if (!type_ok(out_type))
+        return MXFP8_ERR_FORMAT;
+    if (Q < 0 || P < 0 || K < 0 || Q >= kMaxDim || P >= kMaxDim || K >= kMaxDim || ldo < P)
+        return MXFP8_ERR_SHAPE;
+    const int64_t tiles = ceil_div(P, kGemmRows) * ceil_div(Q, 128);
+    if (tiles >= kMaxDim)
+        return MXFP8_ERR_SHAPE;
+    if (Q > 0 && P > 0) {
+        if (out == nullptr || (K > 0 && (q_codes == nullptr || q_scale == nullptr || p_codes == nullptr || p_scale == nullptr)))
+            return MXFP8_ERR_NULL;
+    }
+    if (!is_aligned(q_codes, 16) || !is_aligned(q_scale, 16) || !is_aligned(p_codes, 16) || !is_aligned(p_scale, 16) ||
+        !is_aligned(out, out_type == MXFP4_F32 ? 4 : 2))
+        return MXFP8_ERR_ALIGN;
+    const int64_t pad = ceil_div(K, 32) * 32;
+    *p = GemmParams{};
+    p->p_scale = static_cast<const uint8_t *>(p_scale);
+    p->q_scale = static_cast<const uint8_t *>(q_scale);
+    p->P = P;
+    p->Q = Q;
+    p->kc = static_cast<int>(ceil_div(K, 128));
+    p->k_iters = static_cast<int>(ceil_div(K, 256));
+    p->k64 = static_cast<int>(ceil_div(pad, 64));
+    p->p_tiles = static_cast<int>(ceil_div(P, kGemmRows));
+    p->q_tiles = static_cast<int>(ceil_div(Q, 128));
+    p->out = out;
+    p->ldo = ldo;
+    return MXFP8_OK;
+}
+
+mxfp8_status_t zero_rows(void *out, int64_t rows, int64_t cols, int64_t ld, int type, cudaStream_t stream)
+{
+    const size_t e = type == MXFP4_F32 ? 4 : 2;
+    if (cudaMemset2DAsync(out, static_cast<size_t>(ld) * e, 0, static_cast<size_t>(cols) * e, static_cast<size_t>(rows), stream) != cudaSuccess) {
+        cudaGetLastError();
+        return MXFP8_ERR_LAUNCH;
+    }
+    return MXFP8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mxfp4_row_bytes(int64_t cols) { return cols <= 0 ? 0 : static_cast<size_t>(ceil_div(cols, 32)) * 16; }
+
+size_t mxfp4_scale_bytes(int64_t rows, int64_t cols)
+{
+    return rows <= 0 || cols <= 0 ? 0 : static_cast<size_t>(ceil_div(rows, 128)) * static_cast<size_t>(ceil_div(cols, 128)) * 512;
+}
+
+size_t mxfp4_grouped_scale_bytes(int64_t total_rows, int64_t cols, int num_groups)
+{
+    if (total_rows <= 0 || cols <= 0 || num_groups < 1)
+        return 0;
+    const int64_t tiles = total_rows / 128 + (num_groups < total_rows ? num_groups : total_rows);
+    return static_cast<size_t>(tiles) * static_cast<size_t>(ceil_div(cols, 128)) * 512;
+}
+
+mxfp8_status_t mxfp4_quantize(const void *x, int x_type, int64_t M, int64_t N, int64_t ldx, void *out_row, void *scale_row, void *out_col,
+                              void *scale_col, const float *noop, void *stream_)
+{
+    if (!type_ok(x_type))
+        return MXFP8_ERR_FORMAT;
+    if (M < 0 || N < 0 || N % 8 || ldx % 8 || ldx < N || M >= kMaxDim || N >= kMaxDim || ldx >= kMaxDim)
+        return MXFP8_ERR_SHAPE;
+    const int64_t tiles = ceil_div(M, kCastTile) * ceil_div(N, kCastTile);
+    if (tiles >= kMaxDim - (int64_t{1} << 20))
+        return MXFP8_ERR_SHAPE;
+    if (tiles > 0) {
+        if (x == nullptr || (out_row == nullptr) != (scale_row == nullptr) || (out_col == nullptr) != (scale_col == nullptr) ||
+            (out_row == nullptr && out_col == nullptr))
+            return MXFP8_ERR_NULL;
+    }
+    if (!is_aligned(x, 16) || !is_aligned(out_row, 16) || !is_aligned(out_col, 16) || !is_aligned(scale_row, 4) || !is_aligned(scale_col, 4) ||
+        !is_aligned(noop, 4))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    mxfp8_status_t st = active_device(&device);
+    if (st != MXFP8_OK)
+        return st;
+    for (const void *ptr : {x, static_cast<const void *>(out_row), static_cast<const void *>(scale_row), static_cast<const void *>(out_col),
+                            static_cast<const void *>(scale_col), static_cast<const void *>(noop)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (tiles == 0)
+        return MXFP8_OK;
+    CastParams p{};
+    p.x = x;
+    p.M = M;
+    p.N = N;
+    p.ldx = ldx;
+    p.T = M;
+    p.out_row = static_cast<uint8_t *>(out_row);
+    p.scale_row = static_cast<uint8_t *>(scale_row);
+    p.out_col = static_cast<uint8_t *>(out_col);
+    p.scale_col = static_cast<uint8_t *>(scale_col);
+    p.noop = noop;
+    p.row_tiles = static_cast<int>(ceil_div(M, kCastTile));
+    p.col_tiles = static_cast<int>(ceil_div(N, kCastTile));
+    p.row_pitch = ceil_div(N, 32) * 16;
+    p.col_pitch = ceil_div(M, 32) * 16;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const bool col = out_col != nullptr;
+    if (x_type == MXFP4_F32)
+        return col ? launch_cast_as<true, true, false>(p, tiles, device, stream) : launch_cast_as<true, false, false>(p, tiles, device, stream);
+    return col ? launch_cast_as<false, true, false>(p, tiles, device, stream) : launch_cast_as<false, false, false>(p, tiles, device, stream);
+}
+
+mxfp8_status_t mxfp4_quantize_grouped(const void *x, int x_type, int64_t T, int64_t N, int64_t ldx, const int32_t *rows, int64_t total_rows,
+                                      int num_groups, const int64_t *offsets, void *out, void *scale, int *err_flag, void *stream_)
+{
+    if (!type_ok(x_type))
+        return MXFP8_ERR_FORMAT;
+    if (T < 0 || total_rows < 0 || N < 0 || N % 8 || ldx % 8 || ldx < N || T >= kMaxDim || total_rows >= kMaxDim || N >= kMaxDim ||
+        ldx >= kMaxDim || (rows == nullptr && total_rows > T))
+        return MXFP8_ERR_SHAPE;
+    if (num_groups < 1 || num_groups > MXFP8_MAX_GROUPS || offsets == nullptr)
+        return MXFP8_ERR_GROUPS;
+    const int64_t col_tiles = ceil_div(N, kCastTile);
+    const int64_t bound = (total_rows / kCastTile + num_groups) * col_tiles;
+    if (bound >= kMaxDim - (int64_t{1} << 20))
+        return MXFP8_ERR_SHAPE;
+    const bool empty = total_rows == 0 || N == 0;
+    if (!empty && (out == nullptr || scale == nullptr || (x == nullptr && T > 0)))
+        return MXFP8_ERR_NULL;
+    if (!is_aligned(x, 16) || !is_aligned(out, 16) || !is_aligned(scale, 4) || !is_aligned(rows, 4) || !is_aligned(offsets, 8) ||
+        !is_aligned(err_flag, 4))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    mxfp8_status_t st = active_device(&device);
+    if (st != MXFP8_OK)
+        return st;
+    for (const void *ptr : {x, static_cast<const void *>(rows), static_cast<const void *>(offsets), static_cast<const void *>(out),
+                            static_cast<const void *>(scale), static_cast<const void *>(err_flag)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (empty)
+        return MXFP8_OK;
+    CastParams p{};
+    p.x = x;
+    p.M = total_rows;
+    p.N = N;
+    p.ldx = ldx;
+    p.T = T;
+    p.out_row = static_cast<uint8_t *>(out);
+    p.scale_row = static_cast<uint8_t *>(scale);
+    p.col_tiles = static_cast<int>(col_tiles);
+    p.row_pitch = ceil_div(N, 32) * 16;
+    p.rows = rows;
+    p.offsets = offsets;
+    p.err_flag = err_flag;
+    p.num_groups = num_groups;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    return x_type == MXFP4_F32 ? launch_cast_as<true, false, true>(p, bound, device, stream)
+                               : launch_cast_as<false, false, true>(p, bound, device, stream);
+}
+
+mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t rows, int64_t cols, void *out, int out_type, void *stream_)
+{
+    if (!type_ok(out_type))
+        return MXFP8_ERR_FORMAT;
+    if (rows < 0 || cols < 0 || rows >= kMaxDim || cols >= kMaxDim)
+        return MXFP8_ERR_SHAPE;
+    const bool empty = rows == 0 || cols == 0;
+    if (!empty && (codes == nullptr || scale == nullptr || out == nullptr))
+        return MXFP8_ERR_NULL;
+    if (!is_aligned(codes, 16) || !is_aligned(out, 16))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    mxfp8_status_t st = active_device(&device);
+    if (st != MXFP8_OK)
+        return st;
+    if (!pointer_on_device(codes, device) || !pointer_on_device(scale, device) || !pointer_on_device(out, device))
+        return MXFP8_ERR_DEVICE;
+    if (empty)
+        return MXFP8_OK;
+    const int64_t n = rows * ceil_div(cols, 8);
+    const int64_t blocks = ceil_div(n, 256);
+    const unsigned grid = static_cast<unsigned>(blocks < (int64_t{1} << 20) ? blocks : (int64_t{1} << 20));
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const auto *c = static_cast<const uint8_t *>(codes);
+    const auto *s = static_cast<const uint8_t *>(scale);
+    const int64_t pitch = ceil_div(cols, 32) * 16, col_tiles = ceil_div(cols, 128);
+    auto launch = [&](auto *kern) { return launch_serialized(kern, dim3(grid), 256, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
+    if (cols % 8)
+        return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false>) : launch(mxfp4_decode_kernel<false, false>);
+    return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true>) : launch(mxfp4_decode_kernel<false, true>);
+}
+
+mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M, const void *b_codes, const void *b_scale, int64_t N, int64_t K,
+                            void *out, int out_type, int64_t ldo, void *stream_)
+{
+    GemmParams p;
+    mxfp8_status_t st = gemm_params(&p, a_codes, a_scale, M, b_codes, b_scale, N, K, out, out_type, ldo);
+    if (st != MXFP8_OK)
+        return st;
+    int device = 0;
+    if ((st = active_device(&device)) != MXFP8_OK)
+        return st;
+    for (const void *ptr : {a_codes, a_scale, b_codes, b_scale, static_cast<const void *>(out)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (M == 0 || N == 0)
+        return MXFP8_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (K == 0)
+        return zero_rows(out, M, N, ldo, out_type, stream);
+    if ((p.fault = fault_word_address(device)) == nullptr)
+        return MXFP8_ERR_DEVICE;
+    const int64_t row_bytes = ceil_div(K, 32) * 16;
+    CUtensorMap pm, qm;
+    if ((st = code_map(&pm, b_codes, N, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, a_codes, M, row_bytes, kGemmQBox)) != MXFP8_OK)
+        return st;
+    const int64_t tiles = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
+    return out_type == MXFP4_F32 ? launch_gemm_as<128, true, false>(pm, qm, p, tiles, device, stream)
+                                 : launch_gemm_as<128, false, false>(pm, qm, p, tiles, device, stream);
+}
+
+mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, int64_t total_rows, int num_groups, const int64_t *offsets,
+                                    const void *b_codes, const void *b_scale, int64_t N, int64_t K, void *out, int out_type, int *err_flag,
+                                    void *stream_)
+{
+    GemmParams p;
+    mxfp8_status_t st = gemm_params(&p, a_codes, a_scale, total_rows, b_codes, b_scale, N, K, out, out_type, N);
+    if (st != MXFP8_OK)
+        return st;
+    if (num_groups < 1 || num_groups > MXFP8_MAX_GROUPS || offsets == nullptr)
+        return MXFP8_ERR_GROUPS;
+    const int64_t bound = (total_rows / 128 + num_groups) * static_cast<int64_t>(p.p_tiles);
+    if (bound >= kMaxDim - (int64_t{1} << 20) || num_groups * N >= kMaxDim)
+        return MXFP8_ERR_SHAPE;
+    if (!is_aligned(offsets, 8) || !is_aligned(err_flag, 4))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    if ((st = active_device(&device)) != MXFP8_OK)
+        return st;
+    for (const void *ptr : {a_codes, a_scale, b_codes, b_scale, static_cast<const void *>(out), static_cast<const void *>(offsets),
+                            static_cast<const void *>(err_flag)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (total_rows == 0 || N == 0)
+        return MXFP8_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (K == 0)
+        return zero_rows(out, total_rows, N, N, out_type, stream);
+    if ((p.fault = fault_word_address(device)) == nullptr)
+        return MXFP8_ERR_DEVICE;
+    p.offsets = offsets;
+    p.num_groups = num_groups;
+    p.err_flag = err_flag;
+    const int64_t row_bytes = ceil_div(K, 32) * 16;
+    CUtensorMap pm, qm;
+    if ((st = code_map(&pm, b_codes, num_groups * N, row_bytes, kGemmRows)) != MXFP8_OK ||
+        (st = code_map(&qm, a_codes, total_rows, row_bytes, kGemmQBox)) != MXFP8_OK)
+        return st;
+    return out_type == MXFP4_F32 ? launch_gemm_as<128, true, true>(pm, qm, p, bound, device, stream)
+                                 : launch_gemm_as<128, false, true>(pm, qm, p, bound, device, stream);
+}
+
+}  // extern "C"

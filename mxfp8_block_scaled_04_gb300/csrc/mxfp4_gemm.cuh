@@ -1,0 +1,268 @@
+// MXFP4 products on the tensor cores (sm_103a): out[q, p] = sum_k Q[q, k] * P[p, k].
+//
+// P (a layer's weights) takes the 128 accumulator lanes and Q (the tokens) the columns, so that a warp writes
+// 32 neighbouring elements of an output row and the MMA's n shrinks with the tokens: one kernel serves a
+// single token and a training batch.  Each block of 32 is scaled inside the MMA (kind::mxf4, two E8M0 scales
+// per 64 elements), so the operands go from HBM to the tensor core as they are stored.
+//
+// Roles (8 warps): warp 0 feeds a ring of shared-memory stages of 256 elements of K (TMA tiles of the codes, plain
+// bulk copies of the scale tiles), warp 1 copies scales to TMEM and issues the MMAs, warp 2 owns the TMEM
+// allocation, warps 4-7 read the accumulators and write the output while the next tile accumulates in the other
+// TMEM buffer.  The CTAs are persistent over a round-robin tile list.  Every wait is bounded: on expiry the CTA
+// sets the library's fault word, waits (bounded) for its own copies and MMAs, frees its TMEM and returns.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "groups.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace mxfp8 {
+
+constexpr int kGemmThreads = 256;
+constexpr int kGemmRows = 128;   // rows of P per tile
+constexpr int kGemmQBox = 32;    // rows of Q per TMA box
+constexpr uint64_t kGemmWaitNs = 2000000000ull;
+constexpr uint64_t kGemmDrainNs = 200000000ull;
+
+struct GemmParams {
+    const uint8_t *p_scale, *q_scale;
+    int64_t P, Q;        // rows of each operand (P of one expert when grouped)
+    int kc;              // scale tiles along K: ceil(K / 128)
+    int k_iters;         // stages along K: ceil(K / 256)
+    int k64;             // MMA steps along K: ceil(K / 64)
+    int p_tiles, q_tiles;
+    void *out;
+    int64_t ldo;
+    unsigned *fault;
+    const int64_t *offsets;  // grouped
+    int num_groups;
+    int *err_flag;
+};
+
+template <int QT>
+struct GemmShape {
+    static constexpr int kPBytes = kGemmRows * 128;
+    static constexpr int kQBytes = QT * 128;
+    static constexpr int kPScale = 1024;               // two 512-byte scale tiles
+    static constexpr int kQScale = QT / 128 * 1024;
+    static constexpr int kStage = kPBytes + kQBytes + kPScale + kQScale;
+    static constexpr int kStages = 6;
+    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr int kScaleCols = 8 + QT / 128 * 8;  // TMEM columns of one stage's scales
+    static constexpr int kScaleBase = 2 * QT;
+};
+
+struct GemmTile {
+    int32_t p_row, q_row;      // TMA rows
+    int64_t p_plane, q_plane;  // scale tile rows
+    int64_t p0;                // first output column
+    int valid;                 // rows of Q in the tile
+};
+
+// Tile t.  Dense: bands of 8 Q tiles, P tiles in turn within a band, so that the CTAs at work share operands in
+// L2.  Grouped: an expert's Q tiles in turn, each over all of the expert's P tiles.
+template <int QT, bool GROUPED>
+__device__ __forceinline__ GemmTile gemm_tile(int t, const GemmParams &p, const GroupTable<GROUPED> &groups)
+{
+    GemmTile r;
+    if constexpr (GROUPED) {
+        const int rt = t / p.p_tiles, pt = t - rt * p.p_tiles;
+        const int g = groups.find(rt, p.num_groups);
+        const int local = rt - groups.tile[g];
+        const int64_t q0 = groups.offset[g] + static_cast<int64_t>(local) * QT;
+        const int64_t left = groups.offset[g + 1] - q0;
+        r.valid = left < QT ? static_cast<int>(left) : QT;
+        r.q_row = static_cast<int32_t>(q0);
+        r.q_plane = groups.plane[g] + static_cast<int64_t>(local) * (QT / 128);
+        r.p0 = static_cast<int64_t>(pt) * kGemmRows;
+        r.p_row = static_cast<int32_t>(g * p.P + r.p0);
+        r.p_plane = static_cast<int64_t>(g) * p.p_tiles + pt;
+    } else {
+        constexpr int kBand = 8;
+        const int band = t / (kBand * p.p_tiles);
+        const int in = t - band * kBand * p.p_tiles;
+        const int width = min(kBand, p.q_tiles - band * kBand);
+        const int pt = in / width, qt = band * kBand + in - pt * width;
+        const int64_t left = p.Q - static_cast<int64_t>(qt) * QT;
+        r.valid = left < QT ? static_cast<int>(left) : QT;
+        r.q_row = qt * QT;
+        r.q_plane = static_cast<int64_t>(qt) * (QT / 128);
+        r.p0 = static_cast<int64_t>(pt) * kGemmRows;
+        r.p_row = static_cast<int32_t>(r.p0);
+        r.p_plane = pt;
+    }
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_out(void *out, int64_t at, uint32_t bits)
+{
+    if constexpr (F32)
+        static_cast<float *>(out)[at] = __uint_as_float(bits);
+    else
+        static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(__uint_as_float(bits));
+}
+
+template <int QT, bool F32, bool GROUPED>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p)
+{
+    using S = GemmShape<QT>;
+    extern __shared__ unsigned char gemm_smem[];
+    __shared__ GroupTable<GROUPED> groups;
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int failed;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_u32(gemm_smem) + 1023u) & ~1023u;
+    if (tid == 0) {
+        prefetch_tensormap(&p_map);
+        prefetch_tensormap(&q_map);
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), 4);
+        }
+        mbar_init(smem_u32(&drain), 1);
+        fence_mbar_init();
+        failed = 0;
+    }
+    if (warp == 2)
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait_and_release();
+
+    int num_tiles = p.p_tiles * p.q_tiles;
+    if constexpr (GROUPED) {
+        const int rt = group_setup<kGemmThreads, QT>(groups, p.offsets, p.num_groups, p.Q);
+        num_tiles = rt < 0 ? 0 : rt * p.p_tiles;
+        if (rt < 0 && blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
+            atomicOr(p.err_flag, 1);
+    }
+    auto give_up = [&]() {
+        failed = 1;
+        atomicOr(p.fault, 1u);
+    };
+
+    if (warp == 0 && lane == 0) {
+        // ---- producer ----
+        int it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+            const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
+            const int boxes = (c.valid + kGemmQBox - 1) / kGemmQBox;
+            const int q_blocks = (c.valid + 127) / 128;
+            for (int k = 0; k < p.k_iters; ++k, ++it) {
+                const int s = it % S::kStages;
+                if (it >= S::kStages && !mbar_wait_bounded(smem_u32(&empty[s]), ((it / S::kStages) - 1) & 1, kGemmWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_u32(&full[s]);
+                const uint32_t dp = base + s * S::kStage, dq = dp + S::kPBytes, dps = dq + S::kQBytes, dqs = dps + S::kPScale;
+                const uint32_t sb = 512u * min(2, p.kc - 2 * k);
+                mbar_arrive_expect_tx(bar, S::kPBytes + boxes * kGemmQBox * 128 + sb * (1 + q_blocks));
+                tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                for (int b = 0; b < boxes; ++b)
+                    tma_load_2d_shared(dq + b * kGemmQBox * 128, &q_map, bar, k * 128, c.q_row + b * kGemmQBox);
+                bulk_load(dps, p.p_scale + (c.p_plane * p.kc + 2 * k) * 512, sb, bar);
+                for (int b = 0; b < q_blocks; ++b)
+                    bulk_load(dqs + b * 1024, p.q_scale + ((c.q_plane + b) * p.kc + 2 * k) * 512, sb, bar);
+            }
+        }
+        if (!ok) {
+            give_up();
+            for (int j = it < S::kStages ? 0 : it - S::kStages; j < it; ++j)  // copies in flight
+                mbar_wait_bounded(smem_u32(&full[j % S::kStages]), (j / S::kStages) & 1, kGemmDrainNs);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- MMA ----
+        int it = 0, n_tile = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++n_tile) {
+            const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
+            const int n = (c.valid + 15) & ~15;
+            const int q_blocks = (c.valid + 127) / 128;
+            const int buf = n_tile & 1;
+            const uint32_t d = tmem + buf * QT;
+            if (n_tile >= 2 && !mbar_wait_bounded(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWaitNs)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int k = 0; k < p.k_iters; ++k, ++it) {
+                const int s = it % S::kStages;
+                if (!mbar_wait_bounded(smem_u32(&full[s]), (it / S::kStages) & 1, kGemmWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dp = base + s * S::kStage, dq = dp + S::kPBytes, dps = dq + S::kQBytes, dqs = dps + S::kPScale;
+                const uint32_t sf = tmem + S::kScaleBase + (it & 1) * S::kScaleCols;
+                const int chunks = min(2, p.kc - 2 * k);
+                for (int ch = 0; ch < chunks; ++ch) {
+                    tc_copy_scales(sf + ch * 4, desc_scales(dps + ch * 512));
+                    for (int b = 0; b < q_blocks; ++b)
+                        tc_copy_scales(sf + 8 + (ch * (QT / 128) + b) * 4, desc_scales(dqs + b * 1024 + ch * 512));
+                }
+                const int steps = min(4, p.k64 - 4 * k);
+                for (int j = 0; j < steps; ++j)
+                    tc_mma_mxf4(d, desc_sw128(dp + j * 32), desc_sw128(dq + j * 32), mxf4_idesc(kGemmRows, n, j & 1), sf + (j >> 1) * 4,
+                                sf + 8 + (j >> 1) * (QT / 128) * 4, k > 0 || j > 0);
+                tc_commit(smem_u32(&empty[s]));
+            }
+            if (ok)
+                tc_commit(smem_u32(&acc_full[buf]));
+        }
+        if (!ok) {
+            give_up();
+            tc_commit(smem_u32(&drain));
+            mbar_wait_bounded(smem_u32(&drain), 0, kGemmDrainNs);
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue ----
+        const int quarter = warp & 3;
+        int n_tile = 0;
+        for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
+            const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
+            const int buf = n_tile & 1;
+            const bool done = mbar_wait_bounded(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWaitNs);
+            if (!__all_sync(0xFFFFFFFFu, done)) {
+                if (lane == 0)
+                    give_up();
+                break;
+            }
+            tc_fence_after();
+            const int64_t col = c.p0 + quarter * 32 + lane;
+            const bool live = col < p.P;
+            for (int q = 0; q < c.valid; q += 32) {
+                uint32_t v[32];
+                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * QT + q, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (live && q + j < c.valid)
+                        store_out<F32>(p.out, (c.q_row + int64_t{q} + j) * p.ldo + col, v[j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&acc_empty[buf]));
+        }
+    }
+    __syncthreads();
+    if (warp == 2)
+        tmem_dealloc(tmem, 512);
+}
+
+}  // namespace mxfp8

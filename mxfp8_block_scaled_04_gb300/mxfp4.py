@@ -1,0 +1,218 @@
+"""MXFP4 (4-bit microscaled) cast and products: binding of the C ABI in include/mxfp4.h.
+
+The functions named ``mxfp4_*`` mirror the C entry points one for one and return the status code;
+``quantize_mxfp4``, ``quantize_mxfp4_grouped``, ``dequantize_mxfp4``, ``matmul_mxfp4`` and
+``matmul_mxfp4_grouped`` check their tensors, allocate the outputs with torch (on ``stream`` when one is
+given) and raise :class:`MXFP8Error` on a non-OK status.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import NamedTuple, Optional
+
+import torch
+
+from .binding import MXFP8Error, _addr, _stream, lib
+
+TYPE_BF16 = 0
+TYPE_F32 = 1
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+
+
+class MXFP4Matrix(NamedTuple):
+    """A 4-bit matrix [rows, cols]: blocks of 32 along the columns.  Experts' matrices of one shape are held
+    together with a leading dimension on ``codes`` and ``scales``."""
+    codes: torch.Tensor   # uint8 [rows, 16 * ceil(cols / 32)]
+    scales: torch.Tensor  # uint8, 1-D: the GEMM-ready E8M0 plane
+    rows: int
+    cols: int
+
+
+class MXFP4Tensor(NamedTuple):
+    """Outputs of quantize_mxfp4; a direction that was not requested is None."""
+    row: Optional[MXFP4Matrix]  # x [M, N]
+    col: Optional[MXFP4Matrix]  # x transposed [N, M]
+
+
+# ---- one-for-one C entry points --------------------------------------------------
+
+def mxfp4_row_bytes(cols: int) -> int:
+    return -(-cols // 32) * 16 if cols > 0 else 0
+
+
+def mxfp4_scale_bytes(rows: int, cols: int) -> int:
+    return -(-rows // 128) * -(-cols // 128) * 512 if rows > 0 and cols > 0 else 0
+
+
+def mxfp4_grouped_scale_bytes(total_rows: int, cols: int, num_groups: int) -> int:
+    return int(lib().mxfp4_grouped_scale_bytes(total_rows, cols, num_groups))
+
+
+def mxfp4_quantize(x, x_type, M, N, ldx, out_row, scale_row, out_col, scale_col, noop=None, stream=None) -> int:
+    return lib().mxfp4_quantize(_addr(x), x_type, M, N, ldx, _addr(out_row), _addr(scale_row), _addr(out_col),
+                                _addr(scale_col), _addr(noop), _stream(stream))
+
+
+def mxfp4_quantize_grouped(x, x_type, T, N, ldx, rows, total_rows, num_groups, offsets, out, scale, err_flag=None,
+                           stream=None) -> int:
+    return lib().mxfp4_quantize_grouped(_addr(x), x_type, T, N, ldx, _addr(rows), total_rows, num_groups,
+                                        _addr(offsets), _addr(out), _addr(scale), _addr(err_flag), _stream(stream))
+
+
+def mxfp4_dequantize(codes, scale, rows, cols, out, out_type, stream=None) -> int:
+    return lib().mxfp4_dequantize(_addr(codes), _addr(scale), rows, cols, _addr(out), out_type, _stream(stream))
+
+
+def mxfp4_matmul(a_codes, a_scale, M, b_codes, b_scale, N, K, out, out_type, ldo, stream=None) -> int:
+    return lib().mxfp4_matmul(_addr(a_codes), _addr(a_scale), M, _addr(b_codes), _addr(b_scale), N, K, _addr(out),
+                              out_type, ldo, _stream(stream))
+
+
+def mxfp4_matmul_grouped(a_codes, a_scale, total_rows, num_groups, offsets, b_codes, b_scale, N, K, out, out_type,
+                         err_flag=None, stream=None) -> int:
+    return lib().mxfp4_matmul_grouped(_addr(a_codes), _addr(a_scale), total_rows, num_groups, _addr(offsets),
+                                      _addr(b_codes), _addr(b_scale), N, K, _addr(out), out_type, _addr(err_flag),
+                                      _stream(stream))
+
+
+# ---- torch conveniences ----------------------------------------------------------
+
+def _on(stream):
+    """Make ``stream`` (a torch stream or a cudaStream_t address) current, so that outputs belong to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _check(status: int, what: str) -> None:
+    if status != 0:
+        raise MXFP8Error(status, what)
+
+
+def _check_input(x: torch.Tensor, name: str = "x") -> int:
+    """Row pitch of a 2-D bf16 / fp32 tensor whose rows are contiguous."""
+    if x.dtype not in _TYPES or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D bfloat16 or float32 tensor with contiguous rows")
+    return max(x.shape[1], x.stride(0)) if min(x.shape[0] - 1, x.shape[1]) > 0 else x.shape[1]
+
+
+def _check_offsets(offsets: torch.Tensor) -> int:
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous 1-D int64 tensor of num_groups + 1 entries")
+    return offsets.numel() - 1
+
+
+def _check_err(err_flag) -> None:
+    if err_flag is not None and (err_flag.dtype != torch.int32 or err_flag.numel() < 1):
+        raise ValueError("err_flag must be an int32 tensor")
+
+
+def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None) -> None:
+    lead = () if groups is None else (groups,)
+    plane = mxfp4_scale_bytes(m.rows, m.cols)
+    if (m.codes.dtype != torch.uint8 or tuple(m.codes.shape) != lead + (m.rows, mxfp4_row_bytes(m.cols)) or
+            not m.codes.is_contiguous()):
+        raise ValueError(f"{name}.codes must be a contiguous uint8 tensor {lead + (m.rows, mxfp4_row_bytes(m.cols))}")
+    if m.scales.dtype != torch.uint8 or not m.scales.is_contiguous() or (
+            m.scales.numel() < plane if groups is None else tuple(m.scales.shape) != (groups, plane)):
+        raise ValueError(f"{name}.scales must be a contiguous uint8 tensor of {plane} bytes per matrix")
+
+
+def _empty_matrix(rows: int, cols: int, device) -> MXFP4Matrix:
+    u8 = torch.uint8
+    return MXFP4Matrix(torch.empty((rows, mxfp4_row_bytes(cols)), dtype=u8, device=device),
+                       torch.empty((mxfp4_scale_bytes(rows, cols),), dtype=u8, device=device), rows, cols)
+
+
+def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, noop: Optional[torch.Tensor] = None,
+                   stream=None) -> MXFP4Tensor:
+    """MXFP4-quantize a CUDA bf16 or fp32 tensor [M, N] (any M, N a multiple of 8, rows contiguous).
+
+    ``row`` is x with blocks along its rows; ``col`` is x transposed with blocks along M, the operand of
+    the products that sum over M (input and weight gradients).
+    """
+    ld = _check_input(x)
+    M, N = x.shape
+    with _on(stream):
+        row = _empty_matrix(M, N, x.device) if rowwise else None
+        col = _empty_matrix(N, M, x.device) if colwise else None
+        _check(mxfp4_quantize(x, _TYPES[x.dtype], M, N, ld, row and row.codes, row and row.scales, col and col.codes,
+                              col and col.scales, noop), "mxfp4_quantize")
+    return MXFP4Tensor(row, col)
+
+
+def quantize_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                           err_flag: Optional[torch.Tensor] = None, stream=None) -> MXFP4Matrix:
+    """The rowwise cast of x's rows gathered for experts: output row i is x[rows[i]] (x[i] without ``rows``),
+    expert g owns rows [offsets[g], offsets[g + 1]) (device int64) and has a scale plane of its own."""
+    ld = _check_input(x)
+    groups = _check_offsets(offsets)
+    _check_err(err_flag)
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous()):
+        raise ValueError("rows must be a contiguous 1-D int32 tensor")
+    T, N = x.shape
+    total = T if rows is None else rows.numel()
+    with _on(stream):
+        u8 = dict(dtype=torch.uint8, device=x.device)
+        codes = torch.empty((total, mxfp4_row_bytes(N)), **u8)
+        scales = torch.empty((mxfp4_grouped_scale_bytes(total, N, groups),), **u8)
+        _check(mxfp4_quantize_grouped(x, _TYPES[x.dtype], T, N, ld, rows, total, groups, offsets, codes, scales,
+                                      err_flag), "mxfp4_quantize_grouped")
+    return MXFP4Matrix(codes, scales, total, N)
+
+
+def dequantize_mxfp4(m: MXFP4Matrix, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values [rows, cols] of a 4-bit matrix (exact in bf16 and fp32)."""
+    if dtype not in _TYPES:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    _check_matrix(m, "m")
+    with _on(stream):
+        out = torch.empty((m.rows, m.cols), dtype=dtype, device=m.codes.device)
+        _check(mxfp4_dequantize(m.codes, m.scales, m.rows, m.cols, out, _TYPES[dtype]), "mxfp4_dequantize")
+    return out
+
+
+def matmul_mxfp4(a: MXFP4Matrix, b: MXFP4Matrix, out_dtype: torch.dtype = torch.bfloat16,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """a [M, K] times b [N, K] transposed: [M, N] in ``out_dtype``, or into ``out`` (rows contiguous)."""
+    _check_matrix(a, "a")
+    _check_matrix(b, "b")
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns, b has {b.cols}")
+    with _on(stream):
+        if out is None:
+            if out_dtype not in _TYPES:
+                raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+            out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
+            ldo = b.rows
+        else:
+            if tuple(out.shape) != (a.rows, b.rows):
+                raise ValueError(f"out must be [{a.rows}, {b.rows}]")
+            ldo = _check_input(out, "out")
+        _check(mxfp4_matmul(a.codes, a.scales, a.rows, b.codes, b.scales, b.rows, a.cols, out, _TYPES[out.dtype], ldo),
+               "mxfp4_matmul")
+    return out
+
+
+def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, out_dtype: torch.dtype = torch.bfloat16,
+                         err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Experts' products: rows [offsets[g], offsets[g + 1]) of a (from quantize_mxfp4_grouped) times expert g's
+    b [N, K] transposed; b.codes [G, N, .], b.scales [G, .].  Returns [total_rows, N]."""
+    groups = _check_offsets(offsets)
+    _check_err(err_flag)
+    _check_matrix(b, "b", groups)
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns, b has {b.cols}")
+    if a.codes.dtype != torch.uint8 or tuple(a.codes.shape) != (a.rows, mxfp4_row_bytes(a.cols)) or not a.codes.is_contiguous():
+        raise ValueError("a.codes must be a contiguous uint8 tensor [rows, 16 * ceil(cols / 32)]")
+    if a.scales.dtype != torch.uint8 or a.scales.numel() < mxfp4_grouped_scale_bytes(a.rows, a.cols, groups):
+        raise ValueError("a.scales must hold mxfp4_grouped_scale_bytes(rows, cols, groups) bytes")
+    if out_dtype not in _TYPES:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    with _on(stream):
+        out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
+        _check(mxfp4_matmul_grouped(a.codes, a.scales, a.rows, groups, offsets, b.codes, b.scales, b.rows, a.cols, out,
+                                    _TYPES[out_dtype], err_flag), "mxfp4_matmul_grouped")
+    return out
