@@ -304,7 +304,8 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
         return MXFP8_ERR_DEVICE;
     const int64_t row_bytes = ceil_div(K, 32) * 16;
     CUtensorMap pm, qm;
-    if ((st = code_map(&pm, b_codes, N, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, a_codes, M, row_bytes, kGemmQBox)) != MXFP8_OK)
+    p.q_box = M > 64 ? 128 : 32;  // few rows: a small box leaves most of the tile unread
+    if ((st = code_map(&pm, b_codes, N, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, a_codes, M, row_bytes, p.q_box)) != MXFP8_OK)
         return st;
     const int64_t tiles = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
     return out_type == MXFP4_F32 ? launch_gemm_as<128, true, false>(pm, qm, p, tiles, device, stream)
@@ -345,8 +346,9 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
     p.err_flag = err_flag;
     const int64_t row_bytes = ceil_div(K, 32) * 16;
     CUtensorMap pm, qm;
+    p.q_box = total_rows > int64_t{64} * num_groups ? 128 : 32;
     if ((st = code_map(&pm, b_codes, num_groups * N, row_bytes, kGemmRows)) != MXFP8_OK ||
-        (st = code_map(&qm, a_codes, total_rows, row_bytes, kGemmQBox)) != MXFP8_OK)
+        (st = code_map(&qm, a_codes, total_rows, row_bytes, p.q_box)) != MXFP8_OK)
         return st;
     return out_type == MXFP4_F32 ? launch_gemm_as<128, true, true>(pm, qm, p, bound, device, stream)
                                  : launch_gemm_as<128, false, true>(pm, qm, p, bound, device, stream);

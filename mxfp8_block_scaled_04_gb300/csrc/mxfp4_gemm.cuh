@@ -5,8 +5,8 @@
 // single token and a training batch.  Each block of 32 is scaled inside the MMA (kind::mxf4, two E8M0 scales
 // per 64 elements), so the operands go from HBM to the tensor core as they are stored.
 //
-// Roles (8 warps): warp 0 feeds a ring of shared-memory stages of 256 elements of K (TMA tiles of the codes, plain
-// bulk copies of the scale tiles), warp 1 copies scales to TMEM and issues the MMAs, warp 2 owns the TMEM
+// Roles (8 warps): warps 0 and 3 feed a ring of shared-memory stages of 256 elements of K (TMA tiles of the codes;
+// plain bulk copies of the scale tiles), warp 1 copies scales to TMEM and issues the MMAs, warp 2 owns the TMEM
 // allocation, warps 4-7 read the accumulators and write the output while the next tile accumulates in the other
 // TMEM buffer.  The CTAs are persistent over a round-robin tile list.  Every wait is bounded: on expiry the CTA
 // sets the library's fault word, waits (bounded) for its own copies and MMAs, frees its TMEM and returns.
@@ -24,9 +24,8 @@ namespace mxfp8 {
 
 constexpr int kGemmThreads = 256;
 constexpr int kGemmRows = 128;   // rows of P per tile
-constexpr int kGemmQBox = 32;    // rows of Q per TMA box
-constexpr uint64_t kGemmWaitNs = 2000000000ull;
-constexpr uint64_t kGemmDrainNs = 200000000ull;
+constexpr int64_t kGemmWait = 4000000000;   // cycles: about 2 s
+constexpr int64_t kGemmDrain = 400000000;
 
 struct GemmParams {
     const uint8_t *p_scale, *q_scale;
@@ -35,6 +34,7 @@ struct GemmParams {
     int k_iters;         // stages along K: ceil(K / 256)
     int k64;             // MMA steps along K: ceil(K / 64)
     int p_tiles, q_tiles;
+    int q_box;           // rows of Q per TMA box: 32 or 128
     void *out;
     int64_t ldo;
     unsigned *fault;
@@ -118,13 +118,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // warp-uniform for the compiler too
     const uint32_t base = (smem_u32(gemm_smem) + 1023u) & ~1023u;
     if (tid == 0) {
         prefetch_tensormap(&p_map);
         prefetch_tensormap(&q_map);
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&full[s]), 2);  // codes, scales
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -155,80 +156,124 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         atomicOr(p.fault, 1u);
     };
 
-    if (warp == 0 && lane == 0) {
-        // ---- producer ----
-        int it = 0;
+    // stage of the ring and the phase parity of its barriers, for a role's next iteration
+    int slot = 0;
+    uint32_t phase = 0;
+    auto advance = [&]() {
+        if (++slot == S::kStages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
+
+    if (warp == 0 || warp == 3) {
+        // ---- producers: codes (warp 0), scales (warp 3) ----
         bool ok = true;
+        int issued = 0;
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
             const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
-            const int boxes = (c.valid + kGemmQBox - 1) / kGemmQBox;
             const int q_blocks = (c.valid + 127) / 128;
-            for (int k = 0; k < p.k_iters; ++k, ++it) {
-                const int s = it % S::kStages;
-                if (it >= S::kStages && !mbar_wait_bounded(smem_u32(&empty[s]), ((it / S::kStages) - 1) & 1, kGemmWaitNs)) {
+            const int boxes = (c.valid + p.q_box - 1) / p.q_box;
+            const uint32_t code_bytes = S::kPBytes + boxes * p.q_box * 128;
+            const uint8_t *ps = p.p_scale + c.p_plane * p.kc * 512, *qs = p.q_scale + c.q_plane * p.kc * 512;
+            for (int k = 0; k < p.k_iters; ++k) {
+                // a fresh barrier's phase -1 counts as complete: the first round waits for nothing
+                ok = mbar_wait_cycles(empty0 + 8 * slot, phase ^ 1, kGemmWait);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
-                const uint32_t bar = smem_u32(&full[s]);
-                const uint32_t dp = base + s * S::kStage, dq = dp + S::kPBytes, dps = dq + S::kQBytes, dqs = dps + S::kPScale;
-                const uint32_t sb = 512u * min(2, p.kc - 2 * k);
-                mbar_arrive_expect_tx(bar, S::kPBytes + boxes * kGemmQBox * 128 + sb * (1 + q_blocks));
-                tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
-                for (int b = 0; b < boxes; ++b)
-                    tma_load_2d_shared(dq + b * kGemmQBox * 128, &q_map, bar, k * 128, c.q_row + b * kGemmQBox);
-                bulk_load(dps, p.p_scale + (c.p_plane * p.kc + 2 * k) * 512, sb, bar);
-                for (int b = 0; b < q_blocks; ++b)
-                    bulk_load(dqs + b * 1024, p.q_scale + ((c.q_plane + b) * p.kc + 2 * k) * 512, sb, bar);
+                const uint32_t bar = full0 + 8 * slot, dp = base + slot * S::kStage;
+                if (elect_one()) {
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx(bar, code_bytes);
+                        tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d_shared(dp + S::kPBytes + b * p.q_box * 128, &q_map, bar, k * 128, c.q_row + b * p.q_box);
+                    } else {
+                        const uint32_t sb = 512u * min(2, p.kc - 2 * k), ds = dp + S::kPBytes + S::kQBytes;
+                        mbar_arrive_expect_tx(bar, sb * (1 + q_blocks));
+                        bulk_load(ds, ps + k * 1024, sb, bar);
+                        for (int b = 0; b < q_blocks; ++b)
+                            bulk_load(ds + S::kPScale + b * 1024, qs + static_cast<int64_t>(b) * p.kc * 512 + k * 1024, sb, bar);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                advance();
             }
         }
         if (!ok) {
-            give_up();
-            for (int j = it < S::kStages ? 0 : it - S::kStages; j < it; ++j)  // copies in flight
-                mbar_wait_bounded(smem_u32(&full[j % S::kStages]), (j / S::kStages) & 1, kGemmDrainNs);
+            if (lane == 0)
+                give_up();
+            for (int j = 0; j < S::kStages && j < issued; ++j) {  // copies in flight, the newest first
+                if (--slot < 0) {
+                    slot = S::kStages - 1;
+                    phase ^= 1;
+                }
+                mbar_wait_cycles(full0 + 8 * slot, phase, kGemmDrain);
+            }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---- MMA ----
-        int it = 0, n_tile = 0;
+        int n_tile = 0;
         bool ok = true;
+        const uint64_t p_desc = desc_sw128(base), q_desc = desc_sw128(base + S::kPBytes);
+        const uint64_t s_desc = desc_scales(base + S::kPBytes + S::kQBytes);
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++n_tile) {
             const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
             const int n = (c.valid + 15) & ~15;
-            const int q_blocks = (c.valid + 127) / 128;
             const int buf = n_tile & 1;
-            const uint32_t d = tmem + buf * QT;
-            if (n_tile >= 2 && !mbar_wait_bounded(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWaitNs)) {
+            const uint32_t d = tmem + buf * QT, sf = tmem + S::kScaleBase;
+            const uint32_t idesc0 = mxf4_idesc(kGemmRows, n, 0), idesc1 = mxf4_idesc(kGemmRows, n, 1);
+            if (n_tile >= 2)
+                ok = mbar_wait_cycles(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWait);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            for (int k = 0; k < p.k_iters; ++k, ++it) {
-                const int s = it % S::kStages;
-                if (!mbar_wait_bounded(smem_u32(&full[s]), (it / S::kStages) & 1, kGemmWaitNs)) {
+            for (int k = 0; k < p.k_iters; ++k) {
+                ok = mbar_wait_cycles(full0 + 8 * slot, phase, kGemmWait);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t dp = base + s * S::kStage, dq = dp + S::kPBytes, dps = dq + S::kQBytes, dqs = dps + S::kPScale;
-                const uint32_t sf = tmem + S::kScaleBase + (it & 1) * S::kScaleCols;
-                const int chunks = min(2, p.kc - 2 * k);
-                for (int ch = 0; ch < chunks; ++ch) {
-                    tc_copy_scales(sf + ch * 4, desc_scales(dps + ch * 512));
-                    for (int b = 0; b < q_blocks; ++b)
-                        tc_copy_scales(sf + 8 + (ch * (QT / 128) + b) * 4, desc_scales(dqs + b * 1024 + ch * 512));
+                if (elect_one()) {
+                    const uint32_t step = slot * (S::kStage >> 4);  // descriptors count 16-byte units
+                    const uint64_t pd = p_desc + step, qd = q_desc + step, sd = s_desc + step;
+                    const int left = p.k64 - 4 * k;  // MMA steps from here on
+#pragma unroll
+                    for (int ch = 0; ch < 2; ++ch) {
+                        if (left <= 2 * ch)
+                            break;
+                        // each half of a stage has its own TMEM columns for its scales; copies and MMAs run in issue order
+                        const uint32_t sp = sf + ch * (S::kScaleCols / 2), sq = sp + 4;
+                        tc_copy_scales(sp, sd + ch * 32);
+#pragma unroll
+                        for (int b = 0; b < QT / 128; ++b)
+                            tc_copy_scales(sq + b * 4, sd + (S::kPScale + b * 1024 + ch * 512) / 16);
+                        tc_mma_mxf4(d, pd + ch * 4, qd + ch * 4, idesc0, sp, sq, k > 0 || ch > 0);
+                        if (left > 2 * ch + 1)
+                            tc_mma_mxf4(d, pd + ch * 4 + 2, qd + ch * 4 + 2, idesc1, sp, sq, true);
+                    }
+                    tc_commit(empty0 + 8 * slot);
+                    if (k == p.k_iters - 1)
+                        tc_commit(smem_u32(&acc_full[buf]));
                 }
-                const int steps = min(4, p.k64 - 4 * k);
-                for (int j = 0; j < steps; ++j)
-                    tc_mma_mxf4(d, desc_sw128(dp + j * 32), desc_sw128(dq + j * 32), mxf4_idesc(kGemmRows, n, j & 1), sf + (j >> 1) * 4,
-                                sf + 8 + (j >> 1) * (QT / 128) * 4, k > 0 || j > 0);
-                tc_commit(smem_u32(&empty[s]));
+                __syncwarp();
+                advance();
             }
-            if (ok)
-                tc_commit(smem_u32(&acc_full[buf]));
         }
         if (!ok) {
-            give_up();
-            tc_commit(smem_u32(&drain));
-            mbar_wait_bounded(smem_u32(&drain), 0, kGemmDrainNs);
+            if (elect_one()) {
+                give_up();
+                tc_commit(smem_u32(&drain));
+            }
+            __syncwarp();
+            mbar_wait_cycles(smem_u32(&drain), 0, kGemmDrain);
         }
     } else if (warp >= 4) {
         // ---- epilogue ----
@@ -237,7 +282,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
             const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
-            const bool done = mbar_wait_bounded(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWaitNs);
+            const bool done = mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait);
             if (!__all_sync(0xFFFFFFFFu, done)) {
                 if (lane == 0)
                     give_up();

@@ -5,11 +5,35 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "ptx.cuh"
+
 namespace mxfp8 {
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Wait for the phase with the given parity; gives up after `limit` clock cycles.
+__device__ __forceinline__ bool mbar_wait_cycles(uint32_t bar, uint32_t parity, int64_t limit)
+{
+    if (mbar_try_wait_parity(bar, parity))
+        return true;
+    const int64_t t0 = clock64();
+    while (!mbar_try_wait_parity(bar, parity)) {
+        if (clock64() - t0 > limit)
+            return false;
+    }
+    return true;
+}
+
+// One lane of a converged warp.  The warps that issue copies and MMAs run their loops as whole warps and elect a
+// lane for the issue alone, so that addresses and descriptors stay warp-uniform.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.

@@ -11,8 +11,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _addr, _stream, lib
-from .mxfp4 import _TYPES, _check, _check_input, _on
+from .binding import _addr, lib
+from .mxfp4 import _check, _check_input, _on, _stream
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_TOPK = 32
@@ -67,10 +67,12 @@ def moe_combine_backward_c(dout, y, R, H, slots, weights, T, k, dy, dweights, st
 
 
 # ---- torch conveniences ----------------------------------------------------------
+# A given ``stream`` is made current around the whole call, so that outputs and workspace belong to it.
 
-def _check_like(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
-    if t.dtype != dtype or t.dim() != 2 or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+def _check_like(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
+    if t.dtype != dtype or t.dim() != 2 or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" {list(shape)}" if shape else " [., .]"))
+    return t.shape
 
 
 def make_route_config(top_k: int, score="softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
@@ -88,61 +90,64 @@ def moe_route(logits: torch.Tensor, k: int, score="softmax", bias: Optional[torc
     ``groups`` the choice is limited to the best groups of consecutive experts; ``renormalize`` divides the
     weights by their sum; ``scale`` multiplies them.
     """
-    ld = _check_input(logits, "logits")
-    T, E = logits.shape
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or not bias.is_contiguous()):
+    if stream is not None:
+        with _on(stream):
+            return moe_route(logits, k, score, bias, groups, topk_groups, renormalize, scale)
+    kind, T, E, ld = _check_input(logits, "logits")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 tensor [{E}]")
     cfg = make_route_config(k, score, bias, groups, topk_groups, renormalize, scale)
-    with _on(stream):
-        indices = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-        _check(moe_route_c(logits, _TYPES[logits.dtype], T, E, ld, cfg, indices, weights), "moe_route")
+    dev = logits.device
+    indices = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _check(moe_route_c(logits, kind, T, E, ld, cfg, indices, weights), "moe_route")
     return MoERoute(indices, weights)
 
 
 def moe_route_backward(logits: torch.Tensor, indices: torch.Tensor, grad_weights: torch.Tensor, score="softmax",
                        renormalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
     """Gradient of moe_route's weights with respect to the logits (the choice and the bias are constants)."""
-    ld = _check_input(logits, "logits")
-    T, E = logits.shape
-    _check_like(indices, "indices", torch.int32)
-    _check_like(grad_weights, "grad_weights", torch.float32, tuple(indices.shape))
-    if indices.shape[0] != T:
+    if stream is not None:
+        with _on(stream):
+            return moe_route_backward(logits, indices, grad_weights, score, renormalize, scale)
+    kind, T, E, ld = _check_input(logits, "logits")
+    rows, k = _check_like(indices, "indices", torch.int32)
+    _check_like(grad_weights, "grad_weights", torch.float32, (rows, k))
+    if rows != T:
         raise ValueError(f"indices must have {T} rows")
-    cfg = make_route_config(indices.shape[1], score, None, 1, 1, renormalize, scale)
-    with _on(stream):
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        _check(moe_route_backward_c(logits, _TYPES[logits.dtype], T, E, ld, cfg, indices, grad_weights, out),
-               "moe_route_backward")
+    cfg = make_route_config(k, score, None, 1, 1, renormalize, scale)
+    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check(moe_route_backward_c(logits, kind, T, E, ld, cfg, indices, grad_weights, out), "moe_route_backward")
     return out
 
 
 def moe_plan(indices: torch.Tensor, num_experts: int, stream=None) -> MoEPlan:
     """Sort the choices ``indices`` (int32 [T, k]) by expert, in order within an expert."""
-    _check_like(indices, "indices", torch.int32)
-    T, k = indices.shape
+    if stream is not None:
+        with _on(stream):
+            return moe_plan(indices, num_experts)
+    T, k = _check_like(indices, "indices", torch.int32)
     dev = indices.device
-    with _on(stream):
-        offsets = torch.empty((num_experts + 1,), dtype=torch.int64, device=dev)
-        slots = torch.empty((T, k), dtype=torch.int32, device=dev)
-        tokens = torch.empty((T * k,), dtype=torch.int32, device=dev)
-        nbytes = moe_plan_workspace_bytes(T * k, num_experts)
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
-        _check(moe_plan_c(indices, T * k, k, num_experts, offsets, slots, tokens, workspace), "moe_plan")
+    offsets = torch.empty((num_experts + 1,), dtype=torch.int64, device=dev)
+    slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+    tokens = torch.empty((T * k,), dtype=torch.int32, device=dev)
+    nbytes = moe_plan_workspace_bytes(T * k, num_experts)
+    workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    _check(moe_plan_c(indices, T * k, k, num_experts, offsets, slots, tokens, workspace), "moe_plan")
     return MoEPlan(offsets, slots, tokens)
 
 
 def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * y[slots[t, j]] (bf16 rows, fp32 sums; no ``weights``: all 1)."""
-    _check_like(y, "y", torch.bfloat16)
-    _check_like(slots, "slots", torch.int32)
+    if stream is not None:
+        with _on(stream):
+            return moe_combine(y, slots, weights)
+    R, H = _check_like(y, "y", torch.bfloat16)
+    T, k = _check_like(slots, "slots", torch.int32)
     if weights is not None:
-        _check_like(weights, "weights", torch.float32, tuple(slots.shape))
-    T, k = slots.shape
-    R, H = y.shape
-    with _on(stream):
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-        _check(moe_combine_c(y, R, H, slots, weights, T, k, out), "moe_combine")
+        _check_like(weights, "weights", torch.float32, (T, k))
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    _check(moe_combine_c(y, R, H, slots, weights, T, k, out), "moe_combine")
     return out
 
 
@@ -150,15 +155,15 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tenso
                          stream=None):
     """(grad_y, grad_weights) of moe_combine.  The slots name every row of y (as moe_plan's do, dropped choices
     included); rows past T * k get zeros."""
-    _check_like(y, "y", torch.bfloat16)
-    _check_like(slots, "slots", torch.int32)
-    T, k = slots.shape
-    R, H = y.shape
+    if stream is not None:
+        with _on(stream):
+            return moe_combine_backward(grad, y, slots, weights)
+    R, H = _check_like(y, "y", torch.bfloat16)
+    T, k = _check_like(slots, "slots", torch.int32)
     _check_like(grad, "grad", torch.bfloat16, (T, H))
     if weights is not None:
         _check_like(weights, "weights", torch.float32, (T, k))
-    with _on(stream):
-        dy = (torch.zeros if R > T * k else torch.empty)((R, H), dtype=torch.bfloat16, device=y.device)
-        dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
-        _check(moe_combine_backward_c(grad, y, R, H, slots, weights, T, k, dy, dweights), "moe_combine_backward")
+    dy = (torch.zeros if R > T * k else torch.empty)((R, H), dtype=torch.bfloat16, device=y.device)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    _check(moe_combine_backward_c(grad, y, R, H, slots, weights, T, k, dy, dweights), "moe_combine_backward")
     return dy, dweights

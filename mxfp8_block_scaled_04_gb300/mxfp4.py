@@ -7,12 +7,12 @@ given) and raise :class:`MXFP8Error` on a non-OK status.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import MXFP8Error, _addr, _stream, lib
+from .binding import MXFP8Error, _addr, lib
+from .binding import _stream as _any_stream
 
 TYPE_BF16 = 0
 TYPE_F32 = 1
@@ -34,6 +34,14 @@ class MXFP4Tensor(NamedTuple):
     col: Optional[MXFP4Matrix]  # x transposed [N, M]
 
 
+def _stream(stream) -> Optional[int]:
+    """The cudaStream_t of ``stream``, or of the current device's current stream (by torch's raw getter, which
+    costs a tenth of a microsecond where torch.cuda.current_stream() costs three)."""
+    if stream is None and torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _any_stream(stream)
+
+
 # ---- one-for-one C entry points --------------------------------------------------
 
 def mxfp4_row_bytes(cols: int) -> int:
@@ -45,7 +53,9 @@ def mxfp4_scale_bytes(rows: int, cols: int) -> int:
 
 
 def mxfp4_grouped_scale_bytes(total_rows: int, cols: int, num_groups: int) -> int:
-    return int(lib().mxfp4_grouped_scale_bytes(total_rows, cols, num_groups))
+    if total_rows <= 0 or cols <= 0 or num_groups < 1:
+        return 0
+    return (total_rows // 128 + min(num_groups, total_rows)) * -(-cols // 128) * 512
 
 
 def mxfp4_quantize(x, x_type, M, N, ldx, out_row, scale_row, out_col, scale_col, noop=None, stream=None) -> int:
@@ -76,14 +86,11 @@ def mxfp4_matmul_grouped(a_codes, a_scale, total_rows, num_groups, offsets, b_co
 
 
 # ---- torch conveniences ----------------------------------------------------------
+# A given ``stream`` is made current around the whole call, so that the outputs belong to it.
 
 def _on(stream):
-    """Make ``stream`` (a torch stream or a cudaStream_t address) current, so that outputs belong to it."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+    """The context of ``stream`` (a torch stream or a cudaStream_t address)."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 def _check(status: int, what: str) -> None:
@@ -91,11 +98,16 @@ def _check(status: int, what: str) -> None:
         raise MXFP8Error(status, what)
 
 
-def _check_input(x: torch.Tensor, name: str = "x") -> int:
-    """Row pitch of a 2-D bf16 / fp32 tensor whose rows are contiguous."""
-    if x.dtype not in _TYPES or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+def _check_input(x: torch.Tensor, name: str = "x"):
+    """(type, rows, columns, row pitch) of a 2-D bf16 / fp32 tensor whose rows are contiguous."""
+    kind = _TYPES.get(x.dtype)
+    if kind is None or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bfloat16 or float32 tensor with contiguous rows")
-    return max(x.shape[1], x.stride(0)) if min(x.shape[0] - 1, x.shape[1]) > 0 else x.shape[1]
+    rows, cols = x.shape
+    pitch, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D bfloat16 or float32 tensor with contiguous rows")
+    return kind, rows, cols, pitch if rows > 1 and pitch > cols and cols > 0 else cols
 
 
 def _check_offsets(offsets: torch.Tensor) -> int:
@@ -110,20 +122,28 @@ def _check_err(err_flag) -> None:
 
 
 def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None) -> None:
-    lead = () if groups is None else (groups,)
-    plane = mxfp4_scale_bytes(m.rows, m.cols)
-    if (m.codes.dtype != torch.uint8 or tuple(m.codes.shape) != lead + (m.rows, mxfp4_row_bytes(m.cols)) or
-            not m.codes.is_contiguous()):
-        raise ValueError(f"{name}.codes must be a contiguous uint8 tensor {lead + (m.rows, mxfp4_row_bytes(m.cols))}")
-    if m.scales.dtype != torch.uint8 or not m.scales.is_contiguous() or (
-            m.scales.numel() < plane if groups is None else tuple(m.scales.shape) != (groups, plane)):
+    codes, scales, rows, cols = m
+    pitch = -(-cols // 32) * 16
+    plane = -(-rows // 128) * -(-cols // 128) * 512
+    shape = (rows, pitch) if groups is None else (groups, rows, pitch)
+    if codes.dtype != torch.uint8 or codes.shape != shape or not codes.is_contiguous():
+        raise ValueError(f"{name}.codes must be a contiguous uint8 tensor {list(shape)}")
+    if scales.dtype != torch.uint8 or not scales.is_contiguous() or (
+            scales.numel() < plane if groups is None else scales.shape != (groups, plane)):
         raise ValueError(f"{name}.scales must be a contiguous uint8 tensor of {plane} bytes per matrix")
+
+
+def _check_out_dtype(dtype: torch.dtype) -> int:
+    kind = _TYPES.get(dtype)
+    if kind is None:
+        raise ValueError("the output type must be torch.bfloat16 or torch.float32")
+    return kind
 
 
 def _empty_matrix(rows: int, cols: int, device) -> MXFP4Matrix:
     u8 = torch.uint8
-    return MXFP4Matrix(torch.empty((rows, mxfp4_row_bytes(cols)), dtype=u8, device=device),
-                       torch.empty((mxfp4_scale_bytes(rows, cols),), dtype=u8, device=device), rows, cols)
+    return MXFP4Matrix(torch.empty((rows, -(-cols // 32) * 16), dtype=u8, device=device),
+                       torch.empty((-(-rows // 128) * -(-cols // 128) * 512,), dtype=u8, device=device), rows, cols)
 
 
 def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, noop: Optional[torch.Tensor] = None,
@@ -133,13 +153,15 @@ def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False,
     ``row`` is x with blocks along its rows; ``col`` is x transposed with blocks along M, the operand of
     the products that sum over M (input and weight gradients).
     """
-    ld = _check_input(x)
-    M, N = x.shape
-    with _on(stream):
-        row = _empty_matrix(M, N, x.device) if rowwise else None
-        col = _empty_matrix(N, M, x.device) if colwise else None
-        _check(mxfp4_quantize(x, _TYPES[x.dtype], M, N, ld, row and row.codes, row and row.scales, col and col.codes,
-                              col and col.scales, noop), "mxfp4_quantize")
+    if stream is not None:
+        with _on(stream):
+            return quantize_mxfp4(x, rowwise, colwise, noop)
+    kind, M, N, ld = _check_input(x)
+    dev = x.device
+    row = _empty_matrix(M, N, dev) if rowwise else None
+    col = _empty_matrix(N, M, dev) if colwise else None
+    _check(mxfp4_quantize(x, kind, M, N, ld, row and row.codes, row and row.scales, col and col.codes,
+                          col and col.scales, noop), "mxfp4_quantize")
     return MXFP4Tensor(row, col)
 
 
@@ -147,52 +169,54 @@ def quantize_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: Optiona
                            err_flag: Optional[torch.Tensor] = None, stream=None) -> MXFP4Matrix:
     """The rowwise cast of x's rows gathered for experts: output row i is x[rows[i]] (x[i] without ``rows``),
     expert g owns rows [offsets[g], offsets[g + 1]) (device int64) and has a scale plane of its own."""
-    ld = _check_input(x)
+    if stream is not None:
+        with _on(stream):
+            return quantize_mxfp4_grouped(x, offsets, rows, err_flag)
+    kind, T, N, ld = _check_input(x)
     groups = _check_offsets(offsets)
     _check_err(err_flag)
     if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous()):
         raise ValueError("rows must be a contiguous 1-D int32 tensor")
-    T, N = x.shape
     total = T if rows is None else rows.numel()
-    with _on(stream):
-        u8 = dict(dtype=torch.uint8, device=x.device)
-        codes = torch.empty((total, mxfp4_row_bytes(N)), **u8)
-        scales = torch.empty((mxfp4_grouped_scale_bytes(total, N, groups),), **u8)
-        _check(mxfp4_quantize_grouped(x, _TYPES[x.dtype], T, N, ld, rows, total, groups, offsets, codes, scales,
-                                      err_flag), "mxfp4_quantize_grouped")
+    dev = x.device
+    codes = torch.empty((total, mxfp4_row_bytes(N)), dtype=torch.uint8, device=dev)
+    scales = torch.empty((mxfp4_grouped_scale_bytes(total, N, groups),), dtype=torch.uint8, device=dev)
+    _check(mxfp4_quantize_grouped(x, kind, T, N, ld, rows, total, groups, offsets, codes, scales, err_flag),
+           "mxfp4_quantize_grouped")
     return MXFP4Matrix(codes, scales, total, N)
 
 
 def dequantize_mxfp4(m: MXFP4Matrix, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """The values [rows, cols] of a 4-bit matrix (exact in bf16 and fp32)."""
-    if dtype not in _TYPES:
-        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    if stream is not None:
+        with _on(stream):
+            return dequantize_mxfp4(m, dtype)
+    kind = _check_out_dtype(dtype)
     _check_matrix(m, "m")
-    with _on(stream):
-        out = torch.empty((m.rows, m.cols), dtype=dtype, device=m.codes.device)
-        _check(mxfp4_dequantize(m.codes, m.scales, m.rows, m.cols, out, _TYPES[dtype]), "mxfp4_dequantize")
+    out = torch.empty((m.rows, m.cols), dtype=dtype, device=m.codes.device)
+    _check(mxfp4_dequantize(m.codes, m.scales, m.rows, m.cols, out, kind), "mxfp4_dequantize")
     return out
 
 
 def matmul_mxfp4(a: MXFP4Matrix, b: MXFP4Matrix, out_dtype: torch.dtype = torch.bfloat16,
                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a [M, K] times b [N, K] transposed: [M, N] in ``out_dtype``, or into ``out`` (rows contiguous)."""
+    if stream is not None:
+        with _on(stream):
+            return matmul_mxfp4(a, b, out_dtype, out)
     _check_matrix(a, "a")
     _check_matrix(b, "b")
-    if a.cols != b.cols:
-        raise ValueError(f"a has {a.cols} columns, b has {b.cols}")
-    with _on(stream):
-        if out is None:
-            if out_dtype not in _TYPES:
-                raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-            out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
-            ldo = b.rows
-        else:
-            if tuple(out.shape) != (a.rows, b.rows):
-                raise ValueError(f"out must be [{a.rows}, {b.rows}]")
-            ldo = _check_input(out, "out")
-        _check(mxfp4_matmul(a.codes, a.scales, a.rows, b.codes, b.scales, b.rows, a.cols, out, _TYPES[out.dtype], ldo),
-               "mxfp4_matmul")
+    M, N, K = a.rows, b.rows, a.cols
+    if K != b.cols:
+        raise ValueError(f"a has {K} columns, b has {b.cols}")
+    if out is None:
+        kind, ldo = _check_out_dtype(out_dtype), N
+        out = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
+    else:
+        kind, rows, cols, ldo = _check_input(out, "out")
+        if (rows, cols) != (M, N):
+            raise ValueError(f"out must be [{M}, {N}]")
+    _check(mxfp4_matmul(a.codes, a.scales, M, b.codes, b.scales, N, K, out, kind, ldo), "mxfp4_matmul")
     return out
 
 
@@ -200,19 +224,21 @@ def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, 
                          err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Experts' products: rows [offsets[g], offsets[g + 1]) of a (from quantize_mxfp4_grouped) times expert g's
     b [N, K] transposed; b.codes [G, N, .], b.scales [G, .].  Returns [total_rows, N]."""
+    if stream is not None:
+        with _on(stream):
+            return matmul_mxfp4_grouped(a, offsets, b, out_dtype, err_flag)
     groups = _check_offsets(offsets)
     _check_err(err_flag)
     _check_matrix(b, "b", groups)
-    if a.cols != b.cols:
-        raise ValueError(f"a has {a.cols} columns, b has {b.cols}")
-    if a.codes.dtype != torch.uint8 or tuple(a.codes.shape) != (a.rows, mxfp4_row_bytes(a.cols)) or not a.codes.is_contiguous():
+    kind = _check_out_dtype(out_dtype)
+    codes, scales, R, K = a
+    if K != b.cols:
+        raise ValueError(f"a has {K} columns, b has {b.cols}")
+    if codes.dtype != torch.uint8 or codes.shape != (R, mxfp4_row_bytes(K)) or not codes.is_contiguous():
         raise ValueError("a.codes must be a contiguous uint8 tensor [rows, 16 * ceil(cols / 32)]")
-    if a.scales.dtype != torch.uint8 or a.scales.numel() < mxfp4_grouped_scale_bytes(a.rows, a.cols, groups):
+    if scales.dtype != torch.uint8 or scales.numel() < mxfp4_grouped_scale_bytes(R, K, groups) or not scales.is_contiguous():
         raise ValueError("a.scales must hold mxfp4_grouped_scale_bytes(rows, cols, groups) bytes")
-    if out_dtype not in _TYPES:
-        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-    with _on(stream):
-        out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
-        _check(mxfp4_matmul_grouped(a.codes, a.scales, a.rows, groups, offsets, b.codes, b.scales, b.rows, a.cols, out,
-                                    _TYPES[out_dtype], err_flag), "mxfp4_matmul_grouped")
+    out = torch.empty((R, b.rows), dtype=out_dtype, device=codes.device)
+    _check(mxfp4_matmul_grouped(codes, scales, R, groups, offsets, b.codes, b.scales, b.rows, K, out, kind, err_flag),
+           "mxfp4_matmul_grouped")
     return out
