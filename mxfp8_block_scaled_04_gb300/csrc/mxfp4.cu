@@ -7,6 +7,7 @@
 #include "host.h"
 #include "mxfp4_cast.cuh"
 #include "mxfp4_gemm.cuh"
+#include "mxfp4_pair.cuh"
 
 namespace {
 
@@ -14,6 +15,9 @@ using namespace mxfp8;
 
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxDim = int64_t{1} << 31;
+
+constexpr int64_t kPairMinTiles = 76;       // tiles of CTA pairs: one for each pair of the GPU's 152 SMs
+constexpr int64_t kPairMinGroupRows = 192;  // rows per expert on average
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -88,6 +92,41 @@ mxfp8_status_t launch_gemm_as(const CUtensorMap &pm, const CUtensorMap &qm, cons
     return launch_serialized(mxfp4_gemm_kernel<QT, F32, GROUPED>, dim3(grid), kGemmThreads, smem, 1, stream, pm, qm, p);
 }
 
+// The scale plane as rows of 512-byte tiles, in boxes of 1024 bytes (one stage) x box_rows tile rows.
+mxfp8_status_t scale_map(CUtensorMap *map, const void *scale, int64_t tile_rows, int64_t kc, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr)
+        return MXFP8_ERR_DEVICE;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kc) * 128, static_cast<cuuint64_t>(tile_rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(kc) * 512};
+    cuuint32_t box[2] = {256, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(scale), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? MXFP8_OK
+               : MXFP8_ERR_LAUNCH;
+}
+
+// The pair kernel.  p_rows: rows of P's map (all experts); plane rows likewise.
+template <bool F32, bool GROUPED>
+mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t p_rows, int64_t p_plane_rows, const void *q_codes,
+                              int64_t q_plane_rows, int64_t row_bytes, int64_t tiles, int device, cudaStream_t stream)
+{
+    static KernelSetup setup;
+    int ctas = 0;
+    mxfp8_status_t st = setup(mxfp4_pair_kernel<F32, GROUPED>, device, kGemmThreads, kPairSmem, &ctas);
+    if (st != MXFP8_OK)
+        return st;
+    CUtensorMap pm, qm, psm, qsm;
+    if ((st = code_map(&pm, p_codes, p_rows, row_bytes, 128)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, 128)) != MXFP8_OK ||
+        (st = scale_map(&psm, p.p_scale, p_plane_rows, p.kc, 1)) != MXFP8_OK || (st = scale_map(&qsm, p.q_scale, q_plane_rows, p.kc, 2)) != MXFP8_OK)
+        return st;
+    const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
+    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, kPairSmem, 2, stream, pm, qm, psm,
+                             qsm, p);
+}
+
 // Checks and parameters that both products share.  Q: the tokens' rows; P: the weights' rows (per expert).
 mxfp8_status_t gemm_params(GemmParams *p, const void *q_codes, const void *q_scale, int64_t Q, const void *p_codes, const void *p_scale, int64_t P,
                            int64_t K, void *out, int out_type, int64_t ldo)
@@ -116,6 +155,7 @@ mxfp8_status_t gemm_params(GemmParams *p, const void *q_codes, const void *q_sca
     p->k_iters = static_cast<int>(ceil_div(K, 256));
     p->k64 = static_cast<int>(ceil_div(pad, 64));
     p->p_tiles = static_cast<int>(ceil_div(P, kGemmRows));
+    p->p_planes = p->p_tiles;
     p->q_tiles = static_cast<int>(ceil_div(Q, 128));
     p->out = out;
     p->ldo = ldo;
@@ -303,6 +343,15 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     const int64_t row_bytes = ceil_div(K, 32) * 16;
+    // 256 x 256 tiles of CTA pairs once they fill the GPU; below that 128 x 128 tiles occupy more SMs
+    const int64_t pair_tiles = ceil_div(N, kPairRows) * ceil_div(M, kPairRows);
+    if (pair_tiles >= kPairMinTiles) {
+        p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
+        p.q_tiles = static_cast<int>(ceil_div(M, kPairRows));
+        return out_type == MXFP4_F32
+                   ? launch_pair_as<true, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream)
+                   : launch_pair_as<false, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream);
+    }
     CUtensorMap pm, qm;
     p.q_box = M > 64 ? 128 : 32;  // few rows: a small box leaves most of the tile unread
     if ((st = code_map(&pm, b_codes, N, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, a_codes, M, row_bytes, p.q_box)) != MXFP8_OK)
@@ -345,6 +394,16 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
     p.num_groups = num_groups;
     p.err_flag = err_flag;
     const int64_t row_bytes = ceil_div(K, 32) * 16;
+    // CTA pairs where an expert has more than one 128-row tile on average
+    if (total_rows >= kPairMinGroupRows * num_groups && total_rows / kPairRows * ceil_div(N, kPairRows) >= kPairMinTiles) {
+        const int64_t q_planes = static_cast<int64_t>(mxfp4_grouped_scale_bytes(total_rows, K, num_groups) / 512) / p.kc;
+        p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
+        const int64_t pair_bound = (total_rows / kPairRows + num_groups) * p.p_tiles;
+        return out_type == MXFP4_F32 ? launch_pair_as<true, true>(p, b_codes, num_groups * N, int64_t{num_groups} * p.p_planes, a_codes, q_planes,
+                                                                  row_bytes, pair_bound, device, stream)
+                                     : launch_pair_as<false, true>(p, b_codes, num_groups * N, int64_t{num_groups} * p.p_planes, a_codes, q_planes,
+                                                                   row_bytes, pair_bound, device, stream);
+    }
     CUtensorMap pm, qm;
     p.q_box = total_rows > int64_t{64} * num_groups ? 128 : 32;
     if ((st = code_map(&pm, b_codes, num_groups * N, row_bytes, kGemmRows)) != MXFP8_OK ||

@@ -34,6 +34,7 @@ struct GemmParams {
     int k_iters;         // stages along K: ceil(K / 256)
     int k64;             // MMA steps along K: ceil(K / 64)
     int p_tiles, q_tiles;
+    int p_planes;        // 128-row scale tiles of P (of one expert)
     int q_box;           // rows of Q per TMA box: 32 or 128
     void *out;
     int64_t ldo;
@@ -65,7 +66,7 @@ struct GemmTile {
 
 // Tile t.  Dense: bands of 8 Q tiles, P tiles in turn within a band, so that the CTAs at work share operands in
 // L2.  Grouped: an expert's Q tiles in turn, each over all of the expert's P tiles.
-template <int QT, bool GROUPED>
+template <int PT, int QT, bool GROUPED>
 __device__ __forceinline__ GemmTile gemm_tile(int t, const GemmParams &p, const GroupTable<GROUPED> &groups)
 {
     GemmTile r;
@@ -78,9 +79,9 @@ __device__ __forceinline__ GemmTile gemm_tile(int t, const GemmParams &p, const 
         r.valid = left < QT ? static_cast<int>(left) : QT;
         r.q_row = static_cast<int32_t>(q0);
         r.q_plane = groups.plane[g] + static_cast<int64_t>(local) * (QT / 128);
-        r.p0 = static_cast<int64_t>(pt) * kGemmRows;
+        r.p0 = static_cast<int64_t>(pt) * PT;
         r.p_row = static_cast<int32_t>(g * p.P + r.p0);
-        r.p_plane = static_cast<int64_t>(g) * p.p_tiles + pt;
+        r.p_plane = static_cast<int64_t>(g) * p.p_planes + pt * (PT / 128);
     } else {
         constexpr int kBand = 8;
         const int band = t / (kBand * p.p_tiles);
@@ -91,9 +92,9 @@ __device__ __forceinline__ GemmTile gemm_tile(int t, const GemmParams &p, const 
         r.valid = left < QT ? static_cast<int>(left) : QT;
         r.q_row = qt * QT;
         r.q_plane = static_cast<int64_t>(qt) * (QT / 128);
-        r.p0 = static_cast<int64_t>(pt) * kGemmRows;
+        r.p0 = static_cast<int64_t>(pt) * PT;
         r.p_row = static_cast<int32_t>(r.p0);
-        r.p_plane = pt;
+        r.p_plane = pt * (PT / 128);
     }
     return r;
 }
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         bool ok = true;
         int issued = 0;
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-            const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
+            const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
             const int q_blocks = (c.valid + 127) / 128;
             const int boxes = (c.valid + p.q_box - 1) / p.q_box;
             const uint32_t code_bytes = S::kPBytes + boxes * p.q_box * 128;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint64_t p_desc = desc_sw128(base), q_desc = desc_sw128(base + S::kPBytes);
         const uint64_t s_desc = desc_scales(base + S::kPBytes + S::kQBytes);
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++n_tile) {
-            const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
+            const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
             const int n = (c.valid + 15) & ~15;
             const int buf = n_tile & 1;
             const uint32_t d = tmem + buf * QT, sf = tmem + S::kScaleBase;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int quarter = warp & 3;
         int n_tile = 0;
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
-            const GemmTile c = gemm_tile<QT, GROUPED>(t, p, groups);
+            const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
             const bool done = mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait);
             if (!__all_sync(0xFFFFFFFFu, done)) {

@@ -224,7 +224,35 @@ def test_linear_layer_gradients(T, K, N):
     assert abs(slope - dx) <= 1e-9 * (dv[t].abs() @ wv[:, k].abs())
 
 
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(2048, 2560, 256), (2300, 2433, 1064), (257, 20000, 320), (19500, 140, 96)])
+def test_product_pair_tiles(M, N, K, out_dtype):
+    """Sizes of the 256 x 256 tiles: whole, ragged in every dimension, several tiles per CTA pair."""
+    check_product(M, N, K, out_dtype)
+
+
+def test_product_pair_tiles_exact_positions():
+    """Rows of P and Q that tell themselves apart (powers of two and small integers): exact results."""
+    M, N, K = 2304, 2304, 512
+    g = torch.Generator().manual_seed(4)
+    lv = torch.tensor([0.0, 0.5, 1.0, -1.0, 2.0, 3.0, -4.0, 6.0])
+    a, b = (lv[torch.randint(0, 8, (r, K), generator=g)] for r in (M, N))
+    a[:, ::32] = 6.0
+    b[:, ::32] = 6.0
+    a *= 2.0 ** torch.randint(-2, 3, (M, 1), generator=g)
+    b *= 2.0 ** torch.randint(-2, 3, (N, 1), generator=g)
+    qa, qb = mx.quantize_mxfp4(a.cuda()).row, mx.quantize_mxfp4(b.cuda()).row
+    got = mx.matmul_mxfp4(qa, qb, F32).cpu()
+    assert torch.equal(got, a @ b.t())
+
+
 # ---- experts' products -----------------------------------------------------------------------------------
+
+def test_experts_product_pair_tiles():
+    """Experts of several 256-row tiles, ragged, one of them empty."""
+    test_experts_product([700, 0, 1025, 256, 3, 1700], 1416, 328, BF16)
+    test_experts_product([5120, 1], 1000, 256, F32)
+
 
 SIZES = [[5], [0, 3, 0], [128, 0, 1, 127, 129], [1] * 40, [300, 2, 0, 0, 61], [0, 0, 257]]
 
