@@ -83,7 +83,7 @@ template <int QT, bool F32, bool GROUPED>
 mxfp8_status_t launch_gemm_as(const CUtensorMap &pm, const CUtensorMap &qm, const GemmParams &p, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr int smem = GemmShape<QT>::kSmem;
+    constexpr int smem = GemmShape<QT>::kSmem + kEpiBytes<F32>;
     int ctas = 0;
     const mxfp8_status_t st = setup(mxfp4_gemm_kernel<QT, F32, GROUPED>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
@@ -114,8 +114,9 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
                               int64_t q_plane_rows, int64_t row_bytes, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
+    constexpr int smem = kPairSmem + kEpiBytes<F32>;
     int ctas = 0;
-    mxfp8_status_t st = setup(mxfp4_pair_kernel<F32, GROUPED>, device, kGemmThreads, kPairSmem, &ctas);
+    mxfp8_status_t st = setup(mxfp4_pair_kernel<F32, GROUPED>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
     CUtensorMap pm, qm, psm, qsm;
@@ -123,7 +124,7 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
         (st = scale_map(&psm, p.p_scale, p_plane_rows, p.kc, 1)) != MXFP8_OK || (st = scale_map(&qsm, p.q_scale, q_plane_rows, p.kc, 2)) != MXFP8_OK)
         return st;
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
-    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, kPairSmem, 2, stream, pm, qm, psm,
+    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, pm, qm, psm,
                              qsm, p);
 }
 
@@ -159,6 +160,8 @@ mxfp8_status_t gemm_params(GemmParams *p, const void *q_codes, const void *q_sca
     p->q_tiles = static_cast<int>(ceil_div(Q, 128));
     p->out = out;
     p->ldo = ldo;
+    const int size = out_type == MXFP4_F32 ? 4 : 2;
+    p->vec_out = is_aligned(out, 16) && ldo * size % 16 == 0 && P * size % 16 == 0;
     return MXFP8_OK;
 }
 

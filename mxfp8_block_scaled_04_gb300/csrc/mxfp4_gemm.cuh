@@ -38,6 +38,7 @@ struct GemmParams {
     int q_box;           // rows of Q per TMA box: 32 or 128
     void *out;
     int64_t ldo;
+    bool vec_out;        // output rows are whole 16-byte vectors
     unsigned *fault;
     const int64_t *offsets;  // grouped
     int num_groups;
@@ -51,8 +52,8 @@ struct GemmShape {
     static constexpr int kPScale = 1024;               // two 512-byte scale tiles
     static constexpr int kQScale = QT / 128 * 1024;
     static constexpr int kStage = kPBytes + kQBytes + kPScale + kQScale;
-    static constexpr int kStages = 6;
-    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr int kStages = 5;
+    static constexpr int kSmem = kStages * kStage + 1024;  // + the epilogue's buffers
     static constexpr int kScaleCols = 8 + QT / 128 * 8;  // TMEM columns of one stage's scales
     static constexpr int kScaleBase = 2 * QT;
 };
@@ -106,6 +107,67 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, uint32_t bits)
         static_cast<float *>(out)[at] = __uint_as_float(bits);
     else
         static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(__uint_as_float(bits));
+}
+
+// ---- epilogue --------------------------------------------------------------------------------------------
+// A warp holds 32 output columns (its lanes) of 32 rows (registers).  Where output rows are whole 16-byte vectors
+// the four warps transpose through shared memory and write 32 rows of 128 columns in 16-byte pieces: a warp then
+// writes two 256-byte (fp32: one 512-byte) row pieces per instruction instead of 32 elements of one row, which made the
+// epilogue the bound (13 us per 256 x 256 tile, twice the time of its MMAs at K = 4096).
+
+constexpr int kEpiRows = 32;
+template <bool F32>
+constexpr int kEpiBytes = 2 * kEpiRows * kGemmRows * (F32 ? 4 : 2);  // two buffers
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+// Whether all 128 epilogue threads say so.
+__device__ __forceinline__ bool epilogue_all(bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(static_cast<uint32_t>(ok))
+                 : "memory");
+    return r != 0;
+}
+
+// Rows q0 .. q0 + 31 (of which `rows` are written) of 128 columns from col0; quarter: the warp's 32 lanes.
+template <bool F32>
+__device__ __forceinline__ void store_chunk(const GemmParams &p, const uint32_t (&v)[32], unsigned char *buffer, int quarter, int lane,
+                                            int64_t row0, int rows, int64_t col0)
+{
+    constexpr int kSize = F32 ? 4 : 2;
+    if (!p.vec_out) {
+        const int64_t col = col0 + quarter * 32 + lane;
+        if (col < p.P) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < rows)
+                    store_out<F32>(p.out, (row0 + j) * p.ldo + col, v[j]);
+        }
+        return;
+    }
+    constexpr int kRowBytes = kGemmRows * kSize;
+    unsigned char *dst = buffer + (quarter * 32 + lane) * kSize;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if constexpr (F32)
+            *reinterpret_cast<uint32_t *>(dst + j * kRowBytes) = v[j];
+        else
+            *reinterpret_cast<__nv_bfloat16 *>(dst + j * kRowBytes) = __float2bfloat16_rn(__uint_as_float(v[j]));
+    }
+    epilogue_sync();
+    constexpr int kVecs = kRowBytes / 16, kPerPass = 128 / kVecs;
+    const int tid = quarter * 32 + lane;
+    const int vec = tid % kVecs, r0 = tid / kVecs;
+    const bool live = col0 + vec * (16 / kSize) < p.P;
+    unsigned char *out = static_cast<unsigned char *>(p.out) + ((row0 + r0) * p.ldo + col0) * kSize + vec * 16;
+#pragma unroll
+    for (int i = 0; i < kEpiRows / kPerPass; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(buffer + (r0 + i * kPerPass) * kRowBytes + vec * 16);
+        if (live && r0 + i * kPerPass < rows)
+            *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(i) * kPerPass * p.ldo * kSize) = q;
+    }
 }
 
 template <int QT, bool F32, bool GROUPED>
@@ -279,26 +341,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= 4) {
         // ---- epilogue ----
         const int quarter = warp & 3;
-        int n_tile = 0;
+        unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + S::kStages * S::kStage;
+        int n_tile = 0, chunk = 0;
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
             const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
-            const bool done = mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait);
-            if (!__all_sync(0xFFFFFFFFu, done)) {
+            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     give_up();
                 break;
             }
             tc_fence_after();
-            const int64_t col = c.p0 + quarter * 32 + lane;
-            const bool live = col < p.P;
             for (int q = 0; q < c.valid; q += 32) {
                 uint32_t v[32];
                 tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * QT + q, v);
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (live && q + j < c.valid)
-                        store_out<F32>(p.out, (c.q_row + int64_t{q} + j) * p.ldo + col, v[j]);
+                store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q, c.p0);
             }
             tc_fence_before();
             __syncwarp();

@@ -14,11 +14,11 @@
 namespace mxfp8 {
 
 constexpr int kPairRows = 256;                    // rows of P, and of Q, per tile
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kPairCodes = 128 * 128;             // bytes of either operand's rows in one CTA
 constexpr int kPairPScale = 1024, kPairQScale = 2048;
 constexpr int kPairStage = 2 * kPairCodes + kPairPScale + kPairQScale;
-constexpr int kPairSmem = kPairStages * kPairStage + 1024;
+constexpr int kPairSmem = kPairStages * kPairStage + 1024;  // + the epilogue's buffers
 constexpr int kPairAcc1 = 224, kPairShared = 32, kPairScaleCol = 480;
 
 template <bool F32, bool GROUPED>
@@ -181,38 +181,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // ---- epilogue of this CTA's 128 columns of the output ----
         const int quarter = warp & 3;
         const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
-        int n_tile = 0;
+        unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kPairStages * kPairStage;
+        int n_tile = 0, chunk = 0;
         for (int t = first; t < num_tiles; t += stride, ++n_tile) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
-            const bool done = mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait);
-            if (!__all_sync(0xFFFFFFFFu, done)) {
+            if (!epilogue_all(mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
             }
             tc_fence_after();
-            const int64_t col = c.p0 + rank * 128 + quarter * 32 + lane;
-            const bool live = col < p.P;
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kPairAcc1;
             // the columns shared with the other accumulator first: 224..255 of accumulator 0, 0..31 of accumulator 1
             const int start = buf == 0 ? kPairAcc1 : 0;
             for (int i = 0; i < kPairRows / 32; ++i) {
                 const int q = (start + 32 * i) & (kPairRows - 1);
-                if (q < c.valid) {
-                    uint32_t v[32];
+                uint32_t v[32];
+                if (q < c.valid)
                     tmem_load32(d + q, v);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (live && q + j < c.valid)
-                            store_out<F32>(p.out, (c.q_row + int64_t{q} + j) * p.ldo + col, v[j]);
-                }
                 if (i == 0) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_cluster(lead_empty);
                 }
+                if (q < c.valid)
+                    store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q,
+                                     c.p0 + rank * 128);
             }
         }
     }
