@@ -42,7 +42,8 @@ FALLBACK_HBM_GBS = 6800.0
 # while these are unchanged since it was taken.
 KERNEL_SOURCES = [f"mxfp8_block_scaled_04_gb300/csrc/{f}"
                   for f in ("api.cu", "dact.cuh", "dbias_reduce.cuh", "dgated.cuh", "groups.cuh", "moe.cu", "moe.cuh",
-                            "mxfp4.cu", "mxfp4_cast.cuh", "mxfp4_gemm.cuh", "mxfp4_pair.cuh", "ptx.cuh", "quantize.cuh", "tcgen05.cuh")]
+                            "mxfp4.cu", "mxfp4_cast.cuh", "mxfp4_gemm.cuh", "mxfp4_pair.cuh",
+                            "mxfp4_split.cuh", "ptx.cuh", "quantize.cuh", "tcgen05.cuh")]
 
 
 def parse_args():

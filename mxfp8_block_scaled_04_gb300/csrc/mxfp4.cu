@@ -8,6 +8,7 @@
 #include "mxfp4_cast.cuh"
 #include "mxfp4_gemm.cuh"
 #include "mxfp4_pair.cuh"
+#include "mxfp4_split.cuh"
 
 namespace {
 
@@ -126,6 +127,42 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
     return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, pm, qm, psm,
                              qsm, p);
+}
+
+// The kernel for few tiles.  The number of CTAs that share a tile's K is the one with the least estimated time: rounds
+// of resident CTAs times the stages of each, plus the start and end of a CTA (about four stages, six with the
+// cluster's two barriers and the sum).
+template <int QROWS, bool F32>
+mxfp8_status_t launch_split_as(const GemmParams &p_, const void *p_codes, const void *q_codes, int64_t row_bytes, int device, cudaStream_t stream)
+{
+    static KernelSetup setup;
+    constexpr int smem = SplitShape<QROWS>::kSmem;
+    static_assert(SplitShape<QROWS>::kStage * SplitShape<QROWS>::kStages >= QROWS * kGemmRows * 4 &&
+                      SplitShape<QROWS>::kStage * SplitShape<QROWS>::kStages >= kEpiBytes<F32>,
+                  "partial sums and the epilogue's buffers fit the stages");
+    int slots = 0;
+    mxfp8_status_t st = setup(mxfp4_split_kernel<QROWS, F32>, device, kGemmThreads, smem, &slots);
+    if (st != MXFP8_OK)
+        return st;
+    GemmParams p = p_;
+    p.q_box = QROWS;
+    CUtensorMap pm, qm;
+    if ((st = code_map(&pm, p_codes, p.P, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, QROWS)) != MXFP8_OK)
+        return st;
+    // two CTAs share an SM (shared memory and TMEM halves); the occupancy query counts one for kernels that allocate TMEM
+    slots *= 2;
+    const int64_t tiles = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
+    int splits = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= 8 && s <= p.k_iters; s *= 2) {
+        const int64_t time = ceil_div(tiles * s, slots) * (ceil_div(p.k_iters, s) + (s > 1 ? 6 : 4));
+        if (time < least) {
+            least = time;
+            splits = s;
+        }
+    }
+    return launch_serialized(mxfp4_split_kernel<QROWS, F32>, dim3(static_cast<unsigned>(tiles * splits)), kGemmThreads, smem, splits, stream, pm, qm, p,
+                             splits);
 }
 
 // Checks and parameters that both products share.  Q: the tokens' rows; P: the weights' rows (per expert).
@@ -348,20 +385,18 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
     const int64_t row_bytes = ceil_div(K, 32) * 16;
     // 256 x 256 tiles of CTA pairs once they fill the GPU; below that 128 x 128 tiles occupy more SMs
     const int64_t pair_tiles = ceil_div(N, kPairRows) * ceil_div(M, kPairRows);
-    if (pair_tiles >= kPairMinTiles) {
+    if (M > 128 && pair_tiles >= kPairMinTiles) {
         p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
         p.q_tiles = static_cast<int>(ceil_div(M, kPairRows));
         return out_type == MXFP4_F32
                    ? launch_pair_as<true, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream)
                    : launch_pair_as<false, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream);
     }
-    CUtensorMap pm, qm;
-    p.q_box = M > 64 ? 128 : 32;  // few rows: a small box leaves most of the tile unread
-    if ((st = code_map(&pm, b_codes, N, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, a_codes, M, row_bytes, p.q_box)) != MXFP8_OK)
-        return st;
-    const int64_t tiles = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
-    return out_type == MXFP4_F32 ? launch_gemm_as<128, true, false>(pm, qm, p, tiles, device, stream)
-                                 : launch_gemm_as<128, false, false>(pm, qm, p, tiles, device, stream);
+    if (M <= 32)
+        return out_type == MXFP4_F32 ? launch_split_as<32, true>(p, b_codes, a_codes, row_bytes, device, stream)
+                                     : launch_split_as<32, false>(p, b_codes, a_codes, row_bytes, device, stream);
+    return out_type == MXFP4_F32 ? launch_split_as<128, true>(p, b_codes, a_codes, row_bytes, device, stream)
+                                 : launch_split_as<128, false>(p, b_codes, a_codes, row_bytes, device, stream);
 }
 
 mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, int64_t total_rows, int num_groups, const int64_t *offsets,

@@ -109,6 +109,11 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, uint32_t bits)
         static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(__uint_as_float(bits));
 }
 
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) | (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
+}
+
 // ---- epilogue --------------------------------------------------------------------------------------------
 // A warp holds 32 output columns (its lanes) of 32 rows (registers).  Where output rows are whole 16-byte vectors
 // the four warps transpose through shared memory and write 32 rows of 128 columns in 16-byte pieces: a warp then
