@@ -78,10 +78,16 @@ size_t mxfp4_grouped_scale_bytes(int64_t total_rows, int64_t cols, int num_group
  *   offsets      device int64 [num_groups + 1] from 0 to total_rows, non-decreasing, else nothing is
  *                written and *err_flag is set to 1.  1 <= num_groups <= MXFP8_MAX_GROUPS.
  *   err_flag     device int or NULL, never cleared here.
+ *   workspace    NULL, or device memory of mxfp4_quantize_grouped_workspace_bytes(T, N, total_rows) bytes,
+ *                16-byte aligned: with it, a gather of more rows than T casts every row of x once and gathers
+ *                the codes, to the same result (measured 3 times faster at 8 rows per token).
  */
 mxfp8_status_t mxfp4_quantize_grouped(const void *x, int x_type, int64_t T, int64_t N, int64_t ldx, const int32_t *rows,
                                       int64_t total_rows, int num_groups, const int64_t *offsets, void *out,
-                                      void *scale, int *err_flag, void *stream);
+                                      void *scale, int *err_flag, void *workspace, void *stream);
+
+/* 0 unless total_rows > T. */
+size_t mxfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t N, int64_t total_rows);
 
 /*
  * The values of a 4-bit matrix: out [rows, cols] (row pitch cols, any cols) in out_type.  Exact in both types, but

@@ -26,7 +26,7 @@ from .binding import (  # noqa: F401
 from .mxfp4 import (  # noqa: F401
     MXFP4Matrix, MXFP4Tensor, dequantize_mxfp4, matmul_mxfp4, matmul_mxfp4_grouped, mxfp4_dequantize,
     mxfp4_grouped_scale_bytes, mxfp4_matmul, mxfp4_matmul_grouped, mxfp4_quantize, mxfp4_quantize_grouped,
-    mxfp4_row_bytes, mxfp4_scale_bytes, quantize_mxfp4, quantize_mxfp4_grouped,
+    mxfp4_quantize_grouped_workspace_bytes,    mxfp4_row_bytes, mxfp4_scale_bytes, quantize_mxfp4, quantize_mxfp4_grouped,
 )
 from .moe import (  # noqa: F401
     MoEPlan, MoERoute, RouteConfig, make_route_config, moe_combine, moe_combine_backward, moe_combine_backward_c,

@@ -93,7 +93,8 @@ def lib():
                     ("mxfp4_scale_bytes", sz, [i64, i64]),
                     ("mxfp4_grouped_scale_bytes", sz, [i64, i64, i32]),
                     ("mxfp4_quantize", i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp]),
-                    ("mxfp4_quantize_grouped", i32, [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, vp]),
+                    ("mxfp4_quantize_grouped", i32, [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp]),
+                    ("mxfp4_quantize_grouped_workspace_bytes", sz, [i64, i64, i64]),
                     ("mxfp4_dequantize", i32, [vp, vp, i64, i64, vp, i32, vp]),
                     ("mxfp4_matmul", i32, [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]),
                     ("mxfp4_matmul_grouped", i32, [vp, vp, i64, i32, vp, vp, vp, i64, i64, vp, i32, vp, vp]),

@@ -56,7 +56,7 @@ template <bool F32, bool COL, bool GROUPED>
 mxfp8_status_t launch_cast_as(const CastParams &p, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr int smem = cast_smem_bytes<F32>(COL);
+    constexpr int smem = kCastSmem;
     int ctas = 0;
     const mxfp8_status_t st = setup(mxfp4_cast_kernel<F32, COL, GROUPED>, device, kCastThreads, smem, &ctas);
     if (st != MXFP8_OK)
@@ -281,8 +281,16 @@ mxfp8_status_t mxfp4_quantize(const void *x, int x_type, int64_t M, int64_t N, i
     return col ? launch_cast_as<false, true, false>(p, tiles, device, stream) : launch_cast_as<false, false, false>(p, tiles, device, stream);
 }
 
+// The two-step form's cast of the T rows: codes, then (16-byte aligned) the plane.
+size_t mxfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t N, int64_t total_rows)
+{
+    if (T <= 0 || N <= 0 || total_rows <= T)
+        return 0;
+    return static_cast<size_t>(T) * mxfp4_row_bytes(N) + mxfp4_scale_bytes(T, N);
+}
+
 mxfp8_status_t mxfp4_quantize_grouped(const void *x, int x_type, int64_t T, int64_t N, int64_t ldx, const int32_t *rows, int64_t total_rows,
-                                      int num_groups, const int64_t *offsets, void *out, void *scale, int *err_flag, void *stream_)
+                                      int num_groups, const int64_t *offsets, void *out, void *scale, int *err_flag, void *workspace, void *stream_)
 {
     if (!type_ok(x_type))
         return MXFP8_ERR_FORMAT;
@@ -299,13 +307,13 @@ mxfp8_status_t mxfp4_quantize_grouped(const void *x, int x_type, int64_t T, int6
     if (!empty && (out == nullptr || scale == nullptr || (x == nullptr && T > 0)))
         return MXFP8_ERR_NULL;
     if (!is_aligned(x, 16) || !is_aligned(out, 16) || !is_aligned(scale, 4) || !is_aligned(rows, 4) || !is_aligned(offsets, 8) ||
-        !is_aligned(err_flag, 4))
+        !is_aligned(err_flag, 4) || !is_aligned(workspace, 16))
         return MXFP8_ERR_ALIGN;
     int device = 0;
     mxfp8_status_t st = active_device(&device);
     if (st != MXFP8_OK)
         return st;
-    for (const void *ptr : {x, static_cast<const void *>(rows), static_cast<const void *>(offsets), static_cast<const void *>(out),
+    for (const void *ptr : {x, static_cast<const void *>(rows), static_cast<const void *>(workspace), static_cast<const void *>(offsets), static_cast<const void *>(out),
                             static_cast<const void *>(scale), static_cast<const void *>(err_flag)})
         if (!pointer_on_device(ptr, device))
             return MXFP8_ERR_DEVICE;
@@ -326,6 +334,32 @@ mxfp8_status_t mxfp4_quantize_grouped(const void *x, int x_type, int64_t T, int6
     p.err_flag = err_flag;
     p.num_groups = num_groups;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (rows != nullptr && workspace != nullptr && total_rows > T && T > 0) {
+        // more rows than tokens: cast every token once, then gather
+        auto *codes = static_cast<uint8_t *>(workspace), *plane = codes + T * p.row_pitch;
+        if ((st = mxfp4_quantize(x, x_type, T, N, ldx, codes, plane, nullptr, nullptr, nullptr, stream_)) != MXFP8_OK)
+            return st;
+        GatherParams g{};
+        g.codes = codes;
+        g.scale = plane;
+        g.T = T;
+        g.R = total_rows;
+        g.N = N;
+        g.pitch = p.row_pitch;
+        g.col_tiles = p.col_tiles;
+        g.rows = rows;
+        g.offsets = offsets;
+        g.num_groups = num_groups;
+        g.out = p.out_row;
+        g.out_scale = p.scale_row;
+        g.err_flag = err_flag;
+        static KernelSetup setup;
+        int ctas = 0;
+        if ((st = setup(mxfp4_gather_kernel, device, 256, 0, &ctas)) != MXFP8_OK)
+            return st;
+        const int64_t units = (total_rows / kCastTile + num_groups) * ceil_div(col_tiles, kGatherTiles);
+        return launch_serialized(mxfp4_gather_kernel, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), 256, 0, 1, stream, g);
+    }
     return x_type == MXFP4_F32 ? launch_cast_as<true, false, true>(p, bound, device, stream)
                                : launch_cast_as<false, false, true>(p, bound, device, stream);
 }
@@ -349,14 +383,14 @@ mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t ro
         return MXFP8_ERR_DEVICE;
     if (empty)
         return MXFP8_OK;
-    const int64_t n = rows * ceil_div(cols, 8);
-    const int64_t blocks = ceil_div(n, 256);
-    const unsigned grid = static_cast<unsigned>(blocks < (int64_t{1} << 20) ? blocks : (int64_t{1} << 20));
+    const int64_t vecs = ceil_div(cols, 8) + (cols % 8 ? 1 : 0);  // a row that starts off a vector touches one more
+    const int64_t groups = ceil_div(rows, kDecodeRows);
+    const dim3 grid(static_cast<unsigned>(ceil_div(vecs, 128)), static_cast<unsigned>(groups < 65535 ? groups : 65535));
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const auto *c = static_cast<const uint8_t *>(codes);
     const auto *s = static_cast<const uint8_t *>(scale);
     const int64_t pitch = ceil_div(cols, 32) * 16, col_tiles = ceil_div(cols, 128);
-    auto launch = [&](auto *kern) { return launch_serialized(kern, dim3(grid), 256, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
+    auto launch = [&](auto *kern) { return launch_serialized(kern, grid, 128, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
     if (cols % 8)
         return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false>) : launch(mxfp4_decode_kernel<false, false>);
     return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true>) : launch(mxfp4_decode_kernel<false, true>);

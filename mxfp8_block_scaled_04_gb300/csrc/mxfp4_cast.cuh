@@ -1,10 +1,12 @@
 // MXFP4 cast and its inverse (sm_103a); formulas and layouts in include/mxfp4.h.
 //
-// One pass over HBM.  A CTA takes a 128x128 tile: its rows' and its columns' scales are then one 512-byte
-// tile of each GEMM-ready plane.  Rowwise, a thread holds 16 consecutive elements of a row and a block is two
-// lanes; columnwise, the tile goes through shared memory and a thread takes two neighbouring columns of 32
-// rows, so that the four lanes of a column write 64 consecutive bytes of the transposed codes.  Bound by HBM:
-// 2 (or 4) bytes in and 17/32 byte out per element and direction.
+// One pass over HBM.  CTAs take tiles of 128 rows x 256 bytes (128 BF16 or 64 fp32 columns) in turn, so that the
+// tiles at work cover whole rows (a run of tiles per CTA instead measured 30% slower: it keeps ten times as many
+// DRAM pages open), through a ring of shared-memory stages filled by 16-byte asynchronous copies, which serve gathered
+// rows and ragged edges (zero fill) alike and keep two tiles in flight per CTA while a third is cast.  Rowwise, a thread holds 32
+// bytes of a row that it copied itself and a block is two (fp32: four) lanes; columnwise, a thread takes one word
+// (two BF16 columns or one fp32) of 32 rows, so that the four lanes of a column write 64 consecutive bytes of the
+// transposed codes.  Bound by HBM: 2 (or 4) bytes in and 17/32 byte out per element and direction.
 //
 // The scale exponent comes from the bits of amax (exact), x * 2^(127 - e) is exact wherever the rounding to
 // E2M1 depends on it (powers of two, fp32 subnormals kept), so the codes are those of the definition.
@@ -70,48 +72,32 @@ __device__ __forceinline__ void fp4x2_to_f32(uint32_t byte, float &lo, float &hi
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h));
 }
 
-// 16 consecutive elements of a row in registers: 8 words of BF16 pairs, or 16 fp32.
-template <bool F32>
-struct Seg {
-    uint32_t w[F32 ? 16 : 8];
-    __device__ __forceinline__ float get(int i) const
-    {
-        if constexpr (F32)
-            return __uint_as_float(w[i]);
-        else
-            return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-    }
-    // fp32 bits of max |x|
-    __device__ __forceinline__ uint32_t amax() const
-    {
-        uint32_t m = 0;
-        if constexpr (F32) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                m = max(m, w[i] & 0x7FFFFFFFu);
-            return m;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
-            return max(m & 0xFFFFu, m >> 16) << 16;
-        }
-    }
-};
-
-// Shared memory of the columnwise direction: rows of 128 elements, each group of 32 rows shifted by a
-// quarter of the banks, so that a warp's reads of 8 column pairs x 4 row blocks hit 32 banks.
-template <bool F32>
-constexpr int kCastWords = F32 ? 128 : 64;
-template <bool F32>
-__host__ __device__ constexpr int cast_smem_bytes(bool col)
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool live)
 {
-    return col ? (kCastTile * kCastWords<F32> + 3 * kCastWords<F32> / 8) * 4 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Stages of 128 rows of 64 words; each group of 32 rows is shifted by a quarter of the banks, so that a warp's
+// reads of 8 words x 4 row blocks hit 32 banks.
+constexpr int kCastWords = 64;
+constexpr int kCastStages = 3;
+constexpr int kCastStage = (kCastTile * kCastWords + 3 * 8) * 4;
+constexpr int kCastSmem = kCastStages * kCastStage;
+__device__ __forceinline__ int cast_word(int row) { return row * kCastWords + (row >> 5) * 8; }
+
 template <bool F32, bool COL, bool GROUPED>
-__global__ void __launch_bounds__(kCastThreads) mxfp4_cast_kernel(const CastParams p)
+__global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastParams p)
 {
+    constexpr int kSize = F32 ? 4 : 2;
+    constexpr int kCols = 256 / kSize;        // columns of a tile
+    constexpr int kPer = 32 / kSize;          // elements of a row that a thread holds
+    constexpr int kHalves = F32 ? 2 : 1;      // tiles that share a 128-column scale tile
     extern __shared__ uint4 cast_smem[];
     __shared__ uint32_t sc_row[kCastTile], sc_col[kCastTile];  // one plane tile each, as its 4-byte entries
     __shared__ GroupTable<GROUPED> groups;
@@ -119,7 +105,8 @@ __global__ void __launch_bounds__(kCastThreads) mxfp4_cast_kernel(const CastPara
     if (!GROUPED && p.noop != nullptr && *p.noop == 1.0f)
         return;
     const int tid = threadIdx.x;
-    int num_tiles = p.row_tiles * p.col_tiles;
+    const int ct_all = p.col_tiles * kHalves;
+    int64_t num_tiles = static_cast<int64_t>(p.row_tiles) * ct_all;
     if constexpr (GROUPED) {
         const int rt = group_setup<kCastThreads, kCastTile>(groups, p.offsets, p.num_groups, p.M);
         if (rt < 0) {
@@ -127,120 +114,163 @@ __global__ void __launch_bounds__(kCastThreads) mxfp4_cast_kernel(const CastPara
                 atomicOr(p.err_flag, 1);
             return;
         }
-        num_tiles = rt * p.col_tiles;
+        num_tiles = static_cast<int64_t>(rt) * ct_all;
     }
+    if (blockIdx.x >= num_tiles)
+        return;
+    const int count = static_cast<int>((num_tiles - 1 - blockIdx.x) / gridDim.x) + 1;
     const int nb = static_cast<int>((p.N + 31) / 32);
-    uint32_t *tile = reinterpret_cast<uint32_t *>(cast_smem);
-    constexpr int W = kCastWords<F32>;
-    constexpr int V = F32 ? 4 : 2;  // 16-byte loads per segment
+    const uint32_t smem = smem_u32(cast_smem);
+    const void *nowhere = p.x != nullptr ? p.x : p.out_row;  // an address for copies of no bytes
+    const int seg = tid & 7, r0 = tid >> 3;  // 32-byte piece, first of four rows 32 apart
 
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
-        const int rt = t / p.col_tiles, ct = t - rt * p.col_tiles;
-        int64_t row0 = static_cast<int64_t>(rt) * kCastTile, row_end = p.M;
+    struct Tile {
+        int rt, ct;
+        int64_t row0, row_end;
+    };
+    auto tile_at = [&](int n) {
+        Tile w;
+        const int64_t t = blockIdx.x + static_cast<int64_t>(n) * gridDim.x;
+        w.rt = static_cast<int>(t / ct_all);
+        w.ct = static_cast<int>(t - static_cast<int64_t>(w.rt) * ct_all);
+        w.row0 = static_cast<int64_t>(w.rt) * kCastTile;
+        w.row_end = p.M;
         if constexpr (GROUPED) {
-            const int g = groups.find(rt, p.num_groups);
-            row0 = groups.offset[g] + static_cast<int64_t>(rt - groups.tile[g]) * kCastTile;
-            row_end = groups.offset[g + 1];
+            const int g = groups.find(w.rt, p.num_groups);
+            w.row0 = groups.offset[g] + static_cast<int64_t>(w.rt - groups.tile[g]) * kCastTile;
+            w.row_end = groups.offset[g + 1];
         }
-        const int64_t col0 = static_cast<int64_t>(ct) * kCastTile;
-        const int seg = tid & 7, r0 = tid >> 3;
-        const int64_t c = col0 + seg * 16;
-        const int valid = c >= p.N ? 0 : p.N - c >= 16 ? 16 : 8;  // N is a multiple of 8
-
-        Seg<F32> s[4];
-        bool bad[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = row0 + r0 + 32 * i;
-            bool live = r < row_end;
-            int64_t src = r;
-            bad[i] = false;
-            if (GROUPED && live && p.rows != nullptr) {
-                src = p.rows[r];
-                if (src < 0 || src >= p.T) {
-                    live = false;
-                    bad[i] = true;
-                }
-            }
-            const uint4 *g = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p.x) + (src * p.ldx + c) * (F32 ? 4 : 2));
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                uint4 q = make_uint4(0, 0, 0, 0);
-                if (live && v * (16 / V) < valid)
-                    q = __ldg(g + v);
-                s[i].w[4 * v] = q.x;
-                s[i].w[4 * v + 1] = q.y;
-                s[i].w[4 * v + 2] = q.z;
-                s[i].w[4 * v + 3] = q.w;
-            }
-        }
-        if constexpr (COL) {
+        return w;
+    };
+    // The copies run two tiles ahead of the casts, and the gathered rows' indices one tile ahead of the copies.
+    Tile next = tile_at(0);
+    int32_t index[4];
+    auto fetch_indices = [&]() {
+        if (GROUPED && p.rows != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t *d = tile + (r0 + 32 * i) * W + i * (W / 8) + seg * (W / 8);
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    reinterpret_cast<uint4 *>(d)[v] = make_uint4(s[i].w[4 * v], s[i].w[4 * v + 1], s[i].w[4 * v + 2], s[i].w[4 * v + 3]);
+                const int64_t r = next.row0 + r0 + 32 * i;
+                index[i] = r < next.row_end ? p.rows[r] : -1;
             }
         }
+    };
+    fetch_indices();
+    uint32_t lost = 0;  // GROUPED: bits 4 s + i: row i of stage s names a row outside x
+    int issued = 0;
+    auto issue = [&]() {
+        if (issued < count) {
+            const int stage = issued % kCastStages;
+            const uint32_t dst = smem + stage * kCastStage + seg * 32;
+            const int64_t c = static_cast<int64_t>(next.ct) * kCols + seg * kPer;
+            if (GROUPED)
+                lost &= ~(0xFu << (4 * stage));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int64_t from = next.row0 + r0 + 32 * i;
+                bool live = from < next.row_end;
+                if (GROUPED && live && p.rows != nullptr) {
+                    from = index[i];
+                    live = from >= 0 && from < p.T;
+                    if (!live)
+                        lost |= 1u << (4 * stage + i);
+                }
+                const unsigned char *src = static_cast<const unsigned char *>(p.x) + (from * p.ldx + c) * kSize;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool ok = live && c + h * (kPer / 2) < p.N;  // N is a multiple of 8: a whole vector or none
+                    copy16_async(dst + cast_word(r0 + 32 * i) * 4 + h * 16, ok ? src + h * 16 : nowhere, ok);
+                }
+            }
+            if (++issued < count) {
+                next = tile_at(issued);
+                fetch_indices();
+            }
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < kCastStages - 1; ++s)
+        issue();
+
+    for (int n = 0; n < count; ++n) {
+        issue();
+        copy_wait<kCastStages - 1>();
+        const Tile at = tile_at(n);
+        const uint32_t gone = GROUPED ? lost >> (4 * (n % kCastStages)) : 0;
+        const uint32_t *tile = reinterpret_cast<const uint32_t *>(reinterpret_cast<const unsigned char *>(cast_smem) + n % kCastStages * kCastStage);
+        const int64_t col0 = static_cast<int64_t>(at.ct) * kCols;
+        const int plane_ct = at.ct / kHalves, half = at.ct % kHalves;
         if (p.out_row != nullptr) {
+            const int64_t c = col0 + seg * kPer;
+            const bool in_blk = c / 32 < nb;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int lr = r0 + 32 * i;
-                const int64_t r = row0 + lr;
-                uint32_t m = bad[i] ? 0x7F800000u : s[i].amax();
+                const int64_t r = at.row0 + lr;
+                const uint4 *q = reinterpret_cast<const uint4 *>(tile + cast_word(lr) + seg * 8);  // this thread's own copies
+                const uint4 q0 = q[0], q1 = q[1];
+                const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    m = F32 ? max(m, w[j] & 0x7FFFFFFFu) : max_u16x2(m, w[j] & 0x7FFF7FFFu);
+                if (!F32)
+                    m = max(m & 0xFFFFu, m >> 16) << 16;
+                if (GROUPED && (gone >> i) & 1)
+                    m = 0x7F800000u;
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                if (F32)
+                    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 const int e = fp4_exponent(m);
                 const float mul = fp4_multiplier(e);
-                float v[16];
+                float v[kPer];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    v[j] = s[i].get(j) * mul;
-                uint32_t lo = cvt_fp4x8(v), hi = cvt_fp4x8(v + 8);
-                if (e == 255)
-                    lo = hi = 0;
-                const int64_t blk = c / 32;
-                if (r < row_end && blk < nb)
-                    *reinterpret_cast<uint2 *>(p.out_row + r * p.row_pitch + c / 2) = make_uint2(lo, hi);
-                if ((seg & 1) == 0)
-                    reinterpret_cast<uint8_t *>(sc_row)[((lr & 31) << 4) | ((lr >> 5) << 2) | (seg >> 1)] =
-                        static_cast<uint8_t>(r < row_end && blk < nb ? e : 0);
-                if (GROUPED && bad[i] && ct == 0 && seg == 0 && p.err_flag != nullptr)
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (F32) {
+                        v[j] = __uint_as_float(w[j]) * mul;
+                    } else {
+                        v[2 * j] = bf16_lo(w[j]) * mul;
+                        v[2 * j + 1] = bf16_hi(w[j]) * mul;
+                    }
+                }
+                const bool keep = r < at.row_end && in_blk;
+                unsigned char *out = p.out_row + r * p.row_pitch + c / 2;
+                if constexpr (F32) {
+                    const uint32_t o = e == 255 ? 0u : cvt_fp4x8(v);
+                    if (keep)
+                        *reinterpret_cast<uint32_t *>(out) = o;
+                } else {
+                    const uint32_t lo = e == 255 ? 0u : cvt_fp4x8(v), hi = e == 255 ? 0u : cvt_fp4x8(v + 8);
+                    if (keep)
+                        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+                }
+                const int blk = F32 ? half * 2 + (seg >> 2) : seg >> 1;  // of the scale tile's four
+                if ((seg & (F32 ? 3 : 1)) == 0)
+                    reinterpret_cast<uint8_t *>(sc_row)[((lr & 31) << 4) | ((lr >> 5) << 2) | blk] = static_cast<uint8_t>(keep ? e : 0);
+                if (GROUPED && ((gone >> i) & 1) && at.ct == 0 && seg == 0 && p.err_flag != nullptr)
                     atomicOr(p.err_flag, 1);
             }
         }
-        if (COL || p.out_row != nullptr)
-            __syncthreads();
-        if (p.out_row != nullptr && tid < kCastTile)
-            reinterpret_cast<uint32_t *>(p.scale_row)[static_cast<int64_t>(t) * kCastTile + tid] = sc_row[tid];
+        __syncthreads();
+        if (p.out_row != nullptr && tid < kCastTile) {
+            const int64_t to = (static_cast<int64_t>(at.rt) * p.col_tiles + plane_ct) * kCastTile + tid;
+            if constexpr (F32)
+                reinterpret_cast<uint16_t *>(p.scale_row)[2 * to + half] = reinterpret_cast<const uint16_t *>(sc_row)[2 * tid + half];
+            else
+                reinterpret_cast<uint32_t *>(p.scale_row)[to] = sc_row[tid];
+        }
         if constexpr (COL) {
-            const int cp = (tid >> 5) * 8 + (tid & 7), rb = (tid >> 3) & 3;  // column pair, row block
-            uint32_t m0 = 0, m1 = 0;
-            uint32_t w0[32], w1[F32 ? 32 : 1];
-            if constexpr (F32) {
+            const int word = (tid >> 5) * 8 + (tid & 7), rb = (tid >> 3) & 3;  // word of the row, row block
+            uint32_t w[32], m = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(tile + (rb * 32 + i) * W + rb * (W / 8) + 2 * cp);
-                    w0[i] = q.x;
-                    w1[i] = q.y;
-                    m0 = max(m0, q.x & 0x7FFFFFFFu);
-                    m1 = max(m1, q.y & 0x7FFFFFFFu);
-                }
-            } else {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    w0[i] = tile[(rb * 32 + i) * W + rb * (W / 8) + cp];
-                    m = max_u16x2(m, w0[i] & 0x7FFF7FFFu);
-                }
-                m0 = m << 16;
-                m1 = m & 0xFFFF0000u;
+            for (int i = 0; i < 32; ++i) {
+                w[i] = tile[cast_word(rb * 32 + i) + word];
+                m = F32 ? max(m, w[i] & 0x7FFFFFFFu) : max_u16x2(m, w[i] & 0x7FFF7FFFu);
             }
-            const int64_t blk = row0 / 32 + rb;
+            const int64_t blk = at.row0 / 32 + rb;
             const bool live_blk = blk * 32 < p.M;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int e = fp4_exponent(h ? m1 : m0);
+            for (int h = 0; h < (F32 ? 1 : 2); ++h) {
+                const int e = fp4_exponent(F32 ? m : h ? m & 0xFFFF0000u : m << 16);
                 const float mul = fp4_multiplier(e);
                 uint32_t o[4];
 #pragma unroll
@@ -248,69 +278,207 @@ __global__ void __launch_bounds__(kCastThreads) mxfp4_cast_kernel(const CastPara
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const uint32_t w = w0[8 * q + j];
-                        float f;
-                        if constexpr (F32)
-                            f = __uint_as_float(h ? w1[8 * q + j] : w);
-                        else
-                            f = h ? bf16_hi(w) : bf16_lo(w);
-                        v[j] = f * mul;
+                        const uint32_t x = w[8 * q + j];
+                        v[j] = (F32 ? __uint_as_float(x) : h ? bf16_hi(x) : bf16_lo(x)) * mul;
                     }
                     o[q] = e == 255 ? 0u : cvt_fp4x8(v);
                 }
-                const int lc = 2 * cp + h;
-                const bool live = live_blk && col0 + lc < p.N;
-                if (live)
-                    *reinterpret_cast<uint4 *>(p.out_col + (col0 + lc) * p.col_pitch + blk * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-                reinterpret_cast<uint8_t *>(sc_col)[((lc & 31) << 4) | ((lc >> 5) << 2) | rb] = static_cast<uint8_t>(live ? e : 0);
+                const int tc = F32 ? word : 2 * word + h;        // column of the tile
+                const int lc = half * kCols + tc;                // column of the scale tile
+                const bool keep = live_blk && col0 + tc < p.N;
+                if (keep)
+                    *reinterpret_cast<uint4 *>(p.out_col + (col0 + tc) * p.col_pitch + blk * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<uint8_t *>(sc_col)[((lc & 31) << 4) | ((lc >> 5) << 2) | rb] = static_cast<uint8_t>(keep ? e : 0);
             }
             __syncthreads();
-            if (tid < kCastTile)
-                reinterpret_cast<uint32_t *>(p.scale_col)[(static_cast<int64_t>(ct) * p.row_tiles + rt) * kCastTile + tid] = sc_col[tid];
+            const int64_t to = (static_cast<int64_t>(plane_ct) * p.row_tiles + at.rt) * kCastTile;
+            if (tid < kCastTile && (!F32 || (tid & 3) / 2 == half))
+                reinterpret_cast<uint32_t *>(p.scale_col)[to + tid] = sc_col[tid];
         }
-        if (t + static_cast<int>(gridDim.x) < num_tiles)
-            __syncthreads();  // the next tile reuses the shared arrays
+        __syncthreads();  // the stage and the scale arrays are free for the next tiles
+    }
+    copy_wait<0>();
+}
+
+// Rows of a 4-bit matrix gathered for experts: codes row by row, scales into one plane per expert.  With more rows
+// than tokens (each token goes to several experts) casting every token once and gathering 17/32 byte per element
+// replaces a cast per row.  A CTA takes 128 rows x 512 bytes of codes: a warp copies 16 rows, 16 bytes a lane.
+struct GatherParams {
+    const uint8_t *codes, *scale;  // of the T rows
+    int64_t T, R, N;
+    int64_t pitch;
+    int col_tiles;
+    const int32_t *rows;
+    const int64_t *offsets;
+    int num_groups;
+    uint8_t *out, *out_scale;
+    int *err_flag;
+};
+constexpr int kGatherTiles = 8;  // scale tiles of 64 code bytes per CTA
+
+__global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherParams p)
+{
+    __shared__ GroupTable<true> groups;
+    __shared__ int32_t index[kCastTile];
+    pdl_wait_and_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row_tiles = group_setup<256, kCastTile>(groups, p.offsets, p.num_groups, p.R);
+    if (row_tiles < 0) {
+        if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
+            atomicOr(p.err_flag, 1);
+        return;
+    }
+    const int chunks = (p.col_tiles + kGatherTiles - 1) / kGatherTiles;
+    const int nb = static_cast<int>((p.N + 31) / 32);
+    const int64_t units = static_cast<int64_t>(row_tiles) * chunks;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int rt = static_cast<int>(u / chunks), chunk = static_cast<int>(u - static_cast<int64_t>(rt) * chunks);
+        const int g = groups.find(rt, p.num_groups);
+        const int64_t row0 = groups.offset[g] + static_cast<int64_t>(rt - groups.tile[g]) * kCastTile;
+        const int64_t left = groups.offset[g + 1] - row0;
+        const int valid = left < kCastTile ? static_cast<int>(left) : kCastTile;
+        __syncthreads();  // the indices before are done with
+        if (tid < valid) {
+            int32_t i = p.rows[row0 + tid];
+            if (i < 0 || i >= p.T) {
+                i = -1;
+                if (p.err_flag != nullptr)
+                    atomicOr(p.err_flag, 1);
+            }
+            index[tid] = i;
+        }
+        __syncthreads();
+        const int64_t byte = chunk * int64_t{kGatherTiles * 64} + lane * 16;
+        if (byte < p.pitch) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 q[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = warp + 8 * (8 * h + j);
+                    q[j] = make_uint4(0, 0, 0, 0);
+                    if (r < valid && index[r] >= 0)
+                        q[j] = __ldg(reinterpret_cast<const uint4 *>(p.codes + index[r] * p.pitch + byte));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = warp + 8 * (8 * h + j);
+                    if (r < valid)
+                        *reinterpret_cast<uint4 *>(p.out + (row0 + r) * p.pitch + byte) = q[j];
+                }
+            }
+        }
+        const int r = tid & 127;
+        const int32_t from = r < valid ? index[r] : -2;
+#pragma unroll
+        for (int j = 0; j < kGatherTiles / 2; ++j) {
+            const int ct = chunk * kGatherTiles + (tid >> 7) + 2 * j;
+            if (ct < p.col_tiles) {
+                uint32_t v = 0;
+                if (from >= 0)
+                    v = *reinterpret_cast<const uint32_t *>(p.scale + ((static_cast<int64_t>(from) >> 7) * p.col_tiles + ct) * 512 + ((from & 31) << 4) +
+                                                            (((from >> 5) & 3) << 2));
+                else if (from == -1)  // NaN in the row's blocks, 0 past them
+                    v = nb - 4 * ct >= 4 ? 0xFFFFFFFFu : (1u << (8 * (nb - 4 * ct))) - 1;
+                *reinterpret_cast<uint32_t *>(p.out_scale + (static_cast<int64_t>(rt) * p.col_tiles + ct) * 512 + ((r & 31) << 4) + ((r >> 5) << 2)) = v;
+            }
+        }
     }
 }
 
-// Values of a 4-bit matrix.  A thread writes 8 elements of a row: 16 or 32 bytes at once where rows of the output
-// are whole vectors (VEC, cols a multiple of 8), one by one otherwise.  Bound by its writes.
-template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t *codes, const uint8_t *scale, int64_t rows, int64_t cols,
-                                                           int64_t pitch, int64_t col_tiles, void *out)
+// Values of a 4-bit matrix.  A thread writes 8 elements (16 or 32 aligned bytes) of each of 8 rows, whose codes and
+// scales it loads first.  Where rows of the output are no whole vectors, its 8 elements start at the row's first
+// aligned one, anywhere in the codes.  Bound by its writes.
+constexpr int kDecodeRows = 8;
+
+__device__ __forceinline__ float fp4_scale(uint32_t e)
 {
-    pdl_wait_and_release();
-    const int64_t per_row = (cols + 7) / 8, n = rows * per_row;
-    for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < n; i += int64_t{256} * gridDim.x) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-        const uint32_t q = *reinterpret_cast<const uint32_t *>(codes + r * pitch + c / 2);
-        const int64_t blk = c / 32;
-        const uint32_t e = scale[((r >> 7) * col_tiles + (blk >> 2)) * 512 + ((r & 31) << 4) + (((r >> 5) & 3) << 2) + (blk & 3)];
-        const float mul = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e == 0 ? 0x400000u : e << 23);
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            fp4x2_to_f32((q >> (8 * j)) & 0xFF, v[2 * j], v[2 * j + 1]);
-            v[2 * j] *= mul;
-            v[2 * j + 1] *= mul;
-        }
+    return e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e == 0 ? 0x400000u : e << 23);
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void *out, int64_t at, const float (&v)[8])
+{
+    if constexpr (F32) {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)  // exact: the values have two significant bits
             w[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
-        if constexpr (!VEC) {
-            for (int j = 0; j < 8 && c + j < cols; ++j) {
-                if constexpr (F32)
-                    static_cast<float *>(out)[r * cols + c + j] = v[j];
-                else
-                    static_cast<uint16_t *>(out)[r * cols + c + j] = static_cast<uint16_t>(__float_as_uint(v[j]) >> 16);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(128) mxfp4_decode_kernel(const uint8_t *codes, const uint8_t *scale, int64_t rows, int64_t cols,
+                                                           int64_t pitch, int64_t col_tiles, void *out)
+{
+    pdl_wait_and_release();
+    const int64_t j = blockIdx.x * int64_t{128} + threadIdx.x;  // vector of the row
+    for (int64_t first = blockIdx.y * int64_t{kDecodeRows}; first < rows; first += int64_t{kDecodeRows} * gridDim.y) {
+        const int n = static_cast<int>(rows - first < kDecodeRows ? rows - first : kDecodeRows);
+        uint64_t q[kDecodeRows];
+        uint32_t e0[kDecodeRows], e1[kDecodeRows];
+#pragma unroll
+        for (int i = 0; i < kDecodeRows; ++i) {
+            if (i >= n)
+                break;
+            const int64_t r = first + i;
+            // the scale tile entry of (r, block 0); block b is (b / 4) tiles and b % 4 bytes on
+            const uint8_t *s = scale + (r >> 7) * col_tiles * 512 + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
+            const uint8_t *row = codes + r * pitch;
+            if constexpr (VEC) {
+                const int64_t c = 8 * j;
+                if (c < cols) {
+                    q[i] = *reinterpret_cast<const uint32_t *>(row + c / 2);
+                    e0[i] = s[(c >> 7) * 512 + ((c >> 5) & 3)];
+                }
+            } else {
+                // the row's vectors, the first of them from before its start; past the ends any loaded value does
+                const int c = 8 * static_cast<int>(j) - static_cast<int>((r * cols) & 7);
+                const int last = static_cast<int>(cols) - 1;
+                const int w = c >> 3, top = static_cast<int>(pitch / 4) - 1;
+                const uint32_t *words = reinterpret_cast<const uint32_t *>(row);
+                const uint32_t lo = words[min(max(w, 0), top)], hi = words[min(w + 1, top)];
+                q[i] = (static_cast<uint64_t>(hi) << 32 | lo) >> (4 * (c & 7));
+                const int b0 = min(max(c, 0), last) >> 5, b1 = min(c + 7, last) >> 5;
+                e0[i] = s[(b0 >> 2) * 512 + (b0 & 3)];
+                e1[i] = s[(b1 >> 2) * 512 + (b1 & 3)];
             }
-        } else if constexpr (F32) {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + r * cols + c);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + r * cols + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < kDecodeRows; ++i) {
+            if (i >= n)
+                break;
+            const int64_t r = first + i;
+            const int64_t c = VEC ? 8 * j : 8 * j - (r * cols & 7);
+            if (c >= cols)
+                continue;
+            const float m0 = fp4_scale(e0[i]), m1 = VEC ? m0 : fp4_scale(e1[i]);
+            const int turn = VEC ? 8 : static_cast<int>(32 - (c & 31));  // elements of the first block
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                fp4x2_to_f32(static_cast<uint32_t>(q[i] >> (8 * k)) & 0xFF, v[2 * k], v[2 * k + 1]);
+                v[2 * k] *= 2 * k < turn ? m0 : m1;
+                v[2 * k + 1] *= 2 * k + 1 < turn ? m0 : m1;
+            }
+            if (VEC || (c >= 0 && c + 8 <= cols)) {
+                store8<F32>(out, r * cols + c, v);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (c + k >= 0 && c + k < cols) {
+                        if constexpr (F32)
+                            static_cast<float *>(out)[r * cols + c + k] = v[k];
+                        else
+                            static_cast<uint16_t *>(out)[r * cols + c + k] = static_cast<uint16_t>(__float_as_uint(v[k]) >> 16);
+                    }
+                }
+            }
         }
     }
 }

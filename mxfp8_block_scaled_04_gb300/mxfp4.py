@@ -63,10 +63,17 @@ def mxfp4_quantize(x, x_type, M, N, ldx, out_row, scale_row, out_col, scale_col,
                                 _addr(scale_col), _addr(noop), _stream(stream))
 
 
+def mxfp4_quantize_grouped_workspace_bytes(T: int, N: int, total_rows: int) -> int:
+    if T <= 0 or N <= 0 or total_rows <= T:
+        return 0
+    return T * mxfp4_row_bytes(N) + mxfp4_scale_bytes(T, N)
+
+
 def mxfp4_quantize_grouped(x, x_type, T, N, ldx, rows, total_rows, num_groups, offsets, out, scale, err_flag=None,
-                           stream=None) -> int:
+                           workspace=None, stream=None) -> int:
     return lib().mxfp4_quantize_grouped(_addr(x), x_type, T, N, ldx, _addr(rows), total_rows, num_groups,
-                                        _addr(offsets), _addr(out), _addr(scale), _addr(err_flag), _stream(stream))
+                                        _addr(offsets), _addr(out), _addr(scale), _addr(err_flag), _addr(workspace),
+                                        _stream(stream))
 
 
 def mxfp4_dequantize(codes, scale, rows, cols, out, out_type, stream=None) -> int:
@@ -181,7 +188,9 @@ def quantize_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: Optiona
     dev = x.device
     codes = torch.empty((total, mxfp4_row_bytes(N)), dtype=torch.uint8, device=dev)
     scales = torch.empty((mxfp4_grouped_scale_bytes(total, N, groups),), dtype=torch.uint8, device=dev)
-    _check(mxfp4_quantize_grouped(x, kind, T, N, ld, rows, total, groups, offsets, codes, scales, err_flag),
+    nbytes = 0 if rows is None else mxfp4_quantize_grouped_workspace_bytes(T, N, total)
+    workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    _check(mxfp4_quantize_grouped(x, kind, T, N, ld, rows, total, groups, offsets, codes, scales, err_flag, workspace),
            "mxfp4_quantize_grouped")
     return MXFP4Matrix(codes, scales, total, N)
 

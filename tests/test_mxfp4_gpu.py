@@ -284,6 +284,55 @@ def test_experts_product(sizes, N, K, out_dtype):
         assert bool(((got[s] - want).abs() <= tol).all()), g
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [8, 72, 1032])
+@pytest.mark.parametrize("sizes", SIZES)
+def test_grouped_cast_forms(sizes, N, dtype):
+    """Gathered with and without a workspace (several rows per token and fewer rows than tokens), and in order: the
+    same codes and planes; rows from a larger pitch."""
+    G, R = len(sizes), sum(sizes)
+    off = torch.tensor([0] + sizes).cumsum(0)
+    for T in (max(1, R // 3), 2 * R + 1):
+        big = draw(T, N + 16, dtype, T + N)
+        x = big[:, 8:8 + N]
+        rows = torch.randint(0, T, (R,), generator=torch.Generator().manual_seed(T), dtype=torch.int32)
+        rows[R // 2] = T  # outside
+        codes, scale = ref.quantize(x[rows.long().clamp(max=T - 1)])
+        codes[R // 2] = 0
+        scale[R // 2] = 255
+        planes = np.concatenate([ref.plane(scale[off[g]:off[g + 1]]) for g in range(G)])
+        nbytes = mx.mxfp4_grouped_scale_bytes(R, N, G)
+        for ws in (False, True):
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = torch.full((R, mx.mxfp4_row_bytes(N)), 0x77, dtype=torch.uint8, device="cuda")
+            plane = torch.full((nbytes,), 0x77, dtype=torch.uint8, device="cuda")
+            need = mx.mxfp4_quantize_grouped_workspace_bytes(T, N, R)
+            work = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") if ws else None
+            xc = big.cuda()[:, 8:8 + N]
+            assert mx.mxfp4_quantize_grouped(xc, 0 if dtype == BF16 else 1, T, N, N + 16, rows.cuda(), R, G, off.cuda(), out, plane,
+                                             err, work) == 0
+            assert int(err) == 1
+            assert np.array_equal(out.cpu().numpy(), codes)
+            assert np.array_equal(plane.cpu().numpy()[:planes.size], planes)
+    ordered = draw(R, N, dtype, 1)
+    q = mx.quantize_mxfp4_grouped(ordered.cuda(), off.cuda())
+    codes, scale = ref.quantize(ordered)
+    planes = np.concatenate([ref.plane(scale[off[g]:off[g + 1]]) for g in range(G)])
+    assert np.array_equal(q.codes.cpu().numpy(), codes) and np.array_equal(q.scales.cpu().numpy()[:planes.size], planes)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 7), (9, 31), (130, 33), (17, 65), (70, 1023), (3, 4093)])
+def test_decode_any_width(rows, cols):
+    """Rows of the output that start off a 16-byte boundary, and blocks that end inside a thread's elements."""
+    x = draw(cols + (-cols % 8), rows + (-rows % 8), F32, rows + cols)[:, :rows + (-rows % 8)]
+    x[cols:] = 0
+    m = mx.quantize_mxfp4(x.cuda(), False, True).col      # [rows padded to 8, cols padded to 8]
+    m = mx.MXFP4Matrix(m.codes[:rows].contiguous(), m.scales[:mx.mxfp4_scale_bytes(rows, cols)].contiguous(), rows, cols)
+    want = ref.cast(x.t())[:rows, :cols]
+    for dt in (BF16, F32):
+        assert torch.equal(mx.dequantize_mxfp4(m, dt).cpu(), want.to(dt))
+
+
 def test_experts_bad_offsets_and_rows_set_the_flag():
     x = draw(6, 64, BF16, 1).cuda()
     w = mx.quantize_mxfp4(draw(32, 64, BF16, 2).cuda()).row
