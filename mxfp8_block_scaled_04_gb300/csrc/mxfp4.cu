@@ -1,5 +1,6 @@
 // C ABI of the MXFP4 cast and products (declarations and contract in include/mxfp4.h): host-side checks,
 // tensor maps and launches; the device code is in mxfp4_cast.cuh and mxfp4_gemm.cuh.
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -51,6 +52,23 @@ struct KernelSetup {
         return MXFP8_OK;
     }
 };
+
+mxfp8_status_t sm_count(int device, int *sms)
+{
+    static std::atomic<int> cached[kMaxDevices];
+    if (device < 0 || device >= kMaxDevices)
+        return MXFP8_ERR_DEVICE;
+    int n = cached[device].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+            cudaGetLastError();
+            return MXFP8_ERR_DEVICE;
+        }
+        cached[device].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return MXFP8_OK;
+}
 
 template <bool F32, bool COL, bool GROUPED>
 mxfp8_status_t launch_cast_as(const CastParams &p, int64_t tiles, int device, cudaStream_t stream)
@@ -129,40 +147,48 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
                              qsm, p);
 }
 
-// The kernel for few tiles.  The number of CTAs that share a tile's K is the one with the least estimated time: rounds
-// of resident CTAs times the stages of each, plus the start and end of a CTA (about four stages, six with the
-// cluster's two barriers and the sum).
-template <int QROWS, bool F32>
-mxfp8_status_t launch_split_as(const GemmParams &p_, const void *p_codes, const void *q_codes, int64_t row_bytes, int device, cudaStream_t stream)
+// The kernel for few tiles.  S CTAs share a tile's K: the most (1, 2, 4, 8) for which all CTAs are resident at once, two
+// per SM where the weights' bytes are the time (64 rows or fewer), one per SM above.  Measured (us, S = 1 / 2 / 4 / 8,
+// rows x N x K): 1x4096x4096 13.0 / 12.9 / 12.9 / 10.9, 16x8192x28672 50 / 40 / 33 / 40, 100x512x16384 31 / 23 / 17 / 15;
+// where they are not all resident S = 1 is fastest (1x28672x8192 33 / 38 / 42 / 52, 333x4096x4096 15 / 17 / 23 / 33).
+template <int QROWS, int STAGES, bool F32>
+mxfp8_status_t launch_split_as(const GemmParams &p, const CUtensorMap &pm, const CUtensorMap &qm, int64_t tiles, int splits, int device,
+                               cudaStream_t stream)
 {
+    using Shape = SplitShape<QROWS, STAGES>;
     static KernelSetup setup;
-    constexpr int smem = SplitShape<QROWS>::kSmem;
-    static_assert(SplitShape<QROWS>::kStage * SplitShape<QROWS>::kStages >= QROWS * kGemmRows * 4 &&
-                      SplitShape<QROWS>::kStage * SplitShape<QROWS>::kStages >= kEpiBytes<F32>,
+    static_assert(Shape::kStage * STAGES >= QROWS * kGemmRows * 4 && Shape::kStage * STAGES >= kEpiBytes<F32>,
                   "partial sums and the epilogue's buffers fit the stages");
-    int slots = 0;
-    mxfp8_status_t st = setup(mxfp4_split_kernel<QROWS, F32>, device, kGemmThreads, smem, &slots);
+    int ctas = 0;
+    const mxfp8_status_t st = setup(mxfp4_split_kernel<QROWS, STAGES, F32>, device, kGemmThreads, Shape::kSmem, &ctas);
     if (st != MXFP8_OK)
         return st;
+    return launch_serialized(mxfp4_split_kernel<QROWS, STAGES, F32>, dim3(static_cast<unsigned>(tiles * splits)), kGemmThreads, Shape::kSmem, splits,
+                             stream, pm, qm, p, splits);
+}
+
+template <bool F32>
+mxfp8_status_t launch_split(const GemmParams &p_, const void *p_codes, const void *q_codes, int64_t row_bytes, int device, cudaStream_t stream)
+{
     GemmParams p = p_;
-    p.q_box = QROWS;
+    p.q_box = p.Q <= 32 ? 32 : 128;
     CUtensorMap pm, qm;
-    if ((st = code_map(&pm, p_codes, p.P, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, QROWS)) != MXFP8_OK)
+    mxfp8_status_t st;
+    if ((st = code_map(&pm, p_codes, p.P, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, p.q_box)) != MXFP8_OK)
         return st;
-    // two CTAs share an SM (shared memory and TMEM halves); the occupancy query counts one for kernels that allocate TMEM
-    slots *= 2;
-    const int64_t tiles = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
+    int sms = 0;
+    if ((st = sm_count(device, &sms)) != MXFP8_OK)
+        return st;
+    const int64_t tiles = static_cast<int64_t>(p.p_tiles) * p.q_tiles, room = p.Q <= 64 ? 2 * sms : sms;
     int splits = 1;
-    int64_t least = INT64_MAX;
-    for (int s = 1; s <= 8 && s <= p.k_iters; s *= 2) {
-        const int64_t time = ceil_div(tiles * s, slots) * (ceil_div(p.k_iters, s) + (s > 1 ? 6 : 4));
-        if (time < least) {
-            least = time;
-            splits = s;
-        }
-    }
-    return launch_serialized(mxfp4_split_kernel<QROWS, F32>, dim3(static_cast<unsigned>(tiles * splits)), kGemmThreads, smem, splits, stream, pm, qm, p,
-                             splits);
+    while (splits < 8 && tiles * splits * 2 <= room && splits * 2 <= p.k_iters)
+        splits *= 2;
+    if (p.Q <= 32)
+        return launch_split_as<32, 4, F32>(p, pm, qm, tiles, splits, device, stream);
+    // one CTA per SM is all there is: more stages in its shared memory
+    if (tiles * splits <= sms)
+        return launch_split_as<128, 5, F32>(p, pm, qm, tiles, splits, device, stream);
+    return launch_split_as<128, 3, F32>(p, pm, qm, tiles, splits, device, stream);
 }
 
 // Checks and parameters that both products share.  Q: the tokens' rows; P: the weights' rows (per expert).
@@ -383,15 +409,17 @@ mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t ro
         return MXFP8_ERR_DEVICE;
     if (empty)
         return MXFP8_OK;
-    const int64_t vecs = ceil_div(cols, 8) + (cols % 8 ? 1 : 0);  // a row that starts off a vector touches one more
-    const int64_t groups = ceil_div(rows, kDecodeRows);
+    const int per = out_type == MXFP4_F32 ? 4 : 8;  // elements of a 16-byte vector
+    const bool vec = cols % per == 0;
+    const int64_t vecs = ceil_div(cols, per) + (vec ? 0 : 1);  // a row that starts off a vector touches one more
+    const int64_t groups = ceil_div(rows, vec ? kDecodeRows<true> : kDecodeRows<false>);
     const dim3 grid(static_cast<unsigned>(ceil_div(vecs, 128)), static_cast<unsigned>(groups < 65535 ? groups : 65535));
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const auto *c = static_cast<const uint8_t *>(codes);
     const auto *s = static_cast<const uint8_t *>(scale);
     const int64_t pitch = ceil_div(cols, 32) * 16, col_tiles = ceil_div(cols, 128);
     auto launch = [&](auto *kern) { return launch_serialized(kern, grid, 128, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
-    if (cols % 8)
+    if (!vec)
         return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false>) : launch(mxfp4_decode_kernel<false, false>);
     return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true>) : launch(mxfp4_decode_kernel<false, true>);
 }
@@ -426,11 +454,8 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
                    ? launch_pair_as<true, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream)
                    : launch_pair_as<false, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream);
     }
-    if (M <= 32)
-        return out_type == MXFP4_F32 ? launch_split_as<32, true>(p, b_codes, a_codes, row_bytes, device, stream)
-                                     : launch_split_as<32, false>(p, b_codes, a_codes, row_bytes, device, stream);
-    return out_type == MXFP4_F32 ? launch_split_as<128, true>(p, b_codes, a_codes, row_bytes, device, stream)
-                                 : launch_split_as<128, false>(p, b_codes, a_codes, row_bytes, device, stream);
+    return out_type == MXFP4_F32 ? launch_split<true>(p, b_codes, a_codes, row_bytes, device, stream)
+                                 : launch_split<false>(p, b_codes, a_codes, row_bytes, device, stream);
 }
 
 mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, int64_t total_rows, int num_groups, const int64_t *offsets,

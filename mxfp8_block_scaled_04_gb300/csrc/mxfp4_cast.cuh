@@ -99,7 +99,6 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
     constexpr int kPer = 32 / kSize;          // elements of a row that a thread holds
     constexpr int kHalves = F32 ? 2 : 1;      // tiles that share a 128-column scale tile
     extern __shared__ uint4 cast_smem[];
-    __shared__ uint32_t sc_row[kCastTile], sc_col[kCastTile];  // one plane tile each, as its 4-byte entries
     __shared__ GroupTable<GROUPED> groups;
     pdl_wait_and_release();
     if (!GROUPED && p.noop != nullptr && *p.noop == 1.0f)
@@ -192,10 +191,12 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
         issue();
 
     for (int n = 0; n < count; ++n) {
-        issue();
-        copy_wait<kCastStages - 1>();
-        const Tile at = tile_at(n);
+        copy_wait<kCastStages - 2>();
+        if constexpr (COL)
+            __syncthreads();  // tile n is there for every thread, and the stage before it free for the next copies
         const uint32_t gone = GROUPED ? lost >> (4 * (n % kCastStages)) : 0;
+        issue();
+        const Tile at = tile_at(n);
         const uint32_t *tile = reinterpret_cast<const uint32_t *>(reinterpret_cast<const unsigned char *>(cast_smem) + n % kCastStages * kCastStage);
         const int64_t col0 = static_cast<int64_t>(at.ct) * kCols;
         const int plane_ct = at.ct / kHalves, half = at.ct % kHalves;
@@ -243,20 +244,21 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
                     if (keep)
                         *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
                 }
-                const int blk = F32 ? half * 2 + (seg >> 2) : seg >> 1;  // of the scale tile's four
-                if ((seg & (F32 ? 3 : 1)) == 0)
-                    reinterpret_cast<uint8_t *>(sc_row)[((lr & 31) << 4) | ((lr >> 5) << 2) | blk] = static_cast<uint8_t>(keep ? e : 0);
+                // the row's blocks, two (four) lanes apart, as the scale tile's 2 (4) bytes
+                uint32_t sc = keep ? e : 0;
+                sc |= __shfl_down_sync(0xFFFFFFFFu, sc, F32 ? 4 : 2) << 8;
+                if (!F32)
+                    sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 4) << 16;
+                if (seg == 0) {
+                    uint8_t *to = p.scale_row + (static_cast<int64_t>(at.rt) * p.col_tiles + plane_ct) * 512 + (((lr & 31) << 4) | ((lr >> 5) << 2));
+                    if constexpr (F32)
+                        reinterpret_cast<uint16_t *>(to)[half] = static_cast<uint16_t>(sc);
+                    else
+                        *reinterpret_cast<uint32_t *>(to) = sc;
+                }
                 if (GROUPED && ((gone >> i) & 1) && at.ct == 0 && seg == 0 && p.err_flag != nullptr)
                     atomicOr(p.err_flag, 1);
             }
-        }
-        __syncthreads();
-        if (p.out_row != nullptr && tid < kCastTile) {
-            const int64_t to = (static_cast<int64_t>(at.rt) * p.col_tiles + plane_ct) * kCastTile + tid;
-            if constexpr (F32)
-                reinterpret_cast<uint16_t *>(p.scale_row)[2 * to + half] = reinterpret_cast<const uint16_t *>(sc_row)[2 * tid + half];
-            else
-                reinterpret_cast<uint32_t *>(p.scale_row)[to] = sc_row[tid];
         }
         if constexpr (COL) {
             const int word = (tid >> 5) * 8 + (tid & 7), rb = (tid >> 3) & 3;  // word of the row, row block
@@ -288,14 +290,14 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
                 const bool keep = live_blk && col0 + tc < p.N;
                 if (keep)
                     *reinterpret_cast<uint4 *>(p.out_col + (col0 + tc) * p.col_pitch + blk * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-                reinterpret_cast<uint8_t *>(sc_col)[((lc & 31) << 4) | ((lc >> 5) << 2) | rb] = static_cast<uint8_t>(keep ? e : 0);
+                uint32_t sc = keep ? e : 0;  // the column's four blocks, eight lanes apart
+                sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 8) << 8;
+                sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 16) << 16;
+                if (rb == 0)
+                    *reinterpret_cast<uint32_t *>(p.scale_col + (static_cast<int64_t>(plane_ct) * p.row_tiles + at.rt) * 512 +
+                                                  (((lc & 31) << 4) | ((lc >> 5) << 2))) = sc;
             }
-            __syncthreads();
-            const int64_t to = (static_cast<int64_t>(plane_ct) * p.row_tiles + at.rt) * kCastTile;
-            if (tid < kCastTile && (!F32 || (tid & 3) / 2 == half))
-                reinterpret_cast<uint32_t *>(p.scale_col)[to + tid] = sc_col[tid];
         }
-        __syncthreads();  // the stage and the scale arrays are free for the next tiles
     }
     copy_wait<0>();
 }
@@ -386,96 +388,80 @@ __global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherParams p)
     }
 }
 
-// Values of a 4-bit matrix.  A thread writes 8 elements (16 or 32 aligned bytes) of each of 8 rows, whose codes and
-// scales it loads first.  Where rows of the output are no whole vectors, its 8 elements start at the row's first
+// Values of a 4-bit matrix.  A thread writes 16 aligned bytes (8 BF16 or 4 fp32) of each of several rows, whose codes
+// and scales it loads first.  Where rows of the output are no whole vectors, its elements start at the row's first
 // aligned one, anywhere in the codes.  Bound by its writes.
-constexpr int kDecodeRows = 8;
+template <bool VEC>
+constexpr int kDecodeRows = VEC ? 8 : 4;
 
 __device__ __forceinline__ float fp4_scale(uint32_t e)
 {
     return e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e == 0 ? 0x400000u : e << 23);
 }
 
-template <bool F32>
-__device__ __forceinline__ void store8(void *out, int64_t at, const float (&v)[8])
-{
-    if constexpr (F32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // exact: the values have two significant bits
-            w[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(128) mxfp4_decode_kernel(const uint8_t *codes, const uint8_t *scale, int64_t rows, int64_t cols,
                                                            int64_t pitch, int64_t col_tiles, void *out)
 {
+    constexpr int V = F32 ? 4 : 8, kRows = kDecodeRows<VEC>;
     pdl_wait_and_release();
     const int64_t j = blockIdx.x * int64_t{128} + threadIdx.x;  // vector of the row
-    for (int64_t first = blockIdx.y * int64_t{kDecodeRows}; first < rows; first += int64_t{kDecodeRows} * gridDim.y) {
-        const int n = static_cast<int>(rows - first < kDecodeRows ? rows - first : kDecodeRows);
-        uint64_t q[kDecodeRows];
-        uint32_t e0[kDecodeRows], e1[kDecodeRows];
+    for (int64_t first = blockIdx.y * int64_t{kRows}; first < rows; first += int64_t{kRows} * gridDim.y) {
+        uint32_t q[kRows], e0[kRows], e1[kRows];
 #pragma unroll
-        for (int i = 0; i < kDecodeRows; ++i) {
-            if (i >= n)
-                break;
-            const int64_t r = first + i;
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = first + i < rows ? first + i : rows - 1;
             // the scale tile entry of (r, block 0); block b is (b / 4) tiles and b % 4 bytes on
             const uint8_t *s = scale + (r >> 7) * col_tiles * 512 + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
             const uint8_t *row = codes + r * pitch;
+            const int last = static_cast<int>(cols) - 1;
             if constexpr (VEC) {
-                const int64_t c = 8 * j;
-                if (c < cols) {
-                    q[i] = *reinterpret_cast<const uint32_t *>(row + c / 2);
-                    e0[i] = s[(c >> 7) * 512 + ((c >> 5) & 3)];
-                }
+                const int c = static_cast<int>(V * j < cols ? V * j : 0);
+                q[i] = F32 ? *reinterpret_cast<const uint16_t *>(row + c / 2) : *reinterpret_cast<const uint32_t *>(row + c / 2);
+                e0[i] = s[(c >> 7) * 512 + ((c >> 5) & 3)];
             } else {
                 // the row's vectors, the first of them from before its start; past the ends any loaded value does
-                const int c = 8 * static_cast<int>(j) - static_cast<int>((r * cols) & 7);
-                const int last = static_cast<int>(cols) - 1;
-                const int w = c >> 3, top = static_cast<int>(pitch / 4) - 1;
+                const int64_t c = V * j - (r * cols & (V - 1));
+                const int c0 = static_cast<int>(c < 0 ? 0 : c < last ? c : last), c1 = static_cast<int>(c + V - 1 < last ? c + V - 1 : last);
                 const uint32_t *words = reinterpret_cast<const uint32_t *>(row);
-                const uint32_t lo = words[min(max(w, 0), top)], hi = words[min(w + 1, top)];
-                q[i] = (static_cast<uint64_t>(hi) << 32 | lo) >> (4 * (c & 7));
-                const int b0 = min(max(c, 0), last) >> 5, b1 = min(c + 7, last) >> 5;
+                const int top = static_cast<int>(pitch / 4) - 1, w = c < 0 ? -1 : c0 >> 3;
+                const uint32_t lo = words[max(w, 0)], hi = words[min(w + 1, top)];
+                q[i] = static_cast<uint32_t>((static_cast<uint64_t>(hi) << 32 | lo) >> (4 * (static_cast<int>(c) & 7)));
+                const int b0 = c0 >> 5, b1 = c1 >> 5;
                 e0[i] = s[(b0 >> 2) * 512 + (b0 & 3)];
                 e1[i] = s[(b1 >> 2) * 512 + (b1 & 3)];
             }
         }
 #pragma unroll
-        for (int i = 0; i < kDecodeRows; ++i) {
-            if (i >= n)
-                break;
+        for (int i = 0; i < kRows; ++i) {
             const int64_t r = first + i;
-            const int64_t c = VEC ? 8 * j : 8 * j - (r * cols & 7);
-            if (c >= cols)
+            const int64_t c = VEC ? V * j : V * j - (r * cols & (V - 1));
+            if (r >= rows || c >= cols)
                 continue;
             const float m0 = fp4_scale(e0[i]), m1 = VEC ? m0 : fp4_scale(e1[i]);
-            const int turn = VEC ? 8 : static_cast<int>(32 - (c & 31));  // elements of the first block
-            float v[8];
+            const int turn = VEC ? V : static_cast<int>(32 - (c & 31));  // elements of the first block
+            float v[V];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                fp4x2_to_f32(static_cast<uint32_t>(q[i] >> (8 * k)) & 0xFF, v[2 * k], v[2 * k + 1]);
+            for (int k = 0; k < V / 2; ++k) {
+                fp4x2_to_f32((q[i] >> (8 * k)) & 0xFF, v[2 * k], v[2 * k + 1]);
                 v[2 * k] *= 2 * k < turn ? m0 : m1;
                 v[2 * k + 1] *= 2 * k + 1 < turn ? m0 : m1;
             }
-            if (VEC || (c >= 0 && c + 8 <= cols)) {
-                store8<F32>(out, r * cols + c, v);
+            const int64_t at = r * cols + c;
+            if (VEC || (c >= 0 && c + V <= cols)) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // exact: the values have two significant bits
+                    w[k] = F32 ? __float_as_uint(v[k]) : (__float_as_uint(v[(2 * k) % V]) >> 16) | (__float_as_uint(v[(2 * k + 1) % V]) & 0xFFFF0000u);
+                *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(out) + at * (F32 ? 4 : 2)) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < V; ++k) {
                     if (c + k >= 0 && c + k < cols) {
                         if constexpr (F32)
-                            static_cast<float *>(out)[r * cols + c + k] = v[k];
+                            static_cast<float *>(out)[at + k] = v[k];
                         else
-                            static_cast<uint16_t *>(out)[r * cols + c + k] = static_cast<uint16_t>(__float_as_uint(v[k]) >> 16);
+                            static_cast<uint16_t *>(out)[at + k] = static_cast<uint16_t>(__float_as_uint(v[k]) >> 16);
                     }
                 }
             }

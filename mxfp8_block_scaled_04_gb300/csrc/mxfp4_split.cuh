@@ -10,13 +10,14 @@
 
 namespace mxfp8 {
 
-// QROWS: rows of Q that the stages hold (32 for few tokens: more stages).
-template <int QROWS>
+// QROWS: rows of Q that the stages hold.  Two CTAs fit an SM with 4 stages of 32 rows or 3 of 128.  (The occupancy
+// query reports one for any kernel that allocates TMEM; CTAs of 256 columns were seen to run side by side.)
+template <int QROWS, int STAGES>
 struct SplitShape {
     static constexpr int kPBytes = kGemmRows * 128;
     static constexpr int kQBytes = QROWS * 128;
     static constexpr int kStage = kPBytes + kQBytes + 2048;  // + two scale tiles of each operand
-    static constexpr int kStages = QROWS == 32 ? 4 : 3;
+    static constexpr int kStages = STAGES;
     static constexpr int kSmem = kStages * kStage + 1024;
     static constexpr int kColumns = 256;                     // TMEM: accumulator at 0, scales at 128
 };
@@ -28,11 +29,11 @@ __device__ __forceinline__ float4 load_peer(uint32_t mapped)
     return v;
 }
 
-template <int QROWS, bool F32>
+template <int QROWS, int STAGES, bool F32>
 __global__ void __launch_bounds__(kGemmThreads, 2)
     mxfp4_split_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p, int splits)
 {
-    using S = SplitShape<QROWS>;
+    using S = SplitShape<QROWS, STAGES>;
     extern __shared__ unsigned char gemm_smem[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full, drain;
     __shared__ uint32_t tmem_slot;
