@@ -88,6 +88,25 @@ mxfp8_status_t launch_route(const RouteParams &p, int type, int vpl, cudaStream_
     }
 }
 
+template <bool F32>
+mxfp8_status_t launch_sigmoid_backward(const RouteParams &p, cudaStream_t stream)
+{
+    int kp = 1;
+    while (kp < p.k)
+        kp *= 2;
+    const int64_t warps = (p.T * kp + 31) / 32;
+    const dim3 grid(grid_of((warps + kRouteThreads / 32 - 1) / (kRouteThreads / 32)));
+    auto launch = [&](auto *kern) { return launch_serialized(kern, grid, kRouteThreads, 0, 1, stream, p); };
+    switch (kp) {
+    case 1: return launch(moe_route_backward_sigmoid_kernel<1, F32>);
+    case 2: return launch(moe_route_backward_sigmoid_kernel<2, F32>);
+    case 4: return launch(moe_route_backward_sigmoid_kernel<4, F32>);
+    case 8: return launch(moe_route_backward_sigmoid_kernel<8, F32>);
+    case 16: return launch(moe_route_backward_sigmoid_kernel<16, F32>);
+    default: return launch(moe_route_backward_sigmoid_kernel<32, F32>);
+    }
+}
+
 // Whether every lane's share of a row can be read (and written) in vectors: the row pitch in bytes and the base are
 // multiples of the vector, and E of a lane's experts.
 bool vector_rows(const void *base, int64_t pitch, int64_t E, int vpl, int type)
@@ -177,6 +196,10 @@ mxfp8_status_t moe_route_backward(const void *logits, int type, int64_t T, int64
     p.dweights = dweights;
     p.dlogits = dlogits;
     p.vec = vector_rows(logits, ld, E, vpl, type) && vector_rows(dlogits, E, E, vpl, type);
+    p.vec16 = E * (type == MXFP4_F32 ? 4 : 2) % 16 == 0 && is_aligned(dlogits, 16);
+    if (p.sigmoid)
+        return type == MXFP4_F32 ? launch_sigmoid_backward<true>(p, static_cast<cudaStream_t>(stream))
+                                 : launch_sigmoid_backward<false>(p, static_cast<cudaStream_t>(stream));
     return launch_route<true>(p, type, vpl, static_cast<cudaStream_t>(stream));
 }
 

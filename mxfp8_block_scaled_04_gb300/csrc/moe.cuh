@@ -17,7 +17,9 @@ struct RouteParams {
     const void *logits;
     int64_t T, ld;
     int E, k, groups, topk_groups;
-    bool sigmoid, renorm, vec;   // vec: rows of 16-byte loads
+    bool sigmoid, renorm;
+    bool vec;        // a lane's experts load (and store) as vectors
+    bool vec16;      // backward: rows of dlogits are whole 16-byte vectors
     float scale;
     const float *bias;
     int32_t *indices;
@@ -197,9 +199,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
                 for (int i = 0; i < VPL; ++i)
                     row[lane * VPL + i] = kf[i];
                 __syncwarp();
-                uint32_t rank[kRouteMaxE / 32];
+                uint32_t rank[VPL];  // groups lane, lane + 32, ...: no more of them than experts
 #pragma unroll
-                for (int n = 0; n < kRouteMaxE / 32; ++n) {
+                for (int n = 0; n < VPL; ++n) {
                     rank[n] = 0;
                     const int g = lane + 32 * n;
                     if (g < p.groups) {
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
                     uint32_t top = 0;
                     int at = 0;
 #pragma unroll
-                    for (int n = 0; n < kRouteMaxE / 32; ++n)
+                    for (int n = 0; n < VPL; ++n)
                         if (rank[n] > top) {
                             top = rank[n];
                             at = n;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
                     if (lane == (g & 31)) {
                         taken |= 1u << (g >> 5);
 #pragma unroll
-                        for (int n = 0; n < kRouteMaxE / 32; ++n)
+                        for (int n = 0; n < VPL; ++n)
                             rank[n] = n == (g >> 5) ? 0u : rank[n];
                     }
                 }
@@ -246,37 +248,42 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
                 }
             }
         }
-        // the k largest keys, one at a time; lane j keeps the j-th
-        uint32_t bk = 0;
-        int be = 0;
-        float bs = 0.f;
-        auto best_of_lane = [&]() {
-            bk = key[0], be = 0, bs = s[0];
+        // the k largest keys, one at a time; lane j keeps the j-th's expert
+        float *row = keys[warp];
+        __syncwarp();
 #pragma unroll
-            for (int i = 1; i < VPL; ++i)
-                if (key[i] > bk)
-                    bk = key[i], be = i, bs = s[i];
-        };
-        best_of_lane();
+        for (int i = 0; i < VPL; ++i)
+            row[lane * VPL + i] = s[i];
+        uint32_t bk = key[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i)
+            bk = max(bk, key[i]);
         int my_idx = 0;
-        float my_p = 0.f;
         for (int j = 0; j < p.k; ++j) {
             const uint32_t best = __reduce_max_sync(kAll, bk);
             const int src = __ffs(__ballot_sync(kAll, bk == best)) - 1;
-            const int e = __shfl_sync(kAll, be, src);
-            const float ps = __shfl_sync(kAll, bs, src);
-            if (lane == j)
-                my_idx = src * VPL + e, my_p = ps;
-            if (lane == src) {
+            int e = 0;
+            if (lane == src) {  // its first expert with that key leaves
+                bool found = false;
+                bk = 0;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    key[i] = i == be ? 0u : key[i];
-                best_of_lane();
+                for (int i = 0; i < VPL; ++i) {
+                    const bool hit = !found && key[i] == best;
+                    e = hit ? i : e;
+                    key[i] = hit ? 0u : key[i];
+                    found |= hit;
+                    bk = max(bk, key[i]);
+                }
+                e += lane * VPL;
             }
+            e = __shfl_sync(kAll, e, src);
+            my_idx = lane == j ? e : my_idx;
         }
+        __syncwarp();
+        const float my_p = lane < p.k ? row[my_idx] : 0.f;
         float w = my_p;
         if (p.renorm) {
-            float total = lane < p.k ? my_p : 0.f;
+            float total = my_p;
 #pragma unroll
             for (int d = 16; d; d >>= 1)
                 total += __shfl_xor_sync(kAll, total, d);
@@ -289,7 +296,76 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     }
 }
 
-// One warp per token.  Softmax reads the row again; sigmoid only the chosen logits.
+// Gradient of the sigmoid scores: only the chosen logits count.  A warp takes 32 / KP tokens at once (KP: k rounded up
+// to a power of two), one lane per choice, so that the dependent loads of several tokens are in flight together;
+// then it writes the tokens' rows as zeros and the chosen entries over them.
+template <bool F32>
+__device__ __forceinline__ void store_logit(void *out, int64_t at, float v)
+{
+    if constexpr (F32)
+        static_cast<float *>(out)[at] = v;
+    else
+        static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+}
+
+template <int KP, bool F32>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_backward_sigmoid_kernel(const RouteParams p)
+{
+    constexpr int kTokens = 32 / KP;
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = lane % KP;
+    for (int64_t t0 = (blockIdx.x * int64_t{kRouteThreads / 32} + warp) * kTokens; t0 < p.T; t0 += gridDim.x * int64_t{kRouteThreads / 32} * kTokens) {
+        const int64_t t = t0 + lane / KP;
+        const bool there = t < p.T && j < p.k;
+        const int idx = there ? p.idx_in[t * p.k + j] : -1;
+        float d = there ? p.scale * p.dweights[t * p.k + j] : 0.f;
+        const bool live = idx >= 0 && idx < p.E;
+        float pj = 0.f;
+        if (live) {
+            const int64_t at = t * p.ld + idx;
+            pj = sigmoid_exact(F32 ? static_cast<const float *>(p.logits)[at] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]));
+        }
+        // the rows' zeros go out while the loads are under way
+        for (int n = 0; n < kTokens && t0 + n < p.T; ++n) {
+            const int64_t row = (t0 + n) * p.E;
+            if (p.vec16) {
+                constexpr int kElems = F32 ? 4 : 8;
+                for (int e = lane * kElems; e < p.E; e += 32 * kElems)
+                    *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(p.dlogits) + (row + e) * (F32 ? 4 : 2)) = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int e = lane; e < p.E; e += 32)
+                    store_logit<F32>(p.dlogits, row + e, 0.f);
+            }
+        }
+        d = live ? d : 0.f;
+        if (p.renorm) {
+            float total = pj, dot = d * pj;
+#pragma unroll
+            for (int o = KP / 2; o; o >>= 1) {
+                total += __shfl_xor_sync(kAll, total, o);
+                dot += __shfl_xor_sync(kAll, dot, o);
+            }
+            d = total == 0.f || !live ? 0.f : (d - dot / total) / total;
+        }
+        const int name = live ? idx + (lane / KP) * kRouteMaxE : -1 - lane;
+        const unsigned same = __match_any_sync(kAll, name);
+        float sum = d;
+        if (__any_sync(kAll, (same & (same - 1)) != 0)) {  // an index named twice: its parts in order
+            sum = 0.f;
+            for (int i = 0; i < KP; ++i) {
+                const int other = __shfl_sync(kAll, name, (lane & ~(KP - 1)) + i);
+                const float od = __shfl_sync(kAll, d, (lane & ~(KP - 1)) + i);
+                sum += other == name ? od : 0.f;
+            }
+        }
+        __syncwarp();  // the zeros come first
+        if (live)
+            store_logit<F32>(p.dlogits, t * p.E + idx, sum * pj * (1.f - pj));
+    }
+}
+
+// One warp per token for the softmax scores, which every logit of the row moves.
 template <int VPL, bool F32>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const RouteParams p)
 {
@@ -302,25 +378,17 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
         const int idx = lane < p.k ? p.idx_in[t * p.k + lane] : -1;
         const bool live = idx >= 0 && idx < p.E;
         float d = live ? p.scale * p.dweights[t * p.k + lane] : 0.f;
-        float s[VPL], pj = 0.f;
+        float l[VPL], s[VPL], pj = 0.f;
+        load_row<VPL, F32>(p, t, lane, l, kNegInf);
+        softmax_row<VPL>(l, s);
         __syncwarp();
-        if (p.sigmoid) {
-            if (live) {
-                const int64_t at = t * p.ld + idx;
-                pj = sigmoid_exact(F32 ? static_cast<const float *>(p.logits)[at] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]));
-            }
-        } else {
-            float l[VPL];
-            load_row<VPL, F32>(p, t, lane, l, kNegInf);
-            softmax_row<VPL>(l, s);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                row[lane * VPL + i] = s[i];
-            __syncwarp();
-            if (live)
-                pj = row[idx];
-            __syncwarp();
-        }
+        for (int i = 0; i < VPL; ++i)
+            row[lane * VPL + i] = s[i];
+        __syncwarp();
+        if (live)
+            pj = row[idx];
+        __syncwarp();
         float total = pj, dot = d * pj;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -334,8 +402,6 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
             for (int o = 16; o; o >>= 1)
                 dot += __shfl_xor_sync(kAll, dot, o);
         }
-        if (p.sigmoid)
-            d = d * pj * (1.f - pj);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             row[lane * VPL + i] = 0.f;
@@ -353,8 +419,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const float r = row[lane * VPL + i];
-            s[i] = p.sigmoid ? r : s[i] * (r - dot);
+            s[i] *= row[lane * VPL + i] - dot;
         }
         const int e0 = lane * VPL;
         const int64_t at = t * p.E + e0;

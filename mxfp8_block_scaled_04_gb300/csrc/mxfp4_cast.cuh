@@ -64,6 +64,16 @@ __device__ __forceinline__ uint32_t cvt_fp4x8(const float *v)
     return r;
 }
 
+// Eight values times one multiplier (a splat pair) -> codes; the products as packed pairs.
+__device__ __forceinline__ uint32_t cvt_fp4x8_scaled(const float *x, uint64_t mul)
+{
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f2_unpack(f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), mul), v[2 * j], v[2 * j + 1]);
+    return cvt_fp4x8(v);
+}
+
 // Two E2M1 codes (a byte) -> two fp32.
 __device__ __forceinline__ void fp4x2_to_f32(uint32_t byte, float &lo, float &hi)
 {
@@ -127,11 +137,8 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
         int rt, ct;
         int64_t row0, row_end;
     };
-    auto tile_at = [&](int n) {
-        Tile w;
-        const int64_t t = blockIdx.x + static_cast<int64_t>(n) * gridDim.x;
-        w.rt = static_cast<int>(t / ct_all);
-        w.ct = static_cast<int>(t - static_cast<int64_t>(w.rt) * ct_all);
+    const int jump_rt = static_cast<int>(gridDim.x) / ct_all, jump_ct = static_cast<int>(gridDim.x) - jump_rt * ct_all;
+    auto rows_of = [&](Tile &w) {
         w.row0 = static_cast<int64_t>(w.rt) * kCastTile;
         w.row_end = p.M;
         if constexpr (GROUPED) {
@@ -139,10 +146,22 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
             w.row0 = groups.offset[g] + static_cast<int64_t>(w.rt - groups.tile[g]) * kCastTile;
             w.row_end = groups.offset[g + 1];
         }
-        return w;
+    };
+    auto to_next = [&](Tile &w) {  // the CTA's next tile: gridDim.x tiles on
+        w.ct += jump_ct;
+        w.rt += jump_rt;
+        if (w.ct >= ct_all) {
+            w.ct -= ct_all;
+            ++w.rt;
+        }
+        rows_of(w);
     };
     // The copies run two tiles ahead of the casts, and the gathered rows' indices one tile ahead of the copies.
-    Tile next = tile_at(0);
+    Tile next;
+    next.rt = static_cast<int>(blockIdx.x) / ct_all;
+    next.ct = static_cast<int>(blockIdx.x) - next.rt * ct_all;
+    rows_of(next);
+    Tile at = next;
     int32_t index[4];
     auto fetch_indices = [&]() {
         if (GROUPED && p.rows != nullptr) {
@@ -181,7 +200,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
                 }
             }
             if (++issued < count) {
-                next = tile_at(issued);
+                to_next(next);
                 fetch_indices();
             }
         }
@@ -196,65 +215,68 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
             __syncthreads();  // tile n is there for every thread, and the stage before it free for the next copies
         const uint32_t gone = GROUPED ? lost >> (4 * (n % kCastStages)) : 0;
         issue();
-        const Tile at = tile_at(n);
+        if (n > 0)
+            to_next(at);
         const uint32_t *tile = reinterpret_cast<const uint32_t *>(reinterpret_cast<const unsigned char *>(cast_smem) + n % kCastStages * kCastStage);
         const int64_t col0 = static_cast<int64_t>(at.ct) * kCols;
         const int plane_ct = at.ct / kHalves, half = at.ct % kHalves;
         if (p.out_row != nullptr) {
             const int64_t c = col0 + seg * kPer;
             const bool in_blk = c / 32 < nb;
+            unsigned char *out = p.out_row + (at.row0 + r0) * p.row_pitch + c / 2;
+            uint8_t *sc_out = p.scale_row + (static_cast<int64_t>(at.rt) * p.col_tiles + plane_ct) * 512 + (r0 << 4);
+            const int rows_left = static_cast<int>(at.row_end - at.row0 < kCastTile ? at.row_end - at.row0 : kCastTile);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int lr = r0 + 32 * i;
-                const int64_t r = at.row0 + lr;
-                const uint4 *q = reinterpret_cast<const uint4 *>(tile + cast_word(lr) + seg * 8);  // this thread's own copies
+                const uint4 *q = reinterpret_cast<const uint4 *>(tile + cast_word(r0 + 32 * i) + seg * 8);  // this thread's own copies
                 const uint4 q0 = q[0], q1 = q[1];
                 const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
                 uint32_t m = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    m = F32 ? max(m, w[j] & 0x7FFFFFFFu) : max_u16x2(m, w[j] & 0x7FFF7FFFu);
-                if (!F32)
-                    m = max(m & 0xFFFFu, m >> 16) << 16;
+                    m = F32 ? absmax_nan_f32(m, w[j]) : absmax_nan_bf16x2(m, w[j]);
+                if (F32)
+                    m &= 0x7FFFFFFFu;
+                else
+                    m = max(m << 16 & 0x7FFF0000u, m & 0x7FFF0000u);
                 if (GROUPED && (gone >> i) & 1)
                     m = 0x7F800000u;
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 if (F32)
                     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 const int e = fp4_exponent(m);
-                const float mul = fp4_multiplier(e);
+                const uint64_t mul = f2_splat(fp4_multiplier(e));
                 float v[kPer];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if constexpr (F32) {
-                        v[j] = __uint_as_float(w[j]) * mul;
+                        v[j] = __uint_as_float(w[j]);
                     } else {
-                        v[2 * j] = bf16_lo(w[j]) * mul;
-                        v[2 * j + 1] = bf16_hi(w[j]) * mul;
+                        v[2 * j] = bf16_lo(w[j]);
+                        v[2 * j + 1] = bf16_hi(w[j]);
                     }
                 }
-                const bool keep = r < at.row_end && in_blk;
-                unsigned char *out = p.out_row + r * p.row_pitch + c / 2;
+                const bool keep = r0 + 32 * i < rows_left && in_blk;
                 if constexpr (F32) {
-                    const uint32_t o = e == 255 ? 0u : cvt_fp4x8(v);
+                    const uint32_t o = e == 255 ? 0u : cvt_fp4x8_scaled(v, mul);
                     if (keep)
                         *reinterpret_cast<uint32_t *>(out) = o;
                 } else {
-                    const uint32_t lo = e == 255 ? 0u : cvt_fp4x8(v), hi = e == 255 ? 0u : cvt_fp4x8(v + 8);
+                    const uint32_t lo = e == 255 ? 0u : cvt_fp4x8_scaled(v, mul), hi = e == 255 ? 0u : cvt_fp4x8_scaled(v + 8, mul);
                     if (keep)
                         *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
                 }
+                out += 32 * p.row_pitch;
                 // the row's blocks, two (four) lanes apart, as the scale tile's 2 (4) bytes
                 uint32_t sc = keep ? e : 0;
                 sc |= __shfl_down_sync(0xFFFFFFFFu, sc, F32 ? 4 : 2) << 8;
                 if (!F32)
                     sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 4) << 16;
-                if (seg == 0) {
-                    uint8_t *to = p.scale_row + (static_cast<int64_t>(at.rt) * p.col_tiles + plane_ct) * 512 + (((lr & 31) << 4) | ((lr >> 5) << 2));
+                if (seg == 0) {  // row r0 + 32 i: entry 16 r0 + 4 i
                     if constexpr (F32)
-                        reinterpret_cast<uint16_t *>(to)[half] = static_cast<uint16_t>(sc);
+                        reinterpret_cast<uint16_t *>(sc_out + 4 * i)[half] = static_cast<uint16_t>(sc);
                     else
-                        *reinterpret_cast<uint32_t *>(to) = sc;
+                        *reinterpret_cast<uint32_t *>(sc_out + 4 * i) = sc;
                 }
                 if (GROUPED && ((gone >> i) & 1) && at.ct == 0 && seg == 0 && p.err_flag != nullptr)
                     atomicOr(p.err_flag, 1);
@@ -266,14 +288,15 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 w[i] = tile[cast_word(rb * 32 + i) + word];
-                m = F32 ? max(m, w[i] & 0x7FFFFFFFu) : max_u16x2(m, w[i] & 0x7FFF7FFFu);
+                m = F32 ? absmax_nan_f32(m, w[i]) : absmax_nan_bf16x2(m, w[i]);
             }
+            m &= F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
             const int64_t blk = at.row0 / 32 + rb;
             const bool live_blk = blk * 32 < p.M;
 #pragma unroll
             for (int h = 0; h < (F32 ? 1 : 2); ++h) {
                 const int e = fp4_exponent(F32 ? m : h ? m & 0xFFFF0000u : m << 16);
-                const float mul = fp4_multiplier(e);
+                const uint64_t mul = f2_splat(fp4_multiplier(e));
                 uint32_t o[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -281,9 +304,9 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t x = w[8 * q + j];
-                        v[j] = (F32 ? __uint_as_float(x) : h ? bf16_hi(x) : bf16_lo(x)) * mul;
+                        v[j] = F32 ? __uint_as_float(x) : h ? bf16_hi(x) : bf16_lo(x);
                     }
-                    o[q] = e == 255 ? 0u : cvt_fp4x8(v);
+                    o[q] = e == 255 ? 0u : cvt_fp4x8_scaled(v, mul);
                 }
                 const int tc = F32 ? word : 2 * word + h;        // column of the tile
                 const int lc = half * kCols + tc;                // column of the scale tile

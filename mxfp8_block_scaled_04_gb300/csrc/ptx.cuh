@@ -218,6 +218,20 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+// The same, NaN where either operand is: for callers that must see NaN and infinities.
+__device__ __forceinline__ uint32_t absmax_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t absmax_nan_f32(uint32_t a, uint32_t b)
+{
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
+}
+
 // acc + (the low / high BF16 of w), one mixed-precision add (the BF16 operand
 // widens exactly, the sum rounds to nearest as an fp32 add).
 __device__ __forceinline__ float add_bf16_lo(float acc, uint32_t w)
