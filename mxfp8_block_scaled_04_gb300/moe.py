@@ -12,7 +12,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from .binding import _addr, lib
-from .mxfp4 import _check, _check_input, _on, _stream
+from .mxfp4 import _check, _check_input, _lib, _on, _stream
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_TOPK = 32
@@ -70,9 +70,10 @@ def moe_combine_backward_c(dout, y, R, H, slots, weights, T, k, dy, dweights, st
 # A given ``stream`` is made current around the whole call, so that outputs and workspace belong to it.
 
 def _check_like(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
-    if t.dtype != dtype or t.dim() != 2 or not t.is_contiguous() or (shape is not None and t.shape != shape):
+    size = t.shape
+    if t.dtype is not dtype or len(size) != 2 or not t.is_contiguous() or (shape is not None and size != shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" {list(shape)}" if shape else " [., .]"))
-    return t.shape
+    return size
 
 
 def make_route_config(top_k: int, score="softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
@@ -100,7 +101,8 @@ def moe_route(logits: torch.Tensor, k: int, score="softmax", bias: Optional[torc
     dev = logits.device
     indices = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _check(moe_route_c(logits, kind, T, E, ld, cfg, indices, weights), "moe_route")
+    _check(_lib().moe_route(logits.data_ptr(), kind, T, E, ld, ctypes.byref(cfg), indices.data_ptr(), weights.data_ptr(),
+                            _stream(None)), "moe_route")
     return MoERoute(indices, weights)
 
 
@@ -131,9 +133,11 @@ def moe_plan(indices: torch.Tensor, num_experts: int, stream=None) -> MoEPlan:
     offsets = torch.empty((num_experts + 1,), dtype=torch.int64, device=dev)
     slots = torch.empty((T, k), dtype=torch.int32, device=dev)
     tokens = torch.empty((T * k,), dtype=torch.int32, device=dev)
-    nbytes = moe_plan_workspace_bytes(T * k, num_experts)
+    # small plans need none; the library knows from where on
+    nbytes = moe_plan_workspace_bytes(T * k, num_experts) if T * k > 1024 else 0
     workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
-    _check(moe_plan_c(indices, T * k, k, num_experts, offsets, slots, tokens, workspace), "moe_plan")
+    _check(_lib().moe_plan(indices.data_ptr(), T * k, k, num_experts, offsets.data_ptr(), slots.data_ptr(),
+                           tokens.data_ptr(), _addr(workspace), _stream(None)), "moe_plan")
     return MoEPlan(offsets, slots, tokens)
 
 
@@ -147,7 +151,8 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Te
     if weights is not None:
         _check_like(weights, "weights", torch.float32, (T, k))
     out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-    _check(moe_combine_c(y, R, H, slots, weights, T, k, out), "moe_combine")
+    _check(_lib().moe_combine(y.data_ptr(), R, H, slots.data_ptr(), _addr(weights), T, k, out.data_ptr(),
+                              _stream(None)), "moe_combine")
     return out
 
 

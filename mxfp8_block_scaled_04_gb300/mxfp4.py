@@ -38,8 +38,23 @@ def _stream(stream) -> Optional[int]:
     """The cudaStream_t of ``stream``, or of the current device's current stream (by torch's raw getter, which
     costs a tenth of a microsecond where torch.cuda.current_stream() costs three)."""
     if stream is None and torch.cuda.is_initialized():
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current()
     return _any_stream(stream)
+
+
+def _current() -> int:
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+_library = None
+
+
+def _lib():
+    """The loaded library, without binding.lib()'s lock once it is there."""
+    global _library
+    if _library is None:
+        _library = lib()
+    return _library
 
 
 # ---- one-for-one C entry points --------------------------------------------------
@@ -133,9 +148,9 @@ def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None) -> No
     pitch = -(-cols // 32) * 16
     plane = -(-rows // 128) * -(-cols // 128) * 512
     shape = (rows, pitch) if groups is None else (groups, rows, pitch)
-    if codes.dtype != torch.uint8 or codes.shape != shape or not codes.is_contiguous():
+    if codes.dtype is not torch.uint8 or codes.shape != shape or not codes.is_contiguous():
         raise ValueError(f"{name}.codes must be a contiguous uint8 tensor {list(shape)}")
-    if scales.dtype != torch.uint8 or not scales.is_contiguous() or (
+    if scales.dtype is not torch.uint8 or not scales.is_contiguous() or (
             scales.numel() < plane if groups is None else scales.shape != (groups, plane)):
         raise ValueError(f"{name}.scales must be a contiguous uint8 tensor of {plane} bytes per matrix")
 
@@ -165,10 +180,16 @@ def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False,
             return quantize_mxfp4(x, rowwise, colwise, noop)
     kind, M, N, ld = _check_input(x)
     dev = x.device
-    row = _empty_matrix(M, N, dev) if rowwise else None
-    col = _empty_matrix(N, M, dev) if colwise else None
-    _check(mxfp4_quantize(x, kind, M, N, ld, row and row.codes, row and row.scales, col and col.codes,
-                          col and col.scales, noop), "mxfp4_quantize")
+    row = col = rc = rs = cc = cs = None
+    if rowwise:
+        codes, scales, _, _ = row = _empty_matrix(M, N, dev)
+        rc, rs = codes.data_ptr(), scales.data_ptr()
+    if colwise:
+        codes, scales, _, _ = col = _empty_matrix(N, M, dev)
+        cc, cs = codes.data_ptr(), scales.data_ptr()
+    st = _lib().mxfp4_quantize(x.data_ptr(), kind, M, N, ld, rc, rs, cc, cs, _addr(noop), _stream(None))
+    if st:
+        raise MXFP8Error(st, "mxfp4_quantize")
     return MXFP4Tensor(row, col)
 
 
@@ -203,7 +224,10 @@ def dequantize_mxfp4(m: MXFP4Matrix, dtype: torch.dtype = torch.bfloat16, stream
     kind = _check_out_dtype(dtype)
     _check_matrix(m, "m")
     out = torch.empty((m.rows, m.cols), dtype=dtype, device=m.codes.device)
-    _check(mxfp4_dequantize(m.codes, m.scales, m.rows, m.cols, out, kind), "mxfp4_dequantize")
+    st = _lib().mxfp4_dequantize(m.codes.data_ptr(), m.scales.data_ptr(), m.rows, m.cols, out.data_ptr(), kind,
+                                 _stream(None))
+    if st:
+        raise MXFP8Error(st, "mxfp4_dequantize")
     return out
 
 
@@ -225,7 +249,10 @@ def matmul_mxfp4(a: MXFP4Matrix, b: MXFP4Matrix, out_dtype: torch.dtype = torch.
         kind, rows, cols, ldo = _check_input(out, "out")
         if (rows, cols) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
-    _check(mxfp4_matmul(a.codes, a.scales, M, b.codes, b.scales, N, K, out, kind, ldo), "mxfp4_matmul")
+    st = _lib().mxfp4_matmul(a.codes.data_ptr(), a.scales.data_ptr(), M, b.codes.data_ptr(), b.scales.data_ptr(), N, K,
+                             out.data_ptr(), kind, ldo, _stream(None))
+    if st:
+        raise MXFP8Error(st, "mxfp4_matmul")
     return out
 
 
