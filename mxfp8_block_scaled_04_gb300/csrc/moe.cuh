@@ -111,7 +111,7 @@ __device__ __forceinline__ void softmax_row(float (&l)[VPL], float (&s)[VPL])
         s[i] = none ? s[i] : s[i] / r[0];
 }
 
-__device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid_exact(float l) { return __frcp_rn(1.0f + expf(-l)); }
 
 // Order of keys as integers: NaN below every number, -0 equal to 0; 0 is left for "cannot be chosen".
 __device__ __forceinline__ uint32_t order_key(float x)
@@ -264,14 +264,13 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
             const int src = __ffs(__ballot_sync(kAll, bk == best)) - 1;
             int e = 0;
             if (lane == src) {  // its first expert with that key leaves
-                bool found = false;
+#pragma unroll
+                for (int i = VPL - 1; i >= 0; --i)
+                    e = key[i] == best ? i : e;
                 bk = 0;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) {
-                    const bool hit = !found && key[i] == best;
-                    e = hit ? i : e;
-                    key[i] = hit ? 0u : key[i];
-                    found |= hit;
+                    key[i] = i == e ? 0u : key[i];
                     bk = max(bk, key[i]);
                 }
                 e += lane * VPL;
@@ -517,6 +516,7 @@ __global__ void __launch_bounds__(kPlanThreads) moe_rank_kernel(const PlanParams
     for (int e = tid; e <= p.E; e += kPlanThreads) {
         int b = 0, a = 0;
         if (p.chunks > 1) {
+#pragma unroll 8
             for (int c = 0; c < p.chunks; ++c) {
                 const int v = p.counts[static_cast<int64_t>(c) * (p.E + 1) + e];
                 b += c < static_cast<int>(blockIdx.x) ? v : 0;
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const Comb
     }
 }
 
-constexpr int kCombineBwdThreads = 256;
+constexpr int kCombineBwdThreads = 128;
 
 // One CTA per token: dout is read once per eight choices; the dot products are summed per thread over its
 // columns, then over lanes, then over warps, in that order.

@@ -413,12 +413,14 @@ mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t ro
     const bool vec = cols % per == 0;
     const int64_t vecs = ceil_div(cols, per) + (vec ? 0 : 1);  // a row that starts off a vector touches one more
     const int64_t groups = ceil_div(rows, vec ? kDecodeRows<true> : kDecodeRows<false>);
-    const dim3 grid(static_cast<unsigned>(ceil_div(vecs, 128)), static_cast<unsigned>(groups < 65535 ? groups : 65535));
+    // a row's vectors over blocks of up to 256 threads, as evenly as whole warps allow
+    const unsigned threads = static_cast<unsigned>(ceil_div(ceil_div(vecs, ceil_div(vecs, 256)), 32) * 32);
+    const dim3 grid(static_cast<unsigned>(ceil_div(vecs, threads)), static_cast<unsigned>(groups < 65535 ? groups : 65535));
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const auto *c = static_cast<const uint8_t *>(codes);
     const auto *s = static_cast<const uint8_t *>(scale);
     const int64_t pitch = ceil_div(cols, 32) * 16, col_tiles = ceil_div(cols, 128);
-    auto launch = [&](auto *kern) { return launch_serialized(kern, grid, 128, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
+    auto launch = [&](auto *kern) { return launch_serialized(kern, grid, threads, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
     if (!vec)
         return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false>) : launch(mxfp4_decode_kernel<false, false>);
     return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true>) : launch(mxfp4_decode_kernel<false, true>);

@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherParams p)
 // and scales it loads first.  Where rows of the output are no whole vectors, its elements start at the row's first
 // aligned one, anywhere in the codes.  Bound by its writes.
 template <bool VEC>
-constexpr int kDecodeRows = VEC ? 8 : 4;
+constexpr int kDecodeRows = VEC ? 8 : 4;  // a power of two: a thread's rows lie in one 32-row part of a scale tile
 
 __device__ __forceinline__ float fp4_scale(uint32_t e)
 {
@@ -423,46 +423,53 @@ __device__ __forceinline__ float fp4_scale(uint32_t e)
 }
 
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(128) mxfp4_decode_kernel(const uint8_t *codes, const uint8_t *scale, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t *codes, const uint8_t *scale, int64_t rows, int64_t cols,
                                                            int64_t pitch, int64_t col_tiles, void *out)
 {
-    constexpr int V = F32 ? 4 : 8, kRows = kDecodeRows<VEC>;
+    constexpr int V = F32 ? 4 : 8, kRows = kDecodeRows<VEC>, kSize = F32 ? 4 : 2;
     pdl_wait_and_release();
-    const int64_t j = blockIdx.x * int64_t{128} + threadIdx.x;  // vector of the row
+    const int64_t j = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;  // vector of the row
+    const int last = static_cast<int>(cols) - 1, top = static_cast<int>(pitch / 4) - 1;
+    if (V * (j - 1) >= cols)  // off every row, whatever element its vectors start at
+        return;
     for (int64_t first = blockIdx.y * int64_t{kRows}; first < rows; first += int64_t{kRows} * gridDim.y) {
+        const int n = static_cast<int>(rows - first < kRows ? rows - first : kRows);
+        // the scale tile entry of (first, block 0): 16 bytes per row on; block b is b / 4 tiles and b % 4 bytes on
+        const uint8_t *s = scale + (first >> 7) * col_tiles * 512 + ((first & 31) << 4) + (((first >> 5) & 3) << 2);
+        const uint8_t *row = codes + first * pitch;
+        // VEC: the row's column of every row's vector.  Else row i's vectors start (first + i) * cols % V elements early.
+        const int lead0 = VEC ? 0 : static_cast<int>((first * cols) & (V - 1)), lead_step = VEC ? 0 : static_cast<int>(cols & (V - 1));
         uint32_t q[kRows], e0[kRows], e1[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int64_t r = first + i < rows ? first + i : rows - 1;
-            // the scale tile entry of (r, block 0); block b is (b / 4) tiles and b % 4 bytes on
-            const uint8_t *s = scale + (r >> 7) * col_tiles * 512 + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
-            const uint8_t *row = codes + r * pitch;
-            const int last = static_cast<int>(cols) - 1;
+            const int use = i < n ? i : n - 1;
+            const int64_t c = V * j - ((lead0 + use * lead_step) & (V - 1));
             if constexpr (VEC) {
-                const int c = static_cast<int>(V * j < cols ? V * j : 0);
-                q[i] = F32 ? *reinterpret_cast<const uint16_t *>(row + c / 2) : *reinterpret_cast<const uint32_t *>(row + c / 2);
-                e0[i] = s[(c >> 7) * 512 + ((c >> 5) & 3)];
+                const int at = static_cast<int>(c < cols ? c : 0);
+                q[i] = F32 ? *reinterpret_cast<const uint16_t *>(row + use * pitch + at / 2) : *reinterpret_cast<const uint32_t *>(row + use * pitch + at / 2);
+                e0[i] = s[use * 16 + (at >> 7) * 512 + ((at >> 5) & 3)];
             } else {
-                // the row's vectors, the first of them from before its start; past the ends any loaded value does
-                const int64_t c = V * j - (r * cols & (V - 1));
+                // the vector's elements from two words of codes and one or two blocks; past the ends any loaded value does
                 const int c0 = static_cast<int>(c < 0 ? 0 : c < last ? c : last), c1 = static_cast<int>(c + V - 1 < last ? c + V - 1 : last);
-                const uint32_t *words = reinterpret_cast<const uint32_t *>(row);
-                const int top = static_cast<int>(pitch / 4) - 1, w = c < 0 ? -1 : c0 >> 3;
-                const uint32_t lo = words[max(w, 0)], hi = words[min(w + 1, top)];
-                q[i] = static_cast<uint32_t>((static_cast<uint64_t>(hi) << 32 | lo) >> (4 * (static_cast<int>(c) & 7)));
-                const int b0 = c0 >> 5, b1 = c1 >> 5;
-                e0[i] = s[(b0 >> 2) * 512 + (b0 & 3)];
-                e1[i] = s[(b1 >> 2) * 512 + (b1 & 3)];
+                const uint32_t *words = reinterpret_cast<const uint32_t *>(row + use * pitch);
+                const int w = c < 0 ? -1 : c0 >> 3;
+                q[i] = __funnelshift_r(words[max(w, 0)], words[min(w + 1, top)], 4 * (static_cast<int>(c) & 7));
+                e0[i] = s[use * 16 + (c0 >> 7) * 512 + ((c0 >> 5) & 3)];
+                e1[i] = s[use * 16 + (c1 >> 7) * 512 + ((c1 >> 5) & 3)];
             }
         }
+        unsigned char *to = static_cast<unsigned char *>(out) + (first * cols + V * j) * kSize;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int64_t r = first + i;
-            const int64_t c = VEC ? V * j : V * j - (r * cols & (V - 1));
-            if (r >= rows || c >= cols)
+            if (i >= n)
+                break;
+            const int lead = (lead0 + i * lead_step) & (V - 1);
+            const int64_t c = V * j - lead;
+            unsigned char *dst = to + (i * cols - lead) * kSize;
+            if (c > last)
                 continue;
             const float m0 = fp4_scale(e0[i]), m1 = VEC ? m0 : fp4_scale(e1[i]);
-            const int turn = VEC ? V : static_cast<int>(32 - (c & 31));  // elements of the first block
+            const int turn = VEC ? V : 32 - static_cast<int>(c & 31);  // elements of the first block
             float v[V];
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) {
@@ -470,21 +477,20 @@ __global__ void __launch_bounds__(128) mxfp4_decode_kernel(const uint8_t *codes,
                 v[2 * k] *= 2 * k < turn ? m0 : m1;
                 v[2 * k + 1] *= 2 * k + 1 < turn ? m0 : m1;
             }
-            const int64_t at = r * cols + c;
-            if (VEC || (c >= 0 && c + V <= cols)) {
+            if (VEC || (c >= 0 && c + V - 1 <= last)) {
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // exact: the values have two significant bits
-                    w[k] = F32 ? __float_as_uint(v[k]) : (__float_as_uint(v[(2 * k) % V]) >> 16) | (__float_as_uint(v[(2 * k + 1) % V]) & 0xFFFF0000u);
-                *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(out) + at * (F32 ? 4 : 2)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    w[k] = F32 ? __float_as_uint(v[k]) : __byte_perm(__float_as_uint(v[(2 * k) % V]), __float_as_uint(v[(2 * k + 1) % V]), 0x7632);
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    if (c + k >= 0 && c + k < cols) {
+                    if (c + k >= 0 && c + k <= last) {
                         if constexpr (F32)
-                            static_cast<float *>(out)[at + k] = v[k];
+                            reinterpret_cast<float *>(dst)[k] = v[k];
                         else
-                            static_cast<uint16_t *>(out)[at + k] = static_cast<uint16_t>(__float_as_uint(v[k]) >> 16);
+                            reinterpret_cast<uint16_t *>(dst)[k] = static_cast<uint16_t>(__float_as_uint(v[k]) >> 16);
                     }
                 }
             }
