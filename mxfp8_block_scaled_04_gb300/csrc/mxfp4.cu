@@ -138,13 +138,13 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
     mxfp8_status_t st = setup(mxfp4_pair_kernel<F32, GROUPED>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
-    CUtensorMap pm, qm, psm, qsm;
+    CUtensorMap pm, qm, qpm, psm, qsm;
     if ((st = code_map(&pm, p_codes, p_rows, row_bytes, 128)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, 128)) != MXFP8_OK ||
-        (st = scale_map(&psm, p.p_scale, p_plane_rows, p.kc, 1)) != MXFP8_OK || (st = scale_map(&qsm, p.q_scale, q_plane_rows, p.kc, 2)) != MXFP8_OK)
+        (st = code_map(&qpm, q_codes, p.Q, row_bytes, 32)) != MXFP8_OK || (st = scale_map(&psm, p.p_scale, p_plane_rows, p.kc, 1)) != MXFP8_OK || (st = scale_map(&qsm, p.q_scale, q_plane_rows, p.kc, 2)) != MXFP8_OK)
         return st;
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
-    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, pm, qm, psm,
-                             qsm, p);
+    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, pm, qm, qpm,
+                             psm, qsm, p);
 }
 
 // The kernel for few tiles.  S CTAs share a tile's K: the most (1, 2, 4, 8) for which all CTAs are resident at once, two

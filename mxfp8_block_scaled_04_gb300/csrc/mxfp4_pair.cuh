@@ -24,7 +24,7 @@ constexpr int kPairAcc1 = 224, kPairShared = 32, kPairScaleCol = 480;
 template <bool F32, bool GROUPED>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
-                      const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map, const GemmParams p)
+                      const __grid_constant__ CUtensorMap q_part_map, const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map, const GemmParams p)
 {
     extern __shared__ unsigned char gemm_smem[];
     __shared__ GroupTable<GROUPED> groups;
@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (tid == 0) {
         prefetch_tensormap(&p_map);
         prefetch_tensormap(&q_map);
+        prefetch_tensormap(&q_part_map);
         prefetch_tensormap(&ps_map);
         prefetch_tensormap(&qs_map);
         for (int s = 0; s < kPairStages; ++s) {
@@ -85,6 +86,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int t = first; t < num_tiles && ok; t += stride) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int half = ((c.valid + 31) & ~31) / 2;
+            const int boxes = half > 96 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
+            const uint32_t bytes = 2 * (kPairStage - (boxes ? (4 - boxes) * 32 * 128 : 0));  // of both CTAs
             for (int k = 0; k < p.k_iters; ++k) {
                 ok = mbar_wait_cluster(empty0 + 8 * slot, phase ^ 1, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -95,9 +98,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (elect_one()) {
                     if (warp == 0) {
                         if (rank == 0)
-                            mbar_arrive_expect_tx(full0 + 8 * slot, 2 * kPairStage);  // both CTAs' bytes
+                            mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
                         tma_load_2d_pair(dp, &p_map, bar, k * 128, c.p_row + static_cast<int>(rank) * 128);
-                        tma_load_2d_pair(dp + kPairCodes, &q_map, bar, k * 128, c.q_row + static_cast<int>(rank) * half);
+                        if (boxes == 0)
+                            tma_load_2d_pair(dp + kPairCodes, &q_map, bar, k * 128, c.q_row + static_cast<int>(rank) * half);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d_pair(dp + kPairCodes + b * 32 * 128, &q_part_map, bar, k * 128, c.q_row + static_cast<int>(rank) * half + 32 * b);
                     } else {
                         const uint32_t ds = dp + 2 * kPairCodes;
                         tma_load_2d_pair(ds, &ps_map, bar, k * 256, static_cast<int>(c.p_plane) + static_cast<int>(rank));
