@@ -171,7 +171,9 @@ template <bool F32>
 mxfp8_status_t launch_split(const GemmParams &p_, const void *p_codes, const void *q_codes, int64_t row_bytes, int device, cudaStream_t stream)
 {
     GemmParams p = p_;
-    p.q_box = p.Q <= 32 ? 32 : 128;
+    // small boxes for few tokens: rows past Q cost the copy engine as much as others (1x8192x28672: 23.9 us in boxes of 32
+    // rows, 22.0 in boxes of 16)
+    p.q_box = p.Q <= 16 ? 16 : p.Q <= 32 ? 32 : 128;
     CUtensorMap pm, qm;
     mxfp8_status_t st;
     if ((st = code_map(&pm, p_codes, p.P, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, p.q_box)) != MXFP8_OK)
