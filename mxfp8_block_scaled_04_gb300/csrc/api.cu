@@ -26,8 +26,6 @@ namespace {
 
 using namespace mxfp8;
 
-constexpr int kMaxDevices = 64;
-
 std::atomic<uint64_t> g_launches{0};
 
 // Launch with programmatic stream serialisation: the kernel may begin while the

@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -27,6 +29,36 @@ void count_launch();
 unsigned int *fault_word_address(int device);
 
 inline bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int kMaxDevices = 64;
+
+// One per kernel: on its first call on a device opts the kernel in to `smem` bytes; gives the CTAs resident at once.
+struct KernelSetup {
+    std::mutex mu;
+    int sms[kMaxDevices] = {};
+    int per_sm[kMaxDevices] = {};
+
+    template <typename K>
+    mxfp8_status_t operator()(K *kern, int device, int threads, int smem, int *ctas)
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (device < 0 || device >= kMaxDevices)
+            return MXFP8_ERR_DEVICE;
+        if (per_sm[device] == 0) {
+            int n = 0, s = 0;
+            if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                return MXFP8_ERR_LAUNCH;
+            }
+            sms[device] = s;
+            per_sm[device] = n;
+        }
+        *ctas = per_sm[device] * sms[device];
+        return MXFP8_OK;
+    }
+};
 
 // Launch with programmatic stream serialisation (and, with cluster > 1, in thread-block clusters of that
 // many consecutive blocks).  Only kernels whose threads all wait (griddepcontrol.wait) before their first

@@ -64,16 +64,28 @@ int lane_experts(int64_t E)
     return v;
 }
 
+// Resident CTAs that take tokens in turn (the row set-up is paid once per warp).
+template <typename K>
+mxfp8_status_t launch_resident(K *kern, KernelSetup &setup, int64_t blocks, const RouteParams &p, cudaStream_t stream)
+{
+    int device = 0, ctas = 0;
+    mxfp8_status_t st;
+    if ((st = active_device(&device)) != MXFP8_OK || (st = setup(kern, device, kRouteThreads, 0, &ctas)) != MXFP8_OK)
+        return st;
+    return launch_serialized(kern, dim3(static_cast<unsigned>(blocks < ctas ? blocks : ctas)), kRouteThreads, 0, 1, stream, p);
+}
+
 template <bool BACKWARD, int VPL>
 mxfp8_status_t launch_route_vpl(const RouteParams &p, int type, cudaStream_t stream)
 {
-    const dim3 grid(grid_of((p.T + kRouteThreads / 32 - 1) / (kRouteThreads / 32)));
+    static KernelSetup f32, bf16;
+    const int64_t blocks = (p.T + kRouteThreads / 32 - 1) / (kRouteThreads / 32);
     if constexpr (BACKWARD)
-        return type == MXFP4_F32 ? launch_serialized(moe_route_backward_kernel<VPL, true>, grid, kRouteThreads, 0, 1, stream, p)
-                                 : launch_serialized(moe_route_backward_kernel<VPL, false>, grid, kRouteThreads, 0, 1, stream, p);
+        return type == MXFP4_F32 ? launch_resident(moe_route_backward_kernel<VPL, true>, f32, blocks, p, stream)
+                                 : launch_resident(moe_route_backward_kernel<VPL, false>, bf16, blocks, p, stream);
     else
-        return type == MXFP4_F32 ? launch_serialized(moe_route_kernel<VPL, true>, grid, kRouteThreads, 0, 1, stream, p)
-                                 : launch_serialized(moe_route_kernel<VPL, false>, grid, kRouteThreads, 0, 1, stream, p);
+        return type == MXFP4_F32 ? launch_resident(moe_route_kernel<VPL, true>, f32, blocks, p, stream)
+                                 : launch_resident(moe_route_kernel<VPL, false>, bf16, blocks, p, stream);
 }
 
 template <bool BACKWARD>

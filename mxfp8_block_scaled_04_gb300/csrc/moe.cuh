@@ -111,7 +111,37 @@ __device__ __forceinline__ void softmax_row(float (&l)[VPL], float (&s)[VPL])
         s[i] = none ? s[i] : s[i] / r[0];
 }
 
-__device__ __forceinline__ float sigmoid_exact(float l) { return __frcp_rn(1.0f + expf(-l)); }
+// 1 / (1 + exp(-l)), the quotient rounded to nearest.  Up to 2^126 the reciprocal is the hardware's estimate
+// and one correction with fused multiply-adds (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990); against __frcp_rn it was compared on every mantissa and found equal.
+constexpr float kReciprocalMax = 8.507059173023462e37f;  // 2^126
+__device__ __forceinline__ float reciprocal_fast(float y)
+{
+    float q;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(y));
+    return fmaf(q, fmaf(-y, q, 1.0f), q);
+}
+__device__ __forceinline__ float sigmoid_exact(float l)
+{
+    const float y = 1.0f + expf(-l);
+    return y > kReciprocalMax ? __frcp_rn(y) : reciprocal_fast(y);
+}
+template <int VPL>
+__device__ __forceinline__ void sigmoid_row(const float (&l)[VPL], float (&s)[VPL])
+{
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const float y = 1.0f + expf(-l[i]);
+        s[i] = reciprocal_fast(y);
+        top = fmaxf(top, y);
+    }
+    if (top > kReciprocalMax) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            s[i] = sigmoid_exact(l[i]);
+    }
+}
 
 // Order of keys as integers: NaN below every number, -0 equal to 0; 0 is left for "cannot be chosen".
 __device__ __forceinline__ uint32_t order_key(float x)
@@ -120,14 +150,68 @@ __device__ __forceinline__ uint32_t order_key(float x)
     return x != x ? 1u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+// order_key of a number (not NaN, not -0).
+__device__ __forceinline__ uint32_t order_key_number(float x)
+{
+    const uint32_t b = __float_as_uint(x);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Falling order, by Batcher's odd-even merge network (VPL a power of two).
+template <int A, int B, int VPL>
+__device__ __forceinline__ void order_two(uint32_t (&v)[VPL])
+{
+    const uint32_t a = v[A], b = v[B];
+    v[A] = max(a, b);
+    v[B] = min(a, b);
+}
+template <int LO, int N, int R, int VPL>
+__device__ __forceinline__ void merge_keys(uint32_t (&v)[VPL])
+{
+    if constexpr (2 * R < N) {
+        merge_keys<LO, N, 2 * R>(v);
+        merge_keys<LO + R, N, 2 * R>(v);
+#pragma unroll
+        for (int i = LO + R; i + R < LO + N; i += 2 * R) {
+            const uint32_t a = v[i], b = v[i + R];
+            v[i] = max(a, b);
+            v[i + R] = min(a, b);
+        }
+    } else {
+        order_two<LO, LO + R>(v);
+    }
+}
+template <int VPL, int LO = 0, int N = VPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&v)[VPL])
+{
+    if constexpr (N > 1) {
+        sort_keys<VPL, LO, N / 2>(v);
+        sort_keys<VPL, LO + N / 2, N / 2>(v);
+        merge_keys<LO, N, 1>(v);
+    }
+}
+
+// The chosen are found by value: each lane sorts its keys, and k times the largest head of all lanes leaves (one
+// warp-wide maximum, one ballot).  Which expert of the lane it was is looked up once, for all k at a time.  Bound by
+// issue: 256 experts take about 600 warp instructions per token.
 template <int VPL, bool F32>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p)
 {
     constexpr float kNegInf = -__builtin_huge_valf();
-    __shared__ float keys[kRouteThreads / 32][32 * VPL];
+    __shared__ __align__(16) float rows[kRouteThreads / 32][32 * VPL];
+    __shared__ __align__(16) uint32_t keys[kRouteThreads / 32][32 * VPL];
     pdl_wait_and_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *row = rows[warp];
     const int gs = p.E / p.groups;
+    const int run = gs / VPL;  // lanes of a group, where a group is an aligned run of them
+    const bool limited = p.topk_groups < p.groups, runs = run * VPL == gs && (run & (run - 1)) == 0;
     float b[VPL];
     if (p.bias != nullptr) {
 #pragma unroll
@@ -139,146 +223,147 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
         uint32_t key[VPL];
         load_row<VPL, F32>(p, t, lane, l, kNegInf);
         if (p.sigmoid) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                s[i] = sigmoid_exact(l[i]);
+            sigmoid_row<VPL>(l, s);
         } else {
             softmax_row<VPL>(l, s);
         }
-        float kf[VPL];
+        float kf[VPL], nan = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            kf[i] = p.bias != nullptr ? s[i] + b[i] : l[i];
-            key[i] = lane * VPL + i < p.E ? order_key(kf[i]) : 0u;
+            kf[i] = p.bias != nullptr ? s[i] + b[i] : l[i] + 0.0f;  // a sum of a score is never -0
+            key[i] = order_key_number(kf[i]);
+            nan = max_nan(nan, kf[i]);
         }
-        if (p.topk_groups < p.groups) {
-            const int run = gs / VPL;  // lanes of a group
-            if (run * VPL == gs && (run & (run - 1)) == 0) {
-                // a group is an aligned run of lanes
-                uint32_t rank;
-                if (p.bias == nullptr) {
-                    rank = key[0];
+        if (nan != nan || p.E != 32 * VPL) {
 #pragma unroll
-                    for (int i = 1; i < VPL; ++i)
-                        rank = max(rank, key[i]);
-                    for (int d = 1; d < run; d <<= 1)
-                        rank = max(rank, __shfl_xor_sync(kAll, rank, d));
-                } else {
-                    uint32_t a = key[0], c = 0;  // the two largest
+            for (int i = 0; i < VPL; ++i)
+                key[i] = lane * VPL + i >= p.E ? 0u : kf[i] != kf[i] ? 1u : key[i];
+        }
+        __syncwarp();  // the token before is done with the arrays
+        if (limited && !runs) {
+            // lanes rank whole groups from shared memory
 #pragma unroll
-                    for (int i = 1; i < VPL; ++i) {
-                        c = max(c, min(a, key[i]));
-                        a = max(a, key[i]);
-                    }
-                    for (int d = 1; d < run; d <<= 1) {
-                        const uint32_t oa = __shfl_xor_sync(kAll, a, d), oc = __shfl_xor_sync(kAll, c, d);
-                        c = max(max(c, oc), min(a, oa));
-                        a = max(a, oa);
-                    }
-                    auto value = [](uint32_t u) { return u == 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u); };
-                    rank = order_key(gs > 1 ? value(a) + value(c) : value(a));
-                }
-                if (lane * VPL >= p.E || (lane & (run - 1)) != 0)
-                    rank = 0;  // one lane stands for a group
-                bool keep = false;
-                for (int j = 0; j < p.topk_groups; ++j) {
-                    const uint32_t best = __reduce_max_sync(kAll, rank);
-                    const int src = __ffs(__ballot_sync(kAll, rank == best)) - 1;
-                    if (lane == src)
-                        rank = 0;
-                    keep |= (lane & ~(run - 1)) == src;
-                }
+            for (int i = 0; i < VPL; ++i)
+                row[lane * VPL + i] = kf[i];
+            __syncwarp();
+            uint32_t rank[VPL];  // groups lane, lane + 32, ...: no more of them than experts
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    key[i] = keep ? key[i] : 0u;
-            } else {
-                // any other group size: lanes rank whole groups from shared memory
-                float *row = keys[warp];
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    row[lane * VPL + i] = kf[i];
-                __syncwarp();
-                uint32_t rank[VPL];  // groups lane, lane + 32, ...: no more of them than experts
-#pragma unroll
-                for (int n = 0; n < VPL; ++n) {
-                    rank[n] = 0;
-                    const int g = lane + 32 * n;
-                    if (g < p.groups) {
-                        uint32_t a = 0, c = 0;
-                        float va = 0.f, vc = 0.f;
-                        for (int i = 0; i < gs; ++i) {
-                            const float v = row[g * gs + i];
-                            const uint32_t u = order_key(v);
-                            if (u > a) {
-                                c = a, vc = va;
-                                a = u, va = v;
-                            } else if (u > c) {
-                                c = u, vc = v;
-                            }
+            for (int n = 0; n < VPL; ++n) {
+                rank[n] = 0;
+                const int g = lane + 32 * n;
+                if (g < p.groups) {
+                    uint32_t a = 0, c = 0;
+                    float va = 0.f, vc = 0.f;
+                    for (int i = 0; i < gs; ++i) {
+                        const float v = row[g * gs + i];
+                        const uint32_t u = order_key(v);
+                        if (u > a) {
+                            c = a, vc = va;
+                            a = u, va = v;
+                        } else if (u > c) {
+                            c = u, vc = v;
                         }
-                        rank[n] = p.bias == nullptr || gs == 1 ? a : order_key(va + vc);
                     }
+                    rank[n] = p.bias == nullptr || gs == 1 ? a : order_key(va + vc);
                 }
-                uint32_t taken = 0;  // bit n: group lane + 32 n is kept
-                for (int j = 0; j < p.topk_groups; ++j) {
-                    uint32_t top = 0;
-                    int at = 0;
+            }
+            uint32_t taken = 0;  // bit n: group lane + 32 n is kept
+            for (int j = 0; j < p.topk_groups; ++j) {
+                uint32_t top = 0;
+                int at = 0;
+#pragma unroll
+                for (int n = 0; n < VPL; ++n)
+                    if (rank[n] > top) {
+                        top = rank[n];
+                        at = n;
+                    }
+                const uint32_t best = __reduce_max_sync(kAll, top);
+                const int g = __reduce_min_sync(kAll, top == best ? lane + 32 * at : 1 << 20);
+                if (lane == (g & 31)) {
+                    taken |= 1u << (g >> 5);
 #pragma unroll
                     for (int n = 0; n < VPL; ++n)
-                        if (rank[n] > top) {
-                            top = rank[n];
-                            at = n;
-                        }
-                    const uint32_t best = __reduce_max_sync(kAll, top);
-                    const int g = __reduce_min_sync(kAll, top == best ? lane + 32 * at : 1 << 20);
-                    if (lane == (g & 31)) {
-                        taken |= 1u << (g >> 5);
-#pragma unroll
-                        for (int n = 0; n < VPL; ++n)
-                            rank[n] = n == (g >> 5) ? 0u : rank[n];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    const int g = (lane * VPL + i) / gs;
-                    const uint32_t kept = __shfl_sync(kAll, taken, g & 31);
-                    if (!(g < p.groups && (kept >> (g >> 5)) & 1))
-                        key[i] = 0;
+                        rank[n] = n == (g >> 5) ? 0u : rank[n];
                 }
             }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int g = (lane * VPL + i) / gs;
+                const uint32_t kept = __shfl_sync(kAll, taken, g & 31);
+                if (!(g < p.groups && (kept >> (g >> 5)) & 1))
+                    key[i] = 0;
+            }
+            __syncwarp();
         }
-        // the k largest keys, one at a time; lane j keeps the j-th's expert
-        float *row = keys[warp];
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
+        for (int i = 0; i < VPL; ++i) {
             row[lane * VPL + i] = s[i];
-        uint32_t bk = key[0];
-#pragma unroll
-        for (int i = 1; i < VPL; ++i)
-            bk = max(bk, key[i]);
-        int my_idx = 0;
+            keys[warp][lane * VPL + i] = key[i];
+        }
+        sort_keys<VPL>(key);
+        if (limited && runs) {
+            uint32_t rank = key[0];
+            if (p.bias == nullptr) {
+                for (int d = 1; d < run; d <<= 1)
+                    rank = max(rank, __shfl_xor_sync(kAll, rank, d));
+            } else {
+                uint32_t a = key[0], c = VPL > 1 ? key[VPL > 1 ? 1 : 0] : 0u;  // the two largest
+                for (int d = 1; d < run; d <<= 1) {
+                    const uint32_t oa = __shfl_xor_sync(kAll, a, d), oc = __shfl_xor_sync(kAll, c, d);
+                    c = max(max(c, oc), min(a, oa));
+                    a = max(a, oa);
+                }
+                auto value = [](uint32_t u) { return u == 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u); };
+                rank = order_key(gs > 1 ? value(a) + value(c) : value(a));
+            }
+            if (lane * VPL >= p.E || (lane & (run - 1)) != 0)
+                rank = 0;  // one lane stands for a group
+            bool keep = false;
+            for (int j = 0; j < p.topk_groups; ++j) {
+                const uint32_t best = __reduce_max_sync(kAll, rank);
+                const int src = __ffs(__ballot_sync(kAll, rank == best)) - 1;
+                rank = lane == src ? 0u : rank;
+                keep |= (lane & ~(run - 1)) == src;
+            }
+            key[0] = keep ? key[0] : 0u;  // a lane whose head cannot be chosen is never asked for the next
+        }
+        uint32_t my_key = 0;
+        int my_src = 0;
         for (int j = 0; j < p.k; ++j) {
-            const uint32_t best = __reduce_max_sync(kAll, bk);
-            const int src = __ffs(__ballot_sync(kAll, bk == best)) - 1;
-            int e = 0;
-            if (lane == src) {  // its first expert with that key leaves
+            const uint32_t best = __reduce_max_sync(kAll, key[0]);
+            const int src = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+            if (lane == j)
+                my_key = best, my_src = src;
+            if (lane == src) {
+#pragma unroll
+                for (int i = 0; i + 1 < VPL; ++i)
+                    key[i] = key[i + 1];
+                key[VPL - 1] = 0;
+            }
+        }
+        __syncwarp();
+        // the expert: the first of lane my_src's with that key, past those that earlier choices of the same key took
+        int my_idx = 0;
+        {
+            const bool mine = lane < p.k;
+            const unsigned same = __match_any_sync(kAll, mine ? my_key : 0u) & __match_any_sync(kAll, mine ? my_src : 32 + lane);
+            int skip = __popc(same & ((1u << lane) - 1));
+            uint32_t their[VPL];
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                their[i] = keys[warp][my_src * VPL + i];
+            if (__any_sync(kAll, mine && skip > 0)) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (their[i] == my_key && skip-- == 0)
+                        my_idx = i;
+            } else {
 #pragma unroll
                 for (int i = VPL - 1; i >= 0; --i)
-                    e = key[i] == best ? i : e;
-                bk = 0;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    key[i] = i == e ? 0u : key[i];
-                    bk = max(bk, key[i]);
-                }
-                e += lane * VPL;
+                    my_idx = their[i] == my_key ? i : my_idx;
             }
-            e = __shfl_sync(kAll, e, src);
-            my_idx = lane == j ? e : my_idx;
+            my_idx += my_src * VPL;
         }
-        __syncwarp();
         const float my_p = lane < p.k ? row[my_idx] : 0.f;
         float w = my_p;
         if (p.renorm) {

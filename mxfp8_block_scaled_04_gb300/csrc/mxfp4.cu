@@ -15,7 +15,6 @@ namespace {
 
 using namespace mxfp8;
 
-constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 
 constexpr int64_t kPairMinTiles = 76;       // tiles of CTA pairs: one for each pair of the GPU's 152 SMs
@@ -24,34 +23,6 @@ constexpr int64_t kPairMinGroupRows = 192;  // rows per expert on average
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool type_ok(int t) { return t == MXFP4_BF16 || t == MXFP4_F32; }
-
-// SMs of the device; opts the kernel in to `smem` bytes once per device (`done` is the kernel's own).
-struct KernelSetup {
-    std::mutex mu;
-    int sms[kMaxDevices] = {};
-    int per_sm[kMaxDevices] = {};
-
-    template <typename K>
-    mxfp8_status_t operator()(K *kern, int device, int threads, int smem, int *ctas)
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (device < 0 || device >= kMaxDevices)
-            return MXFP8_ERR_DEVICE;
-        if (per_sm[device] == 0) {
-            int n = 0, s = 0;
-            if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) {
-                cudaGetLastError();
-                return MXFP8_ERR_LAUNCH;
-            }
-            sms[device] = s;
-            per_sm[device] = n;
-        }
-        *ctas = per_sm[device] * sms[device];
-        return MXFP8_OK;
-    }
-};
 
 mxfp8_status_t sm_count(int device, int *sms)
 {

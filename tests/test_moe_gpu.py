@@ -118,6 +118,43 @@ def test_route_ties_masks_and_nan():
     assert r.indices.tolist() == [[0, 1]] and r.weights.tolist() == [[0.0, 0.0]]
 
 
+@pytest.mark.parametrize("E", [8, 32, 60, 256, 512])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_many_equal_keys(E, bias):
+    """Logits of a few values only: ties within and across lanes, all the way down the order."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.randint(-2, 3, (300, E), generator=g).float()
+    b = (torch.randint(0, 2, (E,), generator=g).float() * 0.5) if bias else None
+    k = min(E, 32)
+    r = mx.moe_route(l.cuda(), k, "sigmoid", None if b is None else b.cuda())
+    key = l.double() if b is None else torch.sigmoid(l.double()).float().double() + b.double()
+    # sigmoid(-x) + 0.5 and sigmoid(x) are never closer than 1e-3 on these values: equal keys are equal logits and biases
+    assert torch.equal(r.indices.cpu().long(), key.sort(dim=1, descending=True, stable=True).indices[:, :k])
+
+
+def test_route_extreme_logits():
+    """Infinite, huge and tiny logits among others: scores 0, 1 and subnormal, in every lane."""
+    inf = float("inf")
+    l = torch.randn(64, 64, generator=torch.Generator().manual_seed(3))
+    for i, v in enumerate((inf, -inf, 100.0, -100.0, -88.0, -87.5, -103.0, 3e38, -3e38, 0.0)):
+        l[i * 3, (i * 7) % 64] = v
+    want = torch.sigmoid(l.double())
+    r = mx.moe_route(l.cuda(), 16, "sigmoid", renormalize=False)
+    assert torch.equal(r.indices.cpu().long(), l.sort(dim=1, descending=True, stable=True).indices[:, :16])
+    w = want.gather(1, r.indices.cpu().long())
+    assert bool(((r.weights.cpu().double() - w).abs() <= 1e-6 * w + 1.5e-45).all())
+    # scores near the end of fp32: exp(-l) overflows beyond l = -88.72, where the score, below 2^-127, becomes 0; before
+    # that the argument's rounding adds |l| 2^-24 and a subnormal score half its spacing
+    low = torch.full((4, 64), -200.0)
+    low[:, 1], low[:, 9] = -88.2, -95.0
+    r = mx.moe_route(low.cuda(), 2, "sigmoid", renormalize=False)
+    assert r.indices.tolist() == [[1, 9]] * 4
+    w = torch.sigmoid(low.double()).gather(1, r.indices.cpu().long())
+    got = r.weights.cpu().double()
+    assert bool(((got - w).abs()[:, 0] <= (1e-6 + 88.2 * 2.0 ** -24) * w[:, 0] + 1.5e-45).all()) and bool((w[:, 0] > 0).all())
+    assert bool(((got - w).abs()[:, 1] <= 2.0 ** -127).all())
+
+
 def test_route_strided_logits_and_many_tokens():
     l, _ = draw_logits(3000, 64, F32, 4, False, "softmax", 8, 1, 1)
     big = torch.zeros(3000, 72)

@@ -371,3 +371,32 @@ def test_products_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want.flip(0))
+
+
+def test_past_2_32_elements():
+    """Offsets beyond 32 bits: the ends of a cast, a decode and a product of more than 2^32 elements equal those of
+    the same rows and columns on their own."""
+    M, N = 66048, 65664
+    assert M * N > 1 << 32
+    x = torch.empty((M, N), dtype=BF16, device="cuda").normal_()
+    q = mx.quantize_mxfp4(x, colwise=True)
+    tail, right = x[-256:].clone(), x[:, -256:].contiguous()
+    small = mx.quantize_mxfp4(tail, colwise=True)
+    assert torch.equal(q.row.codes[-256:], small.row.codes) and torch.equal(q.row.scales[-small.row.scales.numel():], small.row.scales)
+    assert torch.equal(q.col.codes[:, -128:], small.col.codes)
+    small = mx.quantize_mxfp4(right, colwise=True)
+    assert torch.equal(q.row.codes[:, -128:], small.row.codes)
+    assert torch.equal(q.col.codes[-256:], small.col.codes) and torch.equal(q.col.scales[-small.col.scales.numel():], small.col.scales)
+    del x, right, small
+    v = mx.dequantize_mxfp4(q.row)
+    assert torch.equal(v[-256:], mx.dequantize_mxfp4(mx.quantize_mxfp4(tail).row))
+    del v, q, tail
+    torch.cuda.empty_cache()
+    K = 64
+    a, b = torch.randn(M, K, device="cuda").to(BF16), torch.randn(N, K, device="cuda").to(BF16)
+    y = mx.matmul_mxfp4(mx.quantize_mxfp4(a).row, mx.quantize_mxfp4(b).row)
+    for rows, cols in ((slice(M - 300, M), slice(N - 300, N)), (slice(0, 300), slice(N - 300, N)), (slice(M - 300, M), slice(0, 300))):
+        part = mx.matmul_mxfp4(mx.quantize_mxfp4(a[rows].contiguous()).row, mx.quantize_mxfp4(b[cols].contiguous()).row)
+        assert torch.equal(y[rows, cols], part)
+    del y
+    torch.cuda.empty_cache()
