@@ -14,7 +14,7 @@
  *     scales  one plane of mxfp4_scale_bytes(R, C) bytes, GEMM-ready (MXFP8_SCALES_SWIZZLED): tiles of
  *             128 rows x 4 blocks, row-tile major, entry (r, b) of a tile at
  *             16 * (r % 32) + 4 * (r / 32) + b.  The cast writes every byte; those past R or past
- *             C / 32 are 0.
+ *             ceil(C / 32) are 0.  (In a plane from elsewhere those past ceil(C / 32) may hold anything but 255.)
  * The conventions of mxfp8.h hold for every call here: the caller's buffers, host-side checks that return a
  * status, work ordered on `stream` and launched with programmatic stream serialization, nothing read on
  * the host, no allocation.
@@ -110,8 +110,8 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
 
 /*
  * The experts' products in one launch: rows [offsets[g], offsets[g+1]) of out [total_rows, N] are those rows
- * of A (a grouped cast) times B_g^T.  b_codes [num_groups, N, row_bytes(K)]; b_scale [num_groups] planes of
- * mxfp4_scale_bytes(N, K).  offsets and err_flag as for mxfp4_quantize_grouped.
+ * of A (a grouped cast; a_scale of mxfp4_grouped_scale_bytes(total_rows, K, num_groups) bytes) times B_g^T.
+ * b_codes [num_groups, N, row_bytes(K)]; b_scale [num_groups] planes of mxfp4_scale_bytes(N, K).  offsets and err_flag as for mxfp4_quantize_grouped.
  */
 mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, int64_t total_rows, int num_groups,
                                     const int64_t *offsets, const void *b_codes, const void *b_scale, int64_t N,

@@ -17,8 +17,13 @@ using namespace mxfp8;
 
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 
-constexpr int64_t kPairMinTiles = 76;       // tiles of CTA pairs: one for each pair of the GPU's 152 SMs
-constexpr int64_t kPairMinGroupRows = 192;  // rows per expert on average
+// Products by CTA pairs need more rows than one 128-row tile and tiles for most of the 76 pairs; experts' products that
+// many rows per expert on average.  Measured (us, pairs / the other kernel), dense rows x N x K: 256x8192x8192 (32 tiles)
+// 14.7 / 12.5, 1024x4096x4096 (64) 10.5 / 10.7, 512x8192x8192 (64) 15.5 / 17.3, 128x28672x8192 (one row tile) 28 / 25,
+// 192x28672x8192 (112) 30 / 35; 64 experts of 2048 x 7168 with 64, 96, 128, 192, 256 rows: 95 / 87, 98 / 90, 101 / 107,
+// 107 / 139, 131 / 177.
+constexpr int64_t kPairMinTiles = 64;
+constexpr int64_t kPairMinGroupRows = 128;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -69,17 +74,17 @@ mxfp8_status_t code_map(CUtensorMap *map, const void *codes, int64_t rows, int64
                : MXFP8_ERR_LAUNCH;
 }
 
-template <int QT, bool F32, bool GROUPED>
-mxfp8_status_t launch_gemm_as(const CUtensorMap &pm, const CUtensorMap &qm, const GemmParams &p, int64_t tiles, int device, cudaStream_t stream)
+template <bool F32>
+mxfp8_status_t launch_group_as(const CUtensorMap &pm, const CUtensorMap &qm, const GemmParams &p, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr int smem = GemmShape<QT>::kSmem + kEpiBytes<F32>;
+    constexpr int smem = kGroupSmem + kEpiBytes<F32>;
     int ctas = 0;
-    const mxfp8_status_t st = setup(mxfp4_gemm_kernel<QT, F32, GROUPED>, device, kGemmThreads, smem, &ctas);
+    const mxfp8_status_t st = setup(mxfp4_group_kernel<F32>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
     const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
-    return launch_serialized(mxfp4_gemm_kernel<QT, F32, GROUPED>, dim3(grid), kGemmThreads, smem, 1, stream, pm, qm, p);
+    return launch_serialized(mxfp4_group_kernel<F32>, dim3(grid), kGemmThreads, smem, 1, stream, pm, qm, p);
 }
 
 // The scale plane as rows of 512-byte tiles, in boxes of 1024 bytes (one stage) x box_rows tile rows.
@@ -420,7 +425,6 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     const int64_t row_bytes = ceil_div(K, 32) * 16;
-    // 256 x 256 tiles of CTA pairs once they fill the GPU; below that 128 x 128 tiles occupy more SMs
     const int64_t pair_tiles = ceil_div(N, kPairRows) * ceil_div(M, kPairRows);
     if (M > 128 && pair_tiles >= kPairMinTiles) {
         p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
@@ -466,7 +470,6 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
     p.num_groups = num_groups;
     p.err_flag = err_flag;
     const int64_t row_bytes = ceil_div(K, 32) * 16;
-    // CTA pairs where an expert has more than one 128-row tile on average
     if (total_rows >= kPairMinGroupRows * num_groups && total_rows / kPairRows * ceil_div(N, kPairRows) >= kPairMinTiles) {
         const int64_t q_planes = static_cast<int64_t>(mxfp4_grouped_scale_bytes(total_rows, K, num_groups) / 512) / p.kc;
         p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
@@ -481,8 +484,8 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
     if ((st = code_map(&pm, b_codes, num_groups * N, row_bytes, kGemmRows)) != MXFP8_OK ||
         (st = code_map(&qm, a_codes, total_rows, row_bytes, p.q_box)) != MXFP8_OK)
         return st;
-    return out_type == MXFP4_F32 ? launch_gemm_as<128, true, true>(pm, qm, p, bound, device, stream)
-                                 : launch_gemm_as<128, false, true>(pm, qm, p, bound, device, stream);
+    return out_type == MXFP4_F32 ? launch_group_as<true>(pm, qm, p, bound, device, stream)
+                                 : launch_group_as<false>(pm, qm, p, bound, device, stream);
 }
 
 }  // extern "C"

@@ -1,15 +1,22 @@
-// MXFP4 products on the tensor cores (sm_103a): out[q, p] = sum_k Q[q, k] * P[p, k].
+// MXFP4 products on the tensor cores (sm_103a): out[q, p] = sum_k Q[q, k] * P[p, k].  What the three kernels share,
+// and the experts' kernel for few rows per expert.
 //
-// P (a layer's weights) takes the 128 accumulator lanes and Q (the tokens) the columns, so that a warp writes
-// 32 neighbouring elements of an output row and the MMA's n shrinks with the tokens: one kernel serves a
-// single token and a training batch.  Each block of 32 is scaled inside the MMA (kind::mxf4, two E8M0 scales
-// per 64 elements), so the operands go from HBM to the tensor core as they are stored.
+// P (a layer's weights) takes the accumulator's lanes and Q (the tokens) its columns, so that a warp writes
+// neighbouring elements of an output row and the MMA's n shrinks with the tokens: the same layout serves a single
+// token and a training batch.  Each block of 32 is scaled inside the MMA (kind::mxf4, two E8M0 scales per 64
+// elements), so the operands go from HBM to the tensor core as they are stored; products are exact, sums fp32.
 //
-// Roles (8 warps): warps 0 and 3 feed a ring of shared-memory stages of 256 elements of K (TMA tiles of the codes;
-// plain bulk copies of the scale tiles), warp 1 copies scales to TMEM and issues the MMAs, warp 2 owns the TMEM
-// allocation, warps 4-7 read the accumulators and write the output while the next tile accumulates in the other
-// TMEM buffer.  The CTAs are persistent over a round-robin tile list.  Every wait is bounded: on expiry the CTA
-// sets the library's fault word, waits (bounded) for its own copies and MMAs, frees its TMEM and returns.
+//   mxfp4_pair.cuh    many rows: 256 x 256 tiles by CTA pairs, bound by the tensor cores
+//   mxfp4_split.cuh   few tiles: one per CTA, or K shared by a cluster, bound by the weights' bytes
+//   mxfp4_group_kernel (below)   experts with few rows each: persistent 128 x 128 tiles, bound by the weights' bytes
+//                     (128 rows over 64 experts of 2048 x 7168: 67 us, 6.5 TB/s)
+//
+// Roles of a CTA (8 warps): warps 0 and 3 feed a ring of shared-memory stages of 256 elements of K (TMA tiles of the
+// codes; the scale tiles), warp 1 copies scales to TMEM and issues the MMAs, warp 2 owns the TMEM allocation, warps
+// 4-7 read the accumulators and write the output, here while the next tile accumulates in the other TMEM buffer.
+// The issuing warps run as whole warps and elect a lane per issue: from one diverged lane the issue itself bound every
+// stage (8192x8192x28672: 2018 us against 824 with this change alone).  Every wait is bounded: on expiry the CTA sets
+// the library's fault word, waits (bounded) for its own copies and MMAs, frees its TMEM and returns.
 #pragma once
 
 #include <cstdint>
@@ -35,7 +42,7 @@ struct GemmParams {
     int k64;             // MMA steps along K: ceil(K / 64)
     int p_tiles, q_tiles;
     int p_planes;        // 128-row scale tiles of P (of one expert)
-    int q_box;           // rows of Q per TMA box: 32 or 128
+    int q_box;           // rows of Q per TMA box
     void *out;
     int64_t ldo;
     bool vec_out;        // output rows are whole 16-byte vectors
@@ -45,18 +52,12 @@ struct GemmParams {
     int *err_flag;
 };
 
-template <int QT>
-struct GemmShape {
-    static constexpr int kPBytes = kGemmRows * 128;
-    static constexpr int kQBytes = QT * 128;
-    static constexpr int kPScale = 1024;               // two 512-byte scale tiles
-    static constexpr int kQScale = QT / 128 * 1024;
-    static constexpr int kStage = kPBytes + kQBytes + kPScale + kQScale;
-    static constexpr int kStages = 5;
-    static constexpr int kSmem = kStages * kStage + 1024;  // + the epilogue's buffers
-    static constexpr int kScaleCols = 8 + QT / 128 * 8;  // TMEM columns of one stage's scales
-    static constexpr int kScaleBase = 2 * QT;
-};
+// The experts' kernel: 128 rows of either operand per stage, two 512-byte scale tiles each.
+constexpr int kGroupBytes = kGemmRows * 128;
+constexpr int kGroupStage = 2 * kGroupBytes + 2048;
+constexpr int kGroupStages = 5;
+constexpr int kGroupSmem = kGroupStages * kGroupStage + 1024;  // + the epilogue's buffers
+constexpr int kGroupScaleCol = 256;                            // TMEM: accumulators at 0 and 128, scales from here
 
 struct GemmTile {
     int32_t p_row, q_row;      // TMA rows
@@ -175,16 +176,14 @@ __device__ __forceinline__ void store_chunk(const GemmParams &p, const uint32_t 
     }
 }
 
-template <int QT, bool F32, bool GROUPED>
+template <bool F32>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p)
+    mxfp4_group_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p)
 {
-    using S = GemmShape<QT>;
     extern __shared__ unsigned char gemm_smem[];
-    __shared__ GroupTable<GROUPED> groups;
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
+    __shared__ GroupTable<true> groups;
+    __shared__ uint64_t full[kGroupStages], empty[kGroupStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_slot;
-    __shared__ int failed;
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // warp-uniform for the compiler too
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (tid == 0) {
         prefetch_tensormap(&p_map);
         prefetch_tensormap(&q_map);
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < kGroupStages; ++s) {
             mbar_init(smem_u32(&full[s]), 2);  // codes, scales
             mbar_init(smem_u32(&empty[s]), 1);
         }
@@ -202,7 +201,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         mbar_init(smem_u32(&drain), 1);
         fence_mbar_init();
-        failed = 0;
     }
     if (warp == 2)
         tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -212,23 +210,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = tmem_slot;
     pdl_wait_and_release();
 
-    int num_tiles = p.p_tiles * p.q_tiles;
-    if constexpr (GROUPED) {
-        const int rt = group_setup<kGemmThreads, QT>(groups, p.offsets, p.num_groups, p.Q);
-        num_tiles = rt < 0 ? 0 : rt * p.p_tiles;
-        if (rt < 0 && blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
-            atomicOr(p.err_flag, 1);
-    }
-    auto give_up = [&]() {
-        failed = 1;
-        atomicOr(p.fault, 1u);
-    };
+    const int row_tiles = group_setup<kGemmThreads, kGemmRows>(groups, p.offsets, p.num_groups, p.Q);
+    const int num_tiles = row_tiles < 0 ? 0 : row_tiles * p.p_tiles;
+    if (row_tiles < 0 && blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
+        atomicOr(p.err_flag, 1);
+    auto give_up = [&]() { atomicOr(p.fault, 1u); };
 
     // stage of the ring and the phase parity of its barriers, for a role's next iteration
     int slot = 0;
     uint32_t phase = 0;
     auto advance = [&]() {
-        if (++slot == S::kStages) {
+        if (++slot == kGroupStages) {
             slot = 0;
             phase ^= 1;
         }
@@ -240,10 +232,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         bool ok = true;
         int issued = 0;
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-            const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
-            const int q_blocks = (c.valid + 127) / 128;
+            const GemmTile c = gemm_tile<kGemmRows, kGemmRows, true>(t, p, groups);
             const int boxes = (c.valid + p.q_box - 1) / p.q_box;
-            const uint32_t code_bytes = S::kPBytes + boxes * p.q_box * 128;
+            const uint32_t code_bytes = kGroupBytes + boxes * p.q_box * 128;
             const uint8_t *ps = p.p_scale + c.p_plane * p.kc * 512, *qs = p.q_scale + c.q_plane * p.kc * 512;
             for (int k = 0; k < p.k_iters; ++k) {
                 // a fresh barrier's phase -1 counts as complete: the first round waits for nothing
@@ -252,19 +243,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t bar = full0 + 8 * slot, dp = base + slot * S::kStage;
+                const uint32_t bar = full0 + 8 * slot, dp = base + slot * kGroupStage;
                 if (elect_one()) {
                     if (warp == 0) {
                         mbar_arrive_expect_tx(bar, code_bytes);
                         tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d_shared(dp + S::kPBytes + b * p.q_box * 128, &q_map, bar, k * 128, c.q_row + b * p.q_box);
+                            tma_load_2d_shared(dp + kGroupBytes + b * p.q_box * 128, &q_map, bar, k * 128, c.q_row + b * p.q_box);
                     } else {
-                        const uint32_t sb = 512u * min(2, p.kc - 2 * k), ds = dp + S::kPBytes + S::kQBytes;
-                        mbar_arrive_expect_tx(bar, sb * (1 + q_blocks));
+                        const uint32_t sb = 512u * min(2, p.kc - 2 * k), ds = dp + kGroupBytes + kGroupBytes;
+                        mbar_arrive_expect_tx(bar, 2 * sb);
                         bulk_load(ds, ps + k * 1024, sb, bar);
-                        for (int b = 0; b < q_blocks; ++b)
-                            bulk_load(ds + S::kPScale + b * 1024, qs + static_cast<int64_t>(b) * p.kc * 512 + k * 1024, sb, bar);
+                        bulk_load(ds + 1024, qs + k * 1024, sb, bar);
                     }
                 }
                 __syncwarp();
@@ -275,9 +265,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!ok) {
             if (lane == 0)
                 give_up();
-            for (int j = 0; j < S::kStages && j < issued; ++j) {  // copies in flight, the newest first
+            for (int j = 0; j < kGroupStages && j < issued; ++j) {  // copies in flight, the newest first
                 if (--slot < 0) {
-                    slot = S::kStages - 1;
+                    slot = kGroupStages - 1;
                     phase ^= 1;
                 }
                 mbar_wait_cycles(full0 + 8 * slot, phase, kGemmDrain);
@@ -287,13 +277,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // ---- MMA ----
         int n_tile = 0;
         bool ok = true;
-        const uint64_t p_desc = desc_sw128(base), q_desc = desc_sw128(base + S::kPBytes);
-        const uint64_t s_desc = desc_scales(base + S::kPBytes + S::kQBytes);
+        const uint64_t p_desc = desc_sw128(base), q_desc = desc_sw128(base + kGroupBytes);
+        const uint64_t s_desc = desc_scales(base + kGroupBytes + kGroupBytes);
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++n_tile) {
-            const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
+            const GemmTile c = gemm_tile<kGemmRows, kGemmRows, true>(t, p, groups);
             const int n = (c.valid + 15) & ~15;
             const int buf = n_tile & 1;
-            const uint32_t d = tmem + buf * QT, sf = tmem + S::kScaleBase;
+            const uint32_t d = tmem + buf * kGemmRows, sf = tmem + kGroupScaleCol;
             const uint32_t idesc0 = mxf4_idesc(kGemmRows, n, 0), idesc1 = mxf4_idesc(kGemmRows, n, 1);
             if (n_tile >= 2)
                 ok = mbar_wait_cycles(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWait);
@@ -310,7 +300,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t step = slot * (S::kStage >> 4);  // descriptors count 16-byte units
+                    const uint32_t step = slot * (kGroupStage >> 4);  // descriptors count 16-byte units
                     const uint64_t pd = p_desc + step, qd = q_desc + step, sd = s_desc + step;
                     const int left = p.k64 - 4 * k;  // MMA steps from here on
 #pragma unroll
@@ -318,11 +308,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (left <= 2 * ch)
                             break;
                         // each half of a stage has its own TMEM columns for its scales; copies and MMAs run in issue order
-                        const uint32_t sp = sf + ch * (S::kScaleCols / 2), sq = sp + 4;
+                        const uint32_t sp = sf + ch * (8), sq = sp + 4;
                         tc_copy_scales(sp, sd + ch * 32);
-#pragma unroll
-                        for (int b = 0; b < QT / 128; ++b)
-                            tc_copy_scales(sq + b * 4, sd + (S::kPScale + b * 1024 + ch * 512) / 16);
+                        tc_copy_scales(sq, sd + (1024 + ch * 512) / 16);
                         tc_mma_mxf4(d, pd + ch * 4, qd + ch * 4, idesc0, sp, sq, k > 0 || ch > 0);
                         if (left > 2 * ch + 1)
                             tc_mma_mxf4(d, pd + ch * 4 + 2, qd + ch * 4 + 2, idesc1, sp, sq, true);
@@ -346,10 +334,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= 4) {
         // ---- epilogue ----
         const int quarter = warp & 3;
-        unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + S::kStages * S::kStage;
+        unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kGroupStages * kGroupStage;
         int n_tile = 0, chunk = 0;
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
-            const GemmTile c = gemm_tile<kGemmRows, QT, GROUPED>(t, p, groups);
+            const GemmTile c = gemm_tile<kGemmRows, kGemmRows, true>(t, p, groups);
             const int buf = n_tile & 1;
             if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
@@ -359,7 +347,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tc_fence_after();
             for (int q = 0; q < c.valid; q += 32) {
                 uint32_t v[32];
-                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * QT + q, v);
+                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kGemmRows + q, v);
                 store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q, c.p0);
             }
             tc_fence_before();

@@ -4,6 +4,9 @@
 // Two CTAs fit an SM, so one's start and end overlap the other's loads, and every tile of a wide layer is
 // resident at once: at one token the weights' bytes are the time, and all CTAs share HBM evenly whatever the
 // tiles' number.  Roles as in mxfp4_gemm.cuh.
+//
+// Measured: 1x8192x28672 22.0 us (125 MB of weights, 5.7 TB/s), 1x4096x4096 5.6 us (K in eight parts),
+// 1x8192x8192 9.1 us; 333x4096x4096 about 9 us.  What is left over the bytes is the start and end of the CTAs.
 #pragma once
 
 #include "mxfp4_gemm.cuh"
