@@ -2,7 +2,8 @@
 
 BF16 [M, N] -> FP8 (E4M3 / E5M2) with one E8M0 scale per 32-element block,
 rowwise (1x32) and columnwise (32x1) in one pass, with optional fused dbias
-and a device noop flag, plus a grouped (MoE, ragged row offsets) variant.
+and a device noop flag, plus a grouped (MoE, ragged row offsets) variant; the MXFP4 (4-bit)
+cast with its products (``mxfp4``), and expert routing, planning and combination (``moe``).
 The compute runs in the CUDA library built from ``csrc/``; this package is its
 ctypes binding.
 """
