@@ -7,12 +7,13 @@ and raise :class:`MXFP8Error` on a non-OK status.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
 from .binding import _addr, lib
-from .mxfp4 import _check, _check_input, _lib, _on, _stream
+from .mxfp4 import _check, _check_input, _lib, _on, _stream, _stream_of
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_TOPK = 32
@@ -83,6 +84,13 @@ def make_route_config(top_k: int, score="softmax", bias: Optional[torch.Tensor] 
     return RouteConfig(score, top_k, groups, topk_groups, int(bool(renormalize)), scale, _addr(bias))
 
 
+@functools.lru_cache(maxsize=64)
+def _unbiased_config(*how) -> RouteConfig:
+    """make_route_config without a bias, kept for the next call of the same options (the library only reads it)."""
+    top_k, score, groups, topk_groups, renormalize, scale = how
+    return make_route_config(top_k, score, None, groups, topk_groups, renormalize, scale)
+
+
 def moe_route(logits: torch.Tensor, k: int, score="softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
               topk_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None) -> MoERoute:
     """Choose k of E experts for each row of ``logits`` [T, E] (CUDA bf16 or fp32, rows contiguous).
@@ -97,12 +105,15 @@ def moe_route(logits: torch.Tensor, k: int, score="softmax", bias: Optional[torc
     kind, T, E, ld = _check_input(logits, "logits")
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 tensor [{E}]")
-    cfg = make_route_config(k, score, bias, groups, topk_groups, renormalize, scale)
+    if bias is None:
+        cfg = _unbiased_config(k, score, groups, topk_groups, renormalize, scale)
+    else:
+        cfg = make_route_config(k, score, bias, groups, topk_groups, renormalize, scale)
     dev = logits.device
     indices = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     _check(_lib().moe_route(logits.data_ptr(), kind, T, E, ld, ctypes.byref(cfg), indices.data_ptr(), weights.data_ptr(),
-                            _stream(None)), "moe_route")
+                            _stream_of(dev)), "moe_route")
     return MoERoute(indices, weights)
 
 
@@ -117,9 +128,11 @@ def moe_route_backward(logits: torch.Tensor, indices: torch.Tensor, grad_weights
     _check_like(grad_weights, "grad_weights", torch.float32, (rows, k))
     if rows != T:
         raise ValueError(f"indices must have {T} rows")
-    cfg = make_route_config(k, score, None, 1, 1, renormalize, scale)
-    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _check(moe_route_backward_c(logits, kind, T, E, ld, cfg, indices, grad_weights, out), "moe_route_backward")
+    cfg = _unbiased_config(k, score, 1, 1, renormalize, scale)
+    dev = logits.device
+    out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _check(_lib().moe_route_backward(logits.data_ptr(), kind, T, E, ld, ctypes.byref(cfg), indices.data_ptr(), grad_weights.data_ptr(),
+                                     out.data_ptr(), _stream_of(dev)), "moe_route_backward")
     return out
 
 
@@ -137,7 +150,7 @@ def moe_plan(indices: torch.Tensor, num_experts: int, stream=None) -> MoEPlan:
     nbytes = moe_plan_workspace_bytes(T * k, num_experts) if T * k > 1024 else 0
     workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
     _check(_lib().moe_plan(indices.data_ptr(), T * k, k, num_experts, offsets.data_ptr(), slots.data_ptr(),
-                           tokens.data_ptr(), _addr(workspace), _stream(None)), "moe_plan")
+                           tokens.data_ptr(), _addr(workspace), _stream_of(dev)), "moe_plan")
     return MoEPlan(offsets, slots, tokens)
 
 
@@ -150,9 +163,10 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Te
     T, k = _check_like(slots, "slots", torch.int32)
     if weights is not None:
         _check_like(weights, "weights", torch.float32, (T, k))
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    dev = y.device
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     _check(_lib().moe_combine(y.data_ptr(), R, H, slots.data_ptr(), _addr(weights), T, k, out.data_ptr(),
-                              _stream(None)), "moe_combine")
+                              _stream_of(dev)), "moe_combine")
     return out
 
 
@@ -168,7 +182,9 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tenso
     _check_like(grad, "grad", torch.bfloat16, (T, H))
     if weights is not None:
         _check_like(weights, "weights", torch.float32, (T, k))
-    dy = (torch.zeros if R > T * k else torch.empty)((R, H), dtype=torch.bfloat16, device=y.device)
-    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    _check(moe_combine_backward_c(grad, y, R, H, slots, weights, T, k, dy, dweights), "moe_combine_backward")
+    dev = y.device
+    dy = (torch.zeros if R > T * k else torch.empty)((R, H), dtype=torch.bfloat16, device=dev)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _check(_lib().moe_combine_backward(grad.data_ptr(), y.data_ptr(), R, H, slots.data_ptr(), _addr(weights), T, k, dy.data_ptr(),
+                                       dweights.data_ptr(), _stream_of(dev)), "moe_combine_backward")
     return dy, dweights

@@ -19,13 +19,51 @@ TYPE_F32 = 1
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 
 
-class MXFP4Matrix(NamedTuple):
+class MXFP4Matrix:
     """A 4-bit matrix [rows, cols]: blocks of 32 along the columns.  Experts' matrices of one shape are held
-    together with a leading dimension on ``codes`` and ``scales``."""
-    codes: torch.Tensor   # uint8 [rows, 16 * ceil(cols / 32)]
-    scales: torch.Tensor  # uint8, 1-D: the GEMM-ready E8M0 plane
-    rows: int
-    cols: int
+    together with a leading dimension on ``codes`` and ``scales``.
+
+    ``codes``   uint8 [rows, 16 * ceil(cols / 32)]
+    ``scales``  uint8, 1-D: the GEMM-ready E8M0 plane
+
+    The casts put both into one allocation and make the two tensors when they are asked for (an allocation or a
+    view costs a call about two microseconds); the calls of this module use the addresses.
+    """
+    __slots__ = ("rows", "cols", "_codes", "_scales", "_buffer", "_offset", "_plane")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        self.rows, self.cols = rows, cols
+        self._codes, self._scales = codes, scales
+        self._buffer, self._offset, self._plane = None, 0, 0
+
+    @classmethod
+    def _in(cls, buffer: torch.Tensor, offset: int, rows: int, cols: int, plane: int) -> "MXFP4Matrix":
+        """A cast's matrix: codes at ``offset`` of the uint8 ``buffer``, ``plane`` bytes of scales after them."""
+        m = cls.__new__(cls)
+        m.rows, m.cols = rows, cols
+        m._codes = m._scales = None
+        m._buffer, m._offset, m._plane = buffer, offset, plane
+        return m
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n = self.rows * mxfp4_row_bytes(self.cols)
+            self._codes = self._buffer[self._offset:self._offset + n].view(self.rows, mxfp4_row_bytes(self.cols))
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            at = self._offset + self.rows * mxfp4_row_bytes(self.cols)
+            self._scales = self._buffer[at:at + self._plane]
+        return self._scales
+
+    def _replace(self, **changed) -> "MXFP4Matrix":
+        return MXFP4Matrix(**{**dict(codes=self.codes, scales=self.scales, rows=self.rows, cols=self.cols), **changed})
+
+    def __repr__(self) -> str:
+        return f"MXFP4Matrix({self.rows} x {self.cols})"
 
 
 class MXFP4Tensor(NamedTuple):
@@ -34,16 +72,20 @@ class MXFP4Tensor(NamedTuple):
     col: Optional[MXFP4Matrix]  # x transposed [N, M]
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
 def _stream(stream) -> Optional[int]:
-    """The cudaStream_t of ``stream``, or of the current device's current stream (by torch's raw getter, which
-    costs a tenth of a microsecond where torch.cuda.current_stream() costs three)."""
+    """The cudaStream_t of ``stream``, or of the current device's current stream."""
     if stream is None and torch.cuda.is_initialized():
-        return _current()
+        return _raw_stream(torch._C._cuda_getDevice())
     return _any_stream(stream)
 
 
-def _current() -> int:
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _stream_of(device: torch.device) -> Optional[int]:
+    """The current stream of a tensor's device, by torch's raw getter (a tenth of a microsecond, where
+    torch.cuda.current_stream() costs three).  A tensor off the GPU is the library's to refuse."""
+    return None if device.index is None else _raw_stream(device.index)
 
 
 _library = None
@@ -143,9 +185,14 @@ def _check_err(err_flag) -> None:
         raise ValueError("err_flag must be an int32 tensor")
 
 
-def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None) -> None:
-    codes, scales, rows, cols = m
+def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None):
+    """(address of the codes, address of the scales) of a matrix whose tensors have the right types and shapes."""
+    rows, cols = m.rows, m.cols
     pitch = -(-cols // 32) * 16
+    if m._buffer is not None and groups is None and m._plane >= -(-rows // 128) * -(-cols // 128) * 512:
+        at = m._buffer.data_ptr() + m._offset  # laid out by a cast
+        return at, at + rows * pitch
+    codes, scales = m.codes, m.scales
     plane = -(-rows // 128) * -(-cols // 128) * 512
     shape = (rows, pitch) if groups is None else (groups, rows, pitch)
     if codes.dtype is not torch.uint8 or codes.shape != shape or not codes.is_contiguous():
@@ -153,6 +200,11 @@ def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None) -> No
     if scales.dtype is not torch.uint8 or not scales.is_contiguous() or (
             scales.numel() < plane if groups is None else scales.shape != (groups, plane)):
         raise ValueError(f"{name}.scales must be a contiguous uint8 tensor of {plane} bytes per matrix")
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def _device(m: MXFP4Matrix) -> torch.device:
+    return (m._codes if m._buffer is None else m._buffer).device
 
 
 def _check_out_dtype(dtype: torch.dtype) -> int:
@@ -162,10 +214,8 @@ def _check_out_dtype(dtype: torch.dtype) -> int:
     return kind
 
 
-def _empty_matrix(rows: int, cols: int, device) -> MXFP4Matrix:
-    u8 = torch.uint8
-    return MXFP4Matrix(torch.empty((rows, -(-cols // 32) * 16), dtype=u8, device=device),
-                       torch.empty((-(-rows // 128) * -(-cols // 128) * 512,), dtype=u8, device=device), rows, cols)
+# Both matrices of a cast share an allocation up to this size; a larger one keeps each alive on its own.
+_SHARED_BYTES = 1 << 20
 
 
 def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, noop: Optional[torch.Tensor] = None,
@@ -181,13 +231,24 @@ def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False,
     kind, M, N, ld = _check_input(x)
     dev = x.device
     row = col = rc = rs = cc = cs = None
+    codes = M * (-(-N // 32) * 16)
+    codes_t = N * (-(-M // 32) * 16)
+    plane = plane_t = -(-M // 128) * -(-N // 128) * 512
+    first = codes + plane if rowwise else 0
+    second = codes_t + plane_t if colwise else 0
+    buffer = torch.empty((first + second if first + second <= _SHARED_BYTES else first or second,), dtype=torch.uint8, device=dev)
     if rowwise:
-        codes, scales, _, _ = row = _empty_matrix(M, N, dev)
-        rc, rs = codes.data_ptr(), scales.data_ptr()
+        rc = buffer.data_ptr()
+        rs = rc + codes
+        row = MXFP4Matrix._in(buffer, 0, M, N, plane)
     if colwise:
-        codes, scales, _, _ = col = _empty_matrix(N, M, dev)
-        cc, cs = codes.data_ptr(), scales.data_ptr()
-    st = _lib().mxfp4_quantize(x.data_ptr(), kind, M, N, ld, rc, rs, cc, cs, _addr(noop), _stream(None))
+        at = first
+        if rowwise and first + second > _SHARED_BYTES:
+            buffer, at = torch.empty((second,), dtype=torch.uint8, device=dev), 0
+        cc = buffer.data_ptr() + at
+        cs = cc + codes_t
+        col = MXFP4Matrix._in(buffer, at, N, M, plane_t)
+    st = _lib().mxfp4_quantize(x.data_ptr(), kind, M, N, ld, rc, rs, cc, cs, _addr(noop), _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_quantize")
     return MXFP4Tensor(row, col)
@@ -207,13 +268,16 @@ def quantize_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: Optiona
         raise ValueError("rows must be a contiguous 1-D int32 tensor")
     total = T if rows is None else rows.numel()
     dev = x.device
-    codes = torch.empty((total, mxfp4_row_bytes(N)), dtype=torch.uint8, device=dev)
-    scales = torch.empty((mxfp4_grouped_scale_bytes(total, N, groups),), dtype=torch.uint8, device=dev)
+    codes, plane = total * mxfp4_row_bytes(N), mxfp4_grouped_scale_bytes(total, N, groups)
+    buffer = torch.empty((codes + plane,), dtype=torch.uint8, device=dev)
     nbytes = 0 if rows is None else mxfp4_quantize_grouped_workspace_bytes(T, N, total)
     workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
-    _check(mxfp4_quantize_grouped(x, kind, T, N, ld, rows, total, groups, offsets, codes, scales, err_flag, workspace),
-           "mxfp4_quantize_grouped")
-    return MXFP4Matrix(codes, scales, total, N)
+    at = buffer.data_ptr()
+    st = _lib().mxfp4_quantize_grouped(x.data_ptr(), kind, T, N, ld, _addr(rows), total, groups, offsets.data_ptr(), at, at + codes,
+                                       _addr(err_flag), _addr(workspace), _stream_of(dev))
+    if st:
+        raise MXFP8Error(st, "mxfp4_quantize_grouped")
+    return MXFP4Matrix._in(buffer, 0, total, N, plane)
 
 
 def dequantize_mxfp4(m: MXFP4Matrix, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
@@ -222,10 +286,10 @@ def dequantize_mxfp4(m: MXFP4Matrix, dtype: torch.dtype = torch.bfloat16, stream
         with _on(stream):
             return dequantize_mxfp4(m, dtype)
     kind = _check_out_dtype(dtype)
-    _check_matrix(m, "m")
-    out = torch.empty((m.rows, m.cols), dtype=dtype, device=m.codes.device)
-    st = _lib().mxfp4_dequantize(m.codes.data_ptr(), m.scales.data_ptr(), m.rows, m.cols, out.data_ptr(), kind,
-                                 _stream(None))
+    codes, scales = _check_matrix(m, "m")
+    dev = _device(m)
+    out = torch.empty((m.rows, m.cols), dtype=dtype, device=dev)
+    st = _lib().mxfp4_dequantize(codes, scales, m.rows, m.cols, out.data_ptr(), kind, _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_dequantize")
     return out
@@ -237,20 +301,20 @@ def matmul_mxfp4(a: MXFP4Matrix, b: MXFP4Matrix, out_dtype: torch.dtype = torch.
     if stream is not None:
         with _on(stream):
             return matmul_mxfp4(a, b, out_dtype, out)
-    _check_matrix(a, "a")
-    _check_matrix(b, "b")
+    ac, asc = _check_matrix(a, "a")
+    bc, bsc = _check_matrix(b, "b")
+    dev = _device(a)
     M, N, K = a.rows, b.rows, a.cols
     if K != b.cols:
         raise ValueError(f"a has {K} columns, b has {b.cols}")
     if out is None:
         kind, ldo = _check_out_dtype(out_dtype), N
-        out = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
         kind, rows, cols, ldo = _check_input(out, "out")
         if (rows, cols) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
-    st = _lib().mxfp4_matmul(a.codes.data_ptr(), a.scales.data_ptr(), M, b.codes.data_ptr(), b.scales.data_ptr(), N, K,
-                             out.data_ptr(), kind, ldo, _stream(None))
+    st = _lib().mxfp4_matmul(ac, asc, M, bc, bsc, N, K, out.data_ptr(), kind, ldo, _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_matmul")
     return out
@@ -265,16 +329,26 @@ def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, 
             return matmul_mxfp4_grouped(a, offsets, b, out_dtype, err_flag)
     groups = _check_offsets(offsets)
     _check_err(err_flag)
-    _check_matrix(b, "b", groups)
+    bc, bsc = _check_matrix(b, "b", groups)
     kind = _check_out_dtype(out_dtype)
-    codes, scales, R, K = a
+    R, K = a.rows, a.cols
     if K != b.cols:
         raise ValueError(f"a has {K} columns, b has {b.cols}")
-    if codes.dtype != torch.uint8 or codes.shape != (R, mxfp4_row_bytes(K)) or not codes.is_contiguous():
-        raise ValueError("a.codes must be a contiguous uint8 tensor [rows, 16 * ceil(cols / 32)]")
-    if scales.dtype != torch.uint8 or scales.numel() < mxfp4_grouped_scale_bytes(R, K, groups) or not scales.is_contiguous():
-        raise ValueError("a.scales must hold mxfp4_grouped_scale_bytes(rows, cols, groups) bytes")
-    out = torch.empty((R, b.rows), dtype=out_dtype, device=codes.device)
-    _check(mxfp4_matmul_grouped(codes, scales, R, groups, offsets, b.codes, b.scales, b.rows, K, out, kind, err_flag),
-           "mxfp4_matmul_grouped")
+    need = mxfp4_grouped_scale_bytes(R, K, groups)
+    if a._buffer is not None and a._plane >= need:
+        ac = a._buffer.data_ptr() + a._offset
+        asc = ac + R * mxfp4_row_bytes(K)
+    else:
+        codes, scales = a.codes, a.scales
+        if codes.dtype is not torch.uint8 or codes.shape != (R, mxfp4_row_bytes(K)) or not codes.is_contiguous():
+            raise ValueError("a.codes must be a contiguous uint8 tensor [rows, 16 * ceil(cols / 32)]")
+        if scales.dtype is not torch.uint8 or scales.numel() < need or not scales.is_contiguous():
+            raise ValueError("a.scales must hold mxfp4_grouped_scale_bytes(rows, cols, groups) bytes")
+        ac, asc = codes.data_ptr(), scales.data_ptr()
+    dev = _device(a)
+    out = torch.empty((R, b.rows), dtype=out_dtype, device=dev)
+    st = _lib().mxfp4_matmul_grouped(ac, asc, R, groups, offsets.data_ptr(), bc, bsc, b.rows, K, out.data_ptr(), kind, _addr(err_flag),
+                                     _stream_of(dev))
+    if st:
+        raise MXFP8Error(st, "mxfp4_matmul_grouped")
     return out
