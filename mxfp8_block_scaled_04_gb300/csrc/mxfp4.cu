@@ -480,7 +480,7 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
                                                                    row_bytes, pair_bound, device, stream);
     }
     CUtensorMap pm, qm;
-    p.q_box = total_rows > int64_t{64} * num_groups ? 128 : 32;
+    p.q_box = 32;
     if ((st = code_map(&pm, b_codes, num_groups * N, row_bytes, kGemmRows)) != MXFP8_OK ||
         (st = code_map(&qm, a_codes, total_rows, row_bytes, p.q_box)) != MXFP8_OK)
         return st;
