@@ -7,7 +7,7 @@
 // bytes of a row that it copied itself and a block is two (fp32: four) lanes; columnwise, a thread takes one word
 // (two BF16 columns or one fp32) of 32 rows, so that the four lanes of a column write 64 consecutive bytes of the
 // transposed codes.  HBM: 2 (or 4) bytes in and 17/32 byte out per element and direction; one way is bound by that
-// (8192x28672 BF16: 100 us, 5.9 TB/s), both ways by the SM side as well (145 us, 5.0 TB/s; the issue slots are half
+// (8192x28672 BF16: 97 us, 6.1 TB/s), both ways by the SM side as well (145 us, 5.0 TB/s; the issue slots are half
 // used, and neither the conversions nor the tile order nor more stages change it).
 //
 // The scale exponent comes from the bits of amax (exact), x * 2^(127 - e) is exact wherever the rounding to
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
     const uint32_t smem = smem_u32(cast_smem);
     const void *nowhere = p.x != nullptr ? p.x : p.out_row;  // an address for copies of no bytes
     const int seg = tid & 7, r0 = tid >> 3;  // 32-byte piece, first of four rows 32 apart
+    const int flip = seg >> 2;               // the last four pieces of a row go second half first: eight lanes, 32 banks
 
     struct Tile {
         int rt, ct;
@@ -196,7 +197,8 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
                 }
                 const unsigned char *src = static_cast<const unsigned char *>(p.x) + (from * p.ldx + c) * kSize;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int j = 0; j < 2; ++j) {
+                    const int h = j ^ flip;
                     const bool ok = live && c + h * (kPer / 2) < p.N;  // N is a multiple of 8: a whole vector or none
                     copy16_async(dst + cast_word(r0 + 32 * i) * 4 + h * 16, ok ? src + h * 16 : nowhere, ok);
                 }
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint4 *q = reinterpret_cast<const uint4 *>(tile + cast_word(r0 + 32 * i) + seg * 8);  // this thread's own copies
-                const uint4 q0 = q[0], q1 = q[1];
+                const uint4 q0 = q[flip], q1 = q[flip ^ 1];
                 const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
                 uint32_t m = 0;
 #pragma unroll
@@ -260,13 +262,13 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
                 }
                 const bool keep = r0 + 32 * i < rows_left && in_blk;
                 if constexpr (F32) {
-                    const uint32_t o = e == 255 ? 0u : cvt_fp4x8_scaled(v, mul);
+                    const uint32_t c8 = cvt_fp4x8_scaled(v, mul);
                     if (keep)
-                        *reinterpret_cast<uint32_t *>(out) = o;
+                        *reinterpret_cast<uint32_t *>(out) = e == 255 ? 0u : __funnelshift_l(c8, c8, 16 * flip);
                 } else {
                     const uint32_t lo = e == 255 ? 0u : cvt_fp4x8_scaled(v, mul), hi = e == 255 ? 0u : cvt_fp4x8_scaled(v + 8, mul);
                     if (keep)
-                        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+                        *reinterpret_cast<uint2 *>(out) = flip ? make_uint2(hi, lo) : make_uint2(lo, hi);
                 }
                 out += 32 * p.row_pitch;
                 // the row's blocks, two (four) lanes apart, as the scale tile's 2 (4) bytes

@@ -9,7 +9,7 @@
 //   mxfp4_pair.cuh    many rows: 256 x 256 tiles by CTA pairs, bound by the tensor cores
 //   mxfp4_split.cuh   few tiles: one per CTA, or K shared by a cluster, bound by the weights' bytes
 //   mxfp4_group_kernel (below)   experts with few rows each: persistent 128 x 128 tiles, bound by the weights' bytes
-//                     (128 rows over 64 experts of 2048 x 7168: 67 us, 6.5 TB/s)
+//                     (128 rows over 64 experts of 2048 x 7168: 67 us, 6.5 TB/s; 80 cold)
 //
 // Roles of a CTA (8 warps): warps 0 and 3 feed a ring of shared-memory stages of 256 elements of K (TMA tiles of the
 // codes; the scale tiles), warp 1 copies scales to TMEM and issues the MMAs, warp 2 owns the TMEM allocation, warps

@@ -6,7 +6,7 @@
 // not fit TMEM's 512 columns side by side, so the accumulators share 32 columns: the epilogue drains those first
 // and the next tile's MMAs begin while it drains the rest.  Output rows leave as 16-byte pieces (603 -> 511 us).
 //
-// Measured: 8192x8192x28672 490 us alone (7.9 PFLOP/s), 575 us back to back under the power limit.  Bound by the
+// Measured: 8192x8192x28672 490 us alone (7.9 PFLOP/s), about 570 us back to back under the power limit.  Bound by the
 // MMAs: without the output, Q's loads and the scale copies the same loop takes 461 us; the tensor pipe is active
 // 74% of the cycles at 4096x8192x8192 (seven rounds of tiles); three, four and five stages take the same time.
 //
@@ -71,7 +71,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (rt < 0 && blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
             atomicOr(p.err_flag, 1);
     }
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    // The pair's n-th tile: rounds of one tile per pair, every other one backwards, so that a partial last round goes to
+    // the pairs whose tiles in the round before came last (4099 rows: the 3-row tiles, not whole ones).
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    auto tile_of = [&](int n) { return n * pairs + (n & 1 ? pairs - 1 - pair : pair); };
     const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
     int slot = 0;
     uint32_t phase = 0;
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t lead_full = map_to_rank(full0, 0);
         bool ok = true;
         int issued = 0;
-        for (int t = first; t < num_tiles && ok; t += stride) {
+        for (int n = 0, t; (t = tile_of(n)) < num_tiles && ok; ++n) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int half = ((c.valid + 31) & ~31) / 2;
             const int boxes = half > 96 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
@@ -132,11 +135,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         // ---- MMA for both CTAs ----
-        int n_tile = 0;
         bool ok = true;
         const uint64_t p_desc = desc_sw128(base), q_desc = desc_sw128(base + kPairCodes);
         const uint64_t s_desc = desc_scales(base + 2 * kPairCodes);
-        for (int t = first; t < num_tiles && ok; t += stride, ++n_tile) {
+        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles && ok; ++n_tile) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int n = (c.valid + 31) & ~31;  // halves of whole 16-row groups
             const uint32_t d = tmem + (n_tile & 1) * kPairAcc1, sf = tmem + kPairScaleCol;
@@ -192,8 +194,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int quarter = warp & 3;
         const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kPairStages * kPairStage;
-        int n_tile = 0, chunk = 0;
-        for (int t = first; t < num_tiles; t += stride, ++n_tile) {
+        int chunk = 0;
+        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
             if (!epilogue_all(mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
