@@ -400,3 +400,82 @@ def test_past_2_32_elements():
         assert torch.equal(y[rows, cols], part)
     del y
     torch.cuda.empty_cache()
+
+
+def fuzz_shapes(seed, count):
+    rng = np.random.default_rng(seed)
+    for _ in range(count):
+        M = int(np.exp(rng.uniform(0, np.log(3000))))
+        N = int(np.exp(rng.uniform(0, np.log(9000))))
+        K = 8 * int(np.exp(rng.uniform(0, np.log(900))))
+        yield M, N, K, BF16 if rng.random() < 0.5 else F32
+
+
+def bound_on_gpu(a, b, bf16):
+    """ref.product_bound of decoded matrices, on the GPU in 64 bits."""
+    return ref.product_bound(mx.dequantize_mxfp4(a, F32).double(), mx.dequantize_mxfp4(b, F32).double(), bf16)
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_product_fuzz(seed):
+    """Random sizes over every kernel and split of K, against 64 bits of the decoded operands."""
+    for M, N, K, dt in fuzz_shapes(seed, 25):
+        g = torch.Generator(device="cuda").manual_seed(M + N + K)
+        a, b = (mx.quantize_mxfp4(torch.randn(r, K, generator=g, device="cuda").to(BF16)).row for r in (M, N))
+        want, tol = bound_on_gpu(a, b, dt == BF16)
+        got = mx.matmul_mxfp4(a, b, dt).double()
+        assert bool(((got - want).abs() <= tol).all()), (M, N, K, dt)
+    assert mx.mxfp8_device_fault_word() == 0
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_experts_product_fuzz(seed):
+    """Random experts, loads and sizes over both experts' kernels."""
+    rng = np.random.default_rng(100 + seed)
+    for _ in range(8):
+        G, N, K = int(rng.integers(1, 33)), int(np.exp(rng.uniform(0, 7.3))), 8 * int(np.exp(rng.uniform(0, 5.5)))
+        sizes = (rng.integers(0, 2, G) * np.exp(rng.uniform(0, rng.uniform(1, 6.5), G))).astype(int)
+        off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), device="cuda")
+        R = int(off[-1])
+        dt = BF16 if rng.random() < 0.5 else F32
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn(R, K, generator=g, device="cuda").to(BF16)
+        w = [mx.quantize_mxfp4(torch.randn(N, K, generator=g, device="cuda").to(BF16)).row for _ in range(G)]
+        qb = mx.MXFP4Matrix(torch.stack([m.codes for m in w]), torch.stack([m.scales for m in w]), N, K)
+        got = mx.matmul_mxfp4_grouped(mx.quantize_mxfp4_grouped(x, off), off, qb, dt).double()
+        xa = mx.quantize_mxfp4(x).row if R else None
+        for e in range(G):
+            s = slice(int(off[e]), int(off[e + 1]))
+            if s.start == s.stop:
+                continue
+            rows = mx.dequantize_mxfp4(xa, F32).double()[s]
+            want, tol = ref.product_bound(rows, mx.dequantize_mxfp4(w[e], F32).double(), dt == BF16)
+            assert bool(((got[s] - want).abs() <= tol).all()), (G, N, K, e)
+    assert mx.mxfp8_device_fault_word() == 0
+
+
+def test_results_are_the_same_bits_every_time():
+    """Casts, split and paired products and experts' products repeat exactly."""
+    for M, N, K in ((1, 2048, 8192), (100, 512, 16384), (1024, 4096, 1024)):
+        a, b = (mx.quantize_mxfp4(torch.randn(r, K, device="cuda").to(BF16)).row for r in (M, N))
+        first = mx.matmul_mxfp4(a, b, F32)
+        for _ in range(5):
+            assert torch.equal(mx.matmul_mxfp4(a, b, F32), first)
+
+
+def test_concurrent_streams():
+    """Products of every kernel on four streams at once: each result equals the one computed alone."""
+    jobs = []
+    for M, N, K in ((1, 4096, 4096), (300, 1024, 2048), (2048, 2048, 512), (64, 8192, 1024)):
+        a, b = (mx.quantize_mxfp4(torch.randn(r, K, device="cuda").to(BF16)).row for r in (M, N))
+        jobs.append((a, b, mx.matmul_mxfp4(a, b)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = []
+    for _ in range(10):
+        for st, (a, b, _) in zip(streams, jobs):
+            outs.append(mx.matmul_mxfp4(a, b, stream=st))
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, jobs[i % len(jobs)][2])
+    assert mx.mxfp8_device_fault_word() == 0
