@@ -25,22 +25,24 @@ class MXFP4Matrix:
 
     ``codes``   uint8 [rows, 16 * ceil(cols / 32)]
     ``scales``  uint8, 1-D: the GEMM-ready E8M0 plane
+    ``groups``  number of experts of a grouped cast, which has a plane per expert (None: one plane)
 
     The casts put both into one allocation and make the two tensors when they are asked for (an allocation or a
     view costs a call about two microseconds); the calls of this module use the addresses.
     """
-    __slots__ = ("rows", "cols", "_codes", "_scales", "_buffer", "_offset", "_plane")
+    __slots__ = ("rows", "cols", "groups", "_codes", "_scales", "_buffer", "_offset", "_plane")
 
-    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
-        self.rows, self.cols = rows, cols
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, groups: Optional[int] = None):
+        self.rows, self.cols, self.groups = rows, cols, groups
         self._codes, self._scales = codes, scales
         self._buffer, self._offset, self._plane = None, 0, 0
 
     @classmethod
-    def _in(cls, buffer: torch.Tensor, offset: int, rows: int, cols: int, plane: int) -> "MXFP4Matrix":
+    def _in(cls, buffer: torch.Tensor, offset: int, rows: int, cols: int, plane: int,
+            groups: Optional[int] = None) -> "MXFP4Matrix":
         """A cast's matrix: codes at ``offset`` of the uint8 ``buffer``, ``plane`` bytes of scales after them."""
         m = cls.__new__(cls)
-        m.rows, m.cols = rows, cols
+        m.rows, m.cols, m.groups = rows, cols, groups
         m._codes = m._scales = None
         m._buffer, m._offset, m._plane = buffer, offset, plane
         return m
@@ -60,7 +62,8 @@ class MXFP4Matrix:
         return self._scales
 
     def _replace(self, **changed) -> "MXFP4Matrix":
-        return MXFP4Matrix(**{**dict(codes=self.codes, scales=self.scales, rows=self.rows, cols=self.cols), **changed})
+        return MXFP4Matrix(**{**dict(codes=self.codes, scales=self.scales, rows=self.rows, cols=self.cols,
+                                       groups=self.groups), **changed})
 
     def __repr__(self) -> str:
         return f"MXFP4Matrix({self.rows} x {self.cols})"
@@ -185,15 +188,22 @@ def _check_err(err_flag) -> None:
         raise ValueError("err_flag must be an int32 tensor")
 
 
+def _laid_out(m: MXFP4Matrix, codes: int, plane: int) -> bool:
+    """Whether a cast made m with that many bytes of codes and at least that many of scales."""
+    return m._buffer is not None and m._plane >= plane and m._buffer.numel() - m._offset >= codes + m._plane
+
+
 def _check_matrix(m: MXFP4Matrix, name: str, groups: Optional[int] = None):
     """(address of the codes, address of the scales) of a matrix whose tensors have the right types and shapes."""
     rows, cols = m.rows, m.cols
+    if m.groups is not None:
+        raise ValueError(f"{name} is a grouped cast (a scale plane per expert)")
     pitch = -(-cols // 32) * 16
-    if m._buffer is not None and groups is None and m._plane >= -(-rows // 128) * -(-cols // 128) * 512:
-        at = m._buffer.data_ptr() + m._offset  # laid out by a cast
+    plane = -(-rows // 128) * -(-cols // 128) * 512
+    if _laid_out(m, rows * pitch, plane) and groups is None:
+        at = m._buffer.data_ptr() + m._offset
         return at, at + rows * pitch
     codes, scales = m.codes, m.scales
-    plane = -(-rows // 128) * -(-cols // 128) * 512
     shape = (rows, pitch) if groups is None else (groups, rows, pitch)
     if codes.dtype is not torch.uint8 or codes.shape != shape or not codes.is_contiguous():
         raise ValueError(f"{name}.codes must be a contiguous uint8 tensor {list(shape)}")
@@ -273,11 +283,11 @@ def quantize_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: Optiona
     nbytes = 0 if rows is None else mxfp4_quantize_grouped_workspace_bytes(T, N, total)
     workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
     at = buffer.data_ptr()
-    st = _lib().mxfp4_quantize_grouped(x.data_ptr(), kind, T, N, ld, _addr(rows), total, groups, offsets.data_ptr(), at, at + codes,
-                                       _addr(err_flag), _addr(workspace), _stream_of(dev))
+    st = _lib().mxfp4_quantize_grouped(x.data_ptr(), kind, T, N, ld, _addr(rows), total, groups, offsets.data_ptr(), at,
+                                       at + codes, _addr(err_flag), _addr(workspace), _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_quantize_grouped")
-    return MXFP4Matrix._in(buffer, 0, total, N, plane)
+    return MXFP4Matrix._in(buffer, 0, total, N, plane, groups)
 
 
 def dequantize_mxfp4(m: MXFP4Matrix, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
@@ -334,8 +344,10 @@ def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, 
     R, K = a.rows, a.cols
     if K != b.cols:
         raise ValueError(f"a has {K} columns, b has {b.cols}")
+    if a.groups is not None and a.groups != groups:
+        raise ValueError(f"a was cast for {a.groups} experts, offsets name {groups}")
     need = mxfp4_grouped_scale_bytes(R, K, groups)
-    if a._buffer is not None and a._plane >= need:
+    if _laid_out(a, R * mxfp4_row_bytes(K), need):
         ac = a._buffer.data_ptr() + a._offset
         asc = ac + R * mxfp4_row_bytes(K)
     else:
@@ -347,8 +359,8 @@ def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, 
         ac, asc = codes.data_ptr(), scales.data_ptr()
     dev = _device(a)
     out = torch.empty((R, b.rows), dtype=out_dtype, device=dev)
-    st = _lib().mxfp4_matmul_grouped(ac, asc, R, groups, offsets.data_ptr(), bc, bsc, b.rows, K, out.data_ptr(), kind, _addr(err_flag),
-                                     _stream_of(dev))
+    st = _lib().mxfp4_matmul_grouped(ac, asc, R, groups, offsets.data_ptr(), bc, bsc, b.rows, K, out.data_ptr(), kind,
+                                     _addr(err_flag), _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_matmul_grouped")
     return out

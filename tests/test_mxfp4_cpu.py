@@ -199,6 +199,9 @@ def test_wrappers_refuse_bad_tensors(cuda_lib):
             lambda: mx.matmul_mxfp4(m, m, out_dtype=torch.float16),
             lambda: mx.matmul_mxfp4(m, m, out=torch.zeros(4, 5, dtype=bf)),
             lambda: mx.matmul_mxfp4_grouped(m, off, m),
+            lambda: mx.matmul_mxfp4(m._replace(groups=1), m),
+            lambda: mx.dequantize_mxfp4(m._replace(groups=2)),
+            lambda: mx.matmul_mxfp4_grouped(m._replace(groups=2), off, m._replace(codes=m.codes[None], scales=m.scales[None])),
             lambda: mx.moe_route(torch.zeros(3, 8, dtype=torch.float64), 2),
             lambda: mx.moe_route(torch.zeros(3, 8), 2, bias=torch.zeros(7)),
             lambda: mx.moe_route_backward(torch.zeros(3, 8), torch.zeros(3, 2, dtype=i32), torch.zeros(3, 3)),
