@@ -166,7 +166,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _check_input(x: torch.Tensor, name: str = "x"):
-    """(type, rows, columns, row pitch) of a 2-D bf16 / fp32 tensor whose rows are contiguous."""
+    """(type, rows, columns, row pitch) of a 2-D bf16 / fp32 tensor whose rows are contiguous and do not overlap (an
+    expanded row, as the gradient of a sum over rows is, has a stride of 0: no pitch)."""
     kind = _TYPES.get(x.dtype)
     if kind is None or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bfloat16 or float32 tensor with contiguous rows")
@@ -174,7 +175,11 @@ def _check_input(x: torch.Tensor, name: str = "x"):
     pitch, step = x.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must be a 2-D bfloat16 or float32 tensor with contiguous rows")
-    return kind, rows, cols, pitch if rows > 1 and pitch > cols and cols > 0 else cols
+    if rows < 2 or cols == 0:
+        return kind, rows, cols, cols
+    if pitch < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap (row stride {pitch}, {cols} columns)")
+    return kind, rows, cols, pitch
 
 
 def _check_offsets(offsets: torch.Tensor) -> int:

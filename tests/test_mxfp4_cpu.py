@@ -245,3 +245,42 @@ def test_reference_layouts_round_trip():
     v = ref.values(codes, scale, 200)
     assert float((v - x).abs().max()) <= float(x.abs().max()) / 6  # half the widest gap over the largest level
     assert torch.equal(ref.cast(v), v)                             # a cast value casts to itself
+
+
+def overlapping_rows(rows, cols, dtype):
+    """[rows, cols] views whose rows share elements: one row repeated (the gradient of a sum over rows), and rows that
+    start half a row apart."""
+    yield torch.zeros(1, cols, dtype=dtype).expand(rows, cols)
+    yield torch.zeros((rows + 1) * cols, dtype=dtype).as_strided((rows, cols), (cols // 2, 1))
+
+
+@pytest.mark.parametrize("form", [0, 1])
+def test_wrappers_refuse_rows_that_overlap(cuda_lib, form):
+    """A row stride below the row's length is not a pitch: read as whole rows it runs past the tensor's storage."""
+    bf, i32 = torch.bfloat16, torch.int32
+    x = list(overlapping_rows(40, 64, bf))[form]
+    assert x.stride(0) < 64 and x.stride(1) == 1
+    logits = list(overlapping_rows(40, 8, torch.float32))[form]
+    off = torch.tensor([0, 40])
+    m = mx.MXFP4Matrix(torch.zeros(40, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 40, 64)
+    w = mx.MXFP4Matrix(torch.zeros(64, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 64, 64)
+    for call in (
+            lambda: mx.quantize_mxfp4(x),
+            lambda: mx.quantize_mxfp4(x.float().new_zeros(1, 64).expand(40, 64), colwise=True),
+            lambda: mx.quantize_mxfp4_grouped(x, off),
+            lambda: mx.quantize_mxfp4_grouped(x, off, rows=torch.zeros(40, dtype=i32)),
+            lambda: mx.moe_route(logits, 2),
+            lambda: mx.moe_route_backward(logits, torch.zeros(40, 2, dtype=i32), torch.zeros(40, 2)),
+            lambda: mx.matmul_mxfp4(m, w, out=x)):
+        with pytest.raises(ValueError, match="contiguous rows"):
+            call()
+
+
+def test_wrappers_take_rows_of_a_larger_pitch_and_single_rows(cuda_lib):
+    """Row strides of at least a row stay accepted (the library then refuses these tensors for being off the GPU)."""
+    x = torch.zeros(40, 96, dtype=torch.bfloat16)[:, 8:72]
+    row = torch.zeros(64, dtype=torch.bfloat16).as_strided((1, 64), (3, 1))  # the stride of one row means nothing
+    for t in (x, row, x.contiguous()):
+        with pytest.raises(mx.MXFP8Error) as error:
+            mx.quantize_mxfp4(t)
+        assert error.value.status == DEVICE
