@@ -75,8 +75,11 @@ size_t mxfp4_grouped_scale_bytes(int64_t total_rows, int64_t cols, int num_group
  *   x            device, x_type, [T, N], row pitch ldx.
  *   rows         device int32 [total_rows] or NULL.  An index outside [0, T) reads nothing: its row
  *                becomes NaN scales, and *err_flag (if given) is set to 1.
- *   offsets      device int64 [num_groups + 1] from 0 to total_rows, non-decreasing, else nothing is
- *                written and *err_flag is set to 1.  1 <= num_groups <= MXFP8_MAX_GROUPS.
+ *   offsets      device int64 [num_groups + 1] from 0, non-decreasing, none above total_rows, else nothing
+ *                is written and *err_flag is set to 1.  1 <= num_groups <= MXFP8_MAX_GROUPS.
+ *                Rows from offsets[num_groups] to total_rows belong to no expert (the choices that a plan
+ *                drops): their codes are zeros.  Where `rows` does not mark such a row with a negative index,
+ *                as a plan does, and where there are such rows without `rows`, *err_flag is set to 1 too.
  *   err_flag     device int or NULL, never cleared here.
  *   workspace    NULL, or device memory of mxfp4_quantize_grouped_workspace_bytes(T, N, total_rows) bytes,
  *                16-byte aligned: with it, a gather of more rows than T casts every row of x once and gathers
@@ -111,7 +114,9 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
 /*
  * The experts' products in one launch: rows [offsets[g], offsets[g+1]) of out [total_rows, N] are those rows
  * of A (a grouped cast; a_scale of mxfp4_grouped_scale_bytes(total_rows, K, num_groups) bytes) times B_g^T.
- * b_codes [num_groups, N, row_bytes(K)]; b_scale [num_groups] planes of mxfp4_scale_bytes(N, K).  offsets and err_flag as for mxfp4_quantize_grouped.
+ * b_codes [num_groups, N, row_bytes(K)]; b_scale [num_groups] planes of mxfp4_scale_bytes(N, K).  offsets as for
+ * mxfp4_quantize_grouped; rows of no expert become zeros, and *err_flag (if given) is set to 1 where there are any: with a
+ * plan that drops choices, the flag of the gathered cast is the one that tells a fault from a dropped choice.
  */
 mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, int64_t total_rows, int num_groups,
                                     const int64_t *offsets, const void *b_codes, const void *b_scale, int64_t N,

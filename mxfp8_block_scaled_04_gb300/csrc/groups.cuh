@@ -31,9 +31,9 @@ struct GroupTable {
 template <>
 struct GroupTable<false> {};
 
-// Load and check the offsets (0 .. total, non-decreasing); all threads of the CTA.  Returns the number of
-// row tiles of ROWS rows over all groups, or -1 for bad offsets.  Both prefixes come from one scan of a packed
-// count (the low half stays below 2^32: at most total / 128 + groups).
+// Load and check the offsets (from 0, non-decreasing, none past total; rows past the last one belong to no group); all
+// threads of the CTA.  Returns the number of row tiles of ROWS rows over all groups, or -1 for bad offsets.  Both
+// prefixes come from one scan of a packed count (the low half stays below 2^32: at most total / 128 + groups).
 template <int THREADS, int ROWS>
 __device__ __forceinline__ int group_setup(GroupTable<true> &g, const int64_t *offsets, int num_groups, int64_t total)
 {
@@ -42,7 +42,7 @@ __device__ __forceinline__ int group_setup(GroupTable<true> &g, const int64_t *o
     for (int i = tid; i <= num_groups; i += THREADS)
         g.offset[i] = offsets[i];
     __syncthreads();
-    int bad = tid == 0 && (g.offset[0] != 0 || g.offset[num_groups] != total);
+    int bad = tid == 0 && (g.offset[0] != 0 || g.offset[num_groups] > total);
     for (int i = tid; i < num_groups; i += THREADS)
         bad |= g.offset[i + 1] < g.offset[i];
     if (__syncthreads_or(bad))

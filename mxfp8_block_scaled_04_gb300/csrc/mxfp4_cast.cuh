@@ -95,6 +95,25 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The rows past the last group's, of no group: zero codes.  `rows` marks such a row with a negative index; any other
+// one, and any at all without `rows`, is reported.
+template <int THREADS>
+__device__ __forceinline__ void clear_left_over(uint8_t *out, int64_t pitch, int64_t begin, int64_t end, const int32_t *rows, int *err_flag)
+{
+    if (begin >= end)
+        return;
+    const int64_t first = blockIdx.x * int64_t{THREADS} + threadIdx.x, step = gridDim.x * int64_t{THREADS};
+    uint4 *to = reinterpret_cast<uint4 *>(out + begin * pitch);
+    for (int64_t i = first; i < (end - begin) * pitch / 16; i += step)
+        to[i] = make_uint4(0, 0, 0, 0);
+    bool lost = rows == nullptr && first == 0;
+    if (rows != nullptr)
+        for (int64_t r = begin + first; r < end; r += step)
+            lost |= rows[r] >= 0;
+    if (lost && err_flag != nullptr)
+        atomicOr(err_flag, 1);
+}
+
 // Stages of 128 rows of 64 words; each group of 32 rows is shifted by a quarter of the banks, so that a warp's
 // reads of 8 words x 4 row blocks hit 32 banks.
 constexpr int kCastWords = 64;
@@ -126,6 +145,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) mxfp4_cast_kernel(const CastP
             return;
         }
         num_tiles = static_cast<int64_t>(rt) * ct_all;
+        clear_left_over<kCastThreads>(p.out_row, p.row_pitch, groups.offset[p.num_groups], p.M, p.rows, p.err_flag);
     }
     if (blockIdx.x >= num_tiles)
         return;
@@ -345,7 +365,7 @@ struct GatherParams {
 };
 constexpr int kGatherTiles = 8;  // scale tiles of 64 code bytes per CTA
 
-__global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherParams p)
+__global__ void __launch_bounds__(256, 5) mxfp4_gather_kernel(const GatherParams p)
 {
     __shared__ GroupTable<true> groups;
     __shared__ int32_t index[kCastTile];
@@ -357,6 +377,7 @@ __global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherParams p)
             atomicOr(p.err_flag, 1);
         return;
     }
+    clear_left_over<256>(p.out, p.pitch, groups.offset[p.num_groups], p.R, p.rows, p.err_flag);
     const int chunks = (p.col_tiles + kGatherTiles - 1) / kGatherTiles;
     const int nb = static_cast<int>((p.N + 31) / 32);
     const int64_t units = static_cast<int64_t>(row_tiles) * chunks;

@@ -176,6 +176,22 @@ __device__ __forceinline__ void store_chunk(const GemmParams &p, const uint32_t 
     }
 }
 
+// The 128 epilogue threads of every CTA: zeros to the output's rows from `begin` on, which belong to no expert (ldo = P).
+template <bool F32>
+__device__ __forceinline__ void clear_rows_from(const GemmParams &p, int64_t begin, int thread)
+{
+    constexpr int kVec = F32 ? 4 : 8;
+    const int64_t first = begin * p.P, last = p.Q * p.P;
+    const int64_t at = blockIdx.x * int64_t{128} + thread, step = gridDim.x * int64_t{128};
+    if (p.vec_out) {
+        for (int64_t i = first / kVec + at; i < last / kVec; i += step)
+            static_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
+    } else {
+        for (int64_t i = first + at; i < last; i += step)
+            store_out<F32>(p.out, i, 0u);
+    }
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     mxfp4_group_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p)
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     const int row_tiles = group_setup<kGemmThreads, kGemmRows>(groups, p.offsets, p.num_groups, p.Q);
     const int num_tiles = row_tiles < 0 ? 0 : row_tiles * p.p_tiles;
-    if (row_tiles < 0 && blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
+    if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr && (row_tiles < 0 || groups.offset[p.num_groups] < p.Q))
         atomicOr(p.err_flag, 1);
     auto give_up = [&]() { atomicOr(p.fault, 1u); };
 
@@ -336,6 +352,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int quarter = warp & 3;
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kGroupStages * kGroupStage;
         int n_tile = 0, chunk = 0;
+        if (row_tiles >= 0)
+            clear_rows_from<F32>(p, groups.offset[p.num_groups], quarter * 32 + lane);
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
             const GemmTile c = gemm_tile<kGemmRows, kGemmRows, true>(t, p, groups);
             const int buf = n_tile & 1;

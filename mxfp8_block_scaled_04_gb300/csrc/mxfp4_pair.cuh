@@ -65,10 +65,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     pdl_wait_and_release();
 
     int num_tiles = p.p_tiles * p.q_tiles;
+    int64_t no_expert = p.Q;  // the first row of no expert
     if constexpr (GROUPED) {
         const int rt = group_setup<kGemmThreads, kPairRows>(groups, p.offsets, p.num_groups, p.Q);
         num_tiles = rt < 0 ? 0 : rt * p.p_tiles;
-        if (rt < 0 && blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
+        if (rt >= 0)
+            no_expert = groups.offset[p.num_groups];
+        if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr && (rt < 0 || no_expert < p.Q))
             atomicOr(p.err_flag, 1);
     }
     // The pair's n-th tile: rounds of one tile per pair, every other one backwards, so that a partial last round goes to
@@ -195,6 +198,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kPairStages * kPairStage;
         int chunk = 0;
+        if constexpr (GROUPED)
+            clear_rows_from<F32>(p, no_expert, quarter * 32 + lane);
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;

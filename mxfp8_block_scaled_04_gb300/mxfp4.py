@@ -272,7 +272,11 @@ def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False,
 def quantize_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
                            err_flag: Optional[torch.Tensor] = None, stream=None) -> MXFP4Matrix:
     """The rowwise cast of x's rows gathered for experts: output row i is x[rows[i]] (x[i] without ``rows``),
-    expert g owns rows [offsets[g], offsets[g + 1]) (device int64) and has a scale plane of its own."""
+    expert g owns rows [offsets[g], offsets[g + 1]) (device int64) and has a scale plane of its own.
+
+    Rows past the last offset belong to no expert (a plan's dropped choices, whose ``rows`` are negative): zero codes.
+    ``err_flag`` (device int32) is set to 1 for bad offsets, an index outside x, or such rows without a negative index.
+    """
     if stream is not None:
         with _on(stream):
             return quantize_mxfp4_grouped(x, offsets, rows, err_flag)
@@ -338,7 +342,8 @@ def matmul_mxfp4(a: MXFP4Matrix, b: MXFP4Matrix, out_dtype: torch.dtype = torch.
 def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, out_dtype: torch.dtype = torch.bfloat16,
                          err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Experts' products: rows [offsets[g], offsets[g + 1]) of a (from quantize_mxfp4_grouped) times expert g's
-    b [N, K] transposed; b.codes [G, N, .], b.scales [G, .].  Returns [total_rows, N]."""
+    b [N, K] transposed; b.codes [G, N, .], b.scales [G, .].  Returns [total_rows, N], zeros in the rows past the
+    last offset; ``err_flag`` is set to 1 for bad offsets and where there are such rows."""
     if stream is not None:
         with _on(stream):
             return matmul_mxfp4_grouped(a, offsets, b, out_dtype, err_flag)
