@@ -7,6 +7,7 @@ given) and raise :class:`MXFP8Error` on a non-OK status.
 """
 from __future__ import annotations
 
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -28,12 +29,13 @@ class MXFP4Matrix:
     ``groups``  number of experts of a grouped cast, which has a plane per expert (None: one plane)
 
     The casts put both into one allocation and make the two tensors when they are asked for (an allocation or a
-    view costs a call about two microseconds); the calls of this module use the addresses.
+    view costs a call about two microseconds); the calls of this module use the addresses, which follow from the
+    size: ``rows``, ``cols`` and ``groups`` are read-only.
     """
-    __slots__ = ("rows", "cols", "groups", "_codes", "_scales", "_buffer", "_offset", "_plane")
+    __slots__ = ("_rows", "_cols", "_groups", "_codes", "_scales", "_buffer", "_offset", "_plane")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, groups: Optional[int] = None):
-        self.rows, self.cols, self.groups = rows, cols, groups
+        self._rows, self._cols, self._groups = rows, cols, groups
         self._codes, self._scales = codes, scales
         self._buffer, self._offset, self._plane = None, 0, 0
 
@@ -42,10 +44,14 @@ class MXFP4Matrix:
             groups: Optional[int] = None) -> "MXFP4Matrix":
         """A cast's matrix: codes at ``offset`` of the uint8 ``buffer``, ``plane`` bytes of scales after them."""
         m = cls.__new__(cls)
-        m.rows, m.cols, m.groups = rows, cols, groups
+        m._rows, m._cols, m._groups = rows, cols, groups
         m._codes = m._scales = None
         m._buffer, m._offset, m._plane = buffer, offset, plane
         return m
+
+    rows = property(operator.attrgetter("_rows"))
+    cols = property(operator.attrgetter("_cols"))
+    groups = property(operator.attrgetter("_groups"))
 
     @property
     def codes(self) -> torch.Tensor:

@@ -284,3 +284,17 @@ def test_wrappers_take_rows_of_a_larger_pitch_and_single_rows(cuda_lib):
         with pytest.raises(mx.MXFP8Error) as error:
             mx.quantize_mxfp4(t)
         assert error.value.status == DEVICE
+
+
+def test_a_matrix_keeps_its_size(cuda_lib):
+    """The scales' address follows from the size at the cast, so that the size cannot be changed under it."""
+    cast = mx.MXFP4Matrix._in(torch.zeros(64 * 32 + 512, dtype=torch.uint8), 0, 64, 64, 512)
+    held = mx.MXFP4Matrix(cast.codes, cast.scales, 64, 64)
+    for m in (cast, held):
+        for name in ("rows", "cols", "groups"):
+            with pytest.raises(AttributeError):
+                setattr(m, name, 10)
+        assert (m.rows, m.cols, m.groups) == (64, 64, None)
+    # a shorter matrix is another one, whose tensors are given
+    short = cast._replace(rows=10, codes=cast.codes[:10])
+    assert short.rows == 10 and short.scales.data_ptr() == cast.scales.data_ptr() and short.codes.data_ptr() == cast.codes.data_ptr()
