@@ -16,6 +16,7 @@ namespace {
 using namespace mxfp8;
 
 constexpr int64_t kMaxDim = int64_t{1} << 31;
+constexpr int64_t kLongRow = int64_t{1} << 29;  // columns whose scales' offsets pass 31 bits
 
 // Products by CTA pairs need more rows than one 128-row tile and tiles for most of the 76 pairs; experts' products that
 // many rows per expert on average.  Measured (us, pairs / the other kernel), dense rows x N x K: 256x8192x8192 (32 tiles)
@@ -399,9 +400,14 @@ mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t ro
     const auto *s = static_cast<const uint8_t *>(scale);
     const int64_t pitch = ceil_div(cols, 32) * 16, col_tiles = ceil_div(cols, 128);
     auto launch = [&](auto *kern) { return launch_serialized(kern, grid, threads, 0, 1, stream, c, s, rows, cols, pitch, col_tiles, out); };
+    if (cols >= kLongRow) {
+        if (!vec)
+            return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false, true>) : launch(mxfp4_decode_kernel<false, false, true>);
+        return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true, true>) : launch(mxfp4_decode_kernel<false, true, true>);
+    }
     if (!vec)
-        return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false>) : launch(mxfp4_decode_kernel<false, false>);
-    return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true>) : launch(mxfp4_decode_kernel<false, true>);
+        return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, false, false>) : launch(mxfp4_decode_kernel<false, false, false>);
+    return out_type == MXFP4_F32 ? launch(mxfp4_decode_kernel<true, true, false>) : launch(mxfp4_decode_kernel<false, true, false>);
 }
 
 mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M, const void *b_codes, const void *b_scale, int64_t N, int64_t K,

@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     } else {
                         const uint32_t sb = 512u * min(2, p.kc - 2 * k), ds = dp + kGroupBytes + kGroupBytes;
                         mbar_arrive_expect_tx(bar, 2 * sb);
-                        bulk_load(ds, ps + k * 1024, sb, bar);
-                        bulk_load(ds + 1024, qs + k * 1024, sb, bar);
+                        bulk_load(ds, ps + int64_t{k} * 1024, sb, bar);
+                        bulk_load(ds + 1024, qs + int64_t{k} * 1024, sb, bar);
                     }
                 }
                 __syncwarp();
