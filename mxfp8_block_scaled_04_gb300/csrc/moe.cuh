@@ -78,22 +78,29 @@ __device__ __forceinline__ void load_row(const RouteParams &p, int64_t t, int la
     }
 }
 
-// exp(l - max) / sum for the row; experts past E (filled with -inf) get 0.  A row of -inf only: all 0.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// exp(l - max) / sum for the row; experts past E (filled with -inf) get 0.  A row of -inf only: all 0; with a NaN: all NaN.
 template <int VPL>
 __device__ __forceinline__ void softmax_row(float (&l)[VPL], float (&s)[VPL])
 {
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i)
-        m = fmaxf(m, l[i]);
+        m = max_nan(m, l[i]);
 #pragma unroll
     for (int d = 16; d; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
+        m = max_nan(m, __shfl_xor_sync(kAll, m, d));
     const bool none = m == -__int_as_float(0x7F800000);
     float r[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        s[i] = none ? (l[i] != l[i] ? l[i] : 0.f) : expf(l[i] - m);
+        s[i] = none ? 0.f : expf(l[i] - m);
         r[i] = s[i];
     }
 #pragma unroll
@@ -155,12 +162,6 @@ __device__ __forceinline__ uint32_t order_key_number(float x)
 {
     const uint32_t b = __float_as_uint(x);
     return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
 }
 
 // Falling order, by Batcher's odd-even merge network (VPL a power of two).

@@ -241,3 +241,19 @@ def test_combine_gradient_against_differences():
     m[5, 7] += h
     slope = (loss(m, wv) - loss(yv, wv)) / h
     assert abs(slope - float(dy[5, 7])) <= 2.0 ** -8 * abs(slope)
+
+
+@pytest.mark.parametrize("E", [8, 40, 256])
+def test_route_nan_among_masked_logits(E):
+    """A NaN makes the sum of its row's softmax NaN whatever the other logits are, -inf alone included; a row of -inf only
+    keeps its zeros."""
+    inf, nan = float("inf"), float("nan")
+    l = torch.full((3, E), -inf)
+    l[0, 3] = nan
+    l[1, E - 1], l[1, 0] = nan, 1.0
+    for renorm in (False, True):
+        r = mx.moe_route(l.cuda(), 4, renormalize=renorm)
+        assert r.indices[0].tolist() == [0, 1, 2, 4] and int(r.indices[1, 0]) == 0
+        assert bool(torch.isnan(r.weights[:2]).all()) and bool((r.weights[2] == 0).all())
+        d = mx.moe_route_backward(l.cuda(), r.indices, torch.ones(3, 4).cuda(), renormalize=renorm)
+        assert bool(torch.isnan(d[:2]).all()) and bool((d[2] == 0).all())
