@@ -120,7 +120,8 @@ __device__ __forceinline__ void softmax_row(float (&l)[VPL], float (&s)[VPL])
 
 // 1 / (1 + exp(-l)), the quotient rounded to nearest.  Up to 2^126 the reciprocal is the hardware's estimate
 // and one correction with fused multiply-adds (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990); against __frcp_rn it was compared on every mantissa and found equal.
+// System/6000 processor", 1990): the correctly rounded one for every fp32 number in [1, 2^126], which
+// tests/reciprocal_check.cu compares one by one.
 constexpr float kReciprocalMax = 8.507059173023462e37f;  // 2^126
 __device__ __forceinline__ float reciprocal_fast(float y)
 {
