@@ -61,3 +61,53 @@ def test_layer_step_by_step(tokens, hidden, ffn, experts, k, score, groups, topk
     total = p.gather(1, route.indices.cpu().long()).sum(1, keepdim=True)
     tol = (hidden * 2.0 ** -23 + 4e-6) * mag.sum(1, keepdim=True) / total * p
     assert bool(((dlogits.cpu().double() - want).abs() <= tol + 1e-12).all())
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn,experts,k,score", [(1, 256, 128, 8, 2, "softmax"), (37, 264, 136, 8, 3, "sigmoid"),
+                                                               (900, 512, 264, 4, 2, "sigmoid")])
+def test_layer_input_gradient_step_by_step(tokens, hidden, ffn, experts, k, score):
+    """The gradient of x, each step against 64 bits of its own operands, and the layer's result against the steps'."""
+    layer = example.ExpertLayer(hidden, ffn, experts, k, score)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(tokens, hidden, generator=gen, device="cuda").to(torch.bfloat16)
+    grad = torch.randn(tokens, hidden, generator=gen, device="cuda").to(torch.bfloat16)
+    _, saved = layer.forward(x)
+    logits, route, plan, ab, y = saved
+    dx, dlogits = layer.backward(grad, saved)
+    mx, off = example.mx, plan.offsets.cpu()
+    dy, _ = mx.moe_combine_backward(grad, y, plan.slots, route.weights)
+    want = (route.weights.double()[:, :, None] * grad.double()[:, None]).flatten(0, 1)
+    rows = dy.double()[plan.slots.flatten().long()]
+    assert bool(((rows - want).abs() <= 2.0 ** -8 * want.abs()).all())
+    dh = mx.matmul_mxfp4_grouped(mx.quantize_mxfp4_grouped(dy, plan.offsets), plan.offsets, layer.q2t)
+    check_product(dh, dy, layer.w2.transpose(1, 2), off)
+    leaf = ab.double().requires_grad_()
+    a, b = leaf.chunk(2, dim=1)
+    want = torch.autograd.grad(torch.nn.functional.silu(a) * b, leaf, dh.double())[0]
+    a, b, d = ab.float().chunk(2, dim=1)[0], ab.float().chunk(2, dim=1)[1], dh.float()
+    s = torch.sigmoid(a)
+    dab = torch.cat((d * b * s * (1 + a * (1 - s)), d * a * s), dim=1).to(torch.bfloat16)  # as the layer computes it
+    # fewer than 16 fp32 roundings of products below |d b| (1 + |a|) and |d a|, then one to bf16
+    mag = torch.cat(((d * b).abs() * (1 + a.abs()), (d * a).abs()), dim=1).double()
+    assert bool(((dab.double() - want).abs() <= 16 * 2.0 ** -23 * mag + 2.0 ** -8 * (want.abs() + 16 * 2.0 ** -23 * mag)).all())
+    dr = mx.matmul_mxfp4_grouped(mx.quantize_mxfp4_grouped(dab, plan.offsets), plan.offsets, layer.q1t)
+    check_product(dr, dab, layer.w1.transpose(1, 2), off)
+    summed = mx.moe_combine(dr, plan.slots)
+    parts = dr.double()[plan.slots.long()]
+    tol = k * 2.0 ** -23 * parts.abs().sum(1)
+    assert bool(((summed.double() - parts.sum(1)).abs() <= tol + 2.0 ** -8 * (parts.sum(1).abs() + tol)).all())
+    want = summed.double() + dlogits.double() @ layer.router.double()
+    tol = (experts + 2) * 2.0 ** -23 * (summed.double().abs() + dlogits.double().abs() @ layer.router.double().abs())
+    assert bool(((dx.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+
+
+def test_layer_against_the_one_that_casts_nothing():
+    """The example's own comparison.  A cast to levels spaced as E2M1's errs by about 0.12 of a normal block's rms: four
+    casts on the way to the output (those of x and w1 count twice, in a and in b) make an error of at most 0.3 of
+    its rms, a cosine of at least 0.95; the input gradient adds those of a and b again and two products, 0.4 and 0.92.  Held to
+    0.9 and 0.85: an operand in the wrong place gives nearly 0."""
+    layer = example.ExpertLayer(512, 256, 8, 2)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, grad = (torch.randn(600, 512, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    got = example.compare(layer, x, grad)
+    assert got["finite"] and got["out"] >= 0.9 and got["dx"] >= 0.85, got
