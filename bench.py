@@ -38,12 +38,13 @@ METRIC = "MXFP8 quantize effective GB/s and % of GB300 HBM peak (rowwise+colwise
 BYTES_PER_ELEM = 2 + 1 + 1 + 1 / 16
 L2_BYTES = 129 * 2 ** 20
 FALLBACK_HBM_GBS = 6800.0
-# Every source the kernels are built from: a committed ncu traffic figure is only reported
-# while these are unchanged since it was taken.
+# Every source the library is built from, the CUDA sources and the headers with the launch code and the ABI: a
+# committed ncu traffic figure is only reported while these are unchanged since it was taken.
 KERNEL_SOURCES = [f"mxfp8_block_scaled_04_gb300/csrc/{f}"
                   for f in ("api.cu", "dact.cuh", "dbias_reduce.cuh", "dgated.cuh", "groups.cuh", "moe.cu", "moe.cuh",
                             "mxfp4.cu", "mxfp4_cast.cuh", "mxfp4_gemm.cuh", "mxfp4_pair.cuh",
                             "mxfp4_split.cuh", "ptx.cuh", "quantize.cuh", "tcgen05.cuh")]
+HEADERS = ["include/moe.h", "include/mxfp4.h", "include/mxfp8.h", "mxfp8_block_scaled_04_gb300/csrc/host.h"]
 
 
 def parse_args():
@@ -105,7 +106,7 @@ def aggregate_gbs(bytes_per_step: float, steps: int, world: int, total_ms: float
 
 def kernel_source_sha():
     h = hashlib.sha256()
-    for f in KERNEL_SOURCES:
+    for f in KERNEL_SOURCES + HEADERS:
         with open(os.path.join(ROOT, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]

@@ -68,3 +68,20 @@ def test_kernel_sources_cover_every_csrc_file():
     csrc = sorted(os.path.relpath(p, ROOT) for p in glob.glob(os.path.join(ROOT, "mxfp8_block_scaled_04_gb300",
                                                                           "csrc", "*.cu*")))
     assert sorted(bench.KERNEL_SOURCES) == csrc
+
+
+def test_the_source_hash_covers_the_launch_code_and_headers(tmp_path, monkeypatch):
+    """A change of any file that the build reads changes the hash that a committed traffic figure is tied to."""
+    from mxfp8_block_scaled_04_gb300 import build
+    files = sorted(os.path.relpath(p, ROOT) for p in set(build._inputs()))
+    assert sorted(bench.KERNEL_SOURCES + bench.HEADERS) == files
+    for f in files:
+        (tmp_path / f).parent.mkdir(parents=True, exist_ok=True)
+        (tmp_path / f).write_bytes(open(os.path.join(ROOT, f), "rb").read())
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    seen = {bench.kernel_source_sha()}
+    for f in files:
+        with open(tmp_path / f, "a") as fh:
+            fh.write("\n")
+        seen.add(bench.kernel_source_sha())
+    assert len(seen) == len(files) + 1
