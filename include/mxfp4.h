@@ -93,8 +93,8 @@ mxfp8_status_t mxfp4_quantize_grouped(const void *x, int x_type, int64_t T, int6
 size_t mxfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t N, int64_t total_rows);
 
 /*
- * The values of a 4-bit matrix: out [rows, cols] (row pitch cols, any cols) in out_type.  Exact in both types, but
- * for 2^128, which an element of at least 1.75 * 2^127 rounds up to: it comes out as infinity.
+ * The values of a 4-bit matrix: out [rows, cols] (row pitch cols, any cols up to 2^31 - 1) in out_type.  Exact in
+ * both types, but for 2^128, which an element of at least 1.75 * 2^127 rounds up to: it comes out as infinity.
  */
 mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t rows, int64_t cols, void *out,
                                 int out_type, void *stream);
@@ -105,7 +105,7 @@ mxfp8_status_t mxfp4_dequantize(const void *codes, const void *scale, int64_t ro
  * dx = dy (W^T)^T with W's transposed cast, dw = (dy^T) (x^T)^T with both transposed casts.
  *
  *   codes 16-byte aligned, scale planes 16-byte aligned, out aligned to its element; ldo >= N elements.
- *   M, N, K any size >= 0 (K = 0: out is set to zeros).
+ *   M, N, K any size from 0 to 2^31 - 1 (K = 0: out is set to zeros).
  */
 mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M, const void *b_codes,
                             const void *b_scale, int64_t N, int64_t K, void *out, int out_type, int64_t ldo,
