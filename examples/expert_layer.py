@@ -3,7 +3,8 @@
     python examples/expert_layer.py [--tokens 4096] [--hidden 2048] [--ffn 1024] [--experts 64] [--top-k 8]
 
 Each expert is SwiGLU: y = (silu(a) * b) W2^T with [a | b] = x W1^T.  Weights are cast once, both ways: along
-their inputs for the forward products and transposed for the input gradients.  Every step is one call of the
+their inputs for the forward products and transposed for the input gradients; backward gives the gradients of x and of
+the router's logits (the package has no call for the experts' weight gradients).  Every step is one call of the
 package; only the router's own product and the SwiGLU are plain torch.
 """
 from __future__ import annotations
@@ -48,7 +49,7 @@ class ExpertLayer:
         logits = x.float() @ self.router.float().t()
         route = mx.moe_route(logits, self.top_k, bias=self.bias, **self.how, **self.groups)
         plan = mx.moe_plan(route.indices, self.experts)
-        gathered = mx.quantize_mxfp4_grouped(x, plan.offsets, rows=plan.tokens)
+        gathered = mx.quantize_mxfp4_grouped(x, plan.offsets, rows=plan.tokens)  # dropped choices would be rows of zeros
         ab = mx.matmul_mxfp4_grouped(gathered, plan.offsets, self.q1)
         a, b = ab.float().chunk(2, dim=1)
         h = (torch.nn.functional.silu(a) * b).to(torch.bfloat16)
