@@ -34,3 +34,6 @@ from .moe import (  # noqa: F401
     moe_combine_c, moe_plan, moe_plan_c, moe_plan_workspace_bytes, moe_route, moe_route_backward,
     moe_route_backward_c, moe_route_c,
 )
+from .mxfp8_matmul import (  # noqa: F401
+    matmul_mxfp8_grouped, matmul_mxfp8_grouped_dgrad, matmul_mxfp8_grouped_wgrad, mxfp8_matmul_grouped,
+)

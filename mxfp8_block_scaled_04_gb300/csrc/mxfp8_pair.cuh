@@ -1,0 +1,401 @@
+// Experts' products in MXFP8 (sm_103a) by pairs of CTAs: out[q, p] = sum_k Q[q, k] * P[p, k] in tiles of 256 x 256.
+//
+//   forward           Q = x's rows, P = W's rows           summed over K, both operands K-major
+//   input gradient    Q = dy's rows, P = W's columns       summed over N: P's codes lie [N, K], MN-major
+//   weight gradient   Q = dy's columns, P = x's columns    summed over the expert's rows: both MN-major
+//
+// The cast leaves the columns' codes untransposed ([rows, columns], blocks of 32 rows), so the gradients read them as
+// MN-major operands: a TMA box of 128 summed rows x 128 bytes in the 128-byte swizzle is one operand atom wide, and a step
+// of 32 summed elements is 32 of its rows.  No transposed copy exists.
+//
+// The loop is that of mxfp4_pair.cuh: 128 bytes of codes per operand row and stage, here 128 elements in four MMA steps
+// of 32 (kind::mxf8f6f4, one E8M0 scale per step and row).
+//
+// A weight gradient's last stage may hold rows of the next expert.  Steps past the expert's last 32 rows are not issued;
+// where the rows are no multiple of 32 each CTA's warp 2 zeroes the rest of the last step in shared memory (its own
+// barrier says that the copy has landed) before the MMA warp sees the stage.
+#pragma once
+
+#include "mxfp4_gemm.cuh"
+
+namespace mxfp8 {
+
+enum { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+constexpr int kP8Tile = 256;
+constexpr int kP8Stages = 5;
+constexpr int kP8Codes = 128 * 128;           // bytes of either operand in one CTA and stage
+constexpr int kP8Stage = 2 * kP8Codes;
+constexpr int kP8Scales = 3 * 512;            // P's tile of this CTA, Q's two tiles
+constexpr int kP8Smem = kP8Stages * (kP8Stage + kP8Scales) + 1024;  // + the epilogue's buffers
+constexpr int kP8Acc1 = 224, kP8ScaleCol = 480;  // TMEM columns, as in mxfp4_pair.cuh
+
+struct Product8Params : GemmParams {
+    uint32_t formats;      // operand format bits of the instruction descriptor
+    int64_t sum;           // summed elements (forward, input gradient)
+    int64_t a_tile_rows;   // tile rows that a's plane holds (weight gradient: groups of kt tiles, see fits())
+    int64_t b_tile_rows;
+    int p_ct, q_ct;        // weight gradient: 128-column tiles of either operand's planes
+};
+
+struct Tile8 {
+    int32_t p_at, q_at, row;   // P's first row (K-major) or column; Q's; weight gradient: the expert's first row
+    int32_t group;
+    int64_t p_tile, q_tile;    // scale tile rows; weight gradient: linear tiles
+    int64_t out_row;
+    int valid, k_iters, steps, tail;  // rows of Q; stages; MMA steps in all; rows of the last step (0: whole)
+    int kt;
+};
+
+template <int MODE>
+__device__ __forceinline__ Tile8 tile8(int t, const Product8Params &p, const GroupTable<true> &groups)
+{
+    Tile8 r;
+    if constexpr (MODE == kWeightGrad) {
+        const int per = p.p_tiles * p.q_tiles;
+        const int g = t / per, in = t - g * per, qt = in / p.p_tiles, pt = in - qt * p.p_tiles;
+        const int64_t rows = groups.offset[g + 1] - groups.offset[g];
+        r.group = g;
+        r.row = static_cast<int32_t>(groups.offset[g]);
+        r.p_at = pt * kP8Tile;
+        r.q_at = qt * kP8Tile;
+        r.kt = groups.plane[g + 1] - groups.plane[g];
+        r.p_tile = static_cast<int64_t>(groups.plane[g]) * p.p_ct + static_cast<int64_t>(2 * pt) * r.kt;
+        r.q_tile = static_cast<int64_t>(groups.plane[g]) * p.q_ct + static_cast<int64_t>(2 * qt) * r.kt;
+        r.out_row = g * p.Q + r.q_at;
+        const int64_t left = p.Q - r.q_at;
+        r.valid = left < kP8Tile ? static_cast<int>(left) : kP8Tile;
+        r.k_iters = r.kt;
+        r.steps = static_cast<int>((rows + 31) / 32);
+        r.tail = static_cast<int>(rows & 31);
+    } else {
+        const int rt = t / p.p_tiles, pt = t - rt * p.p_tiles;
+        const int g = groups.find(rt, p.num_groups);
+        const int local = rt - groups.tile[g];
+        const int64_t q0 = groups.offset[g] + static_cast<int64_t>(local) * kP8Tile;
+        const int64_t left = groups.offset[g + 1] - q0;
+        r.group = g;
+        r.row = 0;
+        r.p_at = pt * kP8Tile;
+        r.q_at = static_cast<int32_t>(q0);
+        r.kt = 0;
+        r.p_tile = static_cast<int64_t>(g) * p.p_planes + 2 * pt;
+        r.q_tile = groups.plane[g] + static_cast<int64_t>(local) * 2;
+        r.out_row = q0;
+        r.valid = left < kP8Tile ? static_cast<int>(left) : kP8Tile;
+        r.k_iters = p.k_iters;
+        r.steps = static_cast<int>((p.sum + 31) / 32);
+        r.tail = 0;
+    }
+    return r;
+}
+
+// 3-D tiled copy into this CTA's shared memory that signals a barrier of either CTA of its pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t mapped_bar, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mapped_bar)
+                 : "memory");
+}
+
+// Operand whose summed dimension lies across rows of 128 bytes (MN-major, 128-byte swizzle): groups of 8 summed rows 1024
+// bytes apart; one atom of 128 elements wide, so the other stride is not used (set to the same, within the stage).
+__device__ __forceinline__ uint64_t desc_mn128(uint32_t smem)
+{
+    return static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (uint64_t{1024 >> 4} << 16) | (uint64_t{1024 >> 4} << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// Instruction descriptor of kind::mxf8f6f4 with E8M0 scales; formats: operand formats at bits 7 and 10, transposes at 15
+// and 16; step: which of a TMEM column's four scales the 32 elements of this step use.
+__device__ __forceinline__ uint32_t mxf8_idesc(uint32_t formats, int m, int n, int step)
+{
+    return formats | (static_cast<uint32_t>(step) << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(m >> 7) << 27) | (static_cast<uint32_t>(step) << 29);
+}
+
+__device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(accumulate))
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+template <int MODE, bool F32>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    mxfp8_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ CUtensorMap q_part_map, const __grid_constant__ CUtensorMap ps_map,
+                      const __grid_constant__ CUtensorMap qs_map, const Product8Params p)
+{
+    constexpr bool kTails = MODE == kWeightGrad;
+    constexpr bool kPMn = MODE != kForward, kQMn = MODE == kWeightGrad;
+    extern __shared__ unsigned char gemm_smem[];
+    __shared__ GroupTable<true> groups;
+    __shared__ uint64_t full[kP8Stages], empty[kP8Stages], landed[kP8Stages], acc_full[2], acc_empty, drain;
+    __shared__ uint32_t tmem_slot;
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+    const uint32_t rank = cluster_rank();
+    const uint32_t base = (smem_u32(gemm_smem) + 1023u) & ~1023u;
+    const uint32_t scales = base + kP8Stages * kP8Stage;
+    if (tid == 0) {
+        prefetch_tensormap(&p_map);
+        prefetch_tensormap(&q_map);
+        prefetch_tensormap(&q_part_map);
+        prefetch_tensormap(&ps_map);
+        prefetch_tensormap(&qs_map);
+        for (int s = 0; s < kP8Stages; ++s) {
+            mbar_init(smem_u32(&full[s]), kTails ? 3 : 1);  // the expectation; a zeroed stage's two CTAs
+            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&landed[s]), 1);
+        }
+        mbar_init(smem_u32(&acc_full[0]), 1);
+        mbar_init(smem_u32(&acc_full[1]), 1);
+        mbar_init(smem_u32(&acc_empty), 8);  // the epilogue warps of both CTAs
+        mbar_init(smem_u32(&drain), 1);
+        fence_mbar_init();
+    }
+    if (warp == 2)
+        tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait_and_release();
+
+    int rt = group_setup<kGemmThreads, kP8Tile>(groups, p.offsets, p.num_groups, MODE == kWeightGrad ? p.sum : p.Q);
+    const int64_t total = MODE == kWeightGrad ? p.sum : p.Q;
+    if (rt >= 0) {  // offsets that need larger planes than there are
+        const int64_t tiles = groups.plane[p.num_groups];
+        if (MODE == kWeightGrad ? tiles * p.q_ct > p.a_tile_rows || tiles * p.p_ct > p.b_tile_rows : tiles > p.a_tile_rows)
+            rt = -1;
+    }
+    const int num_tiles = rt < 0 ? 0 : MODE == kWeightGrad ? p.num_groups * p.p_tiles * p.q_tiles : rt * p.p_tiles;
+    const int64_t no_expert = rt < 0 ? total : groups.offset[p.num_groups];  // the first row of no expert
+    if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr && (rt < 0 || no_expert < total))
+        atomicOr(p.err_flag, 1);
+    // the pair's n-th tile: rounds of one tile per pair, every other one backwards (as in mxfp4_pair.cuh)
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    auto tile_of = [&](int n) { return n * pairs + (n & 1 ? pairs - 1 - pair : pair); };
+    const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), landed0 = smem_u32(&landed[0]);
+    int slot = 0;
+    uint32_t phase = 0;
+    auto advance = [&]() {
+        if (++slot == kP8Stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+
+    if (warp == 0 || warp == 3) {
+        // ---- producers of this CTA's operands: codes (warp 0), scales (warp 3); they signal the first CTA's barriers ----
+        const uint32_t lead_full = map_to_rank(full0, 0), own_landed = map_to_rank(landed0, rank);
+        bool ok = true;
+        int issued = 0;
+        for (int n = 0, t; (t = tile_of(n)) < num_tiles && ok; ++n) {
+            const Tile8 c = tile8<MODE>(t, p, groups);
+            const int half = ((c.valid + 31) & ~31) / 2;
+            const int boxes = kQMn || half > 96 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
+            const uint32_t code_bytes = kP8Stage - (boxes ? (4 - boxes) * 32 * 128 : 0);
+            for (int k = 0; k < c.k_iters; ++k) {
+                ok = mbar_wait_cluster(empty0 + 8 * slot, phase ^ 1, kGemmWait);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const bool zeroed = kTails && c.tail != 0 && k == c.k_iters - 1;
+                    const uint32_t dp = base + slot * kP8Stage;
+                    if (warp == 0) {
+                        if (rank == 0) {
+                            mbar_arrive_expect_tx(full0 + 8 * slot, 2 * (kP8Scales + (zeroed ? 0 : code_bytes)));
+                            if (kTails && !zeroed)
+                                mbar_arrive_many(full0 + 8 * slot, 2);
+                        }
+                        if (zeroed)
+                            mbar_arrive_expect_tx(landed0 + 8 * slot, code_bytes);
+                        const uint32_t bar = (zeroed ? own_landed : lead_full) + 8 * slot;
+                        const int p_at = c.p_at + static_cast<int>(rank) * 128, q_at = c.q_at + static_cast<int>(rank) * half;
+                        if constexpr (MODE == kForward)
+                            tma_load_3d_pair(dp, &p_map, bar, k * 128, p_at, c.group);
+                        else if constexpr (MODE == kInputGrad)
+                            tma_load_3d_pair(dp, &p_map, bar, p_at, k * 128, c.group);
+                        else
+                            tma_load_2d_pair(dp, &p_map, bar, p_at, c.row + k * 128);
+                        if constexpr (kQMn) {
+                            tma_load_2d_pair(dp + kP8Codes, &q_map, bar, q_at, c.row + k * 128);
+                        } else {
+                            if (boxes == 0)
+                                tma_load_2d_pair(dp + kP8Codes, &q_map, bar, k * 128, q_at);
+                            for (int b = 0; b < boxes; ++b)
+                                tma_load_2d_pair(dp + kP8Codes + b * 32 * 128, &q_part_map, bar, k * 128, q_at + 32 * b);
+                        }
+                    } else {
+                        const uint32_t bar = lead_full + 8 * slot, ds = scales + slot * kP8Scales;
+                        if constexpr (MODE == kWeightGrad) {
+                            tma_load_2d_pair(ds, &ps_map, bar, 0, static_cast<int>(c.p_tile + static_cast<int64_t>(rank) * c.kt + k));
+                            tma_load_2d_pair(ds + 512, &qs_map, bar, 0, static_cast<int>(c.q_tile + k));
+                            tma_load_2d_pair(ds + 1024, &qs_map, bar, 0, static_cast<int>(c.q_tile + c.kt + k));
+                        } else {
+                            tma_load_2d_pair(ds, &ps_map, bar, k * 128, static_cast<int>(c.p_tile) + static_cast<int>(rank));
+                            tma_load_2d_pair(ds + 512, &qs_map, bar, k * 128, static_cast<int>(c.q_tile));
+                        }
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                advance();
+            }
+        }
+        if (!ok && lane == 0)
+            atomicOr(p.fault, 1u);
+        if (rank == 0 && !ok) {
+            for (int j = 0; j < kP8Stages && j < issued; ++j) {  // copies in flight, the newest first
+                if (--slot < 0) {
+                    slot = kP8Stages - 1;
+                    phase ^= 1;
+                }
+                mbar_wait_cluster(full0 + 8 * slot, phase, kGemmDrain);
+            }
+        }
+    } else if (kTails && warp == 2) {
+        // ---- zeros behind an expert's last row, in this CTA's shared memory ----
+        const uint32_t lead_full = map_to_rank(full0, 0);
+        uint32_t phases = 0;
+        for (int n = 0, t; (t = tile_of(n)) < num_tiles; ++n) {
+            const Tile8 c = tile8<MODE>(t, p, groups);
+            if (c.tail != 0) {
+                const int s = (slot + c.k_iters - 1) % kP8Stages;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(landed0 + 8 * s, (phases >> s) & 1, kGemmWait))) {
+                    if (lane == 0)
+                        atomicOr(p.fault, 1u);
+                    break;
+                }
+                phases ^= 1u << s;
+                const int last = (c.steps - 1) % 4 * 32;  // first row of the last step within the stage
+                unsigned char *stage = gemm_smem + (base - smem_u32(gemm_smem)) + s * kP8Stage;
+                for (int i = (last + c.tail) * 8 + lane; i < (last + 32) * 8; i += 32) {  // whole rows: the swizzle stays inside
+                    *reinterpret_cast<uint4 *>(stage + i * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(stage + kP8Codes + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(lead_full + 8 * s);
+            }
+            slot = (slot + c.k_iters) % kP8Stages;
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMA for both CTAs ----
+        bool ok = true;
+        constexpr uint32_t kPStep = kPMn ? 4096 / 16 : 32 / 16, kQStep = kQMn ? 4096 / 16 : 32 / 16;
+        const uint64_t p_desc = kPMn ? desc_mn128(base) : desc_sw128(base);
+        const uint64_t q_desc = kQMn ? desc_mn128(base + kP8Codes) : desc_sw128(base + kP8Codes);
+        const uint64_t s_desc = desc_scales(scales);
+        const uint32_t formats = p.formats | (kPMn ? 1u << 15 : 0u) | (kQMn ? 1u << 16 : 0u);
+        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles && ok; ++n_tile) {
+            const Tile8 c = tile8<MODE>(t, p, groups);
+            const int n = (c.valid + 31) & ~31;  // halves of whole 16-row groups
+            const uint32_t d = tmem + (n_tile & 1) * kP8Acc1;
+            if (n_tile >= 1)  // the columns shared with the tile before are read, and all of the one before that
+                ok = mbar_wait_cluster(smem_u32(&acc_empty), (n_tile - 1) & 1, kGemmWait);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int k = 0; k < c.k_iters; ++k) {
+                ok = mbar_wait_cluster(full0 + 8 * slot, phase, kGemmWait);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t pd = p_desc + slot * (kP8Stage >> 4), qd = q_desc + slot * (kP8Stage >> 4), sd = s_desc + slot * (kP8Scales >> 4);
+                    const uint32_t sp = tmem + kP8ScaleCol + (k & 1) * 12, sq = sp + 4;
+                    const int left = c.steps - 4 * k;
+                    tc_copy_scales_pair(sp, sd);
+                    tc_copy_scales_pair(sq, sd + 512 / 16);
+                    tc_copy_scales_pair(sq + 4, sd + 1024 / 16);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < left)
+                            tc_mma_mxf8_pair(d, pd + j * kPStep, qd + j * kQStep, mxf8_idesc(formats, kP8Tile, n, j), sp, sq, k > 0 || j > 0);
+                    tc_commit_pair(empty0 + 8 * slot);
+                }
+                __syncwarp();
+                advance();
+            }
+            if (!ok)
+                break;
+            if (elect_one())
+                tc_commit_pair(smem_u32(&acc_full[n_tile & 1]));
+            __syncwarp();
+        }
+        if (!ok) {
+            if (elect_one()) {
+                atomicOr(p.fault, 1u);
+                tc_commit_pair(smem_u32(&drain));
+            }
+            __syncwarp();
+            mbar_wait_cluster(smem_u32(&drain), 0, kGemmDrain);
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue of this CTA's 128 columns of the output ----
+        const int quarter = warp & 3;
+        const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
+        unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Stages * (kP8Stage + kP8Scales);
+        int chunk = 0;
+        if constexpr (MODE != kWeightGrad)
+            clear_rows_from<F32>(p, no_expert, quarter * 32 + lane);
+        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
+            const Tile8 c = tile8<MODE>(t, p, groups);
+            const int buf = n_tile & 1;
+            if (!epilogue_all(mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+                if (lane == 0)
+                    atomicOr(p.fault, 1u);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8Acc1;
+            // the columns shared with the other accumulator first: 224..255 of accumulator 0, 0..31 of accumulator 1
+            const int start = buf == 0 ? kP8Acc1 : 0;
+            for (int i = 0; i < kP8Tile / 32; ++i) {
+                const int q = (start + 32 * i) & (kP8Tile - 1);
+                uint32_t v[32];
+                if (q < c.valid)
+                    tmem_load32(d + q, v);
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(lead_empty);
+                }
+                if (q < c.valid) {
+                    if (kTails && c.k_iters == 0) {  // an expert without rows
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = 0;
+                    }
+                    store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.out_row + q, c.valid - q,
+                                     c.p_at + rank * 128);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its pair's MMAs, copies or arrivals may still reach it
+    if (warp == 2)
+        tmem_dealloc_pair(tmem, 512);
+}
+
+}  // namespace mxfp8

@@ -1,0 +1,108 @@
+"""Experts' products in MXFP8 (forward, input gradient, weight gradient) against 64-bit products of the cast operands."""
+import pytest
+import torch
+
+import mxfp8_ref as ref
+import mxfp8_block_scaled_04_gb300 as mx
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def draw(M, N, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(M, N, generator=g) * torch.exp(spread * torch.randn(M, 1, generator=g))).to(BF16)
+
+
+def cast(x, offsets, fmt):
+    return mx.quantize_grouped(x.cuda(), torch.tensor(offsets).cuda(), fmt, swizzled=True)
+
+
+class Layer:
+    """Casts of x [R, K], dy [R, N] and w [E * N, K], and their 64-bit values by expert."""
+
+    def __init__(self, sizes, N, K, x_fmt="e4m3", w_fmt="e4m3", dy_fmt="e5m2", x=None, w=None, dy=None):
+        E, R = len(sizes), sum(sizes)
+        self.N, self.K, self.R, self.E = N, K, R, E
+        self.fmts = (x_fmt, w_fmt, dy_fmt)
+        self.off = torch.tensor([0] + sizes).cumsum(0).tolist()
+        self.w_off = [e * N for e in range(E + 1)]
+        self.x = cast(draw(R, K, 1) if x is None else x, self.off, x_fmt)
+        self.dy = cast(draw(R, N, 2) if dy is None else dy, self.off, dy_fmt)
+        self.w = cast(draw(E * N, K, 3, 0.2) if w is None else w, self.w_off, w_fmt)
+        self.offsets = torch.tensor(self.off).cuda()
+
+    def rows(self, which):
+        t, off, fmt = {"x": (self.x, self.off, self.fmts[0]), "w": (self.w, self.w_off, self.fmts[1]),
+                       "dy": (self.dy, self.off, self.fmts[2])}[which]
+        return ref.groups(t.out_row, t.scale_row, off, fmt, True)
+
+    def cols(self, which):
+        t, off, fmt = {"x": (self.x, self.off, self.fmts[0]), "w": (self.w, self.w_off, self.fmts[1]),
+                       "dy": (self.dy, self.off, self.fmts[2])}[which]
+        return ref.groups(t.out_col, t.scale_col, off, fmt, False)
+
+    def check(self, dtype=BF16):
+        xf, wf, df = self.fmts
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        y = mx.matmul_mxfp8_grouped(self.x, self.offsets, self.w, dtype, xf, wf, err).cpu().double()
+        dx = mx.matmul_mxfp8_grouped_dgrad(self.dy, self.offsets, self.w, dtype, df, wf, err).cpu().double()
+        dw = mx.matmul_mxfp8_grouped_wgrad(self.dy, self.x, self.offsets, dtype, df, xf, err).cpu().double()
+        assert int(err) == 0 and mx.mxfp8_device_fault_word() == 0
+        worst = 0.0
+        for got, pairs in ((y.split([b - a for a, b in zip(self.off, self.off[1:])]), zip(self.rows("x"), self.rows("w"))),
+                           (dx.split([b - a for a, b in zip(self.off, self.off[1:])]), zip(self.rows("dy"), (w.t() for w in self.cols("w")))),
+                           (dw, zip((d.t() for d in self.cols("dy")), (x.t() for x in self.cols("x"))))):
+            for e, (g, (a, b)) in enumerate(zip(got, pairs)):
+                want, tol = ref.product_bound(a, b, dtype == BF16)
+                bad = ~((g - want).abs() <= tol)
+                assert not bool(bad.any()), (e, int(bad.sum()), g.shape, float((g - want).abs().max()), float(want.abs().max()))
+                if g.numel() and dtype == F32:
+                    worst = max(worst, float((g - want).norm() / want.norm().clamp(min=1e-300)))
+        return worst
+
+
+SIZES = [[5], [0, 3, 0], [128, 0, 1, 127, 129], [1] * 40, [300, 2, 0, 0, 61], [0, 0, 257], [32, 64, 31, 33]]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,K", [(48, 80), (256, 128), (272, 528), (16, 16)])
+@pytest.mark.parametrize("sizes", SIZES)
+def test_products(sizes, N, K, dtype):
+    Layer(sizes, N, K).check(dtype)
+
+
+@pytest.mark.parametrize("sizes,N,K", [([700, 0, 1025, 256, 3, 1700], 1424, 336), ([5120, 1], 1008, 256), ([40] * 30, 528, 1040)])
+def test_products_of_many_tiles(sizes, N, K):
+    """More tiles than pairs of CTAs: both accumulators and every stage are reused."""
+    Layer(sizes, N, K).check(BF16)
+
+
+@pytest.mark.parametrize("x_fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("w_fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dy_fmt", ["e4m3", "e5m2"])
+def test_formats(x_fmt, w_fmt, dy_fmt):
+    Layer([100, 37], 144, 208, x_fmt, w_fmt, dy_fmt).check(F32)
+
+
+def test_each_position_counts():
+    """Small integers, equal scales: every sum is exact, whatever the order."""
+    g = torch.Generator().manual_seed(4)
+    sizes, N, K = [300, 77, 512], 272, 400
+    x, dy, w = (torch.randint(-4, 5, s, generator=g).to(BF16) for s in ((889, K), (889, N), (3 * N, K)))
+    layer = Layer(sizes, N, K, x=x, dy=dy, w=w)
+    y = mx.matmul_mxfp8_grouped(layer.x, layer.offsets, layer.w, F32).cpu().double()
+    dx = mx.matmul_mxfp8_grouped_dgrad(layer.dy, layer.offsets, layer.w, F32).cpu().double()
+    dw = mx.matmul_mxfp8_grouped_wgrad(layer.dy, layer.x, layer.offsets, F32).cpu().double()
+    for e in range(3):
+        s = slice(layer.off[e], layer.off[e + 1])
+        we = w[e * N:(e + 1) * N].double()
+        assert torch.equal(y[s], x[s].double() @ we.t())
+        assert torch.equal(dx[s], dy[s].double() @ we)
+        assert torch.equal(dw[e], dy[s].double().t() @ x[s].double())
+
+
+def test_sums_keep_fp32():
+    """Norm-wise error of long sums of random signs: far below one rounding to 2^-14 per step."""
+    assert Layer([4096, 100], 256, 4096).check(F32) < 2e-6
