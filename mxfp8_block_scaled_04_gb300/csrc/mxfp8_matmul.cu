@@ -54,22 +54,32 @@ mxfp8_status_t scale_map(CUtensorMap *map, const void *scale, int64_t tile_rows,
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, scale, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// The weight gradients [groups, N, K] in boxes of 128 bytes x 32 rows: what lies past an expert's rows is not written.
+mxfp8_status_t gradient_map(CUtensorMap *map, void *out, int64_t groups, int64_t N, int64_t K, bool f32)
+{
+    const int64_t size = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K * size), static_cast<cuuint64_t>(N * K * size)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), 32, 1};
+    return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 struct Maps {
-    CUtensorMap p, q, q_part, p_scale, q_scale;
+    CUtensorMap p, q, q_part, p_scale, q_scale, out;
 };
 
 template <int MODE, bool F32>
 mxfp8_status_t launch_pair(const Product8Params &p, const Maps &m, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr int smem = kP8Smem + kEpiBytes<F32>;
+    constexpr int smem = kP8Smem + kP8Epilogue<MODE, F32>;
     int ctas = 0;
     const mxfp8_status_t st = setup(mxfp8_pair_kernel<MODE, F32>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
     return launch_serialized(mxfp8_pair_kernel<MODE, F32>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, m.p, m.q, m.q_part,
-                             m.p_scale, m.q_scale, p);
+                             m.p_scale, m.q_scale, m.out, p);
 }
 
 mxfp8_status_t zero(void *out, int64_t bytes, cudaStream_t stream)
@@ -99,15 +109,16 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
     if (num_groups * N >= kMaxDim)
         return MXFP8_ERR_SHAPE;
     const bool wgrad = product == MXFP8_WEIGHT_GRADIENT;
-    const int64_t P = product == MXFP8_FORWARD ? N : K, sum = wgrad ? total_rows : product == MXFP8_FORWARD ? K : N;
-    const int64_t p_tiles = ceil_div(P, kP8Tile), q_tiles = ceil_div(N, kP8Tile);
-    const int64_t tiles = wgrad ? num_groups * p_tiles * q_tiles : (total_rows / kP8Tile + num_groups) * p_tiles;
+    const int64_t P = product == MXFP8_INPUT_GRADIENT ? K : N, sum = wgrad ? total_rows : product == MXFP8_FORWARD ? K : N;
+    const int64_t p_tiles = ceil_div(P, kP8TileP), q_tiles = ceil_div(K, kP8TileQ);
+    const int64_t tiles = wgrad ? num_groups * p_tiles * q_tiles : (total_rows / kP8TileQ + num_groups) * p_tiles;
     // the weight gradient's tile rows of scales, all planes' together
     const int64_t linear = (total_rows / 128 + num_groups) * ceil_div(N > K ? N : K, 128);
     if (tiles >= kMaxDim - (int64_t{1} << 20) || (wgrad && linear >= kMaxDim))
         return MXFP8_ERR_SHAPE;
     const int64_t out_rows = wgrad ? num_groups * N : total_rows;
-    const bool empty = out_rows == 0 || P == 0;
+    const int64_t cols = wgrad ? K : P;
+    const bool empty = out_rows == 0 || cols == 0;
     const int64_t kc = ceil_div(sum, 128);  // tiles along the summed dimension (forward, input gradient)
     if (!empty) {
         if (out == nullptr || (sum > 0 && (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr)))
@@ -131,45 +142,50 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const int size = out_type == MXFP4_F32 ? 4 : 2;
     if (sum == 0)
-        return zero(out, out_rows * P * size, stream);
+        return zero(out, out_rows * cols * size, stream);
     Product8Params p{};
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     p.P = P;
-    p.Q = wgrad ? N : total_rows;
+    p.Q = wgrad ? K : total_rows;
     p.sum = sum;
     p.kc = static_cast<int>(kc);
     p.k_iters = static_cast<int>(kc);
     p.p_tiles = static_cast<int>(p_tiles);
     p.q_tiles = static_cast<int>(q_tiles);
     p.p_planes = static_cast<int>(ceil_div(P, 128));
-    p.p_ct = static_cast<int>(ceil_div(K, 128));
-    p.q_ct = static_cast<int>(ceil_div(N, 128));
+    p.p_ct = static_cast<int>(ceil_div(N, 128));
+    p.q_ct = static_cast<int>(ceil_div(K, 128));
     p.out = out;
     p.ldo = P;
-    p.vec_out = P * size % 16 == 0;
+    p.vec_out = true;  // N and K are multiples of 16
     p.offsets = offsets;
     p.num_groups = num_groups;
     p.err_flag = err_flag;
-    p.formats = (static_cast<uint32_t>(b_fmt) << 7) | (static_cast<uint32_t>(a_fmt) << 10);  // P is b, Q is a
+    // the weight gradient has the gradient on the accumulator's lanes, the other two the weights
+    const int p_fmt = wgrad ? a_fmt : b_fmt, q_fmt = wgrad ? b_fmt : a_fmt;
+    p.formats = (static_cast<uint32_t>(p_fmt) << 7) | (static_cast<uint32_t>(q_fmt) << 10);
     const int64_t unit = wgrad ? 512 : kc * 512;
-    p.a_tile_rows = static_cast<int64_t>(a_scale_bytes) / unit;
-    p.b_tile_rows = static_cast<int64_t>(b_scale_bytes) / unit;
-    if (p.a_tile_rows < 1 || p.b_tile_rows < 1)
+    const int64_t a_tile_rows = static_cast<int64_t>(a_scale_bytes) / unit, b_tile_rows = static_cast<int64_t>(b_scale_bytes) / unit;
+    if (a_tile_rows < 1 || b_tile_rows < 1)
         return MXFP8_ERR_WORKSPACE;
+    p.p_tile_rows = wgrad ? a_tile_rows : b_tile_rows;
+    p.q_tile_rows = wgrad ? b_tile_rows : a_tile_rows;
+    const bool f32 = out_type == MXFP4_F32;
     Maps m;
     if (wgrad) {
-        if ((st = code_map(&m.p, b, total_rows, K, 128)) != MXFP8_OK || (st = code_map(&m.q, a, total_rows, N, 128)) != MXFP8_OK ||
-            (st = scale_map(&m.p_scale, b_scale, p.b_tile_rows, 1, 1)) != MXFP8_OK || (st = scale_map(&m.q_scale, a_scale, p.a_tile_rows, 1, 1)) != MXFP8_OK)
+        if ((st = code_map(&m.p, a, total_rows, N, 128)) != MXFP8_OK || (st = code_map(&m.q, b, total_rows, K, 128)) != MXFP8_OK ||
+            (st = scale_map(&m.p_scale, a_scale, a_tile_rows, 1, 1)) != MXFP8_OK || (st = scale_map(&m.q_scale, b_scale, b_tile_rows, 1, 1)) != MXFP8_OK ||
+            (st = gradient_map(&m.out, out, num_groups, N, K, f32)) != MXFP8_OK)
             return st;
         m.q_part = m.q;
     } else {
-        if ((st = weight_map(&m.p, b, num_groups, N, K)) != MXFP8_OK || (st = code_map(&m.q, a, total_rows, sum, 128)) != MXFP8_OK ||
-            (st = code_map(&m.q_part, a, total_rows, sum, 32)) != MXFP8_OK || (st = scale_map(&m.p_scale, b_scale, p.b_tile_rows, kc, 1)) != MXFP8_OK ||
-            (st = scale_map(&m.q_scale, a_scale, p.a_tile_rows, kc, 2)) != MXFP8_OK)
+        if ((st = weight_map(&m.p, b, num_groups, N, K)) != MXFP8_OK || (st = code_map(&m.q, a, total_rows, sum, kP8TileQ / 2)) != MXFP8_OK ||
+            (st = code_map(&m.q_part, a, total_rows, sum, 32)) != MXFP8_OK || (st = scale_map(&m.p_scale, b_scale, b_tile_rows, kc, 1)) != MXFP8_OK ||
+            (st = scale_map(&m.q_scale, a_scale, a_tile_rows, kc, 2)) != MXFP8_OK)
             return st;
+        m.out = m.q;
     }
-    const bool f32 = out_type == MXFP4_F32;
     switch (product) {
     case MXFP8_FORWARD:
         return f32 ? launch_pair<kForward, true>(p, m, tiles, device, stream) : launch_pair<kForward, false>(p, m, tiles, device, stream);
