@@ -145,6 +145,13 @@ __device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d, uint64_t a, uint64_
                  : "memory");
 }
 
+// Arrive on a barrier of either CTA.  What these arrivals order is not generic memory (accumulator reads that have
+// completed; zeros already handed to the async proxy), so the default scope does: with .release.cluster an arrival took
+// 1000 to 3000 cycles, and a wait with .acquire.cluster 360 where the phase was already complete.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t mapped)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int boxes = kQMn || half > 64 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
             const uint32_t code_bytes = kP8Codes + (kQMn ? kP8Codes : boxes ? boxes * 32 * 128 : kP8TileQ / 2 * 128);
             for (int k = 0; k < c.k_iters; ++k) {
-                ok = mbar_wait_cluster(empty0 + 8 * slot, phase ^ 1, kGemmWait);
+                ok = mbar_wait_cycles(empty0 + 8 * slot, phase ^ 1, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     slot = kP8Stages - 1;
                     phase ^= 1;
                 }
-                mbar_wait_cluster(full0 + 8 * slot, phase, kGemmDrain);
+                mbar_wait_cycles(full0 + 8 * slot, phase, kGemmDrain);
             }
         }
     } else if (kTails && warp == 2) {
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const Tile8 c = tile8<MODE>(t, p, groups);
             if (c.tail != 0) {
                 const int s = (slot + c.k_iters - 1) % kP8Stages;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(landed0 + 8 * s, (phases >> s) & 1, kGemmWait))) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cycles(landed0 + 8 * s, (phases >> s) & 1, kGemmWait))) {
                     if (lane == 0)
                         atomicOr(p.fault, 1u);
                     break;
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(lead_full + 8 * s);
+                    mbar_arrive_peer(lead_full + 8 * s);
             }
             slot = (slot + c.k_iters) % kP8Stages;
         }
@@ -332,14 +339,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int buf = n_tile & 1;
             const uint32_t d = tmem + buf * kP8TileQ;
             if (n_tile >= 2)
-                ok = mbar_wait_cluster(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWait);
+                ok = mbar_wait_cycles(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWait);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             for (int k = 0; k < c.k_iters; ++k) {
-                ok = mbar_wait_cluster(full0 + 8 * slot, phase, kGemmWait);
+                ok = mbar_wait_cycles(full0 + 8 * slot, phase, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_commit_pair(smem_u32(&drain));
             }
             __syncwarp();
-            mbar_wait_cluster(smem_u32(&drain), 0, kGemmDrain);
+            mbar_wait_cycles(smem_u32(&drain), 0, kGemmDrain);
         }
     } else if (kTails && warp >= 4) {
         // ---- epilogue of this CTA's 128 rows of an expert's gradient: a warp has 32 rows, a thread one ----
@@ -385,7 +392,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const Tile8 c = tile8<MODE>(t, p, groups);
             const int buf = n_tile & 1;
-            if (!epilogue_all(mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(lead_empty + 8 * buf);
+                mbar_arrive_peer(lead_empty + 8 * buf);
         }
         if (lane == 0)
             bulk_store_wait<0>();
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const Tile8 c = tile8<MODE>(t, p, groups);
             const int buf = n_tile & 1;
-            if (!epilogue_all(mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(lead_empty + 8 * buf);
+                mbar_arrive_peer(lead_empty + 8 * buf);
         }
     }
     tc_fence_before();
