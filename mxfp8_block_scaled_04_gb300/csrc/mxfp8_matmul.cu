@@ -110,8 +110,8 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
         return MXFP8_ERR_SHAPE;
     const bool wgrad = product == MXFP8_WEIGHT_GRADIENT;
     const int64_t P = product == MXFP8_INPUT_GRADIENT ? K : N, sum = wgrad ? total_rows : product == MXFP8_FORWARD ? K : N;
-    const int64_t p_tiles = ceil_div(P, kP8TileP), q_tiles = ceil_div(K, kP8TileQ);
-    const int64_t tiles = wgrad ? num_groups * p_tiles * q_tiles : (total_rows / kP8TileQ + num_groups) * p_tiles;
+    const int64_t p_tiles = ceil_div(P, kP8Tile), q_tiles = ceil_div(K, kP8Tile);
+    const int64_t tiles = wgrad ? num_groups * p_tiles * q_tiles : (total_rows / kP8Tile + num_groups) * p_tiles;
     // the weight gradient's tile rows of scales, all planes' together
     const int64_t linear = (total_rows / 128 + num_groups) * ceil_div(N > K ? N : K, 128);
     if (tiles >= kMaxDim - (int64_t{1} << 20) || (wgrad && linear >= kMaxDim))
@@ -180,7 +180,7 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
             return st;
         m.q_part = m.q;
     } else {
-        if ((st = weight_map(&m.p, b, num_groups, N, K)) != MXFP8_OK || (st = code_map(&m.q, a, total_rows, sum, kP8TileQ / 2)) != MXFP8_OK ||
+        if ((st = weight_map(&m.p, b, num_groups, N, K)) != MXFP8_OK || (st = code_map(&m.q, a, total_rows, sum, 128)) != MXFP8_OK ||
             (st = code_map(&m.q_part, a, total_rows, sum, 32)) != MXFP8_OK || (st = scale_map(&m.p_scale, b_scale, b_tile_rows, kc, 1)) != MXFP8_OK ||
             (st = scale_map(&m.q_scale, a_scale, a_tile_rows, kc, 2)) != MXFP8_OK)
             return st;

@@ -1,4 +1,4 @@
-// Experts' products in MXFP8 (sm_103a) by pairs of CTAs: out[q, p] = sum_k Q[q, k] * P[p, k] in tiles of 256 x 192.
+// Experts' products in MXFP8 (sm_103a) by pairs of CTAs: out[q, p] = sum_k Q[q, k] * P[p, k] in tiles of 256 x 256.
 //
 //   forward           Q = x's rows, P = W's rows           summed over K, both operands K-major
 //   input gradient    Q = dy's rows, P = W's columns       summed over N: P's codes lie [N, K], MN-major
@@ -9,10 +9,8 @@
 // of 32 summed elements is 32 of its rows.  No transposed copy exists.
 //
 // The loop is that of mxfp4_pair.cuh: 128 bytes of codes per operand row and stage, here 128 elements in four MMA steps
-// of 32 (kind::mxf8f6f4, one E8M0 scale per step and row).  192 columns rather than 256 let TMEM hold two whole
-// accumulators beside the scales, so that a tile's MMAs do not wait for the epilogue of the one before.  Every other tile's
-// first row of Q lies 64 rows into a scale tile: two 128-row scale tiles are copied, and the MMA's scale address starts
-// two columns later (32 rows are one TMEM column of scales).
+// of 32 (kind::mxf8f6f4, one E8M0 scale per step and row); the accumulators share 32 TMEM columns as there.  Tiles of 192
+// columns, whose two accumulators share nothing, were slower throughout (8192x8192x8192 312 -> 356 us): operand loads.
 //
 // A weight gradient's last stage may hold rows of the next expert.  Steps past the expert's last 32 rows are not issued;
 // where the rows are no multiple of 32 each CTA's warp 2 zeroes the rest of the last step in shared memory (its own
@@ -25,14 +23,14 @@ namespace mxfp8 {
 
 enum { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
-constexpr int kP8TileP = 256, kP8TileQ = 192;
+constexpr int kP8Tile = 256;
 constexpr int kP8Stages = 5;
 constexpr int kP8Codes = 128 * 128;           // bytes of either operand in one CTA and stage
 constexpr int kP8Stage = 2 * kP8Codes;
 constexpr int kP8Scales = 3 * 512;            // P's tile of this CTA, Q's two tiles
 constexpr int kP8Epi = (kP8Stages * (kP8Stage + kP8Scales) + 1023) / 1024 * 1024;  // the epilogue's buffers from here on
 constexpr int kP8Smem = kP8Epi + 1024;
-constexpr int kP8ScaleCol = 384;              // TMEM: accumulators at 0 and 192, scales from here (12 columns per stage)
+constexpr int kP8Acc1 = 224, kP8ScaleCol = 480;  // TMEM columns, as in mxfp4_pair.cuh
 
 // The epilogue's buffers: the weight gradient's warps have two of 32 rows x 128 bytes each.
 template <int MODE, bool F32>
@@ -52,7 +50,7 @@ struct Tile8 {
     int64_t p_tile, q_tile;    // scale tile rows; weight gradient: linear tiles
     int64_t out_row;           // of [total_rows, P]
     int valid, k_iters, steps, tail;  // rows of Q; stages; MMA steps in all; rows of the last step (0: whole)
-    int kt, shift;     // weight gradient: scale tiles along the rows; TMEM columns of scales before Q's first row
+    int kt;            // weight gradient: scale tiles along the rows
 };
 
 template <int MODE>
@@ -65,15 +63,14 @@ __device__ __forceinline__ Tile8 tile8(int t, const Product8Params &p, const Gro
         const int64_t rows = groups.offset[g + 1] - groups.offset[g];
         r.group = g;
         r.row = static_cast<int32_t>(groups.offset[g]);
-        r.p_at = pt * kP8TileP;
-        r.q_at = qt * kP8TileQ;
+        r.p_at = pt * kP8Tile;
+        r.q_at = qt * kP8Tile;
         r.kt = groups.plane[g + 1] - groups.plane[g];
         r.p_tile = static_cast<int64_t>(groups.plane[g]) * p.p_ct + static_cast<int64_t>(2 * pt) * r.kt;
         r.q_tile = static_cast<int64_t>(groups.plane[g]) * p.q_ct + static_cast<int64_t>(r.q_at / 128) * r.kt;
-        r.shift = r.q_at % 128 / 32;
         r.out_row = 0;
         const int64_t left = p.Q - r.q_at;
-        r.valid = left < kP8TileQ ? static_cast<int>(left) : kP8TileQ;
+        r.valid = left < kP8Tile ? static_cast<int>(left) : kP8Tile;
         r.k_iters = r.kt;
         r.steps = static_cast<int>((rows + 31) / 32);
         r.tail = static_cast<int>(rows & 31);
@@ -81,18 +78,17 @@ __device__ __forceinline__ Tile8 tile8(int t, const Product8Params &p, const Gro
         const int rt = t / p.p_tiles, pt = t - rt * p.p_tiles;
         const int g = groups.find(rt, p.num_groups);
         const int local = rt - groups.tile[g];
-        const int64_t q0 = groups.offset[g] + static_cast<int64_t>(local) * kP8TileQ;
+        const int64_t q0 = groups.offset[g] + static_cast<int64_t>(local) * kP8Tile;
         const int64_t left = groups.offset[g + 1] - q0;
         r.group = g;
         r.row = 0;
-        r.p_at = pt * kP8TileP;
+        r.p_at = pt * kP8Tile;
         r.q_at = static_cast<int32_t>(q0);
         r.kt = 0;
         r.p_tile = static_cast<int64_t>(g) * p.p_planes + 2 * pt;
-        r.q_tile = groups.plane[g] + static_cast<int64_t>(local) * kP8TileQ / 128;
-        r.shift = static_cast<int>(static_cast<int64_t>(local) * kP8TileQ % 128 / 32);
+        r.q_tile = groups.plane[g] + static_cast<int64_t>(local) * (kP8Tile / 128);
         r.out_row = q0;
-        r.valid = left < kP8TileQ ? static_cast<int>(left) : kP8TileQ;
+        r.valid = left < kP8Tile ? static_cast<int>(left) : kP8Tile;
         r.k_iters = p.k_iters;
         r.steps = static_cast<int>((p.sum + 31) / 32);
         r.tail = 0;
@@ -167,7 +163,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr bool kPMn = MODE != kForward, kQMn = MODE == kWeightGrad;
     extern __shared__ unsigned char gemm_smem[];
     __shared__ GroupTable<true> groups;
-    __shared__ uint64_t full[kP8Stages], empty[kP8Stages], landed[kP8Stages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[kP8Stages], empty[kP8Stages], landed[kP8Stages], acc_full[2], acc_empty, drain;
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -187,10 +183,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&acc_full[b]), 1);
-            mbar_init(smem_u32(&acc_empty[b]), 8);  // the epilogue warps of both CTAs
-        }
+        mbar_init(smem_u32(&acc_full[0]), 1);
+        mbar_init(smem_u32(&acc_full[1]), 1);
+        mbar_init(smem_u32(&acc_empty), 8);  // the epilogue warps of both CTAs
         mbar_init(smem_u32(&drain), 1);
         fence_mbar_init();
     }
@@ -203,7 +198,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = tmem_slot;
     pdl_wait_and_release();
 
-    int rt = group_setup<kGemmThreads, kP8TileQ>(groups, p.offsets, p.num_groups, MODE == kWeightGrad ? p.sum : p.Q);
+    int rt = group_setup<kGemmThreads, kP8Tile>(groups, p.offsets, p.num_groups, MODE == kWeightGrad ? p.sum : p.Q);
     const int64_t total = MODE == kWeightGrad ? p.sum : p.Q;
     if (rt >= 0) {  // offsets that need larger planes than there are
         const int64_t tiles = groups.plane[p.num_groups];
@@ -235,8 +230,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int n = 0, t; (t = tile_of(n)) < num_tiles && ok; ++n) {
             const Tile8 c = tile8<MODE>(t, p, groups);
             const int half = ((c.valid + 31) & ~31) / 2;
-            const int boxes = kQMn || half > 64 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
-            const uint32_t code_bytes = kP8Codes + (kQMn ? kP8Codes : boxes ? boxes * 32 * 128 : kP8TileQ / 2 * 128);
+            const int boxes = kQMn || half > kP8Tile / 2 - 32 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
+            const uint32_t code_bytes = kP8Codes + (kQMn ? kP8Codes : boxes ? boxes * 32 * 128 : kP8Tile / 2 * 128);
             for (int k = 0; k < c.k_iters; ++k) {
                 ok = mbar_wait_cycles(empty0 + 8 * slot, phase ^ 1, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -337,9 +332,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const Tile8 c = tile8<MODE>(t, p, groups);
             const int n = (c.valid + 31) & ~31;  // halves of whole 16-row groups
             const int buf = n_tile & 1;
-            const uint32_t d = tmem + buf * kP8TileQ;
-            if (n_tile >= 2)
-                ok = mbar_wait_cycles(smem_u32(&acc_empty[buf]), ((n_tile >> 1) - 1) & 1, kGemmWait);
+            const uint32_t d = tmem + buf * kP8Acc1;
+            if (n_tile >= 1)  // the columns shared with the tile before are read, and all of the one before that
+                ok = mbar_wait_cycles(smem_u32(&acc_empty), (n_tile - 1) & 1, kGemmWait);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
@@ -354,7 +349,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t pd = p_desc + slot * (kP8Stage >> 4), qd = q_desc + slot * (kP8Stage >> 4), sd = s_desc + slot * (kP8Scales >> 4);
-                    const uint32_t sp = tmem + kP8ScaleCol + (k & 3) * 16, sq = sp + 4;
+                    const uint32_t sp = tmem + kP8ScaleCol + (k & 1) * 12, sq = sp + 4;
                     const int left = c.steps - 4 * k;
                     tc_copy_scales_pair(sp, sd);
                     tc_copy_scales_pair(sq, sd + 512 / 16);
@@ -362,7 +357,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < left)
-                            tc_mma_mxf8_pair(d, pd + j * kPStep, qd + j * kQStep, mxf8_idesc(formats, kP8TileP, n, j), sp, sq + c.shift, k > 0 || j > 0);
+                            tc_mma_mxf8_pair(d, pd + j * kPStep, qd + j * kQStep, mxf8_idesc(formats, kP8Tile, n, j), sp, sq, k > 0 || j > 0);
                     tc_commit_pair(empty0 + 8 * slot);
                 }
                 __syncwarp();
@@ -386,7 +381,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // ---- epilogue of this CTA's 128 rows of an expert's gradient: a warp has 32 rows, a thread one ----
         constexpr int kCols = F32 ? 32 : 64;  // 128 bytes of a row
         const int quarter = warp & 3;
-        const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty[0]), 0);
+        const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
         unsigned char *rows = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Epi + quarter * 2 * 4096;
         int chunk = 0;
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
@@ -398,13 +393,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8TileQ;
+            const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8Acc1;
             const int row = c.p_at + static_cast<int>(rank) * 128 + quarter * 32;
-            for (int q = 0; q < c.valid && row < p.P; q += kCols) {
+            const int start = buf == 0 ? kP8Tile - kCols : 0;  // the columns that the accumulators share first
+            for (int i = 0; i < kP8Tile / kCols; ++i) {
+                const int q = (start + kCols * i) & (kP8Tile - 1);
+                const bool live = q < c.valid && row < p.P;
                 uint32_t v[kCols];
+                if (live) {
 #pragma unroll
-                for (int h = 0; h < kCols / 32; ++h)
-                    tmem_load32(d + q + 32 * h, *reinterpret_cast<uint32_t (*)[32]>(&v[32 * h]));
+                    for (int h = 0; h < kCols / 32; ++h)
+                        tmem_load32(d + q + 32 * h, *reinterpret_cast<uint32_t (*)[32]>(&v[32 * h]));
+                }
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_peer(lead_empty);
+                }
+                if (!live)
+                    continue;
                 if (lane == 0)
                     bulk_store_wait<1>();
                 __syncwarp();
@@ -428,10 +436,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (lane == 0)
                     tma_store_3d(&out_map, smem_u32(buffer), c.q_at + q, row, c.group);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_peer(lead_empty + 8 * buf);
         }
         if (lane == 0)
             bulk_store_wait<0>();
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= 4) {
         // ---- epilogue of this CTA's 128 columns of the output ----
         const int quarter = warp & 3;
-        const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty[0]), 0);
+        const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Epi;
         int chunk = 0;
         clear_rows_from<F32>(p, no_expert, quarter * 32 + lane);
@@ -452,17 +456,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8TileQ;
-            for (int q = 0; q < c.valid; q += 32) {
+            const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8Acc1;
+            const int start = buf == 0 ? kP8Acc1 : 0;  // the columns that the accumulators share first
+            for (int i = 0; i < kP8Tile / 32; ++i) {
+                const int q = (start + 32 * i) & (kP8Tile - 1);
                 uint32_t v[32];
-                tmem_load32(d + q, v);
-                store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.out_row + q, c.valid - q,
+                if (q < c.valid)
+                    tmem_load32(d + q, v);
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_peer(lead_empty);
+                }
+                if (q < c.valid)
+                    store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.out_row + q, c.valid - q,
                                  c.p_at + rank * 128);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_peer(lead_empty + 8 * buf);
         }
     }
     tc_fence_before();
