@@ -74,11 +74,11 @@ mxfp8_status_t launch_pair(const Product8Params &p, const Maps &m, int64_t tiles
     static KernelSetup setup;
     constexpr int smem = kP8Smem + kP8Epilogue<MODE, F32>;
     int ctas = 0;
-    const mxfp8_status_t st = setup(mxfp8_pair_kernel<MODE, F32>, device, kGemmThreads, smem, &ctas);
+    const mxfp8_status_t st = setup(mxfp8_pair_kernel<MODE, F32>, device, kP8Threads<MODE>, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
-    return launch_serialized(mxfp8_pair_kernel<MODE, F32>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, m.p, m.q, m.q_part,
+    return launch_serialized(mxfp8_pair_kernel<MODE, F32>, dim3(static_cast<unsigned>(2 * pairs)), kP8Threads<MODE>, smem, 2, stream, m.p, m.q, m.q_part,
                              m.p_scale, m.q_scale, m.out, p);
 }
 

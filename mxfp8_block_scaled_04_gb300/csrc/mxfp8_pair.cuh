@@ -32,9 +32,13 @@ constexpr int kP8Epi = (kP8Stages * (kP8Stage + kP8Scales) + 1023) / 1024 * 1024
 constexpr int kP8Smem = kP8Epi + 1024;
 constexpr int kP8Acc1 = 224, kP8ScaleCol = 480;  // TMEM columns, as in mxfp4_pair.cuh
 
-// The epilogue's buffers: the weight gradient's warps have two of 32 rows x 128 bytes each.
+// A weight gradient's tile has few stages and many bytes to write: eight epilogue warps, with a buffer of 32 rows x 128
+// bytes each (four warps with two each, 64 experts of 2048 x 7168, bf16 out: two rows each 352 against 527 us, 1024 rows
+// each 719 against 763).
+template <int MODE>
+constexpr int kP8Threads = MODE == kWeightGrad ? 384 : kGemmThreads;
 template <int MODE, bool F32>
-constexpr int kP8Epilogue = MODE == kWeightGrad ? 4 * 2 * 4096 : kEpiBytes<F32>;
+constexpr int kP8Epilogue = MODE == kWeightGrad ? 8 * 4096 : kEpiBytes<F32>;
 
 struct Product8Params : GemmParams {
     uint32_t formats;      // operand format bits of the instruction descriptor
@@ -154,7 +158,7 @@ __device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
 }
 
 template <int MODE, bool F32>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kP8Threads<MODE>, 1)
     mxfp8_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap q_part_map, const __grid_constant__ CUtensorMap ps_map,
                       const __grid_constant__ CUtensorMap qs_map, const __grid_constant__ CUtensorMap out_map, const Product8Params p)
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         mbar_init(smem_u32(&acc_full[0]), 1);
         mbar_init(smem_u32(&acc_full[1]), 1);
-        mbar_init(smem_u32(&acc_empty), 8);  // the epilogue warps of both CTAs
+        mbar_init(smem_u32(&acc_empty), kTails ? 16 : 8);  // the epilogue warps of both CTAs
         mbar_init(smem_u32(&drain), 1);
         fence_mbar_init();
     }
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = tmem_slot;
     pdl_wait_and_release();
 
-    int rt = group_setup<kGemmThreads, kP8Tile>(groups, p.offsets, p.num_groups, MODE == kWeightGrad ? p.sum : p.Q);
+    int rt = group_setup<kP8Threads<MODE>, kP8Tile>(groups, p.offsets, p.num_groups, MODE == kWeightGrad ? p.sum : p.Q);
     const int64_t total = MODE == kWeightGrad ? p.sum : p.Q;
     if (rt >= 0) {  // offsets that need larger planes than there are
         const int64_t tiles = groups.plane[p.num_groups];
@@ -380,14 +384,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (kTails && warp >= 4) {
         // ---- epilogue of this CTA's 128 rows of an expert's gradient: a warp has 32 rows, a thread one ----
         constexpr int kCols = F32 ? 32 : 64;  // 128 bytes of a row
-        const int quarter = warp & 3;
+        // (two warps to 32 rows, a chunk of 128 bytes of each in turn)
+        const int quarter = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
-        unsigned char *rows = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Epi + quarter * 2 * 4096;
-        int chunk = 0;
+        unsigned char *buffer = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Epi + (warp - 4) * 4096;
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const Tile8 c = tile8<MODE>(t, p, groups);
             const int buf = n_tile & 1;
-            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
@@ -396,7 +400,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8Acc1;
             const int row = c.p_at + static_cast<int>(rank) * 128 + quarter * 32;
             const int start = buf == 0 ? kP8Tile - kCols : 0;  // the columns that the accumulators share first
-            for (int i = 0; i < kP8Tile / kCols; ++i) {
+            if (part == 1 && lane == 0)  // its share of the tile before is read, and none of this tile's is in the shared columns
+                mbar_arrive_peer(lead_empty);
+            for (int i = part; i < kP8Tile / kCols; i += 2) {
                 const int q = (start + kCols * i) & (kP8Tile - 1);
                 const bool live = q < c.valid && row < p.P;
                 uint32_t v[kCols];
@@ -414,9 +420,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (!live)
                     continue;
                 if (lane == 0)
-                    bulk_store_wait<1>();
+                    bulk_store_wait<0>();
                 __syncwarp();
-                unsigned char *buffer = rows + (chunk++ & 1) * 4096;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {  // 16 bytes each, in the store's 128-byte swizzle
                     uint4 w;
