@@ -122,6 +122,39 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
                                     const int64_t *offsets, const void *b_codes, const void *b_scale, int64_t N,
                                     int64_t K, void *out, int out_type, int *err_flag, void *stream);
 
+/*
+ * Products of rows that are not cast with 4-bit weights (serving: weights in 4 bits, tokens as they are):
+ * out [M, N] = x [M, K] * B [N, K]^T, sums in fp32, rounded once to out_type.  x enters as a sum of eight 4-bit rows per row,
+ * which differs from x, per block of 32, by at most 2^-22 of the block's largest magnitude (or 2^-126), so that the
+ * result is that of the unquantized rows to fp32 accuracy.  A NaN or an infinity in a row of x makes that output row NaN.
+ *
+ *   x            device, x_type, 16-byte aligned; K and ldx multiples of 8, ldx >= K; M < 2^28.
+ *   b_codes, b_scale, out, out_type, ldo   as for mxfp4_matmul.  (A block of B with scale 255 makes its output column NaN.)
+ *   workspace    device, mxfp4_linear_workspace_bytes(M, K) bytes, 16-byte aligned; not shared by calls that may overlap.
+ *
+ * Meant for few rows (the weights' bytes are the time up to about 16; every row costs eight of the tensor cores' columns):
+ * for many, cast x and call mxfp4_matmul.
+ */
+size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
+
+mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int64_t ldx, const void *b_codes,
+                            const void *b_scale, int64_t N, void *out, int out_type, int64_t ldo, void *workspace,
+                            void *stream);
+
+/*
+ * The same for experts: row i of out [total_rows, N] is x row rows[i] (row i when rows is NULL, then total_rows <= T) times
+ * B_g^T of the expert g whose rows [offsets[g], offsets[g+1]) it is in.  rows, offsets and err_flag as for
+ * mxfp4_quantize_grouped (an index outside x: a row of NaN; rows past the last offset: zeros, and *err_flag is set where
+ * `rows` does not mark them with a negative index; bad offsets: nothing is written).  b_codes, b_scale as for
+ * mxfp4_matmul_grouped.  workspace: mxfp4_linear_grouped_workspace_bytes(total_rows, K, num_groups) bytes.
+ */
+size_t mxfp4_linear_grouped_workspace_bytes(int64_t total_rows, int64_t K, int num_groups);
+
+mxfp8_status_t mxfp4_linear_grouped(const void *x, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t *rows,
+                                    int64_t total_rows, int num_groups, const int64_t *offsets, const void *b_codes,
+                                    const void *b_scale, int64_t N, void *out, int out_type, int *err_flag,
+                                    void *workspace, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,8 @@ from .mxfp4 import (  # noqa: F401
     MXFP4Matrix, MXFP4Tensor, dequantize_mxfp4, matmul_mxfp4, matmul_mxfp4_grouped, mxfp4_dequantize,
     mxfp4_grouped_scale_bytes, mxfp4_matmul, mxfp4_matmul_grouped, mxfp4_quantize, mxfp4_quantize_grouped,
     mxfp4_quantize_grouped_workspace_bytes,    mxfp4_row_bytes, mxfp4_scale_bytes, quantize_mxfp4, quantize_mxfp4_grouped,
+    linear_mxfp4, linear_mxfp4_grouped, mxfp4_linear, mxfp4_linear_grouped, mxfp4_linear_grouped_workspace_bytes,
+    mxfp4_linear_workspace_bytes,
 )
 from .moe import (  # noqa: F401
     MoEPlan, MoERoute, RouteConfig, make_route_config, moe_combine, moe_combine_backward, moe_combine_backward_c,

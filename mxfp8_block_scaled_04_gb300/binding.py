@@ -98,6 +98,11 @@ def lib():
                     ("mxfp4_dequantize", i32, [vp, vp, i64, i64, vp, i32, vp]),
                     ("mxfp4_matmul", i32, [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]),
                     ("mxfp4_matmul_grouped", i32, [vp, vp, i64, i32, vp, vp, vp, i64, i64, vp, i32, vp, vp]),
+                    ("mxfp4_linear_workspace_bytes", sz, [i64, i64]),
+                    ("mxfp4_linear", i32, [vp, i32, i64, i64, i64, vp, vp, i64, vp, i32, i64, vp, vp]),
+                    ("mxfp4_linear_grouped_workspace_bytes", sz, [i64, i64, i32]),
+                    ("mxfp4_linear_grouped", i32,
+                     [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, i64, vp, i32, vp, vp, vp]),
                     ("mxfp8_matmul_grouped", i32,
                      [i32, vp, vp, sz, i32, vp, vp, sz, i32, i64, i64, i64, i32, vp, vp, i32, vp, vp]),
                     ("moe_route", i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp]),

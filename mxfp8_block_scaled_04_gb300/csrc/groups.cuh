@@ -31,16 +31,27 @@ struct GroupTable {
 template <>
 struct GroupTable<false> {};
 
+// An offset in rows of the operand; one that is out of range (and would overflow) stays out of range.
+template <int TIMES>
+__device__ __forceinline__ int64_t scaled_offset(int64_t offset, int64_t total)
+{
+    if constexpr (TIMES == 1)
+        return offset;
+    else
+        return offset < 0 ? -1 : offset > total ? total + 1 : offset * TIMES;
+}
+
 // Load and check the offsets (from 0, non-decreasing, none past total; rows past the last one belong to no group); all
 // threads of the CTA.  Returns the number of row tiles of ROWS rows over all groups, or -1 for bad offsets.  Both
-// prefixes come from one scan of a packed count (the low half stays below 2^32: at most total / 128 + groups).
-template <int THREADS, int ROWS>
+// prefixes come from one scan of a packed count (the low half stays below 2^32: at most total / 128 + groups).  Offsets and
+// total count rows of the operand, TIMES of which stand for one row that the caller counts.
+template <int THREADS, int ROWS, int TIMES = 1>
 __device__ __forceinline__ int group_setup(GroupTable<true> &g, const int64_t *offsets, int num_groups, int64_t total)
 {
     constexpr int kItems = (kGroupMax + THREADS - 1) / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i <= num_groups; i += THREADS)
-        g.offset[i] = offsets[i];
+        g.offset[i] = scaled_offset<TIMES>(offsets[i], total);
     __syncthreads();
     int bad = tid == 0 && (g.offset[0] != 0 || g.offset[num_groups] > total);
     for (int i = tid; i < num_groups; i += THREADS)

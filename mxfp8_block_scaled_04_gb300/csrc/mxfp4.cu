@@ -9,6 +9,7 @@
 #include "mxfp4_cast.cuh"
 #include "mxfp4_gemm.cuh"
 #include "mxfp4_pair.cuh"
+#include "mxfp4_parts.cuh"
 #include "mxfp4_split.cuh"
 
 namespace {
@@ -75,17 +76,17 @@ mxfp8_status_t code_map(CUtensorMap *map, const void *codes, int64_t rows, int64
                : MXFP8_ERR_LAUNCH;
 }
 
-template <bool F32>
+template <bool F32, int PARTS>
 mxfp8_status_t launch_group_as(const CUtensorMap &pm, const CUtensorMap &qm, const GemmParams &p, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
     constexpr int smem = kGroupSmem + kEpiBytes<F32>;
     int ctas = 0;
-    const mxfp8_status_t st = setup(mxfp4_group_kernel<F32>, device, kGemmThreads, smem, &ctas);
+    const mxfp8_status_t st = setup(mxfp4_group_kernel<F32, PARTS>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
     const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
-    return launch_serialized(mxfp4_group_kernel<F32>, dim3(grid), kGemmThreads, smem, 1, stream, pm, qm, p);
+    return launch_serialized(mxfp4_group_kernel<F32, PARTS>, dim3(grid), kGemmThreads, smem, 1, stream, pm, qm, p);
 }
 
 // The scale plane as rows of 512-byte tiles, in boxes of 1024 bytes (one stage) x box_rows tile rows.
@@ -105,14 +106,14 @@ mxfp8_status_t scale_map(CUtensorMap *map, const void *scale, int64_t tile_rows,
 }
 
 // The pair kernel.  p_rows: rows of P's map (all experts); plane rows likewise.
-template <bool F32, bool GROUPED>
+template <bool F32, bool GROUPED, int PARTS>
 mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t p_rows, int64_t p_plane_rows, const void *q_codes,
                               int64_t q_plane_rows, int64_t row_bytes, int64_t tiles, int device, cudaStream_t stream)
 {
     static KernelSetup setup;
     constexpr int smem = kPairSmem + kEpiBytes<F32>;
     int ctas = 0;
-    mxfp8_status_t st = setup(mxfp4_pair_kernel<F32, GROUPED>, device, kGemmThreads, smem, &ctas);
+    mxfp8_status_t st = setup(mxfp4_pair_kernel<F32, GROUPED, PARTS>, device, kGemmThreads, smem, &ctas);
     if (st != MXFP8_OK)
         return st;
     CUtensorMap pm, qm, qpm, psm, qsm;
@@ -120,7 +121,7 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
         (st = code_map(&qpm, q_codes, p.Q, row_bytes, 32)) != MXFP8_OK || (st = scale_map(&psm, p.p_scale, p_plane_rows, p.kc, 1)) != MXFP8_OK || (st = scale_map(&qsm, p.q_scale, q_plane_rows, p.kc, 2)) != MXFP8_OK)
         return st;
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
-    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, pm, qm, qpm,
+    return launch_serialized(mxfp4_pair_kernel<F32, GROUPED, PARTS>, dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2, stream, pm, qm, qpm,
                              psm, qsm, p);
 }
 
@@ -128,7 +129,7 @@ mxfp8_status_t launch_pair_as(const GemmParams &p, const void *p_codes, int64_t 
 // per SM where the weights' bytes are the time (64 rows or fewer), one per SM above.  Measured (us, S = 1 / 2 / 4 / 8,
 // rows x N x K): 1x4096x4096 13.0 / 12.9 / 12.9 / 10.9, 16x8192x28672 50 / 40 / 33 / 40, 100x512x16384 31 / 23 / 17 / 15;
 // where they are not all resident S = 1 is fastest (1x28672x8192 33 / 38 / 42 / 52, 333x4096x4096 15 / 17 / 23 / 33).
-template <int QROWS, int STAGES, bool F32>
+template <int QROWS, int STAGES, bool F32, int PARTS>
 mxfp8_status_t launch_split_as(const GemmParams &p, const CUtensorMap &pm, const CUtensorMap &qm, int64_t tiles, int splits, int device,
                                cudaStream_t stream)
 {
@@ -137,14 +138,14 @@ mxfp8_status_t launch_split_as(const GemmParams &p, const CUtensorMap &pm, const
     static_assert(Shape::kStage * STAGES >= QROWS * kGemmRows * 4 && Shape::kStage * STAGES >= kEpiBytes<F32>,
                   "partial sums and the epilogue's buffers fit the stages");
     int ctas = 0;
-    const mxfp8_status_t st = setup(mxfp4_split_kernel<QROWS, STAGES, F32>, device, kGemmThreads, Shape::kSmem, &ctas);
+    const mxfp8_status_t st = setup(mxfp4_split_kernel<QROWS, STAGES, F32, PARTS>, device, kGemmThreads, Shape::kSmem, &ctas);
     if (st != MXFP8_OK)
         return st;
-    return launch_serialized(mxfp4_split_kernel<QROWS, STAGES, F32>, dim3(static_cast<unsigned>(tiles * splits)), kGemmThreads, Shape::kSmem, splits,
+    return launch_serialized(mxfp4_split_kernel<QROWS, STAGES, F32, PARTS>, dim3(static_cast<unsigned>(tiles * splits)), kGemmThreads, Shape::kSmem, splits,
                              stream, pm, qm, p, splits);
 }
 
-template <bool F32>
+template <bool F32, int PARTS>
 mxfp8_status_t launch_split(const GemmParams &p_, const void *p_codes, const void *q_codes, int64_t row_bytes, int device, cudaStream_t stream)
 {
     GemmParams p = p_;
@@ -163,11 +164,11 @@ mxfp8_status_t launch_split(const GemmParams &p_, const void *p_codes, const voi
     while (splits < 8 && tiles * splits * 2 <= room && splits * 2 <= p.k_iters)
         splits *= 2;
     if (p.Q <= 32)
-        return launch_split_as<32, 4, F32>(p, pm, qm, tiles, splits, device, stream);
+        return launch_split_as<32, 4, F32, PARTS>(p, pm, qm, tiles, splits, device, stream);
     // one CTA per SM is all there is: more stages in its shared memory
     if (tiles * splits <= sms)
-        return launch_split_as<128, 5, F32>(p, pm, qm, tiles, splits, device, stream);
-    return launch_split_as<128, 3, F32>(p, pm, qm, tiles, splits, device, stream);
+        return launch_split_as<128, 5, F32, PARTS>(p, pm, qm, tiles, splits, device, stream);
+    return launch_split_as<128, 3, F32, PARTS>(p, pm, qm, tiles, splits, device, stream);
 }
 
 // Checks and parameters that both products share.  Q: the tokens' rows; P: the weights' rows (per expert).
@@ -214,6 +215,85 @@ mxfp8_status_t zero_rows(void *out, int64_t rows, int64_t cols, int64_t ld, int 
         cudaGetLastError();
         return MXFP8_ERR_LAUNCH;
     }
+    return MXFP8_OK;
+}
+
+// The dense product of Q = PARTS * M rows of A codes (checked parameters in p, addresses of the device).
+template <int PARTS>
+mxfp8_status_t launch_dense(GemmParams &p, const void *q_codes, const void *p_codes, int64_t K, int out_type, int device, cudaStream_t stream)
+{
+    const int64_t row_bytes = ceil_div(K, 32) * 16;
+    const int64_t pair_tiles = ceil_div(p.P, kPairRows) * ceil_div(p.Q, kPairRows);
+    const bool f32 = out_type == MXFP4_F32;
+    if (p.Q > 128 && pair_tiles >= kPairMinTiles) {
+        p.p_tiles = static_cast<int>(ceil_div(p.P, kPairRows));
+        p.q_tiles = static_cast<int>(ceil_div(p.Q, kPairRows));
+        return f32 ? launch_pair_as<true, false, PARTS>(p, p_codes, p.P, p.p_planes, q_codes, ceil_div(p.Q, 128), row_bytes, pair_tiles, device, stream)
+                   : launch_pair_as<false, false, PARTS>(p, p_codes, p.P, p.p_planes, q_codes, ceil_div(p.Q, 128), row_bytes, pair_tiles, device, stream);
+    }
+    return f32 ? launch_split<true, PARTS>(p, p_codes, q_codes, row_bytes, device, stream)
+               : launch_split<false, PARTS>(p, p_codes, q_codes, row_bytes, device, stream);
+}
+
+// The experts' products, likewise; p.Q rows of the operand over all experts.
+template <int PARTS>
+mxfp8_status_t launch_experts(GemmParams &p, const void *q_codes, const void *p_codes, int64_t K, int out_type, int device, cudaStream_t stream)
+{
+    const int64_t row_bytes = ceil_div(K, 32) * 16, groups = p.num_groups;
+    const bool f32 = out_type == MXFP4_F32;
+    if (p.Q >= kPairMinGroupRows * groups && p.Q / kPairRows * ceil_div(p.P, kPairRows) >= kPairMinTiles) {
+        const int64_t q_planes = static_cast<int64_t>(mxfp4_grouped_scale_bytes(p.Q, K, p.num_groups) / 512) / p.kc;
+        p.p_tiles = static_cast<int>(ceil_div(p.P, kPairRows));
+        const int64_t pair_bound = (p.Q / kPairRows + groups) * p.p_tiles;
+        return f32 ? launch_pair_as<true, true, PARTS>(p, p_codes, groups * p.P, groups * p.p_planes, q_codes, q_planes, row_bytes, pair_bound, device, stream)
+                   : launch_pair_as<false, true, PARTS>(p, p_codes, groups * p.P, groups * p.p_planes, q_codes, q_planes, row_bytes, pair_bound, device, stream);
+    }
+    CUtensorMap pm, qm;
+    p.q_box = 32;
+    mxfp8_status_t st;
+    if ((st = code_map(&pm, p_codes, groups * p.P, row_bytes, kGemmRows)) != MXFP8_OK || (st = code_map(&qm, q_codes, p.Q, row_bytes, p.q_box)) != MXFP8_OK)
+        return st;
+    const int64_t bound = (p.Q / 128 + groups) * static_cast<int64_t>(p.p_tiles);
+    return f32 ? launch_group_as<true, PARTS>(pm, qm, p, bound, device, stream) : launch_group_as<false, PARTS>(pm, qm, p, bound, device, stream);
+}
+
+template <bool GROUPED>
+mxfp8_status_t launch_parts(const PartsParams &p, int x_type, int64_t units, int device, cudaStream_t stream)
+{
+    static KernelSetup f32, bf16;
+    int ctas = 0;
+    const bool is32 = x_type == MXFP4_F32;
+    const mxfp8_status_t st = is32 ? f32(mxfp4_parts_kernel<true, GROUPED>, device, kPartsThreads, 0, &ctas)
+                                   : bf16(mxfp4_parts_kernel<false, GROUPED>, device, kPartsThreads, 0, &ctas);
+    if (st != MXFP8_OK)
+        return st;
+    const dim3 grid(static_cast<unsigned>(units < ctas ? units : ctas));
+    return is32 ? launch_serialized(mxfp4_parts_kernel<true, GROUPED>, grid, kPartsThreads, 0, 1, stream, p)
+                : launch_serialized(mxfp4_parts_kernel<false, GROUPED>, grid, kPartsThreads, 0, 1, stream, p);
+}
+
+// Checks of x, and the operand's place in the workspace: codes, then (16-byte aligned) the planes.
+mxfp8_status_t parts_params(PartsParams *q, const void *x, int x_type, int64_t T, int64_t R, int64_t K, int64_t ldx, void *workspace)
+{
+    if (!type_ok(x_type))
+        return MXFP8_ERR_FORMAT;
+    if (T < 0 || R < 0 || K < 0 || K % 8 || ldx % 8 || ldx < K || T >= kMaxDim || R >= kMaxDim / kParts || K >= kMaxDim || ldx >= kMaxDim)
+        return MXFP8_ERR_SHAPE;
+    if (T > 0 && K > 0 && R > 0 && x == nullptr)
+        return MXFP8_ERR_NULL;
+    if (!is_aligned(x, 16) || !is_aligned(workspace, 16))
+        return MXFP8_ERR_ALIGN;
+    *q = PartsParams{};
+    q->x = x;
+    q->T = T;
+    q->R = R;
+    q->K = K;
+    q->ldx = ldx;
+    q->pitch = ceil_div(K, 32) * 16;
+    q->out = static_cast<uint8_t *>(workspace);
+    q->scale = q->out + R * kParts * q->pitch;
+    q->col_tiles = static_cast<int>(ceil_div(K, 128));
+    q->chunks = static_cast<int>(ceil_div(K, kPartsCols));
     return MXFP8_OK;
 }
 
@@ -430,17 +510,7 @@ mxfp8_status_t mxfp4_matmul(const void *a_codes, const void *a_scale, int64_t M,
         return zero_rows(out, M, N, ldo, out_type, stream);
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
-    const int64_t row_bytes = ceil_div(K, 32) * 16;
-    const int64_t pair_tiles = ceil_div(N, kPairRows) * ceil_div(M, kPairRows);
-    if (M > 128 && pair_tiles >= kPairMinTiles) {
-        p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
-        p.q_tiles = static_cast<int>(ceil_div(M, kPairRows));
-        return out_type == MXFP4_F32
-                   ? launch_pair_as<true, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream)
-                   : launch_pair_as<false, false>(p, b_codes, N, p.p_planes, a_codes, ceil_div(M, 128), row_bytes, pair_tiles, device, stream);
-    }
-    return out_type == MXFP4_F32 ? launch_split<true>(p, b_codes, a_codes, row_bytes, device, stream)
-                                 : launch_split<false>(p, b_codes, a_codes, row_bytes, device, stream);
+    return launch_dense<1>(p, a_codes, b_codes, K, out_type, device, stream);
 }
 
 mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, int64_t total_rows, int num_groups, const int64_t *offsets,
@@ -475,23 +545,96 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
     p.offsets = offsets;
     p.num_groups = num_groups;
     p.err_flag = err_flag;
-    const int64_t row_bytes = ceil_div(K, 32) * 16;
-    if (total_rows >= kPairMinGroupRows * num_groups && total_rows / kPairRows * ceil_div(N, kPairRows) >= kPairMinTiles) {
-        const int64_t q_planes = static_cast<int64_t>(mxfp4_grouped_scale_bytes(total_rows, K, num_groups) / 512) / p.kc;
-        p.p_tiles = static_cast<int>(ceil_div(N, kPairRows));
-        const int64_t pair_bound = (total_rows / kPairRows + num_groups) * p.p_tiles;
-        return out_type == MXFP4_F32 ? launch_pair_as<true, true>(p, b_codes, num_groups * N, int64_t{num_groups} * p.p_planes, a_codes, q_planes,
-                                                                  row_bytes, pair_bound, device, stream)
-                                     : launch_pair_as<false, true>(p, b_codes, num_groups * N, int64_t{num_groups} * p.p_planes, a_codes, q_planes,
-                                                                   row_bytes, pair_bound, device, stream);
-    }
-    CUtensorMap pm, qm;
-    p.q_box = 32;
-    if ((st = code_map(&pm, b_codes, num_groups * N, row_bytes, kGemmRows)) != MXFP8_OK ||
-        (st = code_map(&qm, a_codes, total_rows, row_bytes, p.q_box)) != MXFP8_OK)
+    return launch_experts<1>(p, a_codes, b_codes, K, out_type, device, stream);
+}
+
+size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K)
+{
+    if (M <= 0 || K <= 0 || M >= kMaxDim / kParts)
+        return 0;
+    return static_cast<size_t>(M) * kParts * mxfp4_row_bytes(K) + mxfp4_scale_bytes(M * kParts, K);
+}
+
+mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int64_t ldx, const void *b_codes, const void *b_scale, int64_t N, void *out,
+                            int out_type, int64_t ldo, void *workspace, void *stream_)
+{
+    PartsParams q;
+    mxfp8_status_t st = parts_params(&q, x, x_type, M, M, K, ldx, workspace);
+    if (st != MXFP8_OK)
         return st;
-    return out_type == MXFP4_F32 ? launch_group_as<true>(pm, qm, p, bound, device, stream)
-                                 : launch_group_as<false>(pm, qm, p, bound, device, stream);
+    GemmParams p;
+    if (M > 0 && N > 0 && K > 0 && workspace == nullptr)
+        return MXFP8_ERR_WORKSPACE;
+    if ((st = gemm_params(&p, q.out, q.scale, M * kParts, b_codes, b_scale, N, K, out, out_type, ldo)) != MXFP8_OK)
+        return st;
+    int device = 0;
+    if ((st = active_device(&device)) != MXFP8_OK)
+        return st;
+    for (const void *ptr : {x, b_codes, b_scale, static_cast<const void *>(out), static_cast<const void *>(workspace)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (M == 0 || N == 0)
+        return MXFP8_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (K == 0)
+        return zero_rows(out, M, N, ldo, out_type, stream);
+    if ((p.fault = fault_word_address(device)) == nullptr)
+        return MXFP8_ERR_DEVICE;
+    if ((st = launch_parts<false>(q, x_type, M * q.chunks, device, stream)) != MXFP8_OK)
+        return st;
+    return launch_dense<kParts>(p, q.out, b_codes, K, out_type, device, stream);
+}
+
+size_t mxfp4_linear_grouped_workspace_bytes(int64_t total_rows, int64_t K, int num_groups)
+{
+    if (total_rows <= 0 || K <= 0 || num_groups < 1 || total_rows >= kMaxDim / kParts)
+        return 0;
+    return static_cast<size_t>(total_rows) * kParts * mxfp4_row_bytes(K) + mxfp4_grouped_scale_bytes(total_rows * kParts, K, num_groups);
+}
+
+mxfp8_status_t mxfp4_linear_grouped(const void *x, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t *rows, int64_t total_rows,
+                                    int num_groups, const int64_t *offsets, const void *b_codes, const void *b_scale, int64_t N, void *out,
+                                    int out_type, int *err_flag, void *workspace, void *stream_)
+{
+    PartsParams q;
+    mxfp8_status_t st = parts_params(&q, x, x_type, T, total_rows, K, ldx, workspace);
+    if (st != MXFP8_OK)
+        return st;
+    if (rows == nullptr && total_rows > T)
+        return MXFP8_ERR_SHAPE;
+    if (num_groups < 1 || num_groups > MXFP8_MAX_GROUPS || offsets == nullptr)
+        return MXFP8_ERR_GROUPS;
+    if (total_rows > 0 && N > 0 && K > 0 && workspace == nullptr)
+        return MXFP8_ERR_WORKSPACE;
+    GemmParams p;
+    if ((st = gemm_params(&p, q.out, q.scale, total_rows * kParts, b_codes, b_scale, N, K, out, out_type, N)) != MXFP8_OK)
+        return st;
+    const int64_t bound = (total_rows * kParts / 128 + num_groups) * static_cast<int64_t>(p.p_tiles);
+    if (bound >= kMaxDim - (int64_t{1} << 20) || num_groups * N >= kMaxDim)
+        return MXFP8_ERR_SHAPE;
+    if (!is_aligned(rows, 4) || !is_aligned(offsets, 8) || !is_aligned(err_flag, 4))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    if ((st = active_device(&device)) != MXFP8_OK)
+        return st;
+    for (const void *ptr : {x, static_cast<const void *>(rows), b_codes, b_scale, static_cast<const void *>(out), static_cast<const void *>(offsets),
+                            static_cast<const void *>(err_flag), static_cast<const void *>(workspace)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (total_rows == 0 || N == 0)
+        return MXFP8_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (K == 0)
+        return zero_rows(out, total_rows, N, N, out_type, stream);
+    if ((p.fault = fault_word_address(device)) == nullptr)
+        return MXFP8_ERR_DEVICE;
+    q.rows = rows;
+    q.offsets = p.offsets = offsets;
+    q.num_groups = p.num_groups = num_groups;
+    q.err_flag = err_flag;  // the products have nothing to add to what the parts' kernel reports
+    if ((st = launch_parts<true>(q, x_type, total_rows * q.chunks, device, stream)) != MXFP8_OK)
+        return st;
+    return launch_experts<kParts>(p, q.out, b_codes, K, out_type, device, stream);
 }
 
 }  // extern "C"

@@ -176,12 +176,29 @@ __device__ __forceinline__ void store_chunk(const GemmParams &p, const uint32_t 
     }
 }
 
+// The same where PARTS consecutive rows are parts of one: their sums, the smallest (the last) first.  A warp writes 32
+// neighbouring columns of each of the 32 / PARTS rows.
+template <bool F32, int PARTS>
+__device__ __forceinline__ void store_parts(const GemmParams &p, const uint32_t (&v)[32], int quarter, int lane, int64_t row0, int rows, int64_t col0)
+{
+    const int64_t col = col0 + quarter * 32 + lane;
+#pragma unroll
+    for (int t = 0; t < 32 / PARTS; ++t) {
+        float sum = __uint_as_float(v[PARTS * t + PARTS - 1]);
+#pragma unroll
+        for (int j = PARTS - 2; j >= 0; --j)
+            sum += __uint_as_float(v[PARTS * t + j]);
+        if (col < p.P && PARTS * t < rows)
+            store_out<F32>(p.out, (row0 / PARTS + t) * p.ldo + col, __float_as_uint(sum));
+    }
+}
+
 // The 128 epilogue threads of every CTA: zeros to the output's rows from `begin` on, which belong to no expert (ldo = P).
-template <bool F32>
+template <bool F32, int PARTS = 1>
 __device__ __forceinline__ void clear_rows_from(const GemmParams &p, int64_t begin, int thread)
 {
     constexpr int kVec = F32 ? 4 : 8;
-    const int64_t first = begin * p.P, last = p.Q * p.P;
+    const int64_t first = begin / PARTS * p.P, last = p.Q / PARTS * p.P;
     const int64_t at = blockIdx.x * int64_t{128} + thread, step = gridDim.x * int64_t{128};
     if (p.vec_out) {
         for (int64_t i = first / kVec + at; i < last / kVec; i += step)
@@ -192,7 +209,8 @@ __device__ __forceinline__ void clear_rows_from(const GemmParams &p, int64_t beg
     }
 }
 
-template <bool F32>
+// PARTS: consecutive rows of Q that are parts of one row of the output (mxfp4_parts.cuh); offsets then count output rows.
+template <bool F32, int PARTS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     mxfp4_group_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p)
 {
@@ -226,7 +244,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = tmem_slot;
     pdl_wait_and_release();
 
-    const int row_tiles = group_setup<kGemmThreads, kGemmRows>(groups, p.offsets, p.num_groups, p.Q);
+    const int row_tiles = group_setup<kGemmThreads, kGemmRows, PARTS>(groups, p.offsets, p.num_groups, p.Q);
     const int num_tiles = row_tiles < 0 ? 0 : row_tiles * p.p_tiles;
     if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr && (row_tiles < 0 || groups.offset[p.num_groups] < p.Q))
         atomicOr(p.err_flag, 1);
@@ -353,7 +371,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kGroupStages * kGroupStage;
         int n_tile = 0, chunk = 0;
         if (row_tiles >= 0)
-            clear_rows_from<F32>(p, groups.offset[p.num_groups], quarter * 32 + lane);
+            clear_rows_from<F32, PARTS>(p, groups.offset[p.num_groups], quarter * 32 + lane);
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++n_tile) {
             const GemmTile c = gemm_tile<kGemmRows, kGemmRows, true>(t, p, groups);
             const int buf = n_tile & 1;
@@ -366,7 +384,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int q = 0; q < c.valid; q += 32) {
                 uint32_t v[32];
                 tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kGemmRows + q, v);
-                store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q, c.p0);
+                if constexpr (PARTS > 1)
+                    store_parts<F32, PARTS>(p, v, quarter, lane, c.q_row + q, c.valid - q, c.p0);
+                else
+                    store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q, c.p0);
             }
             tc_fence_before();
             __syncwarp();

@@ -25,7 +25,7 @@ constexpr int kPairStage = 2 * kPairCodes + kPairPScale + kPairQScale;
 constexpr int kPairSmem = kPairStages * kPairStage + 1024;  // + the epilogue's buffers
 constexpr int kPairAcc1 = 224, kPairShared = 32, kPairScaleCol = 480;
 
-template <bool F32, bool GROUPED>
+template <bool F32, bool GROUPED, int PARTS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap q_part_map, const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map, const GemmParams p)
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int num_tiles = p.p_tiles * p.q_tiles;
     int64_t no_expert = p.Q;  // the first row of no expert
     if constexpr (GROUPED) {
-        const int rt = group_setup<kGemmThreads, kPairRows>(groups, p.offsets, p.num_groups, p.Q);
+        const int rt = group_setup<kGemmThreads, kPairRows, PARTS>(groups, p.offsets, p.num_groups, p.Q);
         num_tiles = rt < 0 ? 0 : rt * p.p_tiles;
         if (rt >= 0)
             no_expert = groups.offset[p.num_groups];
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kPairStages * kPairStage;
         int chunk = 0;
         if constexpr (GROUPED)
-            clear_rows_from<F32>(p, no_expert, quarter * 32 + lane);
+            clear_rows_from<F32, PARTS>(p, no_expert, quarter * 32 + lane);
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
@@ -223,9 +223,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (lane == 0)
                         mbar_arrive_cluster(lead_empty);
                 }
-                if (q < c.valid)
-                    store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q,
-                                     c.p0 + rank * 128);
+                if (q < c.valid) {
+                    if constexpr (PARTS > 1)
+                        store_parts<F32, PARTS>(p, v, quarter, lane, c.q_row + q, c.valid - q, c.p0 + rank * 128);
+                    else
+                        store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.q_row + q, c.valid - q,
+                                         c.p0 + rank * 128);
+                }
             }
         }
     }

@@ -1,0 +1,145 @@
+// Rows that are not cast, as exact operands of the MXFP4 products: x = sum of kParts 4-bit rows.
+//
+// Per block of 32, with e the exponent of the MXFP4 cast (6 * 2^e >= amax > 3 * 2^e): part 0 is the cast's q0 at 2^e and
+// leaves |r| <= 2^e; part j is the cast of what is left at 2^(e + 1 - 3j), where it is at most 4 and leaves at most half a
+// unit.  Every remainder is exact in fp32, so after kParts = 8 parts x differs from their sum by at most 2^(e - 21) < amax *
+// 2^-22 (by 2^-126 at most where e + 1 - 3j passes E8M0's least exponent, -127: those parts are zero).  The parts are rows 8i to
+// 8i + 7 of the tokens' operand: one token fills half of the smallest MMA's 16 columns, sixteen fill 128, and the weights'
+// bytes remain the time.  The products' epilogue adds a row's eight sums in fp32, the smallest first.
+//
+// A warp takes 256 columns of a row: four lanes share a block, each with 8 elements.  Bound by launch and latency for the
+// few rows that this serves.
+#pragma once
+
+#include <cstdint>
+
+#include "groups.cuh"
+#include "mxfp4_cast.cuh"
+#include "ptx.cuh"
+
+namespace mxfp8 {
+
+constexpr int kParts = 8;
+constexpr int kPartsThreads = 128;
+constexpr int kPartsCols = 8 * kPartsThreads;  // columns of a row that a CTA takes
+
+struct PartsParams {
+    const void *x;
+    int64_t T, R, K, ldx;        // rows of x, rows of the operand (before parts), columns, pitch
+    uint8_t *out, *scale;
+    int64_t pitch;               // bytes of a row of codes
+    int col_tiles, chunks;       // scale tiles along K, CTAs along K
+    const int32_t *rows;         // grouped
+    const int64_t *offsets;
+    int num_groups;
+    int *err_flag;
+};
+
+template <bool F32, bool GROUPED>
+__global__ void __launch_bounds__(kPartsThreads) mxfp4_parts_kernel(const PartsParams p)
+{
+    __shared__ GroupTable<GROUPED> groups;
+    pdl_wait_and_release();
+    const int tid = threadIdx.x, lane = tid & 31;
+    if constexpr (GROUPED) {
+        const int rt = group_setup<kPartsThreads, kCastTile, kParts>(groups, p.offsets, p.num_groups, p.R * kParts);
+        if (rt < 0) {
+            if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
+                atomicOr(p.err_flag, 1);
+            return;
+        }
+        const int64_t end = groups.offset[p.num_groups] / kParts;  // rows past it belong to no expert: a plan marks them
+        bool lost = false;
+        for (int64_t r = end + blockIdx.x * int64_t{kPartsThreads} + tid; r < p.R; r += gridDim.x * int64_t{kPartsThreads})
+            lost |= p.rows == nullptr || p.rows[r] >= 0;
+        if (lost && p.err_flag != nullptr)
+            atomicOr(p.err_flag, 1);
+    }
+    int64_t all = p.R;
+    if constexpr (GROUPED)
+        all = groups.offset[p.num_groups] / kParts;
+    const int64_t units = all * p.chunks;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t i = u / p.chunks;
+        const int64_t c = (u - i * p.chunks) * kPartsCols + tid * 8;
+        int64_t from = i, tile0 = 0, r0 = i * kParts;
+        bool live = true;
+        if constexpr (GROUPED) {
+            if (p.rows != nullptr) {
+                from = p.rows[i];
+                live = from >= 0 && from < p.T;
+                if (!live && tid == 0 && p.err_flag != nullptr)
+                    atomicOr(p.err_flag, 1);
+            }
+            int lo = 0, hi = p.num_groups;  // the last group that starts at or before the row (those before it may be empty)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (groups.offset[mid] <= r0)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            tile0 = groups.plane[lo];
+            r0 -= groups.offset[lo];
+        }
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = 0.f;
+        if (live && c < p.K) {  // K is a multiple of 8
+            if constexpr (F32) {
+                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + from * p.ldx + c);
+                const float4 a = src[0], b = src[1];
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+                const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + from * p.ldx + c);
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[2 * j] = bf16_lo(w[j]);
+                    v[2 * j + 1] = bf16_hi(w[j]);
+                }
+            }
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);  // as integers a NaN lies above every number
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const int e0 = live ? fp4_exponent(m) : 255;
+        const int64_t blk = c / 32;
+        const bool in_row = c < p.pitch * 2;  // a row's last block is written whole
+        const int64_t r = r0;
+        uint8_t *codes = p.out + i * kParts * p.pitch + c / 2;
+        uint8_t *tile = p.scale + ((tile0 + (r >> 7)) * p.col_tiles + blk / 4) * 512 + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
+        float mul = fp4_multiplier(e0);
+        int e = e0;
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {  // (rows 8i .. 8i + 7 lie in one 32-row part of a scale tile)
+            const bool none = e0 == 255 || e < 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] *= mul;
+            const uint32_t q = none ? 0u : cvt_fp4x8(v);
+            if (in_row)
+                *reinterpret_cast<uint32_t *>(codes + j * p.pitch) = q;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // what the part leaves, in its own units
+                float lo, hi;
+                fp4x2_to_f32((q >> (8 * k)) & 0xFF, lo, hi);
+                v[2 * k] -= lo;
+                v[2 * k + 1] -= hi;
+            }
+            uint32_t sc = !in_row ? 0u : e0 == 255 ? (j == 0 ? 255u : 0u) : none ? 0u : static_cast<uint32_t>(e);
+            sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 4) << 8;  // four blocks, four lanes apart
+            sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 8) << 16;
+            if ((lane & 15) == 0 && blk / 4 < p.col_tiles)
+                *reinterpret_cast<uint32_t *>(tile + j * 16) = sc;
+            mul = j == 0 ? 4.f : 8.f;
+            e -= j == 0 ? 2 : 3;
+        }
+    }
+}
+
+}  // namespace mxfp8

@@ -32,7 +32,7 @@ __device__ __forceinline__ float4 load_peer(uint32_t mapped)
     return v;
 }
 
-template <int QROWS, int STAGES, bool F32>
+template <int QROWS, int STAGES, bool F32, int PARTS>
 __global__ void __launch_bounds__(kGemmThreads, 2)
     mxfp4_split_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map, const GemmParams p, int splits)
 {
@@ -165,7 +165,21 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
                 uint32_t v[32];
                 tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + q, v);
                 if (splits == 1) {
-                    store_chunk<F32>(p, v, smem + (q & 32 ? kEpiBytes<F32> / 2 : 0), quarter, lane, c.q_row + q, c.valid - q, c.p0);
+                    if constexpr (PARTS > 1)
+                        store_parts<F32, PARTS>(p, v, quarter, lane, c.q_row + q, c.valid - q, c.p0);
+                    else
+                        store_chunk<F32>(p, v, smem + (q & 32 ? kEpiBytes<F32> / 2 : 0), quarter, lane, c.q_row + q, c.valid - q, c.p0);
+                } else if constexpr (PARTS > 1) {  // the parts of a row are added here, the smallest first
+                    float *part = reinterpret_cast<float *>(smem) + q / PARTS * kGemmRows + quarter * 32 + lane;
+#pragma unroll
+                    for (int t = 0; t < 32 / PARTS; ++t) {
+                        float sum = __uint_as_float(v[PARTS * t + PARTS - 1]);
+#pragma unroll
+                        for (int j = PARTS - 2; j >= 0; --j)
+                            sum += __uint_as_float(v[PARTS * t + j]);
+                        if (q + PARTS * t < c.valid)
+                            part[t * kGemmRows] = sum;
+                    }
                 } else {
                     float *part = reinterpret_cast<float *>(smem) + q * kGemmRows + quarter * 32 + lane;
 #pragma unroll
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
         tmem_dealloc(tmem, S::kColumns);
     if (splits > 1) {
         cluster_sync();
-        for (int i = rank * kGemmThreads + tid; i < c.valid * (kGemmRows / 4); i += splits * kGemmThreads) {
+        for (int i = rank * kGemmThreads + tid; i < c.valid / PARTS * (kGemmRows / 4); i += splits * kGemmThreads) {
             const int row = i / (kGemmRows / 4), col = i % (kGemmRows / 4) * 4;
             const uint32_t at = base + i * 16;
             float4 sum = load_peer(map_to_rank(at, 0));
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
                 const float4 v = load_peer(map_to_rank(at, r));
                 sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
             }
-            const int64_t to = (int64_t{c.q_row} + row) * p.ldo + c.p0 + col;
+            const int64_t to = (int64_t{c.q_row} / PARTS + row) * p.ldo + c.p0 + col;
             if (p.vec_out) {
                 if (c.p0 + col < p.P) {
                     if constexpr (F32)

@@ -1,8 +1,8 @@
 """MXFP4 (4-bit microscaled) cast and products: binding of the C ABI in include/mxfp4.h.
 
 The functions named ``mxfp4_*`` mirror the C entry points one for one and return the status code;
-``quantize_mxfp4``, ``quantize_mxfp4_grouped``, ``dequantize_mxfp4``, ``matmul_mxfp4`` and
-``matmul_mxfp4_grouped`` check their tensors, allocate the outputs with torch (on ``stream`` when one is
+``quantize_mxfp4``, ``quantize_mxfp4_grouped``, ``dequantize_mxfp4``, ``matmul_mxfp4``, ``matmul_mxfp4_grouped``,
+``linear_mxfp4`` and ``linear_mxfp4_grouped`` check their tensors, allocate the outputs with torch (on ``stream`` when one is
 given) and raise :class:`MXFP8Error` on a non-OK status.
 """
 from __future__ import annotations
@@ -156,6 +156,26 @@ def mxfp4_matmul_grouped(a_codes, a_scale, total_rows, num_groups, offsets, b_co
     return lib().mxfp4_matmul_grouped(_addr(a_codes), _addr(a_scale), total_rows, num_groups, _addr(offsets),
                                       _addr(b_codes), _addr(b_scale), N, K, _addr(out), out_type, _addr(err_flag),
                                       _stream(stream))
+
+
+def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().mxfp4_linear_workspace_bytes(M, K))
+
+
+def mxfp4_linear(x, x_type, M, K, ldx, b_codes, b_scale, N, out, out_type, ldo, workspace, stream=None) -> int:
+    return lib().mxfp4_linear(_addr(x), x_type, M, K, ldx, _addr(b_codes), _addr(b_scale), N, _addr(out), out_type, ldo,
+                              _addr(workspace), _stream(stream))
+
+
+def mxfp4_linear_grouped_workspace_bytes(total_rows: int, K: int, num_groups: int) -> int:
+    return int(lib().mxfp4_linear_grouped_workspace_bytes(total_rows, K, num_groups))
+
+
+def mxfp4_linear_grouped(x, x_type, T, K, ldx, rows, total_rows, num_groups, offsets, b_codes, b_scale, N, out, out_type,
+                         err_flag=None, workspace=None, stream=None) -> int:
+    return lib().mxfp4_linear_grouped(_addr(x), x_type, T, K, ldx, _addr(rows), total_rows, num_groups, _addr(offsets),
+                                      _addr(b_codes), _addr(b_scale), N, _addr(out), out_type, _addr(err_flag),
+                                      _addr(workspace), _stream(stream))
 
 
 # ---- torch conveniences ----------------------------------------------------------
@@ -379,4 +399,62 @@ def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, 
                                      _addr(err_flag), _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_matmul_grouped")
+    return out
+
+
+def linear_mxfp4(x: torch.Tensor, w: MXFP4Matrix, out_dtype: torch.dtype = torch.bfloat16,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x [M, K] (CUDA bf16 or fp32, not cast; K a multiple of 8, rows contiguous) times 4-bit weights w [N, K] transposed:
+    [M, N] in ``out_dtype``, or into ``out`` (rows contiguous).  To fp32 accuracy the product of the unquantized rows; for
+    few rows, as a serving step has (for many, cast them and use ``matmul_mxfp4``)."""
+    if stream is not None:
+        with _on(stream):
+            return linear_mxfp4(x, w, out_dtype, out)
+    kind, M, K, ld = _check_input(x)
+    wc, wsc = _check_matrix(w, "w")
+    dev, N = x.device, w.rows
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, w has {w.cols}")
+    if out is None:
+        out_kind, ldo = _check_out_dtype(out_dtype), N
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        out_kind, rows, cols, ldo = _check_input(out, "out")
+        if (rows, cols) != (M, N):
+            raise ValueError(f"out must be [{M}, {N}]")
+    lib_ = _lib()
+    workspace = torch.empty((lib_.mxfp4_linear_workspace_bytes(M, K),), dtype=torch.uint8, device=dev)
+    st = lib_.mxfp4_linear(x.data_ptr(), kind, M, K, ld, wc, wsc, N, out.data_ptr(), out_kind, ldo, workspace.data_ptr(),
+                           _stream_of(dev))
+    if st:
+        raise MXFP8Error(st, "mxfp4_linear")
+    return out
+
+
+def linear_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, w: MXFP4Matrix, rows: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.bfloat16, err_flag: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """linear_mxfp4 for experts: output row i is x[rows[i]] (x[i] without ``rows``) times expert g's w [N, K] transposed,
+    for i in [offsets[g], offsets[g + 1]); w.codes [G, N, .], w.scales [G, .].  Rows past the last offset become zeros.
+    ``err_flag`` (device int32) is set to 1 for bad offsets (nothing is written then), an index outside x, or rows past the
+    last offset without a negative index."""
+    if stream is not None:
+        with _on(stream):
+            return linear_mxfp4_grouped(x, offsets, w, rows, out_dtype, err_flag)
+    kind, T, K, ld = _check_input(x)
+    groups = _check_offsets(offsets)
+    _check_err(err_flag)
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous()):
+        raise ValueError("rows must be a contiguous 1-D int32 tensor")
+    wc, wsc = _check_matrix(w, "w", groups)
+    out_kind = _check_out_dtype(out_dtype)
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, w has {w.cols}")
+    R, dev, lib_ = T if rows is None else rows.numel(), x.device, _lib()
+    out = torch.empty((R, w.rows), dtype=out_dtype, device=dev)
+    workspace = torch.empty((lib_.mxfp4_linear_grouped_workspace_bytes(R, K, groups),), dtype=torch.uint8, device=dev)
+    st = lib_.mxfp4_linear_grouped(x.data_ptr(), kind, T, K, ld, _addr(rows), R, groups, offsets.data_ptr(), wc, wsc, w.rows,
+                                   out.data_ptr(), out_kind, _addr(err_flag), workspace.data_ptr(), _stream_of(dev))
+    if st:
+        raise MXFP8Error(st, "mxfp4_linear_grouped")
     return out
