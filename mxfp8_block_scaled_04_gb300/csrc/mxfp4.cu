@@ -263,16 +263,20 @@ mxfp8_status_t launch_parts(const PartsParams &p, int x_type, int64_t units, int
     static KernelSetup f32, bf16;
     int ctas = 0;
     const bool is32 = x_type == MXFP4_F32;
-    const mxfp8_status_t st = is32 ? f32(mxfp4_parts_kernel<true, GROUPED>, device, kPartsThreads, 0, &ctas)
-                                   : bf16(mxfp4_parts_kernel<false, GROUPED>, device, kPartsThreads, 0, &ctas);
-    if (st != MXFP8_OK)
-        return st;
+    const mxfp8_status_t st = is32 ? f32(mxfp4_parts_kernel<true, GROUPED>, device, kPartsThreads<GROUPED>, 0, &ctas)
+                                   : bf16(mxfp4_parts_kernel<false, GROUPED>, device, kPartsThreads<GROUPED>, 0, &ctas);
+    int sms = 0;
+    if (st != MXFP8_OK || sm_count(device, &sms) != MXFP8_OK)
+        return st != MXFP8_OK ? st : MXFP8_ERR_DEVICE;
+    if (GROUPED)
+        ctas = kPartsGroupedCtas * sms;
     const dim3 grid(static_cast<unsigned>(units < ctas ? units : ctas));
-    return is32 ? launch_serialized(mxfp4_parts_kernel<true, GROUPED>, grid, kPartsThreads, 0, 1, stream, p)
-                : launch_serialized(mxfp4_parts_kernel<false, GROUPED>, grid, kPartsThreads, 0, 1, stream, p);
+    return is32 ? launch_serialized(mxfp4_parts_kernel<true, GROUPED>, grid, kPartsThreads<GROUPED>, 0, 1, stream, p)
+                : launch_serialized(mxfp4_parts_kernel<false, GROUPED>, grid, kPartsThreads<GROUPED>, 0, 1, stream, p);
 }
 
 // Checks of x, and the operand's place in the workspace: codes, then (16-byte aligned) the planes.
+template <bool GROUPED>
 mxfp8_status_t parts_params(PartsParams *q, const void *x, int x_type, int64_t T, int64_t R, int64_t K, int64_t ldx, void *workspace)
 {
     if (!type_ok(x_type))
@@ -293,7 +297,7 @@ mxfp8_status_t parts_params(PartsParams *q, const void *x, int x_type, int64_t T
     q->out = static_cast<uint8_t *>(workspace);
     q->scale = q->out + R * kParts * q->pitch;
     q->col_tiles = static_cast<int>(ceil_div(K, 128));
-    q->chunks = static_cast<int>(ceil_div(K, kPartsCols));
+    q->chunks = static_cast<int>(ceil_div(K, 8 * kPartsThreads<GROUPED>));
     return MXFP8_OK;
 }
 
@@ -559,7 +563,7 @@ mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int
                             int out_type, int64_t ldo, void *workspace, void *stream_)
 {
     PartsParams q;
-    mxfp8_status_t st = parts_params(&q, x, x_type, M, M, K, ldx, workspace);
+    mxfp8_status_t st = parts_params<false>(&q, x, x_type, M, M, K, ldx, workspace);
     if (st != MXFP8_OK)
         return st;
     GemmParams p;
@@ -597,7 +601,7 @@ mxfp8_status_t mxfp4_linear_grouped(const void *x, int x_type, int64_t T, int64_
                                     int out_type, int *err_flag, void *workspace, void *stream_)
 {
     PartsParams q;
-    mxfp8_status_t st = parts_params(&q, x, x_type, T, total_rows, K, ldx, workspace);
+    mxfp8_status_t st = parts_params<true>(&q, x, x_type, T, total_rows, K, ldx, workspace);
     if (st != MXFP8_OK)
         return st;
     if (rows == nullptr && total_rows > T)

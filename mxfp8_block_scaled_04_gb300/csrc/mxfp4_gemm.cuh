@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait_and_release();
+    if constexpr (PARTS == 1)
+        pdl_wait_and_release();
 
     const int row_tiles = group_setup<kGemmThreads, kGemmRows, PARTS>(groups, p.offsets, p.num_groups, p.Q);
     const int num_tiles = row_tiles < 0 ? 0 : row_tiles * p.p_tiles;
@@ -260,6 +261,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
     };
     const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
+    // With parts, the kernel before on the stream writes Q alone, and began after all before it had ended: the weights of the
+    // first stages are loaded while it runs.
+    int early = 0;
+    if constexpr (PARTS > 1) {
+        if (static_cast<int>(blockIdx.x) < num_tiles && (warp == 0 || warp == 3)) {
+            const GemmTile c = gemm_tile<kGemmRows, kGemmRows, true>(blockIdx.x, p, groups);
+            const int boxes = (c.valid + p.q_box - 1) / p.q_box;
+            early = min(kGroupStages, p.k_iters);
+            for (int k = 0; k < early; ++k) {
+                if (elect_one()) {
+                    const uint32_t bar = full0 + 8 * k, dp = base + k * kGroupStage;
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx(bar, kGroupBytes + boxes * p.q_box * 128);
+                        tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                    } else {
+                        const uint32_t sb = 512u * min(2, p.kc - 2 * k);
+                        mbar_arrive_expect_tx(bar, 2 * sb);
+                        bulk_load(dp + 2 * kGroupBytes, p.p_scale + c.p_plane * p.kc * 512 + int64_t{k} * 1024, sb, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        pdl_wait_and_release();
+    }
 
     if (warp == 0 || warp == 3) {
         // ---- producers: codes (warp 0), scales (warp 3) ----
@@ -278,16 +304,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     break;
                 }
                 const uint32_t bar = full0 + 8 * slot, dp = base + slot * kGroupStage;
+                const bool started = PARTS > 1 && issued < early;  // its weights are on their way
                 if (elect_one()) {
                     if (warp == 0) {
-                        mbar_arrive_expect_tx(bar, code_bytes);
-                        tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                        if (!started) {
+                            mbar_arrive_expect_tx(bar, code_bytes);
+                            tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                        }
                         for (int b = 0; b < boxes; ++b)
                             tma_load_2d_shared(dp + kGroupBytes + b * p.q_box * 128, &q_map, bar, k * 128, c.q_row + b * p.q_box);
                     } else {
                         const uint32_t sb = 512u * min(2, p.kc - 2 * k), ds = dp + kGroupBytes + kGroupBytes;
-                        mbar_arrive_expect_tx(bar, 2 * sb);
-                        bulk_load(ds, ps + int64_t{k} * 1024, sb, bar);
+                        if (!started) {
+                            mbar_arrive_expect_tx(bar, 2 * sb);
+                            bulk_load(ds, ps + int64_t{k} * 1024, sb, bar);
+                        }
                         bulk_load(ds + 1024, qs + int64_t{k} * 1024, sb, bar);
                     }
                 }

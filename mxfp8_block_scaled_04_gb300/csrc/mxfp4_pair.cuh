@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int boxes = half > 96 ? 0 : (half + 31) / 32;  // a partial tile's rows of Q in boxes of 32 (0: whole)
             const uint32_t bytes = 2 * (kPairStage - (boxes ? (4 - boxes) * 32 * 128 : 0));  // of both CTAs
             for (int k = 0; k < p.k_iters; ++k) {
-                ok = mbar_wait_cluster(empty0 + 8 * slot, phase ^ 1, kGemmWait);
+                ok = mbar_wait_cycles(empty0 + 8 * slot, phase ^ 1, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     slot = kPairStages - 1;
                     phase ^= 1;
                 }
-                mbar_wait_cluster(full0 + 8 * slot, phase, kGemmDrain);
+                mbar_wait_cycles(full0 + 8 * slot, phase, kGemmDrain);
             }
         }
     } else if (warp == 1 && rank == 0) {
@@ -147,14 +147,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t d = tmem + (n_tile & 1) * kPairAcc1, sf = tmem + kPairScaleCol;
             const uint32_t idesc0 = mxf4_idesc(kPairRows, n, 0), idesc1 = mxf4_idesc(kPairRows, n, 1);
             if (n_tile >= 1)  // the columns shared with the tile before are read, and all of the one before that
-                ok = mbar_wait_cluster(smem_u32(&acc_empty), (n_tile - 1) & 1, kGemmWait);
+                ok = mbar_wait_cycles(smem_u32(&acc_empty), (n_tile - 1) & 1, kGemmWait);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             for (int k = 0; k < p.k_iters; ++k) {
-                ok = mbar_wait_cluster(full0 + 8 * slot, phase, kGemmWait);
+                ok = mbar_wait_cycles(full0 + 8 * slot, phase, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_commit_pair(smem_u32(&drain));
             }
             __syncwarp();
-            mbar_wait_cluster(smem_u32(&drain), 0, kGemmDrain);
+            mbar_wait_cycles(smem_u32(&drain), 0, kGemmDrain);
         }
     } else if (warp >= 4) {
         // ---- epilogue of this CTA's 128 columns of the output ----
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
             const GemmTile c = gemm_tile<kPairRows, kPairRows, GROUPED>(t, p, groups);
             const int buf = n_tile & 1;
-            if (!epilogue_all(mbar_wait_cluster(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive_cluster(lead_empty);
+                        mbar_arrive_peer(lead_empty);
                 }
                 if (q < c.valid) {
                     if constexpr (PARTS > 1)

@@ -20,8 +20,12 @@
 namespace mxfp8 {
 
 constexpr int kParts = 8;
-constexpr int kPartsThreads = 128;
-constexpr int kPartsCols = 8 * kPartsThreads;  // columns of a row that a CTA takes
+// A thread takes 8 columns of a row.  Grouped, two CTAs of 256 threads per SM, whose tables of groups leave the shared memory
+// that a CTA of the products needs to start beside them (16 tokens to 8 of 64 experts, 7168 -> 2048, over the products' own 69
+// us: 11 us without that limit, 7.2 with it; 64 tokens 22, with CTAs of 128 threads 27).
+template <bool GROUPED>
+constexpr int kPartsThreads = GROUPED ? 256 : 128;
+constexpr int kPartsGroupedCtas = 2;
 
 struct PartsParams {
     const void *x;
@@ -36,13 +40,40 @@ struct PartsParams {
 };
 
 template <bool F32, bool GROUPED>
-__global__ void __launch_bounds__(kPartsThreads) mxfp4_parts_kernel(const PartsParams p)
+__global__ void __launch_bounds__(kPartsThreads<GROUPED>) mxfp4_parts_kernel(const PartsParams p)
 {
+    constexpr int kThreads = kPartsThreads<GROUPED>;
     __shared__ GroupTable<GROUPED> groups;
     pdl_wait_and_release();
     const int tid = threadIdx.x, lane = tid & 31;
+    // A unit's elements are loaded before the one before it is split, the first ones before the table of groups is made.
+    struct Unit {
+        uint4 lo, hi;
+        bool live;  // the row is one of x's
+    };
+    auto fetch = [&](int64_t u) {
+        Unit n{};
+        const int64_t i = u / p.chunks;
+        if (i >= p.R)
+            return n;
+        const int64_t c = (u - i * p.chunks) * (8 * kThreads) + tid * 8;
+        int64_t from = i;
+        n.live = true;
+        if (GROUPED && p.rows != nullptr) {
+            from = p.rows[i];
+            n.live = from >= 0 && from < p.T;
+        }
+        if (n.live && c < p.K) {  // K is a multiple of 8
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p.x) + (from * p.ldx + c) * (F32 ? 4 : 2));
+            n.lo = src[0];
+            if constexpr (F32)
+                n.hi = src[1];
+        }
+        return n;
+    };
+    Unit next = fetch(blockIdx.x);
     if constexpr (GROUPED) {
-        const int rt = group_setup<kPartsThreads, kCastTile, kParts>(groups, p.offsets, p.num_groups, p.R * kParts);
+        const int rt = group_setup<kThreads, kCastTile, kParts>(groups, p.offsets, p.num_groups, p.R * kParts);
         if (rt < 0) {
             if (blockIdx.x == 0 && tid == 0 && p.err_flag != nullptr)
                 atomicOr(p.err_flag, 1);
@@ -50,7 +81,7 @@ __global__ void __launch_bounds__(kPartsThreads) mxfp4_parts_kernel(const PartsP
         }
         const int64_t end = groups.offset[p.num_groups] / kParts;  // rows past it belong to no expert: a plan marks them
         bool lost = false;
-        for (int64_t r = end + blockIdx.x * int64_t{kPartsThreads} + tid; r < p.R; r += gridDim.x * int64_t{kPartsThreads})
+        for (int64_t r = end + blockIdx.x * int64_t{kThreads} + tid; r < p.R; r += gridDim.x * int64_t{kThreads})
             lost |= p.rows == nullptr || p.rows[r] >= 0;
         if (lost && p.err_flag != nullptr)
             atomicOr(p.err_flag, 1);
@@ -61,16 +92,13 @@ __global__ void __launch_bounds__(kPartsThreads) mxfp4_parts_kernel(const PartsP
     const int64_t units = all * p.chunks;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t i = u / p.chunks;
-        const int64_t c = (u - i * p.chunks) * kPartsCols + tid * 8;
-        int64_t from = i, tile0 = 0, r0 = i * kParts;
-        bool live = true;
+        const int64_t c = (u - i * p.chunks) * (8 * kThreads) + tid * 8;
+        int64_t tile0 = 0, r0 = i * kParts;
+        const Unit at = next;
+        next = fetch(u + gridDim.x);
         if constexpr (GROUPED) {
-            if (p.rows != nullptr) {
-                from = p.rows[i];
-                live = from >= 0 && from < p.T;
-                if (!live && tid == 0 && p.err_flag != nullptr)
-                    atomicOr(p.err_flag, 1);
-            }
+            if (!at.live && tid == 0 && p.err_flag != nullptr)
+                atomicOr(p.err_flag, 1);
             int lo = 0, hi = p.num_groups;  // the last group that starts at or before the row (those before it may be empty)
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -83,22 +111,17 @@ __global__ void __launch_bounds__(kPartsThreads) mxfp4_parts_kernel(const PartsP
             r0 -= groups.offset[lo];
         }
         float v[8];
+        if constexpr (F32) {
+            const uint32_t w[8] = {at.lo.x, at.lo.y, at.lo.z, at.lo.w, at.hi.x, at.hi.y, at.hi.z, at.hi.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = 0.f;
-        if (live && c < p.K) {  // K is a multiple of 8
-            if constexpr (F32) {
-                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + from * p.ldx + c);
-                const float4 a = src[0], b = src[1];
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            } else {
-                const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + from * p.ldx + c);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            for (int j = 0; j < 8; ++j)
+                v[j] = __uint_as_float(w[j]);
+        } else {
+            const uint32_t w[4] = {at.lo.x, at.lo.y, at.lo.z, at.lo.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[2 * j] = bf16_lo(w[j]);
-                    v[2 * j + 1] = bf16_hi(w[j]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = bf16_lo(w[j]);
+                v[2 * j + 1] = bf16_hi(w[j]);
             }
         }
         uint32_t m = 0;
@@ -107,7 +130,7 @@ __global__ void __launch_bounds__(kPartsThreads) mxfp4_parts_kernel(const PartsP
             m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);  // as integers a NaN lies above every number
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const int e0 = live ? fp4_exponent(m) : 255;
+        const int e0 = at.live ? fp4_exponent(m) : 255;
         const int64_t blk = c / 32;
         const bool in_row = c < p.pitch * 2;  // a row's last block is written whole
         const int64_t r = r0;

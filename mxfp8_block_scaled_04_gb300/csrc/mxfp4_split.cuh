@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait_and_release();
+    if constexpr (PARTS == 1)
+        pdl_wait_and_release();
 
     const int rank = static_cast<int>(blockIdx.x) % splits;
     const GemmTile c = gemm_tile<kGemmRows, 128, false>(static_cast<int>(blockIdx.x) / splits, p, GroupTable<false>{});
@@ -78,6 +79,29 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
         }
     };
     bool ok = true;
+    // With parts, the kernel before on the stream writes Q alone, and began after all before it had ended: the weights of the
+    // first stages are loaded while it runs (1x8192x8192 11.3 -> 10.3 us, 1x8192x28672 24.2 -> 23.0).
+    const int early = PARTS > 1 ? min(S::kStages, k1 - k0) : 0;
+    if constexpr (PARTS > 1) {
+        if (warp == 0 || warp == 3) {
+            const int boxes = (c.valid + p.q_box - 1) / p.q_box;
+            for (int j = 0; j < early; ++j) {
+                if (elect_one()) {
+                    const uint32_t bar = full0 + 8 * j, dp = base + j * S::kStage;
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx(bar, S::kPBytes + boxes * p.q_box * 128);
+                        tma_load_2d_shared(dp, &p_map, bar, (k0 + j) * 128, c.p_row);
+                    } else {
+                        const uint32_t sb = 512u * min(2, p.kc - 2 * (k0 + j));
+                        mbar_arrive_expect_tx(bar, 2 * sb);
+                        bulk_load(dp + S::kPBytes + S::kQBytes, p.p_scale + c.p_plane * p.kc * 512 + int64_t{k0 + j} * 1024, sb, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        pdl_wait_and_release();
+    }
 
     if (warp == 0 || warp == 3) {
         // ---- producers: codes (warp 0), scales (warp 3) ----
@@ -90,16 +114,21 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
             if (!ok)
                 break;
             const uint32_t bar = full0 + 8 * slot, dp = base + slot * S::kStage;
+            const bool started = k - k0 < early;  // its weights are on their way
             if (elect_one()) {
                 if (warp == 0) {
-                    mbar_arrive_expect_tx(bar, code_bytes);
-                    tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                    if (!started) {
+                        mbar_arrive_expect_tx(bar, code_bytes);
+                        tma_load_2d_shared(dp, &p_map, bar, k * 128, c.p_row);
+                    }
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d_shared(dp + S::kPBytes + b * p.q_box * 128, &q_map, bar, k * 128, c.q_row + b * p.q_box);
                 } else {
                     const uint32_t sb = 512u * min(2, p.kc - 2 * k), ds = dp + S::kPBytes + S::kQBytes;
-                    mbar_arrive_expect_tx(bar, 2 * sb);
-                    bulk_load(ds, ps + int64_t{k} * 1024, sb, bar);
+                    if (!started) {
+                        mbar_arrive_expect_tx(bar, 2 * sb);
+                        bulk_load(ds, ps + int64_t{k} * 1024, sb, bar);
+                    }
                     bulk_load(ds + 1024, qs + int64_t{k} * 1024, sb, bar);
                 }
             }

@@ -145,13 +145,6 @@ __device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d, uint64_t a, uint64_
                  : "memory");
 }
 
-// Arrive on a barrier of either CTA.  What these arrivals order is not generic memory (accumulator reads that have
-// completed; zeros already handed to the async proxy), so the default scope does: with .release.cluster an arrival took
-// 1000 to 3000 cycles, and a wait with .acquire.cluster 360 where the phase was already complete.
-__device__ __forceinline__ void mbar_arrive_peer(uint32_t mapped)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
-}
 __device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
