@@ -16,7 +16,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libmxfp8.so")
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("api.cu", "mxfp4.cu", "moe.cu", "mxfp8_matmul.cu")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("api.cu", "mxfp4.cu", "moe.cu", "mxfp8_matmul.cu", "block_norm.cu")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -1,0 +1,242 @@
+// C ABI of the norms around a block (declarations and contract in include/block_norm.h): host-side checks and launches;
+// the device code is in block_norm.cuh.
+#include <cstdint>
+#include <map>
+#include <mutex>
+#include <tuple>
+
+#include "../../include/block_norm.h"
+#include "block_norm.cuh"
+#include "host.h"
+
+namespace {
+
+using namespace mxfp8;
+
+constexpr int64_t kMaxDim = int64_t{1} << 31;
+constexpr int kMostSmem = 3 * BLOCK_NORM_MAX_H * 4;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool type_ok(int t) { return t == MXFP4_BF16 || t == MXFP4_F32; }
+
+mxfp8_status_t check_config(const block_norm_config_t *cfg, int64_t T, int64_t H)
+{
+    if (cfg == nullptr)
+        return MXFP8_ERR_NULL;
+    for (int r : cfg->reserved)
+        if (r != 0)
+            return MXFP8_ERR_FORMAT;
+    if (!type_ok(cfg->y_type) || !type_ok(cfg->h_type) || cfg->gate_kind < BLOCK_GATE_NONE || cfg->gate_kind > BLOCK_GATE_TOKEN)
+        return MXFP8_ERR_FORMAT;
+    if (T < 0 || T >= kMaxDim || H < 0 || H % 8 || H > BLOCK_NORM_MAX_H)
+        return MXFP8_ERR_SHAPE;
+    if ((cfg->gate_kind == BLOCK_GATE_NONE) != (cfg->gate == nullptr))
+        return MXFP8_ERR_NULL;
+    if (!is_aligned(cfg->pre_weight, 16) || !is_aligned(cfg->post_weight, 16) || !is_aligned(cfg->gate, cfg->gate_kind == BLOCK_GATE_TOKEN ? 4 : 16))
+        return MXFP8_ERR_ALIGN;
+    return MXFP8_OK;
+}
+
+bool pitch_ok(const void *p, int64_t ld, int64_t H) { return p == nullptr || (ld >= H && ld % 8 == 0 && ld < kMaxDim); }
+
+// Vectors per thread and threads: few rows are a chain of latencies, shorter with one vector in up to 1024 threads.
+void shape(int64_t T, int vecs, int *v, int *threads)
+{
+    *v = vecs <= 512 || (vecs <= 1024 && T <= kNormCtas) ? 1 : vecs <= 1024 ? 2 : 4;
+    *threads = static_cast<int>(ceil_div(ceil_div(vecs, *v), 32) * 32);
+}
+
+// CTAs of a kernel that are resident at once: they depend on a call's threads and shared memory, few pairs of which occur.
+template <auto *KERN>
+mxfp8_status_t resident(int device, int threads, int smem, int64_t *ctas)
+{
+    static KernelSetup setup;  // opts the kernel in to the largest size
+    static std::mutex mu;
+    static std::map<std::tuple<int, int, int>, int> known;
+    int all = 0;
+    const mxfp8_status_t st = setup(KERN, device, 32, kMostSmem, &all);
+    if (st != MXFP8_OK)
+        return st;
+    std::lock_guard<std::mutex> lock(mu);
+    int &per_sm = known[{device, threads, smem}];
+    if (per_sm == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, smem) != cudaSuccess || per_sm < 1)) {
+        cudaGetLastError();
+        per_sm = 0;
+        return MXFP8_ERR_LAUNCH;
+    }
+    *ctas = static_cast<int64_t>(per_sm) * setup.sms[device];
+    return MXFP8_OK;
+}
+
+template <auto *KERN>
+mxfp8_status_t launch_rows(const NormParams &p, int threads, int smem, int most, cudaStream_t stream, int *grid)
+{
+    int device = 0;
+    int64_t ctas = 0;
+    mxfp8_status_t st;
+    if ((st = active_device(&device)) != MXFP8_OK || (st = resident<KERN>(device, threads, smem, &ctas)) != MXFP8_OK)
+        return st;
+    ctas = ctas < most ? ctas : most;
+    ctas = ctas < p.T ? ctas : p.T;
+    *grid = static_cast<int>(ctas);
+    return launch_serialized(KERN, dim3(static_cast<unsigned>(ctas)), static_cast<unsigned>(threads), static_cast<size_t>(smem), 1, stream, p);
+}
+
+template <bool YF32, bool HF32, bool BACKWARD>
+mxfp8_status_t launch_v(const NormParams &p, int v, int threads, int smem, cudaStream_t stream, int *grid)
+{
+    const int most = BACKWARD ? kNormCtas : 1 << 20;
+    if constexpr (BACKWARD) {
+        return v == 1   ? launch_rows<block_norm_backward_kernel<YF32, HF32, 1>>(p, threads, smem, most, stream, grid)
+               : v == 2 ? launch_rows<block_norm_backward_kernel<YF32, HF32, 2>>(p, threads, smem, most, stream, grid)
+                        : launch_rows<block_norm_backward_kernel<YF32, HF32, 4>>(p, threads, smem, most, stream, grid);
+    } else {
+        return v == 1   ? launch_rows<block_norm_kernel<YF32, HF32, 1>>(p, threads, smem, most, stream, grid)
+               : v == 2 ? launch_rows<block_norm_kernel<YF32, HF32, 2>>(p, threads, smem, most, stream, grid)
+                        : launch_rows<block_norm_kernel<YF32, HF32, 4>>(p, threads, smem, most, stream, grid);
+    }
+}
+
+template <bool BACKWARD>
+mxfp8_status_t launch(const NormParams &p, const block_norm_config_t *cfg, int smem, cudaStream_t stream, int *grid)
+{
+    int v = 0, threads = 0;
+    shape(p.T, p.vecs, &v, &threads);
+    const bool y32 = cfg->y_type == MXFP4_F32, h32 = cfg->h_type == MXFP4_F32;
+    return y32 ? (h32 ? launch_v<true, true, BACKWARD>(p, v, threads, smem, stream, grid) : launch_v<true, false, BACKWARD>(p, v, threads, smem, stream, grid))
+               : (h32 ? launch_v<false, true, BACKWARD>(p, v, threads, smem, stream, grid) : launch_v<false, false, BACKWARD>(p, v, threads, smem, stream, grid));
+}
+
+NormParams params(const block_norm_config_t *cfg, int64_t T, int64_t H)
+{
+    NormParams p{};
+    p.T = T;
+    p.H = static_cast<int>(H);
+    p.vecs = static_cast<int>(H / 8);
+    p.gate_kind = cfg->gate_kind;
+    p.scale = cfg->scale;
+    p.eps = cfg->eps;
+    p.pre = cfg->pre_weight;
+    p.post = cfg->post_weight;
+    p.gate = cfg->gate;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxfp8_status_t block_norm(const block_norm_config_t *cfg, int64_t T, int64_t H, const void *y, int64_t ldy, const void *h, int64_t ldh, void *h_out, void *x,
+                          void *stream)
+{
+    mxfp8_status_t st = check_config(cfg, T, H);
+    if (st != MXFP8_OK)
+        return st;
+    if (!pitch_ok(y, ldy, H) || !pitch_ok(h, ldh, H))
+        return MXFP8_ERR_SHAPE;
+    if (T > 0 && H > 0) {
+        if (h == nullptr || (h_out == nullptr && x == nullptr) || (x == nullptr) != (cfg->pre_weight == nullptr) ||
+            (y == nullptr && (cfg->post_weight != nullptr || cfg->gate != nullptr)))
+            return MXFP8_ERR_NULL;
+    }
+    if (!is_aligned(y, 16) || !is_aligned(h, 16) || !is_aligned(h_out, 16) || !is_aligned(x, 16))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    if ((st = active_device(&device)) != MXFP8_OK)
+        return st;
+    for (const void *ptr : {y, h, static_cast<const void *>(h_out), static_cast<const void *>(x), static_cast<const void *>(cfg->pre_weight),
+                            static_cast<const void *>(cfg->post_weight), static_cast<const void *>(cfg->gate)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    if (T == 0 || H == 0)
+        return MXFP8_OK;
+    NormParams p = params(cfg, T, H);
+    p.y = y;
+    p.ldy = ldy;
+    p.h = h;
+    p.ldh = ldh;
+    p.h_out = h_out;
+    p.x = x;
+    int grid = 0;
+    return launch<false>(p, cfg, 0, static_cast<cudaStream_t>(stream), &grid);
+}
+
+size_t block_norm_backward_workspace_bytes(int64_t T, int64_t H)
+{
+    if (T <= 0 || T >= kMaxDim || H <= 0 || H > BLOCK_NORM_MAX_H)
+        return 0;
+    return static_cast<size_t>(T < kNormCtas ? T : kNormCtas) * 3 * static_cast<size_t>(H) * sizeof(float);
+}
+
+mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, int64_t H, const void *dh_out, int64_t lddh, const void *dx, int64_t lddx,
+                                   const void *y, int64_t ldy, const void *h_out, int64_t ldh, void *dh, void *dy, float *dpre, float *dpost,
+                                   float *dgate, void *workspace, void *stream_)
+{
+    mxfp8_status_t st = check_config(cfg, T, H);
+    if (st != MXFP8_OK)
+        return st;
+    if (!pitch_ok(dh_out, lddh, H) || !pitch_ok(dx, lddx, H) || !pitch_ok(y, ldy, H) || !pitch_ok(h_out, ldh, H))
+        return MXFP8_ERR_SHAPE;
+    if ((dpost != nullptr && cfg->post_weight == nullptr) || (dgate != nullptr && cfg->gate == nullptr) || (dpre != nullptr && cfg->pre_weight == nullptr))
+        return MXFP8_ERR_NULL;
+    if (T > 0 && H > 0) {
+        const bool needs_y = (cfg->post_weight != nullptr && (dy != nullptr || dpost != nullptr)) || dgate != nullptr;
+        if ((dh_out == nullptr && dx == nullptr) || (dx != nullptr && (cfg->pre_weight == nullptr || h_out == nullptr)) || (needs_y && y == nullptr) ||
+            (dh == nullptr && dy == nullptr && dpre == nullptr && dpost == nullptr && dgate == nullptr))
+            return MXFP8_ERR_NULL;
+        if ((dpre != nullptr || dpost != nullptr || dgate != nullptr) && workspace == nullptr)
+            return MXFP8_ERR_WORKSPACE;
+    }
+    if (!is_aligned(dh_out, 16) || !is_aligned(dx, 16) || !is_aligned(y, 16) || !is_aligned(h_out, 16) || !is_aligned(dh, 16) || !is_aligned(dy, 16) ||
+        !is_aligned(dpre, 4) || !is_aligned(dpost, 4) || !is_aligned(dgate, 4) || !is_aligned(workspace, 16))
+        return MXFP8_ERR_ALIGN;
+    int device = 0;
+    if ((st = active_device(&device)) != MXFP8_OK)
+        return st;
+    for (const void *ptr : {dh_out, dx, y, h_out, static_cast<const void *>(dh), static_cast<const void *>(dy), static_cast<const void *>(dpre),
+                            static_cast<const void *>(dpost), static_cast<const void *>(dgate), static_cast<const void *>(workspace),
+                            static_cast<const void *>(cfg->pre_weight), static_cast<const void *>(cfg->post_weight),
+                            static_cast<const void *>(cfg->gate)})
+        if (!pointer_on_device(ptr, device))
+            return MXFP8_ERR_DEVICE;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (H == 0)
+        return MXFP8_OK;
+    if (T == 0) {  // sums over no rows
+        for (float *out : {dpre, dpost, cfg->gate_kind == BLOCK_GATE_CHANNEL ? dgate : nullptr})
+            if (out != nullptr && cudaMemsetAsync(out, 0, static_cast<size_t>(H) * sizeof(float), stream) != cudaSuccess) {
+                cudaGetLastError();
+                return MXFP8_ERR_LAUNCH;
+            }
+        return MXFP8_OK;
+    }
+    NormParams p = params(cfg, T, H);
+    p.y = y;
+    p.ldy = ldy;
+    p.h = h_out;
+    p.ldh = ldh;
+    p.dh_out = dh_out;
+    p.lddh = lddh;
+    p.dx = dx;
+    p.lddx = lddx;
+    p.dh = dh;
+    p.dy = dy;
+    p.dpre = dpre;
+    p.dpost = dpost;
+    p.dgate = dgate;
+    p.partial = static_cast<float *>(workspace);
+    float *outs[3];
+    int arrays = 0, grid = 0;
+    for (float *out : {dpre, dpost, cfg->gate_kind == BLOCK_GATE_CHANNEL ? dgate : nullptr})
+        if (out != nullptr)
+            outs[arrays++] = out;
+    const int smem = arrays * static_cast<int>(H) * static_cast<int>(sizeof(float));
+    if ((st = launch<true>(p, cfg, smem, stream, &grid)) != MXFP8_OK || arrays == 0)
+        return st;
+    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(arrays * H, 32))), kNormReduceThreads, 0, 1, stream,
+                             static_cast<const float *>(p.partial), grid, arrays, static_cast<int>(H), outs[0], arrays > 1 ? outs[1] : nullptr,
+                             arrays > 2 ? outs[2] : nullptr);
+}
+
+}  // extern "C"
