@@ -14,7 +14,8 @@ namespace {
 using namespace mxfp8;
 
 constexpr int64_t kMaxDim = int64_t{1} << 31;
-constexpr int kMostSmem = 3 * BLOCK_NORM_MAX_H * 4;
+constexpr int kMostSmem = 224 * 1024;
+constexpr int kRingBytes = 128 * 1024;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -40,13 +41,6 @@ mxfp8_status_t check_config(const block_norm_config_t *cfg, int64_t T, int64_t H
 
 bool pitch_ok(const void *p, int64_t ld, int64_t H) { return p == nullptr || (ld >= H && ld % 8 == 0 && ld < kMaxDim); }
 
-// Vectors per thread and threads: few rows are a chain of latencies, shorter with one vector in up to 1024 threads.
-void shape(int64_t T, int vecs, int *v, int *threads)
-{
-    *v = vecs <= 512 || (vecs <= 1024 && T <= kNormCtas) ? 1 : vecs <= 1024 ? 2 : 4;
-    *threads = static_cast<int>(ceil_div(ceil_div(vecs, *v), 32) * 32);
-}
-
 // CTAs of a kernel that are resident at once: they depend on a call's threads and shared memory, few pairs of which occur.
 template <auto *KERN>
 mxfp8_status_t resident(int device, int threads, int smem, int64_t *ctas)
@@ -70,12 +64,11 @@ mxfp8_status_t resident(int device, int threads, int smem, int64_t *ctas)
 }
 
 template <auto *KERN>
-mxfp8_status_t launch_rows(const NormParams &p, int threads, int smem, int most, cudaStream_t stream, int *grid)
+mxfp8_status_t launch_rows(const NormParams &p, int threads, int smem, int64_t most, int device, cudaStream_t stream, int *grid)
 {
-    int device = 0;
     int64_t ctas = 0;
-    mxfp8_status_t st;
-    if ((st = active_device(&device)) != MXFP8_OK || (st = resident<KERN>(device, threads, smem, &ctas)) != MXFP8_OK)
+    const mxfp8_status_t st = resident<KERN>(device, threads, smem, &ctas);
+    if (st != MXFP8_OK)
         return st;
     ctas = ctas < most ? ctas : most;
     ctas = ctas < p.T ? ctas : p.T;
@@ -83,29 +76,38 @@ mxfp8_status_t launch_rows(const NormParams &p, int threads, int smem, int most,
     return launch_serialized(KERN, dim3(static_cast<unsigned>(ctas)), static_cast<unsigned>(threads), static_cast<size_t>(smem), 1, stream, p);
 }
 
+// row_bytes: of all inputs of a row.
 template <bool YF32, bool HF32, bool BACKWARD>
-mxfp8_status_t launch_v(const NormParams &p, int v, int threads, int smem, cudaStream_t stream, int *grid)
+mxfp8_status_t launch_types(NormParams p, int row_bytes, int device, cudaStream_t stream, int *grid)
 {
-    const int most = BACKWARD ? kNormCtas : 1 << 20;
-    if constexpr (BACKWARD) {
-        return v == 1   ? launch_rows<block_norm_backward_kernel<YF32, HF32, 1>>(p, threads, smem, most, stream, grid)
-               : v == 2 ? launch_rows<block_norm_backward_kernel<YF32, HF32, 2>>(p, threads, smem, most, stream, grid)
-                        : launch_rows<block_norm_backward_kernel<YF32, HF32, 4>>(p, threads, smem, most, stream, grid);
-    } else {
-        return v == 1   ? launch_rows<block_norm_kernel<YF32, HF32, 1>>(p, threads, smem, most, stream, grid)
-               : v == 2 ? launch_rows<block_norm_kernel<YF32, HF32, 2>>(p, threads, smem, most, stream, grid)
-                        : launch_rows<block_norm_kernel<YF32, HF32, 4>>(p, threads, smem, most, stream, grid);
+    const int v = p.vecs <= kNormThreads ? 1 : p.vecs <= 2 * kNormThreads ? 2 : 4;
+    const int threads = static_cast<int>(ceil_div(ceil_div(p.vecs, v), 32) * 32);
+    const int64_t most = BACKWARD ? norm_ctas(p.H) : int64_t{1} << 20;
+    if (v == 4) {
+        if constexpr (BACKWARD)
+            return launch_rows<block_norm_backward_long_kernel<YF32, HF32, 4>>(p, threads, 2 * p.H * 4, most, device, stream, grid);
+        else
+            return launch_rows<block_norm_long_kernel<YF32, HF32, 4>>(p, threads, 0, most, device, stream, grid);
     }
+    // an SM's CTAs keep as many rows in flight as leave L1 room for the weights
+    const int per_sm = 1024 / threads < 1 ? 1 : 1024 / threads;
+    const int room = kRingBytes / (BACKWARD && v == 2 ? 1 : per_sm < 8 ? per_sm : 8);
+    p.stages = room / row_bytes < 2 ? 2 : room / row_bytes < kNormMaxStages ? room / row_bytes : kNormMaxStages;
+    const int smem = p.stages * row_bytes;
+    if constexpr (BACKWARD)
+        return v == 1 ? launch_rows<block_norm_backward_ring_kernel<YF32, HF32, 1>>(p, threads, smem, most, device, stream, grid)
+                      : launch_rows<block_norm_backward_ring_kernel<YF32, HF32, 2>>(p, threads, smem, most, device, stream, grid);
+    else
+        return v == 1 ? launch_rows<block_norm_ring_kernel<YF32, HF32, 1>>(p, threads, smem, most, device, stream, grid)
+                      : launch_rows<block_norm_ring_kernel<YF32, HF32, 2>>(p, threads, smem, most, device, stream, grid);
 }
 
 template <bool BACKWARD>
-mxfp8_status_t launch(const NormParams &p, const block_norm_config_t *cfg, int smem, cudaStream_t stream, int *grid)
+mxfp8_status_t launch(const NormParams &p, const block_norm_config_t *cfg, int row_bytes, int device, cudaStream_t stream, int *grid)
 {
-    int v = 0, threads = 0;
-    shape(p.T, p.vecs, &v, &threads);
     const bool y32 = cfg->y_type == MXFP4_F32, h32 = cfg->h_type == MXFP4_F32;
-    return y32 ? (h32 ? launch_v<true, true, BACKWARD>(p, v, threads, smem, stream, grid) : launch_v<true, false, BACKWARD>(p, v, threads, smem, stream, grid))
-               : (h32 ? launch_v<false, true, BACKWARD>(p, v, threads, smem, stream, grid) : launch_v<false, false, BACKWARD>(p, v, threads, smem, stream, grid));
+    return y32 ? (h32 ? launch_types<true, true, BACKWARD>(p, row_bytes, device, stream, grid) : launch_types<true, false, BACKWARD>(p, row_bytes, device, stream, grid))
+               : (h32 ? launch_types<false, true, BACKWARD>(p, row_bytes, device, stream, grid) : launch_types<false, false, BACKWARD>(p, row_bytes, device, stream, grid));
 }
 
 NormParams params(const block_norm_config_t *cfg, int64_t T, int64_t H)
@@ -158,15 +160,18 @@ mxfp8_status_t block_norm(const block_norm_config_t *cfg, int64_t T, int64_t H, 
     p.ldh = ldh;
     p.h_out = h_out;
     p.x = x;
+    if ((p.fault = fault_word_address(device)) == nullptr)
+        return MXFP8_ERR_DEVICE;
+    const int hs = cfg->h_type == MXFP4_F32 ? 4 : 2, ys = cfg->y_type == MXFP4_F32 ? 4 : 2;
     int grid = 0;
-    return launch<false>(p, cfg, 0, static_cast<cudaStream_t>(stream), &grid);
+    return launch<false>(p, cfg, p.H * (hs + (y != nullptr ? ys : 0)), device, static_cast<cudaStream_t>(stream), &grid);
 }
 
 size_t block_norm_backward_workspace_bytes(int64_t T, int64_t H)
 {
     if (T <= 0 || T >= kMaxDim || H <= 0 || H > BLOCK_NORM_MAX_H)
         return 0;
-    return static_cast<size_t>(T < kNormCtas ? T : kNormCtas) * 3 * static_cast<size_t>(H) * sizeof(float);
+    return static_cast<size_t>(T < norm_ctas(H) ? T : norm_ctas(H)) * 2 * static_cast<size_t>(H) * sizeof(float);
 }
 
 mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, int64_t H, const void *dh_out, int64_t lddh, const void *dx, int64_t lddx,
@@ -225,18 +230,16 @@ mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, in
     p.dpre = dpre;
     p.dpost = dpost;
     p.dgate = dgate;
-    p.partial = static_cast<float *>(workspace);
-    float *outs[3];
-    int arrays = 0, grid = 0;
-    for (float *out : {dpre, dpost, cfg->gate_kind == BLOCK_GATE_CHANNEL ? dgate : nullptr})
-        if (out != nullptr)
-            outs[arrays++] = out;
-    const int smem = arrays * static_cast<int>(H) * static_cast<int>(sizeof(float));
-    if ((st = launch<true>(p, cfg, smem, stream, &grid)) != MXFP8_OK || arrays == 0)
+    const bool sums = dpre != nullptr || dpost != nullptr || (dgate != nullptr && cfg->gate_kind == BLOCK_GATE_CHANNEL);
+    p.partial = sums ? static_cast<float *>(workspace) : nullptr;
+    if ((p.fault = fault_word_address(device)) == nullptr)
+        return MXFP8_ERR_DEVICE;
+    const int hs = cfg->h_type == MXFP4_F32 ? 4 : 2, ys = cfg->y_type == MXFP4_F32 ? 4 : 2;
+    const int row_bytes = p.H * ((y != nullptr ? ys : 0) + (dx != nullptr ? hs + 2 : 0) + (dh_out != nullptr ? hs : 0));
+    int grid = 0;
+    if ((st = launch<true>(p, cfg, row_bytes, device, stream, &grid)) != MXFP8_OK || !sums)
         return st;
-    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(arrays * H, 32))), kNormReduceThreads, 0, 1, stream,
-                             static_cast<const float *>(p.partial), grid, arrays, static_cast<int>(H), outs[0], arrays > 1 ? outs[1] : nullptr,
-                             arrays > 2 ? outs[2] : nullptr);
+    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(2 * H, 32))), kNormReduceThreads, 0, 1, stream, p, grid);
 }
 
 }  // extern "C"

@@ -2,20 +2,28 @@
 //
 // A CTA takes a row at a time and a thread V vectors of 8 columns of it, so that every input is read once and each
 // output written once, with the row's sums (of y^2, then of h'^2; backward: y^2, h'^2 and dx w h' together, then b n1) formed
-// between.  The next row is loaded before this one is worked on.  Bound by HBM for many rows, by the
-// chain of loads, two reductions and stores (launch included) for few.
+// between.  Rows up to 8192 columns come through a ring of shared-memory stages, filled by bulk copies while the rows before
+// them are worked on; longer ones are loaded by the threads.  Bound by HBM for many rows, by the chain of loads, two
+// reductions and stores (launch included) for few.
 //
-// The weights' gradients are sums over the rows: a CTA keeps its own in shared memory (each thread its columns), writes them
-// to the workspace at its end, and a second kernel adds the CTAs' in order.
+// The weights' gradients are sums over the rows: each thread adds up its columns' (in registers; in shared memory for long
+// rows), a CTA writes its sums to the workspace at its end, and a second kernel adds the CTAs' in order.  With a
+// gate per channel sum(g n1) serves both: dpost = gate times it, dgate = w_post times it.
 #pragma once
 
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace mxfp8 {
 
-constexpr int kNormCtas = 2 * 152;  // CTAs whose partial sums the workspace holds
+constexpr int kNormSms = 152;
+constexpr int kNormThreads = 512;
+constexpr int kNormMaxStages = 4;
+constexpr int64_t kNormWait = 4000000000;  // cycles: about 2 s
+// CTAs whose partial sums the workspace holds, for rows of H columns.
+inline int norm_ctas(int64_t H) { return kNormSms * (H > 4096 ? 1 : H > 2048 ? 2 : H > 1024 ? 4 : 8); }
 
 struct NormParams {
     const void *y, *h;                 // backward: h is the stream behind the block
@@ -28,6 +36,8 @@ struct NormParams {
     void *h_out, *x;
     void *dh, *dy;
     float *dpre, *dpost, *dgate, *partial;
+    int stages;                        // of the ring
+    unsigned *fault;
 };
 
 // Eight elements of a row as they are stored.
@@ -136,95 +146,113 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float (*buffer)[4][32], 
     turn ^= 1;
 }
 
-template <int V>
-constexpr int kNormThreads = V == 1 ? 1024 : 512;
-
-template <bool YF32, bool HF32, int V>
-__global__ void __launch_bounds__(kNormThreads<V>) block_norm_kernel(const NormParams p)
+// The ring: stage n % stages holds the CTA's n-th row of each input, one after the other.
+struct RowSource {
+    const void *base[4];
+    int64_t pitch[4];  // bytes
+    int bytes[4];      // of a row; 0: not read
+    int at[4];         // offset in a stage
+    int stage;         // bytes
+};
+__device__ __forceinline__ void add_source(RowSource &s, int n, const void *base, int64_t ld, int H, int size)
 {
-    __shared__ float buffer[2][4][32];
-    pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
-    int turn = 0;
-    Row8<YF32> yr[V];
+    s.base[n] = base;
+    s.pitch[n] = ld * size;
+    s.bytes[n] = base != nullptr ? H * size : 0;
+    s.at[n] = s.stage;
+    s.stage += s.bytes[n];
+}
+template <int N>
+__device__ __forceinline__ void fetch_row(const RowSource &s, uint32_t smem, uint32_t bar, int64_t row)
+{
+    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(s.stage));
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (s.bytes[n] != 0)
+            bulk_load(smem + s.at[n], static_cast<const unsigned char *>(s.base[n]) + row * s.pitch[n], static_cast<uint32_t>(s.bytes[n]), bar);
+}
+// Eight elements from a stage (zeros for an input that is not read).
+template <bool F32>
+__device__ __forceinline__ Row8<F32> stage_row8(const unsigned char *stage, const RowSource &s, int n, int j)
+{
+    Row8<F32> r{};
+    if (s.bytes[n] != 0) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(stage + s.at[n]) + j * (F32 ? 2 : 1);
+        r.lo = q[0];
+        if constexpr (F32)
+            r.hi = q[1];
+    }
+    return r;
+}
+
+// y, h -> h', x.  One row; `fetch` gives vector i of it.
+template <bool YF32, bool HF32, int V, typename Fetch, typename Between>
+__device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float inv, float (*buffer)[4][32], int &turn, int lane, int warp, int warps, Fetch &&fetch,
+                                         Between &&between)
+{
+    const int tid = threadIdx.x, nt = blockDim.x;
+    float a[V][8];
     Row8<HF32> hr[V];
-    auto load = [&](int64_t row) {
+    float s[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = tid + i * nt;
-            yr[i] = Row8<YF32>{};
-            hr[i] = Row8<HF32>{};
-            if (j < p.vecs && row < p.T) {
-                if (p.y != nullptr)
-                    yr[i] = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
-                hr[i] = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
+    for (int i = 0; i < V; ++i) {
+        Row8<YF32> yr;
+        fetch(i, yr, hr[i]);
+        widen8<YF32>(yr, a[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            s[0] = fmaf(a[i][k], a[i][k], s[0]);
+    }
+    float factor = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
+    row_sums<1>(s, buffer, turn, lane, warp, warps);
+    between();
+    if (p.post != nullptr)
+        factor *= rsqrtf(s[0] * inv + p.eps);
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j = tid + i * nt;
+        float h[8];
+        widen8<HF32>(hr[i], h);
+        if (j < p.vecs) {
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                a[i][k] *= factor;
+            if (p.post != nullptr) {
+                weight8(p.post, 8 * j, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    a[i][k] *= w[k];
             }
-        }
-    };
-    load(blockIdx.x);
-    const float inv = 1.0f / static_cast<float>(p.H);
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        float a[V][8];
-        float s[1] = {0.f};
+            if (p.gate_kind == 1) {
+                weight8(p.gate, 8 * j, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            widen8<YF32>(yr[i], a[i]);
+                for (int k = 0; k < 8; ++k)
+                    a[i][k] *= w[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                a[i][k] = fmaf(p.scale, h[k], a[i][k]);
+            store8<HF32>(p.h_out, row * p.H + 8 * j, a[i], p.h_out != nullptr);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 s[0] = fmaf(a[i][k], a[i][k], s[0]);
         }
-        float factor = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
-        if (p.post != nullptr) {
-            row_sums<1>(s, buffer, turn, lane, warp, warps);
-            factor *= rsqrtf(s[0] * inv + p.eps);
-        }
-        s[0] = 0.f;
+    }
+    if (p.pre != nullptr) {
+        row_sums<1>(s, buffer, turn, lane, warp, warps);
+        const float r = rsqrtf(s[0] * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
-            float h[8];
-            widen8<HF32>(hr[i], h);
             if (j < p.vecs) {
                 float w[8];
+                weight8(p.pre, 8 * j, w);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    a[i][k] *= factor;
-                if (p.post != nullptr) {
-                    weight8(p.post, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        a[i][k] *= w[k];
-                }
-                if (p.gate_kind == 1) {
-                    weight8(p.gate, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        a[i][k] *= w[k];
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    a[i][k] = fmaf(p.scale, h[k], a[i][k]);
-                store8<HF32>(p.h_out, row * p.H + 8 * j, a[i], p.h_out != nullptr);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    s[0] = fmaf(a[i][k], a[i][k], s[0]);
-            }
-        }
-        load(row + gridDim.x);
-        if (p.pre != nullptr) {
-            row_sums<1>(s, buffer, turn, lane, warp, warps);
-            const float r = rsqrtf(s[0] * inv + p.eps);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int j = tid + i * nt;
-                if (j < p.vecs) {
-                    float w[8];
-                    weight8(p.pre, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        a[i][k] = a[i][k] * r * w[k];
-                    store8<false>(p.x, row * p.H + 8 * j, a[i]);
-                }
+                    a[i][k] = a[i][k] * r * w[k];
+                store8<false>(p.x, row * p.H + 8 * j, a[i]);
             }
         }
     }
@@ -240,200 +268,354 @@ __device__ __forceinline__ void add8(float *acc, const float (&v)[8])
     q[1] = b;
 }
 
-template <bool YF32, bool HF32, int V>
-__global__ void __launch_bounds__(kNormThreads<V>) block_norm_backward_kernel(const NormParams p)
+// One row's gradients; add_pre and add_post take vector i's terms of the sums over rows (dx n2; token gate g n1).
+template <bool YF32, bool HF32, int V, typename Fetch, typename Between, typename AddPre, typename AddPost>
+__device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t row, float inv, float (*buffer)[4][32], int &turn, int lane, int warp, int warps,
+                                                  Fetch &&fetch, Between &&between, AddPre &&add_pre, AddPost &&add_post)
 {
-    extern __shared__ float4 norm_smem[];
-    __shared__ float buffer[2][4][32];
-    pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
-    int turn = 0;
-    // this CTA's sums, an array of H for each that is wanted
-    float *sums = reinterpret_cast<float *>(norm_smem);
+    const int tid = threadIdx.x, nt = blockDim.x;
     const bool channel = p.gate_kind == 1;
-    float *const acc_pre = p.dpre != nullptr ? sums : nullptr;
-    float *const acc_post = p.dpost != nullptr ? sums + (p.dpre != nullptr ? p.H : 0) : nullptr;
-    float *const acc_gate = p.dgate != nullptr && channel ? sums + ((p.dpre != nullptr) + (p.dpost != nullptr)) * p.H : nullptr;
-    const int arrays = (acc_pre != nullptr) + (acc_post != nullptr) + (acc_gate != nullptr);
-    for (int n = 0; n < arrays; ++n)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = tid + i * nt;
-            if (j < p.vecs) {
-                norm_smem[n * 2 * p.vecs + 2 * j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                norm_smem[n * 2 * p.vecs + 2 * j + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        }
+    const bool second = p.post != nullptr || (p.gate_kind == 2 && p.dgate != nullptr);
     Row8<YF32> yr[V];
     Row8<HF32> hr[V], gr[V];
     Row8<false> xr[V];
-    auto load = [&](int64_t row) {
+    float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = tid + i * nt;
-            yr[i] = Row8<YF32>{};
-            hr[i] = gr[i] = Row8<HF32>{};
-            xr[i] = Row8<false>{};
-            if (j < p.vecs && row < p.T) {
-                if (p.y != nullptr)
-                    yr[i] = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
-                if (p.dx != nullptr) {
-                    hr[i] = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
-                    xr[i] = load_row8<false>(p.dx, row * p.lddx + 8 * j);
-                }
-                if (p.dh_out != nullptr)
-                    gr[i] = load_row8<HF32>(p.dh_out, row * p.lddh + 8 * j);
-            }
+    for (int i = 0; i < V; ++i) {
+        const int j = tid + i * nt;
+        fetch(i, yr[i], hr[i], gr[i], xr[i]);
+        float y[8], h[8], d[8], w[8];
+        widen8<YF32>(yr[i], y);
+        widen8<HF32>(hr[i], h);
+        widen8<false>(xr[i], d);
+        const bool pre = p.dx != nullptr && j < p.vecs;
+        if (pre)
+            weight8(p.pre, 8 * j, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            s[0] = fmaf(y[k], y[k], s[0]);
+            s[1] = fmaf(h[k], h[k], s[1]);
+            if (pre)
+                s[2] = fmaf(d[k] * w[k], h[k], s[2]);
         }
-    };
-    const float inv = 1.0f / static_cast<float>(p.H);
-    const bool second = p.post != nullptr || (p.gate_kind == 2 && p.dgate != nullptr);
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        load(row);
-        float s[3] = {0.f, 0.f, 0.f};
+    }
+    row_sums<3>(s, buffer, turn, lane, warp, warps);
+    between();
+    const float r1 = p.post != nullptr ? rsqrtf(s[0] * inv + p.eps) : 1.0f;
+    const float r2 = rsqrtf(s[1] * inv + p.eps);
+    const float c2 = r2 * s[2] * inv;  // mean(t n2)
+    const float token = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
+    float g[V][8];
+    float m[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = tid + i * nt;
-            float y[8], h[8], d[8], w[8];
-            widen8<YF32>(yr[i], y);
-            widen8<HF32>(hr[i], h);
-            widen8<false>(xr[i], d);
-            if (p.pre != nullptr && j < p.vecs)
+    for (int i = 0; i < V; ++i) {
+        const int j = tid + i * nt;
+        widen8<HF32>(gr[i], g[i]);
+        if (j < p.vecs) {
+            float w[8], q[8];
+            if (p.dx != nullptr) {
+                float h[8], d[8];
+                widen8<HF32>(hr[i], h);
+                widen8<false>(xr[i], d);
                 weight8(p.pre, 8 * j, w);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                s[0] = fmaf(y[k], y[k], s[0]);
-                s[1] = fmaf(h[k], h[k], s[1]);
-                if (p.pre != nullptr && j < p.vecs)
-                    s[2] = fmaf(d[k] * w[k], h[k], s[2]);
+                for (int k = 0; k < 8; ++k) {
+                    const float n = h[k] * r2;
+                    g[i][k] = fmaf(r2, fmaf(-n, c2, d[k] * w[k]), g[i][k]);
+                    d[k] *= n;
+                }
+                add_pre(i, d);
+            }
+            if (p.dh != nullptr) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = p.scale * g[i][k];
+                store8<HF32>(p.dh, row * p.H + 8 * j, v);
+            }
+            widen8<YF32>(yr[i], q);
+            {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    q[k] *= r1;  // n1
+                    v[k] = token * g[i][k] * q[k];
+                }
+                add_post(i, v);
+            }
+            if (channel) {
+                weight8(p.gate, 8 * j, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    g[i][k] *= w[k];
+            }
+            if (p.post != nullptr) {
+                weight8(p.post, 8 * j, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    g[i][k] *= w[k];
+            }
+            if (second) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    m[0] = fmaf(g[i][k], q[k], m[0]);
             }
         }
-        row_sums<3>(s, buffer, turn, lane, warp, warps);
-        const float r1 = p.post != nullptr ? rsqrtf(s[0] * inv + p.eps) : 1.0f;
-        const float r2 = rsqrtf(s[1] * inv + p.eps);
-        const float c2 = r2 * s[2] * inv;  // mean(t n2)
-        const float token = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
-        float g[V][8];
-        float m[1] = {0.f};
+    }
+    if (second)
+        row_sums<1>(m, buffer, turn, lane, warp, warps);
+    if (p.gate_kind == 2 && p.dgate != nullptr && tid == 0)
+        p.dgate[row] = m[0];
+    if (p.dy != nullptr) {
+        const float c1 = p.post != nullptr ? r1 * m[0] * inv : 0.f, factor = token * r1;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
-            widen8<HF32>(gr[i], g[i]);
             if (j < p.vecs) {
-                float w[8], y[8];
-                if (p.dx != nullptr) {
-                    float h[8], d[8];
-                    widen8<HF32>(hr[i], h);
-                    widen8<false>(xr[i], d);
-                    weight8(p.pre, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float n = h[k] * r2;
-                        g[i][k] = fmaf(r2, fmaf(-n, c2, d[k] * w[k]), g[i][k]);
-                        d[k] *= n;
-                    }
-                    if (acc_pre != nullptr)
-                        add8(acc_pre + 8 * j, d);
-                }
-                if (p.dh != nullptr) {
-                    float v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = p.scale * g[i][k];
-                    store8<HF32>(p.dh, row * p.H + 8 * j, v);
-                }
+                float y[8];
                 widen8<YF32>(yr[i], y);
-                float q[8];  // n1, times the weight's share below
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    q[k] = y[k] * r1;
-                if (acc_gate != nullptr) {
-                    float v[8];
-                    if (p.post != nullptr)
-                        weight8(p.post, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = g[i][k] * q[k] * (p.post != nullptr ? w[k] : 1.0f);
-                    add8(acc_gate + 8 * j, v);
-                }
-                if (channel) {
-                    weight8(p.gate, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        g[i][k] *= w[k];
-                }
-                if (acc_post != nullptr) {
-                    float v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = token * g[i][k] * q[k];
-                    add8(acc_post + 8 * j, v);
-                }
-                if (p.post != nullptr) {
-                    weight8(p.post, 8 * j, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        g[i][k] *= w[k];
-                }
-                if (second) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        m[0] = fmaf(g[i][k], q[k], m[0]);
-                }
+                    y[k] = factor * fmaf(-y[k], c1, g[i][k]);
+                store8<YF32>(p.dy, row * p.H + 8 * j, y);
             }
         }
-        if (second)
-            row_sums<1>(m, buffer, turn, lane, warp, warps);
-        if (p.gate_kind == 2 && p.dgate != nullptr && tid == 0)
-            p.dgate[row] = m[0];
-        if (p.dy != nullptr) {
-            const float c1 = p.post != nullptr ? r1 * m[0] * inv : 0.f;
+    }
+}
+
+// The ring's part of a kernel: run(row, stage, between) for each of the CTA's rows, where `between` is called by all threads
+// after a barrier that follows their last reads of the stage before.
+template <int N, typename Run>
+__device__ __forceinline__ void ring_rows(const NormParams &p, const RowSource &src, unsigned char *smem, uint64_t *full, Run &&run)
+{
+    const int tid = threadIdx.x;
+    const uint32_t base = smem_u32(smem), full0 = smem_u32(full);
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s)
+            mbar_init(full0 + 8 * s, 1);
+        fence_mbar_init();
+        for (int s = 0; s < p.stages; ++s) {
+            const int64_t row = blockIdx.x + int64_t{s} * gridDim.x;
+            if (row < p.T)
+                fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, row);
+        }
+    }
+    __syncthreads();
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        if (ok && !mbar_wait_cycles(full0 + 8 * slot, phase, kNormWait)) {  // a copy that never lands: its rows are garbage, and told
+            ok = false;
+            atomicOr(p.fault, 1u);
+        }
+        run(row, smem + slot * src.stage, [&]() {
+            const int64_t next = row + (int64_t{p.stages} - 1) * gridDim.x;  // into the stage of the row before
+            if (tid == 0 && row != blockIdx.x && next < p.T) {
+                const int s = slot == 0 ? p.stages - 1 : slot - 1;
+                fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, next);
+            }
+        });
+        if (++slot == p.stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+template <bool YF32, bool HF32, int V>
+__global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_kernel(const NormParams p)
+{
+    extern __shared__ float4 norm_smem[];
+    __shared__ float buffer[2][4][32];
+    __shared__ uint64_t full[kNormMaxStages];
+    pdl_wait_and_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const float inv = 1.0f / static_cast<float>(p.H);
+    int turn = 0;
+    RowSource src{};
+    add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
+    add_source(src, 1, p.h, p.ldh, p.H, HF32 ? 4 : 2);
+    ring_rows<2>(p, src, reinterpret_cast<unsigned char *>(norm_smem), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
+        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h) {
+            const int j = tid + i * nt;
+            y = Row8<YF32>{};
+            h = Row8<HF32>{};
+            if (j < p.vecs) {
+                y = stage_row8<YF32>(stage, src, 0, j);
+                h = stage_row8<HF32>(stage, src, 1, j);
+            }
+        };
+        norm_row<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, between);
+    });
+}
+
+template <bool YF32, bool HF32, int V>
+__global__ void __launch_bounds__(kNormThreads) block_norm_long_kernel(const NormParams p)
+{
+    __shared__ float buffer[2][4][32];
+    pdl_wait_and_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const float inv = 1.0f / static_cast<float>(p.H);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h) {
+            const int j = tid + i * nt;
+            y = Row8<YF32>{};
+            h = Row8<HF32>{};
+            if (j < p.vecs) {
+                if (p.y != nullptr)
+                    y = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
+                h = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
+            }
+        };
+        norm_row<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, [] {});
+    }
+}
+
+// A CTA's sums over its rows: [2][H] of the workspace (dx n2, then g n1).
+template <int V>
+__device__ __forceinline__ float *partial_of(const NormParams &p, int n, int j)
+{
+    return p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + n) * p.H + 8 * j;
+}
+
+template <bool YF32, bool HF32, int V>
+__global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(const NormParams p)
+{
+    extern __shared__ float4 norm_smem[];
+    __shared__ float buffer[2][4][32];
+    __shared__ uint64_t full[kNormMaxStages];
+    pdl_wait_and_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const float inv = 1.0f / static_cast<float>(p.H);
+    int turn = 0;
+    RowSource src{};
+    add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
+    add_source(src, 1, p.dx != nullptr ? p.h : nullptr, p.ldh, p.H, HF32 ? 4 : 2);
+    add_source(src, 2, p.dh_out, p.lddh, p.H, HF32 ? 4 : 2);
+    add_source(src, 3, p.dx, p.lddx, p.H, 2);
+    float acc[2][V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            acc[0][i][k] = acc[1][i][k] = 0.f;
+    ring_rows<4>(p, src, reinterpret_cast<unsigned char *>(norm_smem), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
+        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h, Row8<HF32> &g, Row8<false> &x) {
+            const int j = tid + i * nt;
+            y = Row8<YF32>{};
+            h = g = Row8<HF32>{};
+            x = Row8<false>{};
+            if (j < p.vecs) {
+                y = stage_row8<YF32>(stage, src, 0, j);
+                h = stage_row8<HF32>(stage, src, 1, j);
+                g = stage_row8<HF32>(stage, src, 2, j);
+                x = stage_row8<false>(stage, src, 3, j);
+            }
+        };
+        auto add = [&](int n, int i, const float (&v)[8]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                acc[n][i][k] += v[k];
+        };
+        norm_row_backward<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, between, [&](int i, const float (&v)[8]) { add(0, i, v); },
+                                         [&](int i, const float (&v)[8]) { add(1, i, v); });
+    });
+    if (p.partial != nullptr) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int j = tid + i * nt;
                 if (j < p.vecs) {
-                    float y[8];
-                    widen8<YF32>(yr[i], y);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        y[k] = token * r1 * fmaf(-y[k], c1, g[i][k]);
-                    store8<YF32>(p.dy, row * p.H + 8 * j, y);
+                    float4 *to = reinterpret_cast<float4 *>(partial_of<V>(p, n, j));
+                    to[0] = make_float4(acc[n][i][0], acc[n][i][1], acc[n][i][2], acc[n][i][3]);
+                    to[1] = make_float4(acc[n][i][4], acc[n][i][5], acc[n][i][6], acc[n][i][7]);
                 }
             }
-        }
     }
-    for (int n = 0; n < arrays; ++n)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = tid + i * nt;
-            if (j < p.vecs) {
-                float4 *to = reinterpret_cast<float4 *>(p.partial + (static_cast<int64_t>(blockIdx.x) * arrays + n) * p.H + 8 * j);
-                to[0] = norm_smem[n * 2 * p.vecs + 2 * j];
-                to[1] = norm_smem[n * 2 * p.vecs + 2 * j + 1];
-            }
-        }
 }
 
-// The CTAs' sums, in order: a warp takes 32 columns of an array's rows w, w + 8, ...; the eight warps' are added in order.
+template <bool YF32, bool HF32, int V>
+__global__ void __launch_bounds__(kNormThreads) block_norm_backward_long_kernel(const NormParams p)
+{
+    extern __shared__ float4 norm_smem[];  // the CTA's sums [2][H]
+    __shared__ float buffer[2][4][32];
+    pdl_wait_and_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const float inv = 1.0f / static_cast<float>(p.H);
+    int turn = 0;
+    float *acc = reinterpret_cast<float *>(norm_smem);
+    auto each = [&](auto &&f) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (tid + i * nt < p.vecs)
+                    f(n, tid + i * nt, reinterpret_cast<float4 *>(acc + n * p.H + 8 * (tid + i * nt)));
+    };
+    each([](int, int, float4 *a) { a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f); });
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h, Row8<HF32> &g, Row8<false> &x) {
+            const int j = tid + i * nt;
+            y = Row8<YF32>{};
+            h = g = Row8<HF32>{};
+            x = Row8<false>{};
+            if (j < p.vecs) {
+                if (p.y != nullptr)
+                    y = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
+                if (p.dx != nullptr) {
+                    h = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
+                    x = load_row8<false>(p.dx, row * p.lddx + 8 * j);
+                }
+                if (p.dh_out != nullptr)
+                    g = load_row8<HF32>(p.dh_out, row * p.lddh + 8 * j);
+            }
+        };
+        norm_row_backward<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, [] {},
+                                         [&](int i, const float (&v)[8]) { add8(acc + 8 * (tid + i * nt), v); },
+                                         [&](int i, const float (&v)[8]) { add8(acc + p.H + 8 * (tid + i * nt), v); });
+    }
+    if (p.partial != nullptr)
+        each([&](int n, int j, float4 *a) {
+            float4 *to = reinterpret_cast<float4 *>(partial_of<V>(p, n, j));
+            to[0] = a[0];
+            to[1] = a[1];
+        });
+}
+
+// The CTAs' sums, in order: a warp takes 32 columns of rows w, w + 8, ...; the eight warps' are added in order.
 constexpr int kNormReduceThreads = 256;
-__global__ void __launch_bounds__(kNormReduceThreads) block_norm_reduce_kernel(const float *partial, int ctas, int arrays, int H, float *a, float *b, float *c)
+__global__ void __launch_bounds__(kNormReduceThreads) block_norm_reduce_kernel(const NormParams p, int ctas)
 {
     __shared__ float part[8][32];
     pdl_wait_and_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t col = blockIdx.x * int64_t{32} + lane, width = static_cast<int64_t>(arrays) * H;  // H is a multiple of 8
+    const int64_t col = blockIdx.x * int64_t{32} + lane, width = 2 * static_cast<int64_t>(p.H);
     float s = 0.f;
-    if (col < width)
+    if (col < width) {
+#pragma unroll 4
         for (int r = warp; r < ctas; r += 8)
-            s += partial[r * width + col];
+            s += p.partial[r * width + col];
+    }
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && col < width) {
 #pragma unroll
         for (int w = 1; w < 8; ++w)
             s += part[w][lane];
-        const int n = static_cast<int>(col / H);
-        (n == 0 ? a : n == 1 ? b : c)[col - static_cast<int64_t>(n) * H] = s;
+        const bool channel = p.gate_kind == 1;
+        if (col < p.H) {
+            if (p.dpre != nullptr)
+                p.dpre[col] = s;
+        } else {
+            const int c = static_cast<int>(col) - p.H;
+            if (p.dpost != nullptr)
+                p.dpost[c] = channel ? p.gate[c] * s : s;
+            if (p.dgate != nullptr && channel)
+                p.dgate[c] = p.post != nullptr ? p.post[c] * s : s;
+        }
     }
 }
 
