@@ -16,6 +16,7 @@ using namespace mxfp8;
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 constexpr int kMostSmem = 224 * 1024;
 constexpr int kRingBytes = 128 * 1024;
+constexpr int kKeepBytes = 192 * 1024;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -89,11 +90,15 @@ mxfp8_status_t launch_types(NormParams p, int row_bytes, int device, cudaStream_
         else
             return launch_rows<block_norm_long_kernel<YF32, HF32, 4>>(p, threads, 0, most, device, stream, grid);
     }
-    // an SM's CTAs keep as many rows in flight as leave L1 room for the weights
-    const int per_sm = 1024 / threads < 1 ? 1 : 1024 / threads;
-    const int room = kRingBytes / (BACKWARD && v == 2 ? 1 : per_sm < 8 ? per_sm : 8);
+    // An SM's CTAs share kRingBytes for their rings (the rest is left to L1), with two stages at least, and keep the weights (the
+    // forward pass the factors behind the block alone) where there is room.
+    const int fits = 1024 / threads < 1 ? 1 : 1024 / threads < 8 ? 1024 / threads : 8;
+    const int per_sm = BACKWARD && v == 2 ? 1 : fits;
+    const int room = kRingBytes / per_sm;
     p.stages = room / row_bytes < 2 ? 2 : room / row_bytes < kNormMaxStages ? room / row_bytes : kNormMaxStages;
-    const int smem = p.stages * row_bytes;
+    const int back = p.post != nullptr || p.gate_kind == BLOCK_GATE_CHANNEL ? p.H * 4 : 0, pre = BACKWARD && p.pre != nullptr ? p.H * 4 : 0;
+    p.keep = p.stages * row_bytes + back + pre <= kKeepBytes / per_sm;
+    const int smem = p.stages * row_bytes + (p.keep ? back + pre : 0);
     if constexpr (BACKWARD)
         return v == 1 ? launch_rows<block_norm_backward_ring_kernel<YF32, HF32, 1>>(p, threads, smem, most, device, stream, grid)
                       : launch_rows<block_norm_backward_ring_kernel<YF32, HF32, 2>>(p, threads, smem, most, device, stream, grid);

@@ -37,6 +37,7 @@ struct NormParams {
     void *dh, *dy;
     float *dpre, *dpost, *dgate, *partial;
     int stages;                        // of the ring
+    bool keep;                         // the weights are kept in shared memory, before the ring
     unsigned *fault;
 };
 
@@ -119,32 +120,55 @@ __device__ __forceinline__ void weight8(const float *w, int at, float (&v)[8])
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// Sums of N values over the CTA, the same in every thread; one barrier.  `turn` alternates between two buffers, so that a
-// buffer is written again only after a barrier that follows its last reads.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (*buffer)[4][32], int &turn, int lane, int warp, int warps)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            s[n] += __shfl_xor_sync(0xFFFFFFFFu, s[n], d);
-    if (lane == 0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            buffer[turn][n][warp] = s[n];
+// Sums over the CTA (at most 16 warps), the same in every thread; one barrier.  `turn` alternates between two buffers, so
+// that a buffer is written again only after a barrier that follows its last reads; the warps that a CTA does not have count
+// zeros, which clear() leaves there (before a barrier).
+struct RowSums {
+    float buffer[2][16][4];
+
+    __device__ __forceinline__ void clear()
+    {
+        for (int i = threadIdx.x; i < 2 * 16 * 4; i += blockDim.x)
+            (&buffer[0][0][0])[i] = 0.f;
     }
-    __syncthreads();
+    __device__ __forceinline__ float one(float s, int &turn, int lane, int warp)
+    {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-        s[n] = lane < warps ? buffer[turn][n][lane] : 0.f;
+        for (int d = 16; d > 0; d >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane == 0)
+            buffer[turn][warp][0] = s;
+        __syncthreads();
+        s = buffer[turn][lane & 15][0];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
+        for (int d = 8; d > 0; d >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        turn ^= 1;
+        return s;
+    }
+    // Three sums.  Each exchange with a lane half as far halves the values that a lane carries (12 shuffles for 30).
+    __device__ __forceinline__ void three(float (&s)[3], int &turn, int lane, int warp)
+    {
+        const bool b4 = lane & 16, b3 = lane & 8;
+        const float a0 = (b4 ? s[2] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[0] : s[2], 16);
+        const float a1 = (b4 ? 0.f : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[1] : 0.f, 16);
+        float v = (b3 ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, b3 ? a0 : a1, 8);  // the sum numbered lane / 8
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-            s[n] += __shfl_xor_sync(0xFFFFFFFFu, s[n], d);
-    turn ^= 1;
-}
+        for (int d = 4; d > 0; d >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        if ((lane & 7) == 0)
+            buffer[turn][warp][lane >> 3] = v;
+        __syncthreads();
+        v = buffer[turn][lane >> 2][lane & 3] + buffer[turn][8 + (lane >> 2)][lane & 3];
+#pragma unroll
+        for (int d = 16; d > 2; d >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+            s[n] = __shfl_sync(0xFFFFFFFFu, v, n);
+        turn ^= 1;
+    }
+};
 
 // The ring: stage n % stages holds the CTA's n-th row of each input, one after the other.
 struct RowSource {
@@ -185,48 +209,110 @@ __device__ __forceinline__ Row8<F32> stage_row8(const unsigned char *stage, cons
     return r;
 }
 
-// y, h -> h', x.  One row; `fetch` gives vector i of it.
-template <bool YF32, bool HF32, int V, typename Fetch, typename Between>
-__device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float inv, float (*buffer)[4][32], int &turn, int lane, int warp, int warps, Fetch &&fetch,
+// A row's vectors for the passes over it.  From a stage of the ring they are read each time that they are wanted, which keeps
+// them out of the registers that the sums need; a long row's are loaded once.
+template <bool YF32, bool HF32>
+struct StageRow {
+    const unsigned char *stage;
+    const RowSource &src;
+    int vecs;
+
+    __device__ __forceinline__ Row8<YF32> y(int, int j) const { return at<YF32>(0, j); }
+    __device__ __forceinline__ Row8<HF32> h(int, int j) const { return at<HF32>(1, j); }
+    __device__ __forceinline__ Row8<HF32> g(int, int j) const { return at<HF32>(2, j); }
+    __device__ __forceinline__ Row8<false> x(int, int j) const { return at<false>(3, j); }
+    template <bool F32>
+    __device__ __forceinline__ Row8<F32> at(int n, int j) const
+    {
+        return j < vecs ? stage_row8<F32>(stage, src, n, j) : Row8<F32>{};
+    }
+};
+template <bool YF32, bool HF32, int V, bool BACKWARD>
+struct LoadedRow {
+    Row8<YF32> y_[V];
+    Row8<HF32> h_[V], g_[BACKWARD ? V : 1];
+    Row8<false> x_[BACKWARD ? V : 1];
+
+    __device__ __forceinline__ LoadedRow(const NormParams &p, int64_t row)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = threadIdx.x + i * blockDim.x;
+            y_[i] = Row8<YF32>{};
+            h_[i] = Row8<HF32>{};
+            if (j < p.vecs && p.y != nullptr)
+                y_[i] = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
+            if (j < p.vecs && (!BACKWARD || p.dx != nullptr))
+                h_[i] = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
+            if constexpr (BACKWARD) {
+                g_[i] = Row8<HF32>{};
+                x_[i] = Row8<false>{};
+                if (j < p.vecs && p.dx != nullptr)
+                    x_[i] = load_row8<false>(p.dx, row * p.lddx + 8 * j);
+                if (j < p.vecs && p.dh_out != nullptr)
+                    g_[i] = load_row8<HF32>(p.dh_out, row * p.lddh + 8 * j);
+            }
+        }
+    }
+    __device__ __forceinline__ Row8<YF32> y(int i, int) const { return y_[i]; }
+    __device__ __forceinline__ Row8<HF32> h(int i, int) const { return h_[i]; }
+    __device__ __forceinline__ Row8<HF32> g(int i, int) const { return g_[i]; }
+    __device__ __forceinline__ Row8<false> x(int i, int) const { return x_[i]; }
+};
+
+// w_post * gate of vector j, the factors of a channel behind the block: from `back`, where the CTA keeps the products, or
+// from the two.  False without either.
+__device__ __forceinline__ bool back_weight8(const NormParams &p, const float *back, int j, float (&w)[8])
+{
+    if (back != nullptr) {
+        const float4 a = reinterpret_cast<const float4 *>(back)[2 * j], b = reinterpret_cast<const float4 *>(back)[2 * j + 1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        return true;
+    }
+    const bool channel = p.gate_kind == 1;
+    if (p.post != nullptr)
+        weight8(p.post, 8 * j, w);
+    if (channel) {
+        float v[8];
+        weight8(p.gate, 8 * j, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            w[k] = p.post != nullptr ? w[k] * v[k] : v[k];
+    }
+    return p.post != nullptr || channel;
+}
+
+// y, h -> h', x of one row.
+template <bool YF32, bool HF32, int V, typename Row, typename Between>
+__device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float inv, const float *back, RowSums &sums, int &turn, int lane, int warp, const Row &in,
                                          Between &&between)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
     float a[V][8];
-    Row8<HF32> hr[V];
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        Row8<YF32> yr;
-        fetch(i, yr, hr[i]);
-        widen8<YF32>(yr, a[i]);
+        widen8<YF32>(in.y(i, tid + i * nt), a[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            s[0] = fmaf(a[i][k], a[i][k], s[0]);
+            s = fmaf(a[i][k], a[i][k], s);
     }
     float factor = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
-    row_sums<1>(s, buffer, turn, lane, warp, warps);
+    s = sums.one(s, turn, lane, warp);
     between();
     if (p.post != nullptr)
-        factor *= rsqrtf(s[0] * inv + p.eps);
-    s[0] = 0.f;
+        factor *= rsqrtf(s * inv + p.eps);
+    s = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = tid + i * nt;
-        float h[8];
-        widen8<HF32>(hr[i], h);
         if (j < p.vecs) {
-            float w[8];
+            float w[8], h[8];
+            widen8<HF32>(in.h(i, j), h);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 a[i][k] *= factor;
-            if (p.post != nullptr) {
-                weight8(p.post, 8 * j, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    a[i][k] *= w[k];
-            }
-            if (p.gate_kind == 1) {
-                weight8(p.gate, 8 * j, w);
+            if (back_weight8(p, back, j, w)) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     a[i][k] *= w[k];
@@ -237,12 +323,12 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
             store8<HF32>(p.h_out, row * p.H + 8 * j, a[i], p.h_out != nullptr);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                s[0] = fmaf(a[i][k], a[i][k], s[0]);
+                s = fmaf(a[i][k], a[i][k], s);
         }
     }
     if (p.pre != nullptr) {
-        row_sums<1>(s, buffer, turn, lane, warp, warps);
-        const float r = rsqrtf(s[0] * inv + p.eps);
+        s = sums.one(s, turn, lane, warp);
+        const float r = rsqrtf(s * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
@@ -258,6 +344,13 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
     }
 }
 
+// Eight values of a weight that may be kept in shared memory.
+__device__ __forceinline__ void kept8(const float *w, int j, float (&v)[8])
+{
+    const float4 a = reinterpret_cast<const float4 *>(w)[2 * j], b = reinterpret_cast<const float4 *>(w)[2 * j + 1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
 // acc[0 .. 7] += v, in shared memory that this thread alone uses.
 __device__ __forceinline__ void add8(float *acc, const float (&v)[8])
 {
@@ -269,28 +362,23 @@ __device__ __forceinline__ void add8(float *acc, const float (&v)[8])
 }
 
 // One row's gradients; add_pre and add_post take vector i's terms of the sums over rows (dx n2; token gate g n1).
-template <bool YF32, bool HF32, int V, typename Fetch, typename Between, typename AddPre, typename AddPost>
-__device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t row, float inv, float (*buffer)[4][32], int &turn, int lane, int warp, int warps,
-                                                  Fetch &&fetch, Between &&between, AddPre &&add_pre, AddPost &&add_post)
+template <bool YF32, bool HF32, int V, typename Row, typename Between, typename AddPre, typename AddPost>
+__device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t row, float inv, const float *pre_weight, const float *back, RowSums &sums, int &turn, int lane,
+                                                  int warp, const Row &in, Between &&between, AddPre &&add_pre, AddPost &&add_post)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
-    const bool channel = p.gate_kind == 1;
     const bool second = p.post != nullptr || (p.gate_kind == 2 && p.dgate != nullptr);
-    Row8<YF32> yr[V];
-    Row8<HF32> hr[V], gr[V];
-    Row8<false> xr[V];
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = tid + i * nt;
-        fetch(i, yr[i], hr[i], gr[i], xr[i]);
         float y[8], h[8], d[8], w[8];
-        widen8<YF32>(yr[i], y);
-        widen8<HF32>(hr[i], h);
-        widen8<false>(xr[i], d);
+        widen8<YF32>(in.y(i, j), y);
+        widen8<HF32>(in.h(i, j), h);
+        widen8<false>(in.x(i, j), d);
         const bool pre = p.dx != nullptr && j < p.vecs;
         if (pre)
-            weight8(p.pre, 8 * j, w);
+            kept8(pre_weight, j, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             s[0] = fmaf(y[k], y[k], s[0]);
@@ -299,25 +387,25 @@ __device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t r
                 s[2] = fmaf(d[k] * w[k], h[k], s[2]);
         }
     }
-    row_sums<3>(s, buffer, turn, lane, warp, warps);
+    sums.three(s, turn, lane, warp);
     between();
     const float r1 = p.post != nullptr ? rsqrtf(s[0] * inv + p.eps) : 1.0f;
     const float r2 = rsqrtf(s[1] * inv + p.eps);
     const float c2 = r2 * s[2] * inv;  // mean(t n2)
     const float token = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
     float g[V][8];
-    float m[1] = {0.f};
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = tid + i * nt;
-        widen8<HF32>(gr[i], g[i]);
+        widen8<HF32>(in.g(i, j), g[i]);
         if (j < p.vecs) {
             float w[8], q[8];
             if (p.dx != nullptr) {
                 float h[8], d[8];
-                widen8<HF32>(hr[i], h);
-                widen8<false>(xr[i], d);
-                weight8(p.pre, 8 * j, w);
+                widen8<HF32>(in.h(i, j), h);
+                widen8<false>(in.x(i, j), d);
+                kept8(pre_weight, j, w);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float n = h[k] * r2;
@@ -333,7 +421,7 @@ __device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t r
                     v[k] = p.scale * g[i][k];
                 store8<HF32>(p.dh, row * p.H + 8 * j, v);
             }
-            widen8<YF32>(yr[i], q);
+            widen8<YF32>(in.y(i, j), q);
             {
                 float v[8];
 #pragma unroll
@@ -343,14 +431,7 @@ __device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t r
                 }
                 add_post(i, v);
             }
-            if (channel) {
-                weight8(p.gate, 8 * j, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    g[i][k] *= w[k];
-            }
-            if (p.post != nullptr) {
-                weight8(p.post, 8 * j, w);
+            if (back_weight8(p, back, j, w)) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     g[i][k] *= w[k];
@@ -358,22 +439,22 @@ __device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t r
             if (second) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    m[0] = fmaf(g[i][k], q[k], m[0]);
+                    m = fmaf(g[i][k], q[k], m);
             }
         }
     }
     if (second)
-        row_sums<1>(m, buffer, turn, lane, warp, warps);
+        m = sums.one(m, turn, lane, warp);
     if (p.gate_kind == 2 && p.dgate != nullptr && tid == 0)
-        p.dgate[row] = m[0];
+        p.dgate[row] = m;
     if (p.dy != nullptr) {
-        const float c1 = p.post != nullptr ? r1 * m[0] * inv : 0.f, factor = token * r1;
+        const float c1 = p.post != nullptr ? r1 * m * inv : 0.f, factor = token * r1;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
             if (j < p.vecs) {
                 float y[8];
-                widen8<YF32>(yr[i], y);
+                widen8<YF32>(in.y(i, j), y);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     y[k] = factor * fmaf(-y[k], c1, g[i][k]);
@@ -381,6 +462,26 @@ __device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t r
             }
         }
     }
+}
+
+// The products of w_post and gate of this thread's columns into shared memory at `kept`, which then points behind them.
+// (Only the thread that writes them reads them.)
+template <int V>
+__device__ __forceinline__ const float *keep_back(const NormParams &p, float *&kept)
+{
+    if (!p.keep || (p.post == nullptr && p.gate_kind != 1))
+        return nullptr;
+    float *const back = kept;
+    for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * blockDim.x;
+        if (j < p.vecs) {
+            float w[8];
+            back_weight8(p, nullptr, j, w);
+            store8<true>(back, 8 * j, w);
+        }
+    }
+    kept += p.H;
+    return back;
 }
 
 // The ring's part of a kernel: run(row, stage, between) for each of the CTA's rows, where `between` is called by all threads
@@ -427,49 +528,35 @@ template <bool YF32, bool HF32, int V>
 __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];
-    __shared__ float buffer[2][4][32];
+    __shared__ RowSums sums;
     __shared__ uint64_t full[kNormMaxStages];
     pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const float inv = 1.0f / static_cast<float>(p.H);
     int turn = 0;
+    sums.clear();
     RowSource src{};
     add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
     add_source(src, 1, p.h, p.ldh, p.H, HF32 ? 4 : 2);
-    ring_rows<2>(p, src, reinterpret_cast<unsigned char *>(norm_smem), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
-        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h) {
-            const int j = tid + i * nt;
-            y = Row8<YF32>{};
-            h = Row8<HF32>{};
-            if (j < p.vecs) {
-                y = stage_row8<YF32>(stage, src, 0, j);
-                h = stage_row8<HF32>(stage, src, 1, j);
-            }
-        };
-        norm_row<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, between);
+    float *kept = reinterpret_cast<float *>(norm_smem);
+    const float *back = keep_back<V>(p, kept);
+    ring_rows<2>(p, src, reinterpret_cast<unsigned char *>(kept), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
+        norm_row<YF32, HF32, V>(p, row, inv, back, sums, turn, lane, warp, StageRow<YF32, HF32>{stage, src, p.vecs}, between);
     });
 }
 
 template <bool YF32, bool HF32, int V>
 __global__ void __launch_bounds__(kNormThreads) block_norm_long_kernel(const NormParams p)
 {
-    __shared__ float buffer[2][4][32];
+    __shared__ RowSums sums;
     pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const float inv = 1.0f / static_cast<float>(p.H);
     int turn = 0;
+    sums.clear();
+    __syncthreads();
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h) {
-            const int j = tid + i * nt;
-            y = Row8<YF32>{};
-            h = Row8<HF32>{};
-            if (j < p.vecs) {
-                if (p.y != nullptr)
-                    y = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
-                h = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
-            }
-        };
-        norm_row<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, [] {});
+        norm_row<YF32, HF32, V>(p, row, inv, nullptr, sums, turn, lane, warp, LoadedRow<YF32, HF32, V, false>(p, row), [] {});
     }
 }
 
@@ -484,12 +571,13 @@ template <bool YF32, bool HF32, int V>
 __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];
-    __shared__ float buffer[2][4][32];
+    __shared__ RowSums sums;
     __shared__ uint64_t full[kNormMaxStages];
     pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const float inv = 1.0f / static_cast<float>(p.H);
     int turn = 0;
+    sums.clear();
     RowSource src{};
     add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
     add_source(src, 1, p.dx != nullptr ? p.h : nullptr, p.ldh, p.H, HF32 ? 4 : 2);
@@ -501,25 +589,27 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             acc[0][i][k] = acc[1][i][k] = 0.f;
-    ring_rows<4>(p, src, reinterpret_cast<unsigned char *>(norm_smem), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
-        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h, Row8<HF32> &g, Row8<false> &x) {
+    float *kept = reinterpret_cast<float *>(norm_smem);
+    const float *back = keep_back<V>(p, kept), *pre = p.pre;
+    if (p.keep && p.pre != nullptr) {
+        for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
-            y = Row8<YF32>{};
-            h = g = Row8<HF32>{};
-            x = Row8<false>{};
             if (j < p.vecs) {
-                y = stage_row8<YF32>(stage, src, 0, j);
-                h = stage_row8<HF32>(stage, src, 1, j);
-                g = stage_row8<HF32>(stage, src, 2, j);
-                x = stage_row8<false>(stage, src, 3, j);
+                float w[8];
+                weight8(p.pre, 8 * j, w);
+                store8<true>(kept, 8 * j, w);
             }
-        };
+        }
+        pre = kept;
+        kept += p.H;
+    }
+    ring_rows<4>(p, src, reinterpret_cast<unsigned char *>(kept), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
         auto add = [&](int n, int i, const float (&v)[8]) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 acc[n][i][k] += v[k];
         };
-        norm_row_backward<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, between, [&](int i, const float (&v)[8]) { add(0, i, v); },
+        norm_row_backward<YF32, HF32, V>(p, row, inv, pre, back, sums, turn, lane, warp, StageRow<YF32, HF32>{stage, src, p.vecs}, between, [&](int i, const float (&v)[8]) { add(0, i, v); },
                                          [&](int i, const float (&v)[8]) { add(1, i, v); });
     });
     if (p.partial != nullptr) {
@@ -541,11 +631,13 @@ template <bool YF32, bool HF32, int V>
 __global__ void __launch_bounds__(kNormThreads) block_norm_backward_long_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];  // the CTA's sums [2][H]
-    __shared__ float buffer[2][4][32];
+    __shared__ RowSums sums;
     pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const float inv = 1.0f / static_cast<float>(p.H);
     int turn = 0;
+    sums.clear();
+    __syncthreads();
     float *acc = reinterpret_cast<float *>(norm_smem);
     auto each = [&](auto &&f) {
 #pragma unroll
@@ -557,23 +649,7 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_long_kernel(
     };
     each([](int, int, float4 *a) { a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f); });
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        auto fetch = [&](int i, Row8<YF32> &y, Row8<HF32> &h, Row8<HF32> &g, Row8<false> &x) {
-            const int j = tid + i * nt;
-            y = Row8<YF32>{};
-            h = g = Row8<HF32>{};
-            x = Row8<false>{};
-            if (j < p.vecs) {
-                if (p.y != nullptr)
-                    y = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
-                if (p.dx != nullptr) {
-                    h = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
-                    x = load_row8<false>(p.dx, row * p.lddx + 8 * j);
-                }
-                if (p.dh_out != nullptr)
-                    g = load_row8<HF32>(p.dh_out, row * p.lddh + 8 * j);
-            }
-        };
-        norm_row_backward<YF32, HF32, V>(p, row, inv, buffer, turn, lane, warp, warps, fetch, [] {},
+        norm_row_backward<YF32, HF32, V>(p, row, inv, p.pre, nullptr, sums, turn, lane, warp, LoadedRow<YF32, HF32, V, true>(p, row), [] {},
                                          [&](int i, const float (&v)[8]) { add8(acc + 8 * (tid + i * nt), v); },
                                          [&](int i, const float (&v)[8]) { add8(acc + p.H + 8 * (tid + i * nt), v); });
     }
