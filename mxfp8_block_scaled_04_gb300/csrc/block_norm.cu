@@ -16,7 +16,7 @@ using namespace mxfp8;
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 constexpr int kMostSmem = 224 * 1024;
 constexpr int kRingBytes = 128 * 1024;
-constexpr int kKeepBytes = 192 * 1024;
+constexpr int kKeepBytes = kMostSmem;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

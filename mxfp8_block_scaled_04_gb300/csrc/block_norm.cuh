@@ -68,56 +68,100 @@ __device__ __forceinline__ Row8<F32> load_row8(const void *base, int64_t at)
         r.hi = load_stream(p + 16);
     return r;
 }
+// Eight fp32 values as four pairs, for the packed operations (half the instructions; each lane rounds as a scalar).
+struct Vec8 {
+    uint64_t p[4];
+
+    static __device__ __forceinline__ Vec8 splat(float a) { return {f2_splat(a), f2_splat(a), f2_splat(a), f2_splat(a)}; }
+};
+__device__ __forceinline__ Vec8 operator*(const Vec8 &a, const Vec8 &b) { return {f2_mul(a.p[0], b.p[0]), f2_mul(a.p[1], b.p[1]), f2_mul(a.p[2], b.p[2]), f2_mul(a.p[3], b.p[3])}; }
+__device__ __forceinline__ Vec8 operator*(const Vec8 &a, float b)
+{
+    const uint64_t s = f2_splat(b);
+    return {f2_mul(a.p[0], s), f2_mul(a.p[1], s), f2_mul(a.p[2], s), f2_mul(a.p[3], s)};
+}
+__device__ __forceinline__ Vec8 operator+(const Vec8 &a, const Vec8 &b) { return {f2_add(a.p[0], b.p[0]), f2_add(a.p[1], b.p[1]), f2_add(a.p[2], b.p[2]), f2_add(a.p[3], b.p[3])}; }
+__device__ __forceinline__ Vec8 fma8(const Vec8 &a, const Vec8 &b, const Vec8 &c)
+{
+    return {f2_fma(a.p[0], b.p[0], c.p[0]), f2_fma(a.p[1], b.p[1], c.p[1]), f2_fma(a.p[2], b.p[2], c.p[2]), f2_fma(a.p[3], b.p[3], c.p[3])};
+}
+__device__ __forceinline__ Vec8 fma8(const Vec8 &a, float b, const Vec8 &c)
+{
+    const uint64_t s = f2_splat(b);
+    return {f2_fma(a.p[0], s, c.p[0]), f2_fma(a.p[1], s, c.p[1]), f2_fma(a.p[2], s, c.p[2]), f2_fma(a.p[3], s, c.p[3])};
+}
+// sum += a . b, in two strands that total() adds.
+__device__ __forceinline__ void dot8(uint64_t &sum, const Vec8 &a, const Vec8 &b)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        sum = f2_fma(a.p[k], b.p[k], sum);
+}
+__device__ __forceinline__ float total(uint64_t sum)
+{
+    float lo, hi;
+    f2_unpack(sum, lo, hi);
+    return lo + hi;
+}
+
 template <bool F32>
-__device__ __forceinline__ void widen8(const Row8<F32> &r, float (&v)[8])
+__device__ __forceinline__ Vec8 widen8(const Row8<F32> &r)
 {
     if constexpr (F32) {
         const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+        Vec8 v;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = __uint_as_float(w[k]);
+        for (int k = 0; k < 4; ++k)
+            v.p[k] = f2_pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        return v;
     } else {
         const uint32_t w[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
+        Vec8 v;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = bf16_lo(w[k]);
-            v[2 * k + 1] = bf16_hi(w[k]);
-        }
+        for (int k = 0; k < 4; ++k)
+            v.p[k] = f2_pack(bf16_lo(w[k]), bf16_hi(w[k]));
+        return v;
     }
 }
-__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi)
+__device__ __forceinline__ uint32_t round_bf16x2(uint64_t pair)
 {
+    float lo, hi;
+    f2_unpack(pair, lo, hi);
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 // Store eight elements; v becomes what was stored.
 template <bool F32>
-__device__ __forceinline__ void store8(void *base, int64_t at, float (&v)[8], bool write = true)
+__device__ __forceinline__ void store8(void *base, int64_t at, Vec8 &v, bool write = true)
 {
     unsigned char *p = static_cast<unsigned char *>(base) + at * (F32 ? 4 : 2);
     if constexpr (F32) {
         if (write) {
-            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(p + 16) = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v.p[0], v.p[1]);
+            *reinterpret_cast<ulonglong2 *>(p + 16) = make_ulonglong2(v.p[2], v.p[3]);
         }
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            w[k] = round_bf16x2(v[2 * k], v[2 * k + 1]);
-            v[2 * k] = bf16_lo(w[k]);
-            v[2 * k + 1] = bf16_hi(w[k]);
+            w[k] = round_bf16x2(v.p[k]);
+            v.p[k] = f2_pack(bf16_lo(w[k]), bf16_hi(w[k]));
         }
         if (write)
             *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
-// Eight values of a weight (kept in L1: every row reads them).
-__device__ __forceinline__ void weight8(const float *w, int at, float (&v)[8])
+// Vector j of a weight: through L1 (every row reads them), or from where the CTA may keep it.
+__device__ __forceinline__ Vec8 weight8(const float *w, int j)
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(w + at)), b = __ldg(reinterpret_cast<const float4 *>(w + at + 4));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2 *>(w) + 2 * j), b = __ldg(reinterpret_cast<const ulonglong2 *>(w) + 2 * j + 1);
+    return {a.x, a.y, b.x, b.y};
+}
+__device__ __forceinline__ Vec8 kept8(const float *w, int j)
+{
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(w)[2 * j], b = reinterpret_cast<const ulonglong2 *>(w)[2 * j + 1];
+    return {a.x, a.y, b.x, b.y};
 }
 
 // Sums over the CTA (at most 16 warps), the same in every thread; one barrier.  `turn` alternates between two buffers, so
@@ -146,12 +190,12 @@ struct RowSums {
         turn ^= 1;
         return s;
     }
-    // Three sums.  Each exchange with a lane half as far halves the values that a lane carries (12 shuffles for 30).
-    __device__ __forceinline__ void three(float (&s)[3], int &turn, int lane, int warp)
+    // Four sums.  Each exchange with a lane half as far halves the values that a lane carries (13 shuffles for 40).
+    __device__ __forceinline__ void four(float (&s)[4], int &turn, int lane, int warp)
     {
         const bool b4 = lane & 16, b3 = lane & 8;
         const float a0 = (b4 ? s[2] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[0] : s[2], 16);
-        const float a1 = (b4 ? 0.f : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[1] : 0.f, 16);
+        const float a1 = (b4 ? s[3] : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[1] : s[3], 16);
         float v = (b3 ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, b3 ? a0 : a1, 8);  // the sum numbered lane / 8
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1)
@@ -164,7 +208,7 @@ struct RowSums {
         for (int d = 16; d > 2; d >>= 1)
             v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
 #pragma unroll
-        for (int n = 0; n < 3; ++n)
+        for (int n = 0; n < 4; ++n)
             s[n] = __shfl_sync(0xFFFFFFFFu, v, n);
         turn ^= 1;
     }
@@ -260,26 +304,16 @@ struct LoadedRow {
     __device__ __forceinline__ Row8<false> x(int i, int) const { return x_[i]; }
 };
 
-// w_post * gate of vector j, the factors of a channel behind the block: from `back`, where the CTA keeps the products, or
-// from the two.  False without either.
-__device__ __forceinline__ bool back_weight8(const NormParams &p, const float *back, int j, float (&w)[8])
+// Whether channels have a factor behind the block: w_post, a gate or both.
+__device__ __forceinline__ bool has_back(const NormParams &p) { return p.post != nullptr || p.gate_kind == 1; }
+// Its vector j, from `back`, where the CTA keeps the products, or from the two.
+__device__ __forceinline__ Vec8 back_weight8(const NormParams &p, const float *back, int j)
 {
-    if (back != nullptr) {
-        const float4 a = reinterpret_cast<const float4 *>(back)[2 * j], b = reinterpret_cast<const float4 *>(back)[2 * j + 1];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        return true;
-    }
-    const bool channel = p.gate_kind == 1;
-    if (p.post != nullptr)
-        weight8(p.post, 8 * j, w);
-    if (channel) {
-        float v[8];
-        weight8(p.gate, 8 * j, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            w[k] = p.post != nullptr ? w[k] * v[k] : v[k];
-    }
-    return p.post != nullptr || channel;
+    if (back != nullptr)
+        return kept8(back, j);
+    if (p.gate_kind != 1)
+        return weight8(p.post, j);
+    return p.post != nullptr ? weight8(p.post, j) * weight8(p.gate, j) : weight8(p.gate, j);
 }
 
 // y, h -> h', x of one row.
@@ -288,180 +322,133 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
                                          Between &&between)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
-    float a[V][8];
-    float s = 0.f;
+    Vec8 a[V];
+    uint64_t s2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        widen8<YF32>(in.y(i, tid + i * nt), a[i]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            s = fmaf(a[i][k], a[i][k], s);
+        a[i] = widen8<YF32>(in.y(i, tid + i * nt));
+        dot8(s2, a[i], a[i]);
     }
     float factor = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
-    s = sums.one(s, turn, lane, warp);
+    const float s = sums.one(total(s2), turn, lane, warp);
     between();
     if (p.post != nullptr)
         factor *= rsqrtf(s * inv + p.eps);
-    s = 0.f;
+    s2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = tid + i * nt;
         if (j < p.vecs) {
-            float w[8], h[8];
-            widen8<HF32>(in.h(i, j), h);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                a[i][k] *= factor;
-            if (back_weight8(p, back, j, w)) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    a[i][k] *= w[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                a[i][k] = fmaf(p.scale, h[k], a[i][k]);
+            a[i] = a[i] * factor;
+            if (has_back(p))
+                a[i] = a[i] * back_weight8(p, back, j);
+            a[i] = fma8(widen8<HF32>(in.h(i, j)), p.scale, a[i]);
             store8<HF32>(p.h_out, row * p.H + 8 * j, a[i], p.h_out != nullptr);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                s = fmaf(a[i][k], a[i][k], s);
+            dot8(s2, a[i], a[i]);
         }
     }
     if (p.pre != nullptr) {
-        s = sums.one(s, turn, lane, warp);
-        const float r = rsqrtf(s * inv + p.eps);
+        const float r = rsqrtf(sums.one(total(s2), turn, lane, warp) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
             if (j < p.vecs) {
-                float w[8];
-                weight8(p.pre, 8 * j, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    a[i][k] = a[i][k] * r * w[k];
-                store8<false>(p.x, row * p.H + 8 * j, a[i]);
+                Vec8 x = a[i] * r * weight8(p.pre, j);
+                store8<false>(p.x, row * p.H + 8 * j, x);
             }
         }
     }
 }
 
-// Eight values of a weight that may be kept in shared memory.
-__device__ __forceinline__ void kept8(const float *w, int j, float (&v)[8])
+// The gradients of a row in three passes, with the row's sums between them: y^2, h'^2 and dx w_pre h' before the second, which
+// leaves the sum of b n1 (or of g u) for the third.
+template <bool YF32, bool HF32, int V, typename Row>
+__device__ __forceinline__ void backward_sums(const NormParams &p, const float *pre_weight, const Row &in, float (&s)[4])
 {
-    const float4 a = reinterpret_cast<const float4 *>(w)[2 * j], b = reinterpret_cast<const float4 *>(w)[2 * j + 1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-// acc[0 .. 7] += v, in shared memory that this thread alone uses.
-__device__ __forceinline__ void add8(float *acc, const float (&v)[8])
-{
-    float4 *q = reinterpret_cast<float4 *>(acc);
-    float4 a = q[0], b = q[1];
-    a.x += v[0], a.y += v[1], a.z += v[2], a.w += v[3], b.x += v[4], b.y += v[5], b.z += v[6], b.w += v[7];
-    q[0] = a;
-    q[1] = b;
-}
-
-// One row's gradients; add_pre and add_post take vector i's terms of the sums over rows (dx n2; token gate g n1).
-template <bool YF32, bool HF32, int V, typename Row, typename Between, typename AddPre, typename AddPost>
-__device__ __forceinline__ void norm_row_backward(const NormParams &p, int64_t row, float inv, const float *pre_weight, const float *back, RowSums &sums, int &turn, int lane,
-                                                  int warp, const Row &in, Between &&between, AddPre &&add_pre, AddPost &&add_post)
-{
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const bool second = p.post != nullptr || (p.gate_kind == 2 && p.dgate != nullptr);
-    float s[3] = {0.f, 0.f, 0.f};
+    uint64_t sy = 0, sh = 0, sd = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int j = tid + i * nt;
-        float y[8], h[8], d[8], w[8];
-        widen8<YF32>(in.y(i, j), y);
-        widen8<HF32>(in.h(i, j), h);
-        widen8<false>(in.x(i, j), d);
-        const bool pre = p.dx != nullptr && j < p.vecs;
-        if (pre)
-            kept8(pre_weight, j, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            s[0] = fmaf(y[k], y[k], s[0]);
-            s[1] = fmaf(h[k], h[k], s[1]);
-            if (pre)
-                s[2] = fmaf(d[k] * w[k], h[k], s[2]);
-        }
+        const int j = threadIdx.x + i * blockDim.x;
+        const Vec8 y = widen8<YF32>(in.y(i, j)), h = widen8<HF32>(in.h(i, j));
+        dot8(sy, y, y);
+        dot8(sh, h, h);
+        if (p.dx != nullptr && j < p.vecs)
+            dot8(sd, widen8<false>(in.x(i, j)) * kept8(pre_weight, j), h);
     }
-    sums.three(s, turn, lane, warp);
-    between();
-    const float r1 = p.post != nullptr ? rsqrtf(s[0] * inv + p.eps) : 1.0f;
-    const float r2 = rsqrtf(s[1] * inv + p.eps);
-    const float c2 = r2 * s[2] * inv;  // mean(t n2)
-    const float token = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
-    float g[V][8];
-    float m = 0.f;
+    s[0] = total(sy);
+    s[1] = total(sh);
+    s[2] = total(sd);
+}
+
+struct RowFactors {
+    float r1, r2, c2, token;  // c2: mean(t n2)
+};
+__device__ __forceinline__ RowFactors row_factors(const NormParams &p, int64_t row, float inv, const float (&s)[4])
+{
+    RowFactors f;
+    f.r1 = p.post != nullptr ? rsqrtf(s[0] * inv + p.eps) : 1.0f;
+    f.r2 = rsqrtf(s[1] * inv + p.eps);
+    f.c2 = f.r2 * s[2] * inv;
+    f.token = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
+    return f;
+}
+
+// g becomes b without the token's gate; y the row's elements of y; add_pre and add_post take vector i's terms of the sums over
+// rows (dx n2; token gate g n1).
+template <bool YF32, bool HF32, int V, typename Row, typename AddPre, typename AddPost>
+__device__ __forceinline__ float backward_apply(const NormParams &p, int64_t row, const RowFactors &f, const float *pre_weight, const float *back, const Row &in, Vec8 (&g)[V],
+                                                Row8<YF32> (&y)[V], AddPre &&add_pre, AddPost &&add_post)
+{
+    uint64_t sm = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int j = tid + i * nt;
-        widen8<HF32>(in.g(i, j), g[i]);
+        const int j = threadIdx.x + i * blockDim.x;
+        y[i] = in.y(i, j);
         if (j < p.vecs) {
-            float w[8], q[8];
+            g[i] = widen8<HF32>(in.g(i, j));
             if (p.dx != nullptr) {
-                float h[8], d[8];
-                widen8<HF32>(in.h(i, j), h);
-                widen8<false>(in.x(i, j), d);
-                kept8(pre_weight, j, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float n = h[k] * r2;
-                    g[i][k] = fmaf(r2, fmaf(-n, c2, d[k] * w[k]), g[i][k]);
-                    d[k] *= n;
-                }
-                add_pre(i, d);
+                const Vec8 n = widen8<HF32>(in.h(i, j)) * f.r2, d = widen8<false>(in.x(i, j));
+                g[i] = fma8(fma8(n, -f.c2, d * kept8(pre_weight, j)), f.r2, g[i]);
+                add_pre(i, d, n);
             }
             if (p.dh != nullptr) {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[k] = p.scale * g[i][k];
+                Vec8 v = g[i] * p.scale;
                 store8<HF32>(p.dh, row * p.H + 8 * j, v);
             }
-            widen8<YF32>(in.y(i, j), q);
-            {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    q[k] *= r1;  // n1
-                    v[k] = token * g[i][k] * q[k];
-                }
-                add_post(i, v);
-            }
-            if (back_weight8(p, back, j, w)) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    g[i][k] *= w[k];
-            }
-            if (second) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    m = fmaf(g[i][k], q[k], m);
-            }
+            const Vec8 n1 = widen8<YF32>(y[i]) * f.r1;
+            add_post(i, g[i] * f.token, n1);
+            if (has_back(p))
+                g[i] = g[i] * back_weight8(p, back, j);
+            dot8(sm, g[i], n1);
         }
     }
-    if (second)
-        m = sums.one(m, turn, lane, warp);
-    if (p.gate_kind == 2 && p.dgate != nullptr && tid == 0)
+    return total(sm);
+}
+
+// m: the sum of b n1 without the token's gate.
+template <bool YF32, int V>
+__device__ __forceinline__ void backward_store(const NormParams &p, int64_t row, float inv, const RowFactors &f, float m, const Vec8 (&g)[V], const Row8<YF32> (&y)[V])
+{
+    if (p.gate_kind == 2 && p.dgate != nullptr && threadIdx.x == 0)
         p.dgate[row] = m;
-    if (p.dy != nullptr) {
-        const float c1 = p.post != nullptr ? r1 * m * inv : 0.f, factor = token * r1;
+    if (p.dy == nullptr)
+        return;
+    const float c1 = p.post != nullptr ? f.r1 * m * inv : 0.f, factor = f.token * f.r1;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = tid + i * nt;
-            if (j < p.vecs) {
-                float y[8];
-                widen8<YF32>(in.y(i, j), y);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    y[k] = factor * fmaf(-y[k], c1, g[i][k]);
-                store8<YF32>(p.dy, row * p.H + 8 * j, y);
-            }
+    for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * blockDim.x;
+        if (j < p.vecs) {
+            Vec8 v = fma8(widen8<YF32>(y[i]), -c1, g[i]) * factor;
+            store8<YF32>(p.dy, row * p.H + 8 * j, v);
         }
     }
+}
+
+// Vector j of acc += a b, in shared memory that this thread alone uses.
+__device__ __forceinline__ void add8(float *acc, int j, const Vec8 &a, const Vec8 &b)
+{
+    Vec8 v = fma8(a, b, kept8(acc, j));
+    store8<true>(acc, 8 * j, v);
 }
 
 // The products of w_post and gate of this thread's columns into shared memory at `kept`, which then points behind them.
@@ -475,8 +462,7 @@ __device__ __forceinline__ const float *keep_back(const NormParams &p, float *&k
     for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
         if (j < p.vecs) {
-            float w[8];
-            back_weight8(p, nullptr, j, w);
+            Vec8 w = back_weight8(p, nullptr, j);
             store8<true>(back, 8 * j, w);
         }
     }
@@ -484,45 +470,57 @@ __device__ __forceinline__ const float *keep_back(const NormParams &p, float *&k
     return back;
 }
 
-// The ring's part of a kernel: run(row, stage, between) for each of the CTA's rows, where `between` is called by all threads
-// after a barrier that follows their last reads of the stage before.
-template <int N, typename Run>
-__device__ __forceinline__ void ring_rows(const NormParams &p, const RowSource &src, unsigned char *smem, uint64_t *full, Run &&run)
-{
-    const int tid = threadIdx.x;
-    const uint32_t base = smem_u32(smem), full0 = smem_u32(full);
-    if (tid == 0) {
-        for (int s = 0; s < p.stages; ++s)
-            mbar_init(full0 + 8 * s, 1);
-        fence_mbar_init();
-        for (int s = 0; s < p.stages; ++s) {
-            const int64_t row = blockIdx.x + int64_t{s} * gridDim.x;
-            if (row < p.T)
-                fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, row);
+// The ring's state: each of the CTA's rows in turn.
+struct Ring {
+    unsigned char *smem;
+    uint32_t base, full0;
+    int slot, phase;
+    bool ok;
+
+    template <int N>
+    __device__ __forceinline__ void start(const NormParams &p, const RowSource &src, unsigned char *memory, uint64_t *full)
+    {
+        smem = memory;
+        base = smem_u32(memory);
+        full0 = smem_u32(full);
+        slot = phase = 0;
+        ok = true;
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < p.stages; ++s)
+                mbar_init(full0 + 8 * s, 1);
+            fence_mbar_init();
+            for (int s = 0; s < p.stages; ++s) {
+                const int64_t row = blockIdx.x + int64_t{s} * gridDim.x;
+                if (row < p.T)
+                    fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, row);
+            }
         }
+        __syncthreads();
     }
-    __syncthreads();
-    int slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        if (ok && !mbar_wait_cycles(full0 + 8 * slot, phase, kNormWait)) {  // a copy that never lands: its rows are garbage, and told
+    // The next row's stage, once its copies have landed.
+    __device__ __forceinline__ const unsigned char *next(const NormParams &p, const RowSource &src)
+    {
+        if (ok && !mbar_wait_cycles(full0 + 8 * slot, phase, kNormWait)) {  // a copy that never lands: the rows are garbage, and told
             ok = false;
             atomicOr(p.fault, 1u);
         }
-        run(row, smem + slot * src.stage, [&]() {
-            const int64_t next = row + (int64_t{p.stages} - 1) * gridDim.x;  // into the stage of the row before
-            if (tid == 0 && row != blockIdx.x && next < p.T) {
-                const int s = slot == 0 ? p.stages - 1 : slot - 1;
-                fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, next);
-            }
-        });
+        const unsigned char *at = smem + slot * src.stage;
         if (++slot == p.stages) {
             slot = 0;
             phase ^= 1;
         }
+        return at;
     }
-}
+    // Row `row` into a stage whose readers have all passed a barrier since; behind: how many stages before the next one.
+    template <int N>
+    __device__ __forceinline__ void refill(const NormParams &p, const RowSource &src, int behind, int64_t row)
+    {
+        if (threadIdx.x == 0 && row < p.T) {
+            const int s = slot >= behind ? slot - behind : slot - behind + p.stages;
+            fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, row);
+        }
+    }
+};
 
 template <bool YF32, bool HF32, int V>
 __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_kernel(const NormParams p)
@@ -531,7 +529,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_
     __shared__ RowSums sums;
     __shared__ uint64_t full[kNormMaxStages];
     pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float inv = 1.0f / static_cast<float>(p.H);
     int turn = 0;
     sums.clear();
@@ -540,9 +538,16 @@ __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_
     add_source(src, 1, p.h, p.ldh, p.H, HF32 ? 4 : 2);
     float *kept = reinterpret_cast<float *>(norm_smem);
     const float *back = keep_back<V>(p, kept);
-    ring_rows<2>(p, src, reinterpret_cast<unsigned char *>(kept), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
-        norm_row<YF32, HF32, V>(p, row, inv, back, sums, turn, lane, warp, StageRow<YF32, HF32>{stage, src, p.vecs}, between);
-    });
+    Ring ring;
+    ring.start<2>(p, src, reinterpret_cast<unsigned char *>(kept), full);
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        const StageRow<YF32, HF32> in{ring.next(p, src), src, p.vecs};
+        // behind the row's first barrier nobody reads the row before it any more
+        norm_row<YF32, HF32, V>(p, row, inv, back, sums, turn, lane, warp, in, [&]() {
+            if (row != blockIdx.x)
+                ring.refill<2>(p, src, 2, row + (int64_t{p.stages} - 1) * gridDim.x);
+        });
+    }
 }
 
 template <bool YF32, bool HF32, int V>
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_long_kernel(const Nor
 {
     __shared__ RowSums sums;
     pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float inv = 1.0f / static_cast<float>(p.H);
     int turn = 0;
     sums.clear();
@@ -583,35 +588,49 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
     add_source(src, 1, p.dx != nullptr ? p.h : nullptr, p.ldh, p.H, HF32 ? 4 : 2);
     add_source(src, 2, p.dh_out, p.lddh, p.H, HF32 ? 4 : 2);
     add_source(src, 3, p.dx, p.lddx, p.H, 2);
-    float acc[2][V][8];
+    Vec8 acc[2][V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            acc[0][i][k] = acc[1][i][k] = 0.f;
+        acc[0][i] = acc[1][i] = Vec8::splat(0.f);
     float *kept = reinterpret_cast<float *>(norm_smem);
     const float *back = keep_back<V>(p, kept), *pre = p.pre;
     if (p.keep && p.pre != nullptr) {
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
             if (j < p.vecs) {
-                float w[8];
-                weight8(p.pre, 8 * j, w);
+                Vec8 w = weight8(p.pre, j);
                 store8<true>(kept, 8 * j, w);
             }
         }
         pre = kept;
         kept += p.H;
     }
-    ring_rows<4>(p, src, reinterpret_cast<unsigned char *>(kept), full, [&](int64_t row, const unsigned char *stage, auto &&between) {
-        auto add = [&](int n, int i, const float (&v)[8]) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                acc[n][i][k] += v[k];
-        };
-        norm_row_backward<YF32, HF32, V>(p, row, inv, pre, back, sums, turn, lane, warp, StageRow<YF32, HF32>{stage, src, p.vecs}, between, [&](int i, const float (&v)[8]) { add(0, i, v); },
-                                         [&](int i, const float (&v)[8]) { add(1, i, v); });
-    });
+    Ring ring;
+    ring.start<4>(p, src, reinterpret_cast<unsigned char *>(kept), full);
+    // A row's second pass and the next row's first share one exchange of sums.
+    const unsigned char *stage = ring.next(p, src);
+    float s[4];
+    backward_sums<YF32, HF32, V>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
+    s[3] = 0.f;
+    sums.four(s, turn, lane, warp);
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        const RowFactors f = row_factors(p, row, inv, s);
+        Vec8 g[V];
+        Row8<YF32> y[V];
+        const float m = backward_apply<YF32, HF32, V>(
+            p, row, f, pre, back, StageRow<YF32, HF32>{stage, src, p.vecs}, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { acc[0][i] = fma8(d, n, acc[0][i]); },
+            [&](int i, const Vec8 &v, const Vec8 &n) { acc[1][i] = fma8(v, n, acc[1][i]); });
+        const bool more = row + gridDim.x < p.T;
+        if (more) {
+            stage = ring.next(p, src);
+            backward_sums<YF32, HF32, V>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
+        }
+        s[3] = m;
+        sums.four(s, turn, lane, warp);
+        if (more)
+            ring.refill<4>(p, src, 2, row + int64_t{p.stages} * gridDim.x);
+        backward_store<YF32, V>(p, row, inv, f, s[3], g, y);
+    }
     if (p.partial != nullptr) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -619,9 +638,7 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
             for (int i = 0; i < V; ++i) {
                 const int j = tid + i * nt;
                 if (j < p.vecs) {
-                    float4 *to = reinterpret_cast<float4 *>(partial_of<V>(p, n, j));
-                    to[0] = make_float4(acc[n][i][0], acc[n][i][1], acc[n][i][2], acc[n][i][3]);
-                    to[1] = make_float4(acc[n][i][4], acc[n][i][5], acc[n][i][6], acc[n][i][7]);
+                    store8<true>(partial_of<V>(p, n, j), 0, acc[n][i]);
                 }
             }
     }
@@ -649,9 +666,19 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_long_kernel(
     };
     each([](int, int, float4 *a) { a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f); });
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        norm_row_backward<YF32, HF32, V>(p, row, inv, p.pre, nullptr, sums, turn, lane, warp, LoadedRow<YF32, HF32, V, true>(p, row), [] {},
-                                         [&](int i, const float (&v)[8]) { add8(acc + 8 * (tid + i * nt), v); },
-                                         [&](int i, const float (&v)[8]) { add8(acc + p.H + 8 * (tid + i * nt), v); });
+        const LoadedRow<YF32, HF32, V, true> in(p, row);
+        float s[4];
+        backward_sums<YF32, HF32, V>(p, p.pre, in, s);
+        s[3] = 0.f;
+        sums.four(s, turn, lane, warp);
+        const RowFactors f = row_factors(p, row, inv, s);
+        Vec8 g[V];
+        Row8<YF32> y[V];
+        float m = backward_apply<YF32, HF32, V>(
+            p, row, f, p.pre, nullptr, in, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { add8(acc, tid + i * nt, d, n); },
+            [&](int i, const Vec8 &v, const Vec8 &n) { add8(acc + p.H, tid + i * nt, v, n); });
+        m = sums.one(m, turn, lane, warp);
+        backward_store<YF32, V>(p, row, inv, f, m, g, y);
     }
     if (p.partial != nullptr)
         each([&](int n, int j, float4 *a) {
