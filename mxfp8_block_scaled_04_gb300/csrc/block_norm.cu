@@ -4,6 +4,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <type_traits>
 
 #include "../../include/block_norm.h"
 #include "block_norm.cuh"
@@ -16,7 +17,6 @@ using namespace mxfp8;
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 constexpr int kMostSmem = 224 * 1024;
 constexpr int kRingBytes = 128 * 1024;
-constexpr int kKeepBytes = kMostSmem;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -90,21 +90,25 @@ mxfp8_status_t launch_types(NormParams p, int row_bytes, int device, cudaStream_
         else
             return launch_rows<block_norm_long_kernel<YF32, HF32, 4>>(p, threads, 0, most, device, stream, grid);
     }
-    // An SM's CTAs share kRingBytes for their rings (the rest is left to L1), with two stages at least, and keep the weights (the
-    // forward pass the factors behind the block alone) where there is room.
+    // An SM's CTAs share kRingBytes for their rings (the rest is left to L1), with two stages at least.  With two vectors per
+    // thread the weights are kept in shared memory where there is room (forward the factors behind the block alone), and a
+    // backward ring, whose CTA has the SM to itself, takes all that is left.
     const int fits = 1024 / threads < 1 ? 1 : 1024 / threads < 8 ? 1024 / threads : 8;
     const int per_sm = BACKWARD && v == 2 ? 1 : fits;
-    const int room = kRingBytes / per_sm;
-    p.stages = room / row_bytes < 2 ? 2 : room / row_bytes < kNormMaxStages ? room / row_bytes : kNormMaxStages;
     const int back = p.post != nullptr || p.gate_kind == BLOCK_GATE_CHANNEL ? p.H * 4 : 0, pre = BACKWARD && p.pre != nullptr ? p.H * 4 : 0;
-    p.keep = p.stages * row_bytes + back + pre <= kKeepBytes / per_sm;
-    const int smem = p.stages * row_bytes + (p.keep ? back + pre : 0);
-    if constexpr (BACKWARD)
-        return v == 1 ? launch_rows<block_norm_backward_ring_kernel<YF32, HF32, 1>>(p, threads, smem, most, device, stream, grid)
-                      : launch_rows<block_norm_backward_ring_kernel<YF32, HF32, 2>>(p, threads, smem, most, device, stream, grid);
-    else
-        return v == 1 ? launch_rows<block_norm_ring_kernel<YF32, HF32, 1>>(p, threads, smem, most, device, stream, grid)
-                      : launch_rows<block_norm_ring_kernel<YF32, HF32, 2>>(p, threads, smem, most, device, stream, grid);
+    const bool keep = v == 2 && back + pre > 0 && 2 * row_bytes + back + pre <= kMostSmem / per_sm;
+    const int room = BACKWARD && keep ? kMostSmem - back - pre : kRingBytes / per_sm;
+    p.stages = room / row_bytes < 2 ? 2 : room / row_bytes < kNormMaxStages ? room / row_bytes : kNormMaxStages;
+    const int smem = p.stages * row_bytes + (keep ? back + pre : 0);
+    auto run = [&](auto vectors, auto kept) {
+        if constexpr (BACKWARD)
+            return launch_rows<block_norm_backward_ring_kernel<YF32, HF32, vectors, kept>>(p, threads, smem, most, device, stream, grid);
+        else
+            return launch_rows<block_norm_ring_kernel<YF32, HF32, vectors, kept>>(p, threads, smem, most, device, stream, grid);
+    };
+    if (v == 1)
+        return run(std::integral_constant<int, 1>{}, std::false_type{});
+    return keep ? run(std::integral_constant<int, 2>{}, std::true_type{}) : run(std::integral_constant<int, 2>{}, std::false_type{});
 }
 
 template <bool BACKWARD>

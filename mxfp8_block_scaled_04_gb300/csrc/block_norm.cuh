@@ -37,7 +37,6 @@ struct NormParams {
     void *dh, *dy;
     float *dpre, *dpost, *dgate, *partial;
     int stages;                        // of the ring
-    bool keep;                         // the weights are kept in shared memory, before the ring
     unsigned *fault;
 };
 
@@ -152,7 +151,7 @@ __device__ __forceinline__ void store8(void *base, int64_t at, Vec8 &v, bool wri
             *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
-// Vector j of a weight: through L1 (every row reads them), or from where the CTA may keep it.
+// Vector j of a weight: through L1 (every row reads them), or from shared memory where the CTA keeps it.
 __device__ __forceinline__ Vec8 weight8(const float *w, int j)
 {
     const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2 *>(w) + 2 * j), b = __ldg(reinterpret_cast<const ulonglong2 *>(w) + 2 * j + 1);
@@ -304,12 +303,16 @@ struct LoadedRow {
     __device__ __forceinline__ Row8<false> x(int i, int) const { return x_[i]; }
 };
 
+template <bool KEPT>
+__device__ __forceinline__ Vec8 weight8_of(const float *w, int j) { return KEPT ? kept8(w, j) : weight8(w, j); }
+
 // Whether channels have a factor behind the block: w_post, a gate or both.
 __device__ __forceinline__ bool has_back(const NormParams &p) { return p.post != nullptr || p.gate_kind == 1; }
-// Its vector j, from `back`, where the CTA keeps the products, or from the two.
+// Its vector j, from `back`, where the CTA keeps the products, or (KEPT false) from the two.
+template <bool KEPT>
 __device__ __forceinline__ Vec8 back_weight8(const NormParams &p, const float *back, int j)
 {
-    if (back != nullptr)
+    if constexpr (KEPT)
         return kept8(back, j);
     if (p.gate_kind != 1)
         return weight8(p.post, j);
@@ -317,7 +320,7 @@ __device__ __forceinline__ Vec8 back_weight8(const NormParams &p, const float *b
 }
 
 // y, h -> h', x of one row.
-template <bool YF32, bool HF32, int V, typename Row, typename Between>
+template <bool YF32, bool HF32, int V, bool KEPT, typename Row, typename Between>
 __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float inv, const float *back, RowSums &sums, int &turn, int lane, int warp, const Row &in,
                                          Between &&between)
 {
@@ -341,7 +344,7 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
         if (j < p.vecs) {
             a[i] = a[i] * factor;
             if (has_back(p))
-                a[i] = a[i] * back_weight8(p, back, j);
+                a[i] = a[i] * back_weight8<KEPT>(p, back, j);
             a[i] = fma8(widen8<HF32>(in.h(i, j)), p.scale, a[i]);
             store8<HF32>(p.h_out, row * p.H + 8 * j, a[i], p.h_out != nullptr);
             dot8(s2, a[i], a[i]);
@@ -362,7 +365,7 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
 
 // The gradients of a row in three passes, with the row's sums between them: y^2, h'^2 and dx w_pre h' before the second, which
 // leaves the sum of b n1 (or of g u) for the third.
-template <bool YF32, bool HF32, int V, typename Row>
+template <bool YF32, bool HF32, int V, bool KEPT, typename Row>
 __device__ __forceinline__ void backward_sums(const NormParams &p, const float *pre_weight, const Row &in, float (&s)[4])
 {
     uint64_t sy = 0, sh = 0, sd = 0;
@@ -373,7 +376,7 @@ __device__ __forceinline__ void backward_sums(const NormParams &p, const float *
         dot8(sy, y, y);
         dot8(sh, h, h);
         if (p.dx != nullptr && j < p.vecs)
-            dot8(sd, widen8<false>(in.x(i, j)) * kept8(pre_weight, j), h);
+            dot8(sd, widen8<false>(in.x(i, j)) * weight8_of<KEPT>(pre_weight, j), h);
     }
     s[0] = total(sy);
     s[1] = total(sh);
@@ -395,7 +398,7 @@ __device__ __forceinline__ RowFactors row_factors(const NormParams &p, int64_t r
 
 // g becomes b without the token's gate; y the row's elements of y; add_pre and add_post take vector i's terms of the sums over
 // rows (dx n2; token gate g n1).
-template <bool YF32, bool HF32, int V, typename Row, typename AddPre, typename AddPost>
+template <bool YF32, bool HF32, int V, bool KEPT, typename Row, typename AddPre, typename AddPost>
 __device__ __forceinline__ float backward_apply(const NormParams &p, int64_t row, const RowFactors &f, const float *pre_weight, const float *back, const Row &in, Vec8 (&g)[V],
                                                 Row8<YF32> (&y)[V], AddPre &&add_pre, AddPost &&add_post)
 {
@@ -408,7 +411,7 @@ __device__ __forceinline__ float backward_apply(const NormParams &p, int64_t row
             g[i] = widen8<HF32>(in.g(i, j));
             if (p.dx != nullptr) {
                 const Vec8 n = widen8<HF32>(in.h(i, j)) * f.r2, d = widen8<false>(in.x(i, j));
-                g[i] = fma8(fma8(n, -f.c2, d * kept8(pre_weight, j)), f.r2, g[i]);
+                g[i] = fma8(fma8(n, -f.c2, d * weight8_of<KEPT>(pre_weight, j)), f.r2, g[i]);
                 add_pre(i, d, n);
             }
             if (p.dh != nullptr) {
@@ -418,7 +421,7 @@ __device__ __forceinline__ float backward_apply(const NormParams &p, int64_t row
             const Vec8 n1 = widen8<YF32>(y[i]) * f.r1;
             add_post(i, g[i] * f.token, n1);
             if (has_back(p))
-                g[i] = g[i] * back_weight8(p, back, j);
+                g[i] = g[i] * back_weight8<KEPT>(p, back, j);
             dot8(sm, g[i], n1);
         }
     }
@@ -453,16 +456,16 @@ __device__ __forceinline__ void add8(float *acc, int j, const Vec8 &a, const Vec
 
 // The products of w_post and gate of this thread's columns into shared memory at `kept`, which then points behind them.
 // (Only the thread that writes them reads them.)
-template <int V>
+template <int V, bool KEEP>
 __device__ __forceinline__ const float *keep_back(const NormParams &p, float *&kept)
 {
-    if (!p.keep || (p.post == nullptr && p.gate_kind != 1))
+    if (!KEEP || !has_back(p))
         return nullptr;
     float *const back = kept;
     for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
         if (j < p.vecs) {
-            Vec8 w = back_weight8(p, nullptr, j);
+            Vec8 w = back_weight8<false>(p, nullptr, j);
             store8<true>(back, 8 * j, w);
         }
     }
@@ -522,7 +525,7 @@ struct Ring {
     }
 };
 
-template <bool YF32, bool HF32, int V>
+template <bool YF32, bool HF32, int V, bool KEEP>
 __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];
@@ -537,13 +540,13 @@ __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_
     add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
     add_source(src, 1, p.h, p.ldh, p.H, HF32 ? 4 : 2);
     float *kept = reinterpret_cast<float *>(norm_smem);
-    const float *back = keep_back<V>(p, kept);
+    const float *back = keep_back<V, KEEP>(p, kept);
     Ring ring;
     ring.start<2>(p, src, reinterpret_cast<unsigned char *>(kept), full);
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
         const StageRow<YF32, HF32> in{ring.next(p, src), src, p.vecs};
         // behind the row's first barrier nobody reads the row before it any more
-        norm_row<YF32, HF32, V>(p, row, inv, back, sums, turn, lane, warp, in, [&]() {
+        norm_row<YF32, HF32, V, KEEP>(p, row, inv, back, sums, turn, lane, warp, in, [&]() {
             if (row != blockIdx.x)
                 ring.refill<2>(p, src, 2, row + (int64_t{p.stages} - 1) * gridDim.x);
         });
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_long_kernel(const Nor
     sums.clear();
     __syncthreads();
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        norm_row<YF32, HF32, V>(p, row, inv, nullptr, sums, turn, lane, warp, LoadedRow<YF32, HF32, V, false>(p, row), [] {});
+        norm_row<YF32, HF32, V, false>(p, row, inv, nullptr, sums, turn, lane, warp, LoadedRow<YF32, HF32, V, false>(p, row), [] {});
     }
 }
 
@@ -572,7 +575,7 @@ __device__ __forceinline__ float *partial_of(const NormParams &p, int n, int j)
     return p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + n) * p.H + 8 * j;
 }
 
-template <bool YF32, bool HF32, int V>
+template <bool YF32, bool HF32, int V, bool KEEP>
 __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];
@@ -593,8 +596,8 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
     for (int i = 0; i < V; ++i)
         acc[0][i] = acc[1][i] = Vec8::splat(0.f);
     float *kept = reinterpret_cast<float *>(norm_smem);
-    const float *back = keep_back<V>(p, kept), *pre = p.pre;
-    if (p.keep && p.pre != nullptr) {
+    const float *back = keep_back<V, KEEP>(p, kept), *pre = KEEP ? kept : p.pre;
+    if (KEEP && p.pre != nullptr) {
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
             if (j < p.vecs) {
@@ -602,7 +605,6 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
                 store8<true>(kept, 8 * j, w);
             }
         }
-        pre = kept;
         kept += p.H;
     }
     Ring ring;
@@ -610,20 +612,20 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
     // A row's second pass and the next row's first share one exchange of sums.
     const unsigned char *stage = ring.next(p, src);
     float s[4];
-    backward_sums<YF32, HF32, V>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
+    backward_sums<YF32, HF32, V, KEEP>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
     s[3] = 0.f;
     sums.four(s, turn, lane, warp);
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
         const RowFactors f = row_factors(p, row, inv, s);
         Vec8 g[V];
         Row8<YF32> y[V];
-        const float m = backward_apply<YF32, HF32, V>(
+        const float m = backward_apply<YF32, HF32, V, KEEP>(
             p, row, f, pre, back, StageRow<YF32, HF32>{stage, src, p.vecs}, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { acc[0][i] = fma8(d, n, acc[0][i]); },
             [&](int i, const Vec8 &v, const Vec8 &n) { acc[1][i] = fma8(v, n, acc[1][i]); });
         const bool more = row + gridDim.x < p.T;
         if (more) {
             stage = ring.next(p, src);
-            backward_sums<YF32, HF32, V>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
+            backward_sums<YF32, HF32, V, KEEP>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
         }
         s[3] = m;
         sums.four(s, turn, lane, warp);
@@ -668,13 +670,13 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_long_kernel(
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
         const LoadedRow<YF32, HF32, V, true> in(p, row);
         float s[4];
-        backward_sums<YF32, HF32, V>(p, p.pre, in, s);
+        backward_sums<YF32, HF32, V, false>(p, p.pre, in, s);
         s[3] = 0.f;
         sums.four(s, turn, lane, warp);
         const RowFactors f = row_factors(p, row, inv, s);
         Vec8 g[V];
         Row8<YF32> y[V];
-        float m = backward_apply<YF32, HF32, V>(
+        float m = backward_apply<YF32, HF32, V, false>(
             p, row, f, p.pre, nullptr, in, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { add8(acc, tid + i * nt, d, n); },
             [&](int i, const Vec8 &v, const Vec8 &n) { add8(acc + p.H, tid + i * nt, v, n); });
         m = sums.one(m, turn, lane, warp);
