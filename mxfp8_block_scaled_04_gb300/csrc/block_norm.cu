@@ -64,59 +64,62 @@ mxfp8_status_t resident(int device, int threads, int smem, int64_t *ctas)
     return MXFP8_OK;
 }
 
-template <auto *KERN>
-mxfp8_status_t launch_rows(const NormParams &p, int threads, int smem, int64_t most, int device, cudaStream_t stream, int *grid)
+template <auto *KERN, int CTAS>
+mxfp8_status_t launch_rows(const NormParams &p, int threads, int smem, int64_t most, int device, cudaStream_t stream, int *rows)
 {
-    int64_t ctas = 0;
-    const mxfp8_status_t st = resident<KERN>(device, threads, smem, &ctas);
+    int64_t n = 0;
+    const mxfp8_status_t st = resident<KERN>(device, threads, smem, &n);
     if (st != MXFP8_OK)
         return st;
-    ctas = ctas < most ? ctas : most;
-    ctas = ctas < p.T ? ctas : p.T;
-    *grid = static_cast<int>(ctas);
-    return launch_serialized(KERN, dim3(static_cast<unsigned>(ctas)), static_cast<unsigned>(threads), static_cast<size_t>(smem), 1, stream, p);
+    n = n / CTAS < most ? n / CTAS : most;
+    n = n < 1 ? 1 : n < p.T ? n : p.T;
+    *rows = static_cast<int>(n);
+    return launch_serialized(KERN, dim3(static_cast<unsigned>(n * CTAS)), static_cast<unsigned>(threads), static_cast<size_t>(smem), CTAS, stream, p);
 }
 
-// row_bytes: of all inputs of a row.
+// element_bytes: of all inputs of a row, per column.
 template <bool YF32, bool HF32, bool BACKWARD>
-mxfp8_status_t launch_types(NormParams p, int row_bytes, int device, cudaStream_t stream, int *grid)
+mxfp8_status_t launch_types(NormParams p, int element_bytes, int device, cudaStream_t stream, int *rows)
 {
-    const int v = p.vecs <= kNormThreads ? 1 : p.vecs <= 2 * kNormThreads ? 2 : 4;
-    const int threads = static_cast<int>(ceil_div(ceil_div(p.vecs, v), 32) * 32);
-    const int64_t most = BACKWARD ? norm_ctas(p.H) : int64_t{1} << 20;
-    if (v == 4) {
-        if constexpr (BACKWARD)
-            return launch_rows<block_norm_backward_long_kernel<YF32, HF32, 4>>(p, threads, 2 * p.H * 4, most, device, stream, grid);
-        else
-            return launch_rows<block_norm_long_kernel<YF32, HF32, 4>>(p, threads, 0, most, device, stream, grid);
-    }
+    const bool shared = p.H > kNormShare;  // two CTAs to a row
+    const int vecs = shared ? (p.vecs + 1) / 2 : p.vecs;
+    const int v = vecs <= kNormThreads ? 1 : 2;
+    const int threads = static_cast<int>(ceil_div(ceil_div(vecs, v), 32) * 32);
+    const int64_t most = BACKWARD ? norm_rows(p.H) : int64_t{1} << 20;
     // An SM's CTAs share kRingBytes for their rings (the rest is left to L1), with two stages at least.  With two vectors per
     // thread the weights are kept in shared memory where there is room (forward the factors behind the block alone), and a
     // backward ring, whose CTA has the SM to itself, takes all that is left.
     const int fits = 1024 / threads < 1 ? 1 : 1024 / threads < 8 ? 1024 / threads : 8;
     const int per_sm = BACKWARD && v == 2 ? 1 : fits;
-    const int back = p.post != nullptr || p.gate_kind == BLOCK_GATE_CHANNEL ? p.H * 4 : 0, pre = BACKWARD && p.pre != nullptr ? p.H * 4 : 0;
+    const int row_bytes = 8 * vecs * element_bytes;
+    const int back = p.post != nullptr || p.gate_kind == BLOCK_GATE_CHANNEL ? vecs * 32 : 0, pre = BACKWARD && p.pre != nullptr ? vecs * 32 : 0;
     const bool keep = v == 2 && back + pre > 0 && 2 * row_bytes + back + pre <= kMostSmem / per_sm;
     const int room = BACKWARD && keep ? kMostSmem - back - pre : kRingBytes / per_sm;
     p.stages = room / row_bytes < 2 ? 2 : room / row_bytes < kNormMaxStages ? room / row_bytes : kNormMaxStages;
     const int smem = p.stages * row_bytes + (keep ? back + pre : 0);
-    auto run = [&](auto vectors, auto kept) {
+    auto run = [&](auto vectors, auto kept, auto ctas) {
         if constexpr (BACKWARD)
-            return launch_rows<block_norm_backward_ring_kernel<YF32, HF32, vectors, kept>>(p, threads, smem, most, device, stream, grid);
+            return launch_rows<block_norm_backward_kernel<YF32, HF32, vectors, kept, ctas>, ctas>(p, threads, smem, most, device, stream, rows);
         else
-            return launch_rows<block_norm_ring_kernel<YF32, HF32, vectors, kept>>(p, threads, smem, most, device, stream, grid);
+            return launch_rows<block_norm_kernel<YF32, HF32, vectors, kept, ctas>, ctas>(p, threads, smem, most, device, stream, rows);
     };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (shared && v == 2)
+        return keep ? run(Two{}, std::true_type{}, Two{}) : run(Two{}, std::false_type{}, Two{});
+    if (shared)
+        return run(One{}, std::false_type{}, Two{});
     if (v == 1)
-        return run(std::integral_constant<int, 1>{}, std::false_type{});
-    return keep ? run(std::integral_constant<int, 2>{}, std::true_type{}) : run(std::integral_constant<int, 2>{}, std::false_type{});
+        return run(One{}, std::false_type{}, One{});
+    return keep ? run(Two{}, std::true_type{}, One{}) : run(Two{}, std::false_type{}, One{});
 }
 
 template <bool BACKWARD>
-mxfp8_status_t launch(const NormParams &p, const block_norm_config_t *cfg, int row_bytes, int device, cudaStream_t stream, int *grid)
+mxfp8_status_t launch(const NormParams &p, const block_norm_config_t *cfg, int element_bytes, int device, cudaStream_t stream, int *rows)
 {
     const bool y32 = cfg->y_type == MXFP4_F32, h32 = cfg->h_type == MXFP4_F32;
-    return y32 ? (h32 ? launch_types<true, true, BACKWARD>(p, row_bytes, device, stream, grid) : launch_types<true, false, BACKWARD>(p, row_bytes, device, stream, grid))
-               : (h32 ? launch_types<false, true, BACKWARD>(p, row_bytes, device, stream, grid) : launch_types<false, false, BACKWARD>(p, row_bytes, device, stream, grid));
+    return y32 ? (h32 ? launch_types<true, true, BACKWARD>(p, element_bytes, device, stream, rows) : launch_types<true, false, BACKWARD>(p, element_bytes, device, stream, rows))
+               : (h32 ? launch_types<false, true, BACKWARD>(p, element_bytes, device, stream, rows) : launch_types<false, false, BACKWARD>(p, element_bytes, device, stream, rows));
 }
 
 NormParams params(const block_norm_config_t *cfg, int64_t T, int64_t H)
@@ -172,15 +175,15 @@ mxfp8_status_t block_norm(const block_norm_config_t *cfg, int64_t T, int64_t H, 
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     const int hs = cfg->h_type == MXFP4_F32 ? 4 : 2, ys = cfg->y_type == MXFP4_F32 ? 4 : 2;
-    int grid = 0;
-    return launch<false>(p, cfg, p.H * (hs + (y != nullptr ? ys : 0)), device, static_cast<cudaStream_t>(stream), &grid);
+    int rows = 0;
+    return launch<false>(p, cfg, hs + (y != nullptr ? ys : 0), device, static_cast<cudaStream_t>(stream), &rows);
 }
 
 size_t block_norm_backward_workspace_bytes(int64_t T, int64_t H)
 {
     if (T <= 0 || T >= kMaxDim || H <= 0 || H > BLOCK_NORM_MAX_H)
         return 0;
-    return static_cast<size_t>(T < norm_ctas(H) ? T : norm_ctas(H)) * 2 * static_cast<size_t>(H) * sizeof(float);
+    return static_cast<size_t>(T < norm_rows(H) ? T : norm_rows(H)) * 2 * static_cast<size_t>(H) * sizeof(float);
 }
 
 mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, int64_t H, const void *dh_out, int64_t lddh, const void *dx, int64_t lddx,
@@ -244,11 +247,11 @@ mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, in
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     const int hs = cfg->h_type == MXFP4_F32 ? 4 : 2, ys = cfg->y_type == MXFP4_F32 ? 4 : 2;
-    const int row_bytes = p.H * ((y != nullptr ? ys : 0) + (dx != nullptr ? hs + 2 : 0) + (dh_out != nullptr ? hs : 0));
-    int grid = 0;
-    if ((st = launch<true>(p, cfg, row_bytes, device, stream, &grid)) != MXFP8_OK || !sums)
+    const int element_bytes = (y != nullptr ? ys : 0) + (dx != nullptr ? hs + 2 : 0) + (dh_out != nullptr ? hs : 0);
+    int rows = 0;
+    if ((st = launch<true>(p, cfg, element_bytes, device, stream, &rows)) != MXFP8_OK || !sums)
         return st;
-    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(2 * H, 32))), kNormReduceThreads, 0, 1, stream, p, grid);
+    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(2 * H, 32))), kNormReduceThreads, 0, 1, stream, p, rows);
 }
 
 }  // extern "C"

@@ -2,12 +2,11 @@
 //
 // A CTA takes a row at a time and a thread V vectors of 8 columns of it, so that every input is read once and each
 // output written once, with the row's sums (of y^2, then of h'^2; backward: y^2, h'^2 and dx w h' together, then b n1) formed
-// between.  Rows up to 8192 columns come through a ring of shared-memory stages, filled by bulk copies while the rows before
-// them are worked on; longer ones are loaded by the threads.  Bound by HBM for many rows, by the chain of loads, two
+// between.  Rows come through a ring of shared-memory stages, filled by bulk copies while the rows before them are worked on.
+// Rows of more than 8192 columns are shared by the two CTAs of a cluster, half each, which exchange their sums.  Bound by HBM for many rows, by the chain of loads, two
 // reductions and stores (launch included) for few.
 //
-// The weights' gradients are sums over the rows: each thread adds up its columns' (in registers; in shared memory for long
-// rows), a CTA writes its sums to the workspace at its end, and a second kernel adds the CTAs' in order.  With a
+// The weights' gradients are sums over the rows: each thread adds up its columns' in registers, a CTA writes its sums to the workspace at its end, and a second kernel adds the CTAs' in order.  With a
 // gate per channel sum(g n1) serves both: dpost = gate times it, dgate = w_post times it.
 #pragma once
 
@@ -21,15 +20,16 @@ namespace mxfp8 {
 constexpr int kNormSms = 152;
 constexpr int kNormThreads = 512;
 constexpr int kNormMaxStages = 4;
+constexpr int kNormShare = 8192;           // most columns of a CTA
 constexpr int64_t kNormWait = 4000000000;  // cycles: about 2 s
-// CTAs whose partial sums the workspace holds, for rows of H columns.
-inline int norm_ctas(int64_t H) { return kNormSms * (H > 4096 ? 1 : H > 2048 ? 2 : H > 1024 ? 4 : 8); }
+// Most rows in work at once, whose CTAs' sums the workspace holds, for rows of H columns.
+inline int norm_rows(int64_t H) { return H > kNormShare ? kNormSms / 2 : kNormSms * (H > 4096 ? 1 : H > 2048 ? 2 : H > 1024 ? 4 : 8); }
 
 struct NormParams {
     const void *y, *h;                 // backward: h is the stream behind the block
     const void *dh_out, *dx;
     int64_t T, ldy, ldh, lddh, lddx;
-    int H, vecs;
+    int H, vecs;                       // vecs: of the row
     int gate_kind;
     float scale, eps;
     const float *pre, *post, *gate;
@@ -50,23 +50,6 @@ struct Row8<false> {
     uint4 lo;
 };
 
-__device__ __forceinline__ uint4 load_stream(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
-template <bool F32>
-__device__ __forceinline__ Row8<F32> load_row8(const void *base, int64_t at)
-{
-    Row8<F32> r;
-    const unsigned char *p = static_cast<const unsigned char *>(base) + at * (F32 ? 4 : 2);
-    r.lo = load_stream(p);
-    if constexpr (F32)
-        r.hi = load_stream(p + 16);
-    return r;
-}
 // Eight fp32 values as four pairs, for the packed operations (half the instructions; each lane rounds as a scalar).
 struct Vec8 {
     uint64_t p[4];
@@ -163,35 +146,35 @@ __device__ __forceinline__ Vec8 kept8(const float *w, int j)
     return {a.x, a.y, b.x, b.y};
 }
 
-// Sums over the CTA (at most 16 warps), the same in every thread; one barrier.  `turn` alternates between two buffers, so
-// that a buffer is written again only after a barrier that follows its last reads; the warps that a CTA does not have count
+// Sums over a row's CTAs (of at most 16 warps each), the same in every thread; one barrier.  `count` of the sums so far: they
+// alternate between two buffers, so that a buffer is written again only after a barrier that follows its last reads; the warps that a CTA does not have count
 // zeros, which clear() leaves there (before a barrier).
 struct RowSums {
     float buffer[2][16][4];
+    float4 inbox[2];      // the peer's sums
+    uint64_t arrived[2];
 
+    template <int CTAS>
     __device__ __forceinline__ void clear()
     {
         for (int i = threadIdx.x; i < 2 * 16 * 4; i += blockDim.x)
             (&buffer[0][0][0])[i] = 0.f;
+        if constexpr (CTAS == 2) {
+            if (threadIdx.x == 0) {
+                mbar_init(smem_u32(&arrived[0]), 1);
+                mbar_init(smem_u32(&arrived[1]), 1);
+                fence_mbar_init();
+            }
+            cluster_sync();
+        }
     }
-    __device__ __forceinline__ float one(float s, int &turn, int lane, int warp)
+    // Four sums.  Each exchange with a lane half as far halves the values that a lane carries (13 shuffles for 40).  With two
+    // CTAs to a row each sends its sums to the other's inbox, a store that the other's barrier counts; an inbox is written again
+    // only after the message between has been received, and so after its reads.
+    template <int CTAS>
+    __device__ __forceinline__ void four(float (&s)[4], int &count, bool &lost, int lane, int warp, unsigned *fault)
     {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        if (lane == 0)
-            buffer[turn][warp][0] = s;
-        __syncthreads();
-        s = buffer[turn][lane & 15][0];
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1)
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        turn ^= 1;
-        return s;
-    }
-    // Four sums.  Each exchange with a lane half as far halves the values that a lane carries (13 shuffles for 40).
-    __device__ __forceinline__ void four(float (&s)[4], int &turn, int lane, int warp)
-    {
+        const int turn = count & 1;
         const bool b4 = lane & 16, b3 = lane & 8;
         const float a0 = (b4 ? s[2] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[0] : s[2], 16);
         const float a1 = (b4 ? s[3] : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, b4 ? s[1] : s[3], 16);
@@ -209,23 +192,73 @@ struct RowSums {
 #pragma unroll
         for (int n = 0; n < 4; ++n)
             s[n] = __shfl_sync(0xFFFFFFFFu, v, n);
-        turn ^= 1;
+        if constexpr (CTAS == 2) {
+            const uint32_t bar = smem_u32(&arrived[turn]), peer = cluster_rank() ^ 1;
+            if (threadIdx.x == 0) {
+                mbar_arrive_expect_tx(bar, 16);
+                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                                 map_to_rank(smem_u32(&inbox[turn]), peer)),
+                             "f"(s[0]), "f"(s[1]), "f"(s[2]), "f"(s[3]), "r"(map_to_rank(bar, peer))
+                             : "memory");
+            }
+            if (!lost && !mbar_wait_cluster(bar, (count >> 1) & 1, kNormWait)) {  // sums that never come: waited for once, and told
+                lost = true;
+                atomicOr(fault, 1u);
+            }
+            const float4 other = inbox[turn];
+            s[0] += other.x, s[1] += other.y, s[2] += other.z, s[3] += other.w;
+        }
+        ++count;
+    }
+    template <int CTAS>
+    __device__ __forceinline__ float one(float s, int &count, bool &lost, int lane, int warp, unsigned *fault)
+    {
+        if constexpr (CTAS == 2) {
+            float t[4] = {s, 0.f, 0.f, 0.f};
+            four<2>(t, count, lost, lane, warp, fault);
+            return t[0];
+        }
+        const int turn = count & 1;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane == 0)
+            buffer[turn][warp][0] = s;
+        __syncthreads();
+        s = buffer[turn][lane & 15][0];
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        ++count;
+        return s;
     }
 };
 
 // The ring: stage n % stages holds the CTA's n-th row of each input, one after the other.
 struct RowSource {
-    const void *base[4];
+    const void *base[4];  // at the CTA's first column
     int64_t pitch[4];  // bytes
     int bytes[4];      // of a row; 0: not read
     int at[4];         // offset in a stage
     int stage;         // bytes
 };
-__device__ __forceinline__ void add_source(RowSource &s, int n, const void *base, int64_t ld, int H, int size)
+// The CTA's columns, in vectors.
+struct Share {
+    int first, vecs;
+};
+template <int CTAS>
+__device__ __forceinline__ Share my_share(const NormParams &p)
 {
-    s.base[n] = base;
+    if constexpr (CTAS == 1)
+        return {0, p.vecs};
+    const int half = (p.vecs + 1) / 2, rank = static_cast<int>(cluster_rank());
+    return {rank * half, rank == 0 ? half : p.vecs - half};
+}
+__device__ __forceinline__ void add_source(RowSource &s, int n, const void *base, int64_t ld, const Share &c, int size)
+{
+    s.base[n] = static_cast<const unsigned char *>(base) + c.first * 8 * size;
     s.pitch[n] = ld * size;
-    s.bytes[n] = base != nullptr ? H * size : 0;
+    s.bytes[n] = base != nullptr ? c.vecs * 8 * size : 0;
     s.at[n] = s.stage;
     s.stage += s.bytes[n];
 }
@@ -252,76 +285,44 @@ __device__ __forceinline__ Row8<F32> stage_row8(const unsigned char *stage, cons
     return r;
 }
 
-// A row's vectors for the passes over it.  From a stage of the ring they are read each time that they are wanted, which keeps
-// them out of the registers that the sums need; a long row's are loaded once.
+// A row's vectors for the passes over it, read from its stage each time that they are wanted, which keeps them out of the
+// registers that the sums need.
 template <bool YF32, bool HF32>
 struct StageRow {
     const unsigned char *stage;
     const RowSource &src;
     int vecs;
 
-    __device__ __forceinline__ Row8<YF32> y(int, int j) const { return at<YF32>(0, j); }
-    __device__ __forceinline__ Row8<HF32> h(int, int j) const { return at<HF32>(1, j); }
-    __device__ __forceinline__ Row8<HF32> g(int, int j) const { return at<HF32>(2, j); }
-    __device__ __forceinline__ Row8<false> x(int, int j) const { return at<false>(3, j); }
+    __device__ __forceinline__ Row8<YF32> y(int j) const { return at<YF32>(0, j); }
+    __device__ __forceinline__ Row8<HF32> h(int j) const { return at<HF32>(1, j); }
+    __device__ __forceinline__ Row8<HF32> g(int j) const { return at<HF32>(2, j); }
+    __device__ __forceinline__ Row8<false> x(int j) const { return at<false>(3, j); }
     template <bool F32>
     __device__ __forceinline__ Row8<F32> at(int n, int j) const
     {
         return j < vecs ? stage_row8<F32>(stage, src, n, j) : Row8<F32>{};
     }
 };
-template <bool YF32, bool HF32, int V, bool BACKWARD>
-struct LoadedRow {
-    Row8<YF32> y_[V];
-    Row8<HF32> h_[V], g_[BACKWARD ? V : 1];
-    Row8<false> x_[BACKWARD ? V : 1];
-
-    __device__ __forceinline__ LoadedRow(const NormParams &p, int64_t row)
-    {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            y_[i] = Row8<YF32>{};
-            h_[i] = Row8<HF32>{};
-            if (j < p.vecs && p.y != nullptr)
-                y_[i] = load_row8<YF32>(p.y, row * p.ldy + 8 * j);
-            if (j < p.vecs && (!BACKWARD || p.dx != nullptr))
-                h_[i] = load_row8<HF32>(p.h, row * p.ldh + 8 * j);
-            if constexpr (BACKWARD) {
-                g_[i] = Row8<HF32>{};
-                x_[i] = Row8<false>{};
-                if (j < p.vecs && p.dx != nullptr)
-                    x_[i] = load_row8<false>(p.dx, row * p.lddx + 8 * j);
-                if (j < p.vecs && p.dh_out != nullptr)
-                    g_[i] = load_row8<HF32>(p.dh_out, row * p.lddh + 8 * j);
-            }
-        }
-    }
-    __device__ __forceinline__ Row8<YF32> y(int i, int) const { return y_[i]; }
-    __device__ __forceinline__ Row8<HF32> h(int i, int) const { return h_[i]; }
-    __device__ __forceinline__ Row8<HF32> g(int i, int) const { return g_[i]; }
-    __device__ __forceinline__ Row8<false> x(int i, int) const { return x_[i]; }
-};
-
 template <bool KEPT>
-__device__ __forceinline__ Vec8 weight8_of(const float *w, int j) { return KEPT ? kept8(w, j) : weight8(w, j); }
+__device__ __forceinline__ Vec8 weight8_of(const float *w, int first, int j) { return KEPT ? kept8(w, j) : weight8(w, first + j); }
 
 // Whether channels have a factor behind the block: w_post, a gate or both.
 __device__ __forceinline__ bool has_back(const NormParams &p) { return p.post != nullptr || p.gate_kind == 1; }
-// Its vector j, from `back`, where the CTA keeps the products, or (KEPT false) from the two.
+// Its vector j of the CTA's, which begin at `first`: from `back`, where the CTA keeps the products, or (KEPT false) from the two.
 template <bool KEPT>
-__device__ __forceinline__ Vec8 back_weight8(const NormParams &p, const float *back, int j)
+__device__ __forceinline__ Vec8 back_weight8(const NormParams &p, const float *back, int first, int j)
 {
     if constexpr (KEPT)
         return kept8(back, j);
+    j += first;
     if (p.gate_kind != 1)
         return weight8(p.post, j);
     return p.post != nullptr ? weight8(p.post, j) * weight8(p.gate, j) : weight8(p.gate, j);
 }
 
 // y, h -> h', x of one row.
-template <bool YF32, bool HF32, int V, bool KEPT, typename Row, typename Between>
-__device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float inv, const float *back, RowSums &sums, int &turn, int lane, int warp, const Row &in,
+template <bool YF32, bool HF32, int V, bool KEPT, int CTAS, typename Row, typename Between>
+__device__ __forceinline__ void norm_row(const NormParams &p, const Share &c, int64_t row, float inv, const float *back, RowSums &sums, int &count, bool &lost, int lane, int warp, const Row &in,
                                          Between &&between)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
@@ -329,11 +330,11 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
     uint64_t s2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        a[i] = widen8<YF32>(in.y(i, tid + i * nt));
+        a[i] = widen8<YF32>(in.y(tid + i * nt));
         dot8(s2, a[i], a[i]);
     }
     float factor = p.gate_kind == 2 ? __ldg(p.gate + row) : 1.0f;
-    const float s = sums.one(total(s2), turn, lane, warp);
+    const float s = sums.one<CTAS>(total(s2), count, lost, lane, warp, p.fault);
     between();
     if (p.post != nullptr)
         factor *= rsqrtf(s * inv + p.eps);
@@ -341,23 +342,23 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = tid + i * nt;
-        if (j < p.vecs) {
+        if (j < c.vecs) {
             a[i] = a[i] * factor;
             if (has_back(p))
-                a[i] = a[i] * back_weight8<KEPT>(p, back, j);
-            a[i] = fma8(widen8<HF32>(in.h(i, j)), p.scale, a[i]);
-            store8<HF32>(p.h_out, row * p.H + 8 * j, a[i], p.h_out != nullptr);
+                a[i] = a[i] * back_weight8<KEPT>(p, back, c.first, j);
+            a[i] = fma8(widen8<HF32>(in.h(j)), p.scale, a[i]);
+            store8<HF32>(p.h_out, row * p.H + 8 * (c.first + j), a[i], p.h_out != nullptr);
             dot8(s2, a[i], a[i]);
         }
     }
     if (p.pre != nullptr) {
-        const float r = rsqrtf(sums.one(total(s2), turn, lane, warp) * inv + p.eps);
+        const float r = rsqrtf(sums.one<CTAS>(total(s2), count, lost, lane, warp, p.fault) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
-            if (j < p.vecs) {
-                Vec8 x = a[i] * r * weight8(p.pre, j);
-                store8<false>(p.x, row * p.H + 8 * j, x);
+            if (j < c.vecs) {
+                Vec8 x = a[i] * r * weight8(p.pre, c.first + j);
+                store8<false>(p.x, row * p.H + 8 * (c.first + j), x);
             }
         }
     }
@@ -366,17 +367,17 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, float
 // The gradients of a row in three passes, with the row's sums between them: y^2, h'^2 and dx w_pre h' before the second, which
 // leaves the sum of b n1 (or of g u) for the third.
 template <bool YF32, bool HF32, int V, bool KEPT, typename Row>
-__device__ __forceinline__ void backward_sums(const NormParams &p, const float *pre_weight, const Row &in, float (&s)[4])
+__device__ __forceinline__ void backward_sums(const NormParams &p, const Share &c, const float *pre_weight, const Row &in, float (&s)[4])
 {
     uint64_t sy = 0, sh = 0, sd = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
-        const Vec8 y = widen8<YF32>(in.y(i, j)), h = widen8<HF32>(in.h(i, j));
+        const Vec8 y = widen8<YF32>(in.y(j)), h = widen8<HF32>(in.h(j));
         dot8(sy, y, y);
         dot8(sh, h, h);
-        if (p.dx != nullptr && j < p.vecs)
-            dot8(sd, widen8<false>(in.x(i, j)) * weight8_of<KEPT>(pre_weight, j), h);
+        if (p.dx != nullptr && j < c.vecs)
+            dot8(sd, widen8<false>(in.x(j)) * weight8_of<KEPT>(pre_weight, c.first, j), h);
     }
     s[0] = total(sy);
     s[1] = total(sh);
@@ -399,29 +400,29 @@ __device__ __forceinline__ RowFactors row_factors(const NormParams &p, int64_t r
 // g becomes b without the token's gate; y the row's elements of y; add_pre and add_post take vector i's terms of the sums over
 // rows (dx n2; token gate g n1).
 template <bool YF32, bool HF32, int V, bool KEPT, typename Row, typename AddPre, typename AddPost>
-__device__ __forceinline__ float backward_apply(const NormParams &p, int64_t row, const RowFactors &f, const float *pre_weight, const float *back, const Row &in, Vec8 (&g)[V],
+__device__ __forceinline__ float backward_apply(const NormParams &p, const Share &c, int64_t row, const RowFactors &f, const float *pre_weight, const float *back, const Row &in, Vec8 (&g)[V],
                                                 Row8<YF32> (&y)[V], AddPre &&add_pre, AddPost &&add_post)
 {
     uint64_t sm = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
-        y[i] = in.y(i, j);
-        if (j < p.vecs) {
-            g[i] = widen8<HF32>(in.g(i, j));
+        y[i] = in.y(j);
+        if (j < c.vecs) {
+            g[i] = widen8<HF32>(in.g(j));
             if (p.dx != nullptr) {
-                const Vec8 n = widen8<HF32>(in.h(i, j)) * f.r2, d = widen8<false>(in.x(i, j));
-                g[i] = fma8(fma8(n, -f.c2, d * weight8_of<KEPT>(pre_weight, j)), f.r2, g[i]);
+                const Vec8 n = widen8<HF32>(in.h(j)) * f.r2, d = widen8<false>(in.x(j));
+                g[i] = fma8(fma8(n, -f.c2, d * weight8_of<KEPT>(pre_weight, c.first, j)), f.r2, g[i]);
                 add_pre(i, d, n);
             }
             if (p.dh != nullptr) {
                 Vec8 v = g[i] * p.scale;
-                store8<HF32>(p.dh, row * p.H + 8 * j, v);
+                store8<HF32>(p.dh, row * p.H + 8 * (c.first + j), v);
             }
             const Vec8 n1 = widen8<YF32>(y[i]) * f.r1;
             add_post(i, g[i] * f.token, n1);
             if (has_back(p))
-                g[i] = g[i] * back_weight8<KEPT>(p, back, j);
+                g[i] = g[i] * back_weight8<KEPT>(p, back, c.first, j);
             dot8(sm, g[i], n1);
         }
     }
@@ -430,9 +431,9 @@ __device__ __forceinline__ float backward_apply(const NormParams &p, int64_t row
 
 // m: the sum of b n1 without the token's gate.
 template <bool YF32, int V>
-__device__ __forceinline__ void backward_store(const NormParams &p, int64_t row, float inv, const RowFactors &f, float m, const Vec8 (&g)[V], const Row8<YF32> (&y)[V])
+__device__ __forceinline__ void backward_store(const NormParams &p, const Share &c, int64_t row, float inv, const RowFactors &f, float m, const Vec8 (&g)[V], const Row8<YF32> (&y)[V])
 {
-    if (p.gate_kind == 2 && p.dgate != nullptr && threadIdx.x == 0)
+    if (p.gate_kind == 2 && p.dgate != nullptr && threadIdx.x == 0 && c.first == 0)
         p.dgate[row] = m;
     if (p.dy == nullptr)
         return;
@@ -440,36 +441,29 @@ __device__ __forceinline__ void backward_store(const NormParams &p, int64_t row,
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
-        if (j < p.vecs) {
+        if (j < c.vecs) {
             Vec8 v = fma8(widen8<YF32>(y[i]), -c1, g[i]) * factor;
-            store8<YF32>(p.dy, row * p.H + 8 * j, v);
+            store8<YF32>(p.dy, row * p.H + 8 * (c.first + j), v);
         }
     }
-}
-
-// Vector j of acc += a b, in shared memory that this thread alone uses.
-__device__ __forceinline__ void add8(float *acc, int j, const Vec8 &a, const Vec8 &b)
-{
-    Vec8 v = fma8(a, b, kept8(acc, j));
-    store8<true>(acc, 8 * j, v);
 }
 
 // The products of w_post and gate of this thread's columns into shared memory at `kept`, which then points behind them.
 // (Only the thread that writes them reads them.)
 template <int V, bool KEEP>
-__device__ __forceinline__ const float *keep_back(const NormParams &p, float *&kept)
+__device__ __forceinline__ const float *keep_back(const NormParams &p, const Share &c, float *&kept)
 {
     if (!KEEP || !has_back(p))
         return nullptr;
     float *const back = kept;
     for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
-        if (j < p.vecs) {
-            Vec8 w = back_weight8<false>(p, nullptr, j);
+        if (j < c.vecs) {
+            Vec8 w = back_weight8<false>(p, nullptr, c.first, j);
             store8<true>(back, 8 * j, w);
         }
     }
-    kept += p.H;
+    kept += 8 * c.vecs;
     return back;
 }
 
@@ -481,7 +475,7 @@ struct Ring {
     bool ok;
 
     template <int N>
-    __device__ __forceinline__ void start(const NormParams &p, const RowSource &src, unsigned char *memory, uint64_t *full)
+    __device__ __forceinline__ void start(const NormParams &p, const RowSource &src, unsigned char *memory, uint64_t *full, int64_t first, int64_t step)
     {
         smem = memory;
         base = smem_u32(memory);
@@ -493,7 +487,7 @@ struct Ring {
                 mbar_init(full0 + 8 * s, 1);
             fence_mbar_init();
             for (int s = 0; s < p.stages; ++s) {
-                const int64_t row = blockIdx.x + int64_t{s} * gridDim.x;
+                const int64_t row = first + s * step;
                 if (row < p.T)
                     fetch_row<N>(src, base + s * src.stage, full0 + 8 * s, row);
             }
@@ -525,8 +519,8 @@ struct Ring {
     }
 };
 
-template <bool YF32, bool HF32, int V, bool KEEP>
-__global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_kernel(const NormParams p)
+template <bool YF32, bool HF32, int V, bool KEEP, int CTAS>
+__global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];
     __shared__ RowSums sums;
@@ -534,49 +528,30 @@ __global__ void __launch_bounds__(kNormThreads, V == 2 ? 2 : 1) block_norm_ring_
     pdl_wait_and_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float inv = 1.0f / static_cast<float>(p.H);
-    int turn = 0;
-    sums.clear();
+    const int64_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+    const Share c = my_share<CTAS>(p);
+    int count = 0;
+    bool lost = false;
+    sums.clear<CTAS>();
     RowSource src{};
-    add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
-    add_source(src, 1, p.h, p.ldh, p.H, HF32 ? 4 : 2);
+    add_source(src, 0, p.y, p.ldy, c, YF32 ? 4 : 2);
+    add_source(src, 1, p.h, p.ldh, c, HF32 ? 4 : 2);
     float *kept = reinterpret_cast<float *>(norm_smem);
-    const float *back = keep_back<V, KEEP>(p, kept);
+    const float *back = keep_back<V, KEEP>(p, c, kept);
     Ring ring;
-    ring.start<2>(p, src, reinterpret_cast<unsigned char *>(kept), full);
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        const StageRow<YF32, HF32> in{ring.next(p, src), src, p.vecs};
+    ring.start<2>(p, src, reinterpret_cast<unsigned char *>(kept), full, first, step);
+    for (int64_t row = first; row < p.T; row += step) {
+        const StageRow<YF32, HF32> in{ring.next(p, src), src, c.vecs};
         // behind the row's first barrier nobody reads the row before it any more
-        norm_row<YF32, HF32, V, KEEP>(p, row, inv, back, sums, turn, lane, warp, in, [&]() {
-            if (row != blockIdx.x)
-                ring.refill<2>(p, src, 2, row + (int64_t{p.stages} - 1) * gridDim.x);
+        norm_row<YF32, HF32, V, KEEP, CTAS>(p, c, row, inv, back, sums, count, lost, lane, warp, in, [&]() {
+            if (row != first)
+                ring.refill<2>(p, src, 2, row + (p.stages - 1) * step);
         });
     }
 }
 
-template <bool YF32, bool HF32, int V>
-__global__ void __launch_bounds__(kNormThreads) block_norm_long_kernel(const NormParams p)
-{
-    __shared__ RowSums sums;
-    pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const float inv = 1.0f / static_cast<float>(p.H);
-    int turn = 0;
-    sums.clear();
-    __syncthreads();
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        norm_row<YF32, HF32, V, false>(p, row, inv, nullptr, sums, turn, lane, warp, LoadedRow<YF32, HF32, V, false>(p, row), [] {});
-    }
-}
-
-// A CTA's sums over its rows: [2][H] of the workspace (dx n2, then g n1).
-template <int V>
-__device__ __forceinline__ float *partial_of(const NormParams &p, int n, int j)
-{
-    return p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + n) * p.H + 8 * j;
-}
-
-template <bool YF32, bool HF32, int V, bool KEEP>
-__global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(const NormParams p)
+template <bool YF32, bool HF32, int V, bool KEEP, int CTAS>
+__global__ void __launch_bounds__(kNormThreads) block_norm_backward_kernel(const NormParams p)
 {
     extern __shared__ float4 norm_smem[];
     __shared__ RowSums sums;
@@ -584,110 +559,69 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_ring_kernel(
     pdl_wait_and_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const float inv = 1.0f / static_cast<float>(p.H);
-    int turn = 0;
-    sums.clear();
+    const int64_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+    const Share c = my_share<CTAS>(p);
+    int count = 0;
+    bool lost = false;
+    sums.clear<CTAS>();
     RowSource src{};
-    add_source(src, 0, p.y, p.ldy, p.H, YF32 ? 4 : 2);
-    add_source(src, 1, p.dx != nullptr ? p.h : nullptr, p.ldh, p.H, HF32 ? 4 : 2);
-    add_source(src, 2, p.dh_out, p.lddh, p.H, HF32 ? 4 : 2);
-    add_source(src, 3, p.dx, p.lddx, p.H, 2);
+    add_source(src, 0, p.y, p.ldy, c, YF32 ? 4 : 2);
+    add_source(src, 1, p.dx != nullptr ? p.h : nullptr, p.ldh, c, HF32 ? 4 : 2);
+    add_source(src, 2, p.dh_out, p.lddh, c, HF32 ? 4 : 2);
+    add_source(src, 3, p.dx, p.lddx, c, 2);
     Vec8 acc[2][V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[0][i] = acc[1][i] = Vec8::splat(0.f);
     float *kept = reinterpret_cast<float *>(norm_smem);
-    const float *back = keep_back<V, KEEP>(p, kept), *pre = KEEP ? kept : p.pre;
+    const float *back = keep_back<V, KEEP>(p, c, kept), *pre = KEEP ? kept : p.pre;
     if (KEEP && p.pre != nullptr) {
         for (int i = 0; i < V; ++i) {
             const int j = tid + i * nt;
-            if (j < p.vecs) {
-                Vec8 w = weight8(p.pre, j);
+            if (j < c.vecs) {
+                Vec8 w = weight8(p.pre, c.first + j);
                 store8<true>(kept, 8 * j, w);
             }
         }
-        kept += p.H;
+        kept += 8 * c.vecs;
     }
     Ring ring;
-    ring.start<4>(p, src, reinterpret_cast<unsigned char *>(kept), full);
+    ring.start<4>(p, src, reinterpret_cast<unsigned char *>(kept), full, first, step);
     // A row's second pass and the next row's first share one exchange of sums.
     const unsigned char *stage = ring.next(p, src);
     float s[4];
-    backward_sums<YF32, HF32, V, KEEP>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
+    backward_sums<YF32, HF32, V, KEEP>(p, c, pre, StageRow<YF32, HF32>{stage, src, c.vecs}, s);
     s[3] = 0.f;
-    sums.four(s, turn, lane, warp);
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    sums.four<CTAS>(s, count, lost, lane, warp, p.fault);
+    for (int64_t row = first; row < p.T; row += step) {
         const RowFactors f = row_factors(p, row, inv, s);
         Vec8 g[V];
         Row8<YF32> y[V];
         const float m = backward_apply<YF32, HF32, V, KEEP>(
-            p, row, f, pre, back, StageRow<YF32, HF32>{stage, src, p.vecs}, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { acc[0][i] = fma8(d, n, acc[0][i]); },
+            p, c, row, f, pre, back, StageRow<YF32, HF32>{stage, src, c.vecs}, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { acc[0][i] = fma8(d, n, acc[0][i]); },
             [&](int i, const Vec8 &v, const Vec8 &n) { acc[1][i] = fma8(v, n, acc[1][i]); });
-        const bool more = row + gridDim.x < p.T;
+        const bool more = row + step < p.T;
         if (more) {
             stage = ring.next(p, src);
-            backward_sums<YF32, HF32, V, KEEP>(p, pre, StageRow<YF32, HF32>{stage, src, p.vecs}, s);
+            backward_sums<YF32, HF32, V, KEEP>(p, c, pre, StageRow<YF32, HF32>{stage, src, c.vecs}, s);
         }
         s[3] = m;
-        sums.four(s, turn, lane, warp);
+        sums.four<CTAS>(s, count, lost, lane, warp, p.fault);
         if (more)
-            ring.refill<4>(p, src, 2, row + int64_t{p.stages} * gridDim.x);
-        backward_store<YF32, V>(p, row, inv, f, s[3], g, y);
+            ring.refill<4>(p, src, 2, row + p.stages * step);
+        backward_store<YF32, V>(p, c, row, inv, f, s[3], g, y);
     }
-    if (p.partial != nullptr) {
+    if (p.partial != nullptr) {  // a row of [2][H] per CTA (per cluster): dx n2, then g n1
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int j = tid + i * nt;
-                if (j < p.vecs) {
-                    store8<true>(partial_of<V>(p, n, j), 0, acc[n][i]);
+                if (j < c.vecs) {
+                    store8<true>(p.partial + (first * 2 + n) * p.H, 8 * (c.first + j), acc[n][i]);
                 }
             }
     }
-}
-
-template <bool YF32, bool HF32, int V>
-__global__ void __launch_bounds__(kNormThreads) block_norm_backward_long_kernel(const NormParams p)
-{
-    extern __shared__ float4 norm_smem[];  // the CTA's sums [2][H]
-    __shared__ RowSums sums;
-    pdl_wait_and_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-    const float inv = 1.0f / static_cast<float>(p.H);
-    int turn = 0;
-    sums.clear();
-    __syncthreads();
-    float *acc = reinterpret_cast<float *>(norm_smem);
-    auto each = [&](auto &&f) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (tid + i * nt < p.vecs)
-                    f(n, tid + i * nt, reinterpret_cast<float4 *>(acc + n * p.H + 8 * (tid + i * nt)));
-    };
-    each([](int, int, float4 *a) { a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f); });
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        const LoadedRow<YF32, HF32, V, true> in(p, row);
-        float s[4];
-        backward_sums<YF32, HF32, V, false>(p, p.pre, in, s);
-        s[3] = 0.f;
-        sums.four(s, turn, lane, warp);
-        const RowFactors f = row_factors(p, row, inv, s);
-        Vec8 g[V];
-        Row8<YF32> y[V];
-        float m = backward_apply<YF32, HF32, V, false>(
-            p, row, f, p.pre, nullptr, in, g, y, [&](int i, const Vec8 &d, const Vec8 &n) { add8(acc, tid + i * nt, d, n); },
-            [&](int i, const Vec8 &v, const Vec8 &n) { add8(acc + p.H, tid + i * nt, v, n); });
-        m = sums.one(m, turn, lane, warp);
-        backward_store<YF32, V>(p, row, inv, f, m, g, y);
-    }
-    if (p.partial != nullptr)
-        each([&](int n, int j, float4 *a) {
-            float4 *to = reinterpret_cast<float4 *>(partial_of<V>(p, n, j));
-            to[0] = a[0];
-            to[1] = a[1];
-        });
 }
 
 // The CTAs' sums, in order: a warp takes 32 columns of rows w, w + 8, ...; the eight warps' are added in order.

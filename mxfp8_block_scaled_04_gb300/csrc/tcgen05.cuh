@@ -144,6 +144,22 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// mbar_wait_cycles for a barrier that tells of other CTAs' generic stores into this CTA's shared memory.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int64_t limit)
+{
+    const int64_t t0 = clock64();
+    while (true) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (done)
+            return true;
+        if (clock64() - t0 > limit)
+            return false;
+    }
+}
 // Arrive on a barrier of either CTA.  What these arrivals order is not generic memory (accumulator reads that have
 // completed; zeros already handed to the async proxy), so the default scope does: with .release.cluster an arrival took
 // 1000 to 3000 cycles, and a wait with .acquire.cluster 360 where the phase was already complete.
