@@ -39,7 +39,7 @@ from .moe import (  # noqa: F401
 from .mxfp8_matmul import (  # noqa: F401
     matmul_mxfp8_grouped, matmul_mxfp8_grouped_dgrad, matmul_mxfp8_grouped_wgrad, mxfp8_matmul_grouped,
 )
-from .block_norm import (  # noqa: F401
+from .norm import (  # noqa: F401
     BlockNorm, BlockNormConfig, BlockNormGrads, block_norm, block_norm_backward, block_norm_backward_c,
     block_norm_backward_workspace_bytes, block_norm_c,
 )
