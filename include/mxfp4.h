@@ -130,12 +130,13 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
  *
  *   x            device, x_type, 16-byte aligned; K and ldx multiples of 8, ldx >= K; M < 2^28.
  *   b_codes, b_scale, out, out_type, ldo   as for mxfp4_matmul.  (A block of B with scale 255 makes its output column NaN.)
- *   workspace    device, mxfp4_linear_workspace_bytes(M, K) bytes, 16-byte aligned; not shared by calls that may overlap.
+ *   workspace    device, mxfp4_linear_workspace_bytes(M, K, N) bytes (0 for few rows, two at least: NULL), 16-byte aligned; not
+ *                shared by calls that may overlap.
  *
  * Meant for few rows (the weights' bytes are the time up to about 16; every row costs eight of the tensor cores' columns):
  * for many, cast x and call mxfp4_matmul.
  */
-size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
+size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
 mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int64_t ldx, const void *b_codes,
                             const void *b_scale, int64_t N, void *out, int out_type, int64_t ldo, void *workspace,

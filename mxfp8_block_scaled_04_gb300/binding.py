@@ -102,7 +102,7 @@ def lib():
                     ("block_norm_backward_workspace_bytes", sz, [i64, i64]),
                     ("block_norm_backward", i32,
                      [vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]),
-                    ("mxfp4_linear_workspace_bytes", sz, [i64, i64]),
+                    ("mxfp4_linear_workspace_bytes", sz, [i64, i64, i64]),
                     ("mxfp4_linear", i32, [vp, i32, i64, i64, i64, vp, vp, i64, vp, i32, i64, vp, vp]),
                     ("mxfp4_linear_grouped_workspace_bytes", sz, [i64, i64, i32]),
                     ("mxfp4_linear_grouped", i32,

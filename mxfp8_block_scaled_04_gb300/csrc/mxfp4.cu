@@ -7,6 +7,7 @@
 #include "../../include/mxfp4.h"
 #include "host.h"
 #include "mxfp4_cast.cuh"
+#include "mxfp4_few.cuh"
 #include "mxfp4_gemm.cuh"
 #include "mxfp4_pair.cuh"
 #include "mxfp4_parts.cuh"
@@ -25,6 +26,8 @@ constexpr int64_t kLongRow = int64_t{1} << 29;  // columns whose scales' offsets
 // 192x28672x8192 (112) 30 / 35; 64 experts of 2048 x 7168 with 64, 96, 128, 192, 256 rows: 95 / 87, 98 / 90, 101 / 107,
 // 107 / 139, 131 / 177.
 constexpr int64_t kPairMinTiles = 64;
+constexpr int kFewSms = 152;  // (a constant: the workspace's size, which follows from the kernel, is asked for without a device)
+constexpr int64_t kFewWork = 16;
 constexpr int64_t kPairMinGroupRows = 128;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -255,6 +258,53 @@ mxfp8_status_t launch_experts(GemmParams &p, const void *q_codes, const void *p_
         return st;
     const int64_t bound = (p.Q / 128 + groups) * static_cast<int64_t>(p.p_tiles);
     return f32 ? launch_group_as<true, PARTS>(pm, qm, p, bound, device, stream) : launch_group_as<false, PARTS>(pm, qm, p, bound, device, stream);
+}
+
+template <int MROWS, int STAGES, bool XF32, bool F32>
+mxfp8_status_t launch_few_as(const GemmParams &p, const CUtensorMap &pm, const PartsParams &q, int splits, int device, cudaStream_t stream)
+{
+    using Shape = SplitShape<MROWS * kParts, STAGES>;
+    static KernelSetup setup;
+    int ctas = 0;
+    const mxfp8_status_t st = setup(mxfp4_few_kernel<MROWS, STAGES, XF32, F32>, device, kGemmThreads, Shape::kSmem, &ctas);
+    if (st != MXFP8_OK)
+        return st;
+    return launch_serialized(mxfp4_few_kernel<MROWS, STAGES, XF32, F32>, dim3(static_cast<unsigned>(p.p_tiles * splits)), kGemmThreads, Shape::kSmem, splits,
+                             stream, pm, p, q.x, q.ldx, q.K, static_cast<int>(q.R), splits);
+}
+
+// CTAs that share a tile's K in the kernel for few uncast rows, by the rule of launch_split.
+int few_splits(int64_t p_tiles, int k_iters, int sms)
+{
+    int splits = 1;
+    while (splits < 8 && p_tiles * splits * 2 <= 2 * sms && splits * 2 <= k_iters)
+        splits *= 2;
+    return splits;
+}
+
+// Two rows or fewer, or rows whose splitting is short: kFewWork rows times stages of a CTA, two of which at a time take one of its
+// four warps about half a microsecond.  Measured (us, in the products' kernel / by a kernel before it), rows x K x N:
+// 1x8192x28672 20.9 / 23.1, 2x8192x28672 21.1 / 23.1, 3x8192x28672 28 / 22.7, 4x8192x8192 11.7 / 10.7, 4x4096x4096 5.9 / 6.6,
+// 8x4096x4096 7.9 / 7.7, 8x2048x2048 5.6 / 10.5, 8x1024x8192 5.6 / 6.1.
+bool few_rows(int64_t rows, int64_t K, int64_t N)
+{
+    const int k_iters = static_cast<int>(ceil_div(K, 256));
+    return rows <= 2 || (rows <= kFewRows && rows * ceil_div(k_iters, few_splits(ceil_div(N, kGemmRows), k_iters, kFewSms)) <= kFewWork);
+}
+
+template <bool XF32, bool F32>
+mxfp8_status_t launch_few(const GemmParams &p, const PartsParams &q, const void *p_codes, int device, cudaStream_t stream)
+{
+    CUtensorMap pm;
+    mxfp8_status_t st;
+    if ((st = code_map(&pm, p_codes, p.P, q.pitch, kGemmRows)) != MXFP8_OK)
+        return st;
+    const int splits = few_splits(p.p_tiles, p.k_iters, kFewSms);
+    if (q.R <= 2)
+        return launch_few_as<2, 5, XF32, F32>(p, pm, q, splits, device, stream);
+    if (q.R <= 4)
+        return launch_few_as<4, 4, XF32, F32>(p, pm, q, splits, device, stream);
+    return launch_few_as<8, 4, XF32, F32>(p, pm, q, splits, device, stream);
 }
 
 template <bool GROUPED>
@@ -552,9 +602,9 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
     return launch_experts<1>(p, a_codes, b_codes, K, out_type, device, stream);
 }
 
-size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K)
+size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N)
 {
-    if (M <= 0 || K <= 0 || M >= kMaxDim / kParts)
+    if (M <= 0 || K <= 0 || N <= 0 || M >= kMaxDim / kParts || K >= kMaxDim || N >= kMaxDim || few_rows(M, K, N))
         return 0;
     return static_cast<size_t>(M) * kParts * mxfp4_row_bytes(K) + mxfp4_scale_bytes(M * kParts, K);
 }
@@ -567,9 +617,11 @@ mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int
     if (st != MXFP8_OK)
         return st;
     GemmParams p;
-    if (M > 0 && N > 0 && K > 0 && workspace == nullptr)
+    const bool few = M == 0 || N <= 0 || few_rows(M, K, N);
+    if (!few && K > 0 && workspace == nullptr)
         return MXFP8_ERR_WORKSPACE;
-    if ((st = gemm_params(&p, q.out, q.scale, M * kParts, b_codes, b_scale, N, K, out, out_type, ldo)) != MXFP8_OK)
+    // (few rows have no operand in memory: x stands for it in the checks)
+    if ((st = gemm_params(&p, few ? x : q.out, few ? x : q.scale, M * kParts, b_codes, b_scale, N, K, out, out_type, ldo)) != MXFP8_OK)
         return st;
     int device = 0;
     if ((st = active_device(&device)) != MXFP8_OK)
@@ -584,6 +636,11 @@ mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int
         return zero_rows(out, M, N, ldo, out_type, stream);
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
+    if (few) {
+        if (x_type == MXFP4_F32)
+            return out_type == MXFP4_F32 ? launch_few<true, true>(p, q, b_codes, device, stream) : launch_few<true, false>(p, q, b_codes, device, stream);
+        return out_type == MXFP4_F32 ? launch_few<false, true>(p, q, b_codes, device, stream) : launch_few<false, false>(p, q, b_codes, device, stream);
+    }
     if ((st = launch_parts<false>(q, x_type, M * q.chunks, device, stream)) != MXFP8_OK)
         return st;
     return launch_dense<kParts>(p, q.out, b_codes, K, out_type, device, stream);

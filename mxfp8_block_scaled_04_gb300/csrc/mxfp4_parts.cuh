@@ -1,11 +1,13 @@
 // Rows that are not cast, as exact operands of the MXFP4 products: x = sum of kParts 4-bit rows.
 //
-// Per block of 32, with e the exponent of the MXFP4 cast (6 * 2^e >= amax > 3 * 2^e): part 0 is the cast's q0 at 2^e and
-// leaves |r| <= 2^e; part j is the cast of what is left at 2^(e + 1 - 3j), where it is at most 4 and leaves at most half a
-// unit.  Every remainder is exact in fp32, so after kParts = 8 parts x differs from their sum by at most 2^(e - 21) < amax *
-// 2^-22 (by 2^-126 at most where e + 1 - 3j passes E8M0's least exponent, -127: those parts are zero).  The parts are rows 8i to
-// 8i + 7 of the tokens' operand: one token fills half of the smallest MMA's 16 columns, sixteen fill 128, and the weights'
-// bytes remain the time.  The products' epilogue adds a row's eight sums in fp32, the smallest first.
+// Per block of 32, x * 2^k is rounded to an integer X of 24 bits, with k such that the block's largest magnitude amax becomes at
+// least 1.71 * 2^21: an error of at most 2^-22.7 amax per element (2^-128 where the blocks' values are so small that k would
+// pass 127).  X has eight octal digits, balanced between -4 and 3, which E2M1 holds exactly; part j is the digits of weight
+// 8^(7 - j), with the scale 2^(21 - 3j - k).  X + 4 * (8^8 - 1) / 7 has the digits plus 4 as its octal digits, so that all of
+// this is shifts and logic: a digit of eight elements at a time.  (Casting what the parts before leave, with the conversion
+// instructions, took three times as long.)  The parts are rows 8i to 8i + 7 of the tokens' operand: one token fills half of
+// the smallest MMA's 16 columns, sixteen fill 128, and the weights' bytes remain the time.  The products' epilogue adds a
+// row's eight sums in fp32, the smallest first.
 //
 // A warp takes 256 columns of a row: four lanes share a block, each with 8 elements.  Bound by launch and latency for the
 // few rows that this serves.
@@ -38,6 +40,53 @@ struct PartsParams {
     int num_groups;
     int *err_flag;
 };
+
+// E2M1 codes of eight balanced octal digits plus 4, one to four bits of w: 0 .. 7 stand for -4 .. 3, whose codes are
+// 14, 13, 12, 10, 0, 2, 4, 5.
+__device__ __forceinline__ uint32_t digit_codes(uint32_t w)
+{
+    constexpr uint32_t kOnes = 0x11111111u;
+    const uint32_t b0 = w, b1 = w >> 1, b2 = w >> 2;
+    const uint32_t c2 = (b2 & b1) | (~b2 & ~(b1 & b0));
+    const uint32_t c1 = (b2 & ~b1 & b0) | (~b2 & ~(b1 ^ b0));
+    const uint32_t c0 = (b2 & b1 & b0) | (~b2 & ~b1 & b0);
+    return (c0 & kOnes) | (c1 & kOnes) << 1 | (c2 & kOnes) << 2 | (~b2 & kOnes) << 3;
+}
+
+// Eight elements of x split into parts: put(j, codes of part j, scale bytes of part j for the four blocks from lane & ~15 on).
+// All lanes of the warp, four to a block; `live` false: a row that x does not have.  A block that holds a NaN or an infinity,
+// like such a row, gets the scale 255 in part 0 and zero codes.
+template <typename Put>
+__device__ __forceinline__ void split_parts(const float (&v)[8], bool live, Put &&put)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // as integers a NaN lies above every number
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const bool nan = !live || m >= 0x7F800000u;
+    // 2^k: 22 - exponent, one less for a mantissa above 1.71 (digits of at most 3 reach 0.857 * 2^23)
+    const int e = max(static_cast<int>(m >> 23) - 1 + ((m & 0x7FFFFFu) > 0x5B0000u ? 1 : 0), 21);  // 148 - k, part 0's scale
+    const float mul = __uint_as_float(static_cast<uint32_t>(nan ? 0 : 275 - e) << 23);
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        u[i] = 0x924924u + static_cast<uint32_t>(nan ? 0 : __float2int_rn(v[i] * mul));
+    uint32_t scales = static_cast<uint32_t>(nan ? 255 : e);
+    scales |= __shfl_down_sync(0xFFFFFFFFu, scales, 4) << 8;  // four blocks, four lanes apart
+    scales |= __shfl_down_sync(0xFFFFFFFFu, scales, 8) << 16;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) {
+        const int down = 21 - 3 * j;
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w |= (4 * i >= down ? u[i] << (4 * i - down) : u[i] >> (down - 4 * i)) & (7u << (4 * i));
+        put(j, digit_codes(w), scales);
+        scales -= 0x03030303u;  // every byte is at least 21
+    }
+}
 
 template <bool F32, bool GROUPED>
 __global__ void __launch_bounds__(kPartsThreads<GROUPED>) mxfp4_parts_kernel(const PartsParams p)
@@ -124,44 +173,17 @@ __global__ void __launch_bounds__(kPartsThreads<GROUPED>) mxfp4_parts_kernel(con
                 v[2 * j + 1] = bf16_hi(w[j]);
             }
         }
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);  // as integers a NaN lies above every number
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const int e0 = at.live ? fp4_exponent(m) : 255;
         const int64_t blk = c / 32;
         const bool in_row = c < p.pitch * 2;  // a row's last block is written whole
         const int64_t r = r0;
         uint8_t *codes = p.out + i * kParts * p.pitch + c / 2;
         uint8_t *tile = p.scale + ((tile0 + (r >> 7)) * p.col_tiles + blk / 4) * 512 + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
-        float mul = fp4_multiplier(e0);
-        int e = e0;
-#pragma unroll
-        for (int j = 0; j < kParts; ++j) {  // (rows 8i .. 8i + 7 lie in one 32-row part of a scale tile)
-            const bool none = e0 == 255 || e < 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] *= mul;
-            const uint32_t q = none ? 0u : cvt_fp4x8(v);
+        split_parts(v, at.live, [&](int j, uint32_t q, uint32_t scales) {  // (rows 8i .. 8i + 7 lie in one 32-row part of a scale tile)
             if (in_row)
                 *reinterpret_cast<uint32_t *>(codes + j * p.pitch) = q;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // what the part leaves, in its own units
-                float lo, hi;
-                fp4x2_to_f32((q >> (8 * k)) & 0xFF, lo, hi);
-                v[2 * k] -= lo;
-                v[2 * k + 1] -= hi;
-            }
-            uint32_t sc = !in_row ? 0u : e0 == 255 ? (j == 0 ? 255u : 0u) : none ? 0u : static_cast<uint32_t>(e);
-            sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 4) << 8;  // four blocks, four lanes apart
-            sc |= __shfl_down_sync(0xFFFFFFFFu, sc, 8) << 16;
             if ((lane & 15) == 0 && blk / 4 < p.col_tiles)
-                *reinterpret_cast<uint32_t *>(tile + j * 16) = sc;
-            mul = j == 0 ? 4.f : 8.f;
-            e -= j == 0 ? 2 : 3;
-        }
+                *reinterpret_cast<uint32_t *>(tile + j * 16) = scales;
+        });
     }
 }
 

@@ -158,8 +158,8 @@ def mxfp4_matmul_grouped(a_codes, a_scale, total_rows, num_groups, offsets, b_co
                                       _stream(stream))
 
 
-def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
-    return int(lib().mxfp4_linear_workspace_bytes(M, K))
+def mxfp4_linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().mxfp4_linear_workspace_bytes(M, K, N))
 
 
 def mxfp4_linear(x, x_type, M, K, ldx, b_codes, b_scale, N, out, out_type, ldo, workspace, stream=None) -> int:
@@ -423,8 +423,10 @@ def linear_mxfp4(x: torch.Tensor, w: MXFP4Matrix, out_dtype: torch.dtype = torch
         if (rows, cols) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
     lib_ = _lib()
-    workspace = torch.empty((lib_.mxfp4_linear_workspace_bytes(M, K),), dtype=torch.uint8, device=dev)
-    st = lib_.mxfp4_linear(x.data_ptr(), kind, M, K, ld, wc, wsc, N, out.data_ptr(), out_kind, ldo, workspace.data_ptr(),
+    # few rows need none; the library knows up to how many
+    nbytes = lib_.mxfp4_linear_workspace_bytes(M, K, N) if M > 1 else 0
+    workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    st = lib_.mxfp4_linear(x.data_ptr(), kind, M, K, ld, wc, wsc, N, out.data_ptr(), out_kind, ldo, _addr(workspace),
                            _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_linear")

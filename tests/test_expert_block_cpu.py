@@ -79,7 +79,7 @@ def test_product_wrappers_refuse(cuda_lib):
 
 # ---- uncast rows on 4-bit weights ----------------------------------------------------------------------
 
-def linear(x=A, xt=0, M=4, K=64, ldx=64, b=A, s=A, N=40, out=A, ot=0, ldo=40, ws=A):
+def linear(x=A, xt=0, M=9, K=64, ldx=64, b=A, s=A, N=40, out=A, ot=0, ldo=40, ws=A):
     return mx.mxfp4_linear(x, xt, M, K, ldx, b, s, N, out, ot, ldo, ws, 0)
 
 
@@ -90,7 +90,7 @@ def test_linear_statuses(cuda_lib):
     assert linear(M=-1) == SHAPE and linear(N=-1) == SHAPE
     for hole in ("x", "b", "s", "out"):
         assert linear(**{hole: None}) == NULL, hole
-    assert linear(ws=None) == WORKSPACE
+    assert linear(ws=None) == WORKSPACE and linear(M=2, ws=None) == DEVICE  # few rows need none
     assert linear(x=A + 8) == ALIGN and linear(ws=A + 8) == ALIGN and linear(b=A + 8) == ALIGN and linear(out=A + 1) == ALIGN
 
 
@@ -109,9 +109,9 @@ def test_linear_grouped_statuses(cuda_lib):
 
 
 def test_linear_workspaces(cuda_lib):
-    assert mx.mxfp4_linear_workspace_bytes(3, 40) == 24 * 32 + mx.mxfp4_scale_bytes(24, 40)
+    assert mx.mxfp4_linear_workspace_bytes(9, 40, 40) == 72 * 32 + mx.mxfp4_scale_bytes(72, 40)
     assert mx.mxfp4_linear_grouped_workspace_bytes(3, 40, 2) == 24 * 32 + mx.mxfp4_grouped_scale_bytes(24, 40, 2)
-    for none in (mx.mxfp4_linear_workspace_bytes(0, 40), mx.mxfp4_linear_workspace_bytes(3, 0), mx.mxfp4_linear_workspace_bytes(1 << 28, 8),
+    for none in (mx.mxfp4_linear_workspace_bytes(0, 40, 40), mx.mxfp4_linear_workspace_bytes(2, 8192, 28672), mx.mxfp4_linear_workspace_bytes(9, 0, 40), mx.mxfp4_linear_workspace_bytes(1 << 28, 8, 8),
                  mx.mxfp4_linear_grouped_workspace_bytes(3, 40, 0)):
         assert none == 0
 
