@@ -1,9 +1,7 @@
 // C ABI of the norms around a block (declarations and contract in include/block_norm.h): host-side checks and launches;
 // the device code is in block_norm.cuh.
 #include <cstdint>
-#include <map>
 #include <mutex>
-#include <tuple>
 #include <type_traits>
 
 #include "../../include/block_norm.h"
@@ -42,23 +40,33 @@ mxfp8_status_t check_config(const block_norm_config_t *cfg, int64_t T, int64_t H
 
 bool pitch_ok(const void *p, int64_t ld, int64_t H) { return p == nullptr || (ld >= H && ld % 8 == 0 && ld < kMaxDim); }
 
-// CTAs of a kernel that are resident at once: they depend on a call's threads and shared memory, few pairs of which occur.
+// CTAs of a kernel that are resident at once: they depend on a call's threads and shared memory, few pairs of which occur (the
+// table holds the last ones, without allocating).
 template <auto *KERN>
 mxfp8_status_t resident(int device, int threads, int smem, int64_t *ctas)
 {
+    struct Known {
+        int device, threads, smem, per_sm;
+    };
     static KernelSetup setup;  // opts the kernel in to the largest size
     static std::mutex mu;
-    static std::map<std::tuple<int, int, int>, int> known;
+    static Known known[16];
+    static unsigned used = 0;
     int all = 0;
     const mxfp8_status_t st = setup(KERN, device, 32, kMostSmem, &all);
     if (st != MXFP8_OK)
         return st;
     std::lock_guard<std::mutex> lock(mu);
-    int &per_sm = known[{device, threads, smem}];
-    if (per_sm == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, smem) != cudaSuccess || per_sm < 1)) {
-        cudaGetLastError();
-        per_sm = 0;
-        return MXFP8_ERR_LAUNCH;
+    int per_sm = 0;
+    for (const Known &k : known)
+        if (k.per_sm > 0 && k.device == device && k.threads == threads && k.smem == smem)
+            per_sm = k.per_sm;
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, smem) != cudaSuccess || per_sm < 1) {
+            cudaGetLastError();
+            return MXFP8_ERR_LAUNCH;
+        }
+        known[used++ % 16] = {device, threads, smem, per_sm};
     }
     *ctas = static_cast<int64_t>(per_sm) * setup.sms[device];
     return MXFP8_OK;

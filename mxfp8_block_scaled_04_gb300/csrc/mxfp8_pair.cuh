@@ -15,6 +15,13 @@
 // A weight gradient's last stage may hold rows of the next expert.  Steps past the expert's last 32 rows are not issued;
 // where the rows are no multiple of 32 each CTA's warp 2 zeroes the rest of the last step in shared memory (its own
 // barrier says that the copy has landed) before the MMA warp sees the stage.
+//
+// Measured: 8192x8192x8192 312 us (3.5 PFLOP/s; the bf16 rate measured with cuBLAS twice over is 3.8), 64 experts of 1024 rows on
+// average, 7168 -> 2048: forward 598 us, input gradient 632, weight gradient 944 to fp32 (3.76 GB: 5.7 TB/s were 660 at
+// HBM's rate) and 719 to bf16; two rows per expert 153, 146, 596 and 352.  Many rows: bound by the MMAs under the power limit (tensor
+// pipe active 72% of the forward's cycles at 1.77 GHz), the ragged last tile of each expert and, for the weight gradient, the
+// path between SMs and L2, where a stage's loads take 3600 to 4200 cycles while tiles are stored.  Few: the weights' bytes
+// (6.3 TB/s), or the gradient's.
 #pragma once
 
 #include "mxfp4_gemm.cuh"
