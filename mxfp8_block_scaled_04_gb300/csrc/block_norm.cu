@@ -259,7 +259,8 @@ mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, in
     int rows = 0;
     if ((st = launch<true>(p, cfg, element_bytes, device, stream, &rows)) != MXFP8_OK || !sums)
         return st;
-    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(2 * H, 32))), kNormReduceThreads, 0, 1, stream, p, rows);
+    return launch_serialized(block_norm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(2 * H, 32))),
+                             rows > kNormReduceCtas ? kNormReduceMany : kNormReduceFew, 0, 1, stream, p, rows);
 }
 
 }  // extern "C"

@@ -2,8 +2,8 @@
 
 Roundings that the tolerances count: a row's sum passes at most 32 additions in a thread and 10 in two trees, each off by
 2^-24 of what it adds up; rsqrtf is good to 2 units of the last of 24 bits; a dozen more products follow.  64 * 2^-24
-= 2^-18 of the magnitudes covers them.  A sum over tokens adds the rows of a CTA (T / 152 at least resident) and up to 304 CTAs' in
-eight strands.  Outputs in bf16 are off by half a unit of the last of 8 bits, 2^-8.
+= 2^-18 of the magnitudes covers them.  A sum over tokens adds a CTA's rows, then the CTAs in eight
+strands or more.  Outputs in bf16 are off by half a unit of the last of 8 bits, 2^-8.
 """
 import math
 
