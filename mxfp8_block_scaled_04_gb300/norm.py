@@ -11,8 +11,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _addr, lib
-from .mxfp4 import _check, _check_input, _lib, _on, _stream, _stream_of
+from .binding import MXFP8Error, _addr, lib
+from .mxfp4 import _check_input, _lib, _on, _stream, _stream_of
 
 GATE_NONE = 0
 GATE_CHANNEL = 1
@@ -59,7 +59,9 @@ def block_norm_backward_c(cfg, T, H, dh_out, lddh, dx, lddx, y, ldy, h_out, ldh,
 
 
 # ---- torch conveniences ----------------------------------------------------------
-# A given ``stream`` is made current around the whole call, so that outputs and workspace belong to it.
+# A given ``stream`` is made current around the whole call, so that outputs and workspace belong to it.  The outputs are
+# empty_like an input where one has their type: between launches an allocation takes about 2.8 microseconds so, and half a
+# microsecond more with its type and device spelled out (a view of a common buffer takes as long as an allocation).
 
 def _vector(w: Optional[torch.Tensor], H: int, name: str) -> Optional[int]:
     if w is None:
@@ -113,11 +115,14 @@ def block_norm(y: Optional[torch.Tensor], h: torch.Tensor, pre_weight: Optional[
     kind, ga = _gate(gate, T, H)
     cfg = BlockNormConfig(y_type, h_type, kind, scale, eps, _vector(pre_weight, H, "pre_weight"),
                           _vector(post_weight, H, "post_weight"), ga)
-    dev = h.device
-    h_out = torch.empty((T, H), dtype=h.dtype, device=dev)
-    x = None if pre_weight is None else torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    _check(_lib().block_norm(ctypes.byref(cfg), T, H, ya, ldy, h.data_ptr(), ldh, h_out.data_ptr(), _addr(x),
-                             _stream_of(dev)), "block_norm")
+    h_out = torch.empty_like(h)
+    x = xa = None
+    if pre_weight is not None:
+        x = torch.empty_like(h) if h_type == 0 else h.new_empty((T, H), dtype=torch.bfloat16)
+        xa = x.data_ptr()
+    st = _lib().block_norm(ctypes.byref(cfg), T, H, ya, ldy, h.data_ptr(), ldh, h_out.data_ptr(), xa, _stream_of(h.device))
+    if st:
+        raise MXFP8Error(st, "block_norm")
     return BlockNorm(h_out, x)
 
 
@@ -143,18 +148,18 @@ def block_norm_backward(grad_h: Optional[torch.Tensor], grad_x: Optional[torch.T
     kind, ga = _gate(gate, T, H)
     cfg = BlockNormConfig(y_type, h_type, kind, scale, eps, _vector(pre_weight, H, "pre_weight"),
                           _vector(post_weight, H, "post_weight"), ga)
-    dev = h_out.device
-    f32 = dict(dtype=torch.float32, device=dev)
-    dh = torch.empty((T, H), dtype=h_out.dtype, device=dev)
-    dy = None if y is None else torch.empty((T, H), dtype=y.dtype, device=dev)
-    dpre = None if pre_weight is None else torch.empty((H,), **f32)
-    dpost = None if post_weight is None else torch.empty((H,), **f32)
-    dgate = None if gate is None else torch.empty(gate.shape, **f32)
+    dh = torch.empty_like(h_out)
+    dy = None if y is None else torch.empty_like(y)
+    dpre = None if pre_weight is None else torch.empty_like(pre_weight)
+    dpost = None if post_weight is None else torch.empty_like(post_weight)
+    dgate = None if gate is None else torch.empty_like(gate)
     lib_ = _lib()
     workspace = None
     if dpre is not None or dpost is not None or dgate is not None:
-        workspace = torch.empty((lib_.block_norm_backward_workspace_bytes(T, H),), dtype=torch.uint8, device=dev)
-    _check(lib_.block_norm_backward(ctypes.byref(cfg), T, H, gh, lddh, gx, lddx, ya, ldy, h_out.data_ptr(), ldh, _addr(dh),
-                                    _addr(dy), _addr(dpre), _addr(dpost), _addr(dgate), _addr(workspace), _stream_of(dev)),
-           "block_norm_backward")
+        workspace = h_out.new_empty((lib_.block_norm_backward_workspace_bytes(T, H),), dtype=torch.uint8)
+    st = lib_.block_norm_backward(ctypes.byref(cfg), T, H, gh, lddh, gx, lddx, ya, ldy, h_out.data_ptr(), ldh, dh.data_ptr(),
+                                  _addr(dy), _addr(dpre), _addr(dpost), _addr(dgate), _addr(workspace),
+                                  _stream_of(h_out.device))
+    if st:
+        raise MXFP8Error(st, "block_norm_backward")
     return BlockNormGrads(dy, dh, dpre, dpost, dgate)
