@@ -11,8 +11,8 @@ from typing import Optional
 
 import torch
 
-from .binding import MXFP8Tensor, _addr, _fmt, lib
-from .mxfp4 import _check, _check_err, _check_offsets, _check_out_dtype, _lib, _on, _stream, _stream_of
+from .binding import MXFP8Error, MXFP8Tensor, _addr, _fmt, lib
+from .mxfp4 import _check_err, _check_offsets, _check_out_dtype, _lib, _on, _stream, _stream_of
 
 FORWARD = 0
 INPUT_GRADIENT = 1
@@ -51,9 +51,11 @@ def _run(product, a, a_scale, a_fmt, b, b_scale, b_fmt, R, N, K, offsets, shape,
     kind = _check_out_dtype(out_dtype)
     dev = a.device
     out = torch.empty(shape, dtype=out_dtype, device=dev)
-    _check(_lib().mxfp8_matmul_grouped(product, _addr(a), _addr(a_scale), a_scale.numel(), a_fmt, _addr(b), _addr(b_scale),
-                                       b_scale.numel(), b_fmt, R, N, K, offsets.numel() - 1, offsets.data_ptr(), _addr(out),
-                                       kind, _addr(err_flag), _stream_of(dev)), "mxfp8_matmul_grouped")
+    st = _lib().mxfp8_matmul_grouped(product, a.data_ptr(), a_scale.data_ptr(), a_scale.numel(), a_fmt, b.data_ptr(),
+                                     b_scale.data_ptr(), b_scale.numel(), b_fmt, R, N, K, offsets.numel() - 1,
+                                     offsets.data_ptr(), out.data_ptr(), kind, _addr(err_flag), _stream_of(dev))
+    if st:
+        raise MXFP8Error(st, "mxfp8_matmul_grouped")
     return out
 
 
