@@ -147,7 +147,8 @@ mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int
  * B_g^T of the expert g whose rows [offsets[g], offsets[g+1]) it is in.  rows, offsets and err_flag as for
  * mxfp4_quantize_grouped (an index outside x: a row of NaN; rows past the last offset: zeros, and *err_flag is set where
  * `rows` does not mark them with a negative index; bad offsets: nothing is written).  b_codes, b_scale as for
- * mxfp4_matmul_grouped.  workspace: mxfp4_linear_grouped_workspace_bytes(total_rows, K, num_groups) bytes.
+ * mxfp4_matmul_grouped.  workspace: mxfp4_linear_grouped_workspace_bytes(total_rows, K, num_groups) bytes (0 for few rows on
+ * many experts: NULL).
  */
 size_t mxfp4_linear_grouped_workspace_bytes(int64_t total_rows, int64_t K, int num_groups);
 

@@ -28,6 +28,7 @@ constexpr int64_t kLongRow = int64_t{1} << 29;  // columns whose scales' offsets
 constexpr int64_t kPairMinTiles = 64;
 constexpr int kFewSms = 152;  // (a constant: the workspace's size, which follows from the kernel, is asked for without a device)
 constexpr int64_t kFewWork = 16;
+constexpr int64_t kFewExpertRows = 16;
 constexpr int64_t kPairMinGroupRows = 128;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -260,17 +261,18 @@ mxfp8_status_t launch_experts(GemmParams &p, const void *q_codes, const void *p_
     return f32 ? launch_group_as<true, PARTS>(pm, qm, p, bound, device, stream) : launch_group_as<false, PARTS>(pm, qm, p, bound, device, stream);
 }
 
-template <int MROWS, int STAGES, bool XF32, bool F32>
+template <int MROWS, int STAGES, bool XF32, bool F32, bool GROUPED>
 mxfp8_status_t launch_few_as(const GemmParams &p, const CUtensorMap &pm, const PartsParams &q, int splits, int device, cudaStream_t stream)
 {
     using Shape = SplitShape<MROWS * kParts, STAGES>;
     static KernelSetup setup;
     int ctas = 0;
-    const mxfp8_status_t st = setup(mxfp4_few_kernel<MROWS, STAGES, XF32, F32>, device, kGemmThreads, Shape::kSmem, &ctas);
+    const mxfp8_status_t st = setup(mxfp4_few_kernel<MROWS, STAGES, XF32, F32, GROUPED>, device, kGemmThreads, Shape::kSmem, &ctas);
     if (st != MXFP8_OK)
         return st;
-    return launch_serialized(mxfp4_few_kernel<MROWS, STAGES, XF32, F32>, dim3(static_cast<unsigned>(p.p_tiles * splits)), kGemmThreads, Shape::kSmem, splits,
-                             stream, pm, p, q.x, q.ldx, q.K, static_cast<int>(q.R), splits);
+    const int64_t tiles = (GROUPED ? q.R : 1) * p.p_tiles;
+    return launch_serialized(mxfp4_few_kernel<MROWS, STAGES, XF32, F32, GROUPED>, dim3(static_cast<unsigned>(tiles * splits)), kGemmThreads, Shape::kSmem,
+                             splits, stream, pm, p, q, splits);
 }
 
 // CTAs that share a tile's K in the kernel for few uncast rows, by the rule of launch_split.
@@ -301,10 +303,30 @@ mxfp8_status_t launch_few(const GemmParams &p, const PartsParams &q, const void 
         return st;
     const int splits = few_splits(p.p_tiles, p.k_iters, kFewSms);
     if (q.R <= 2)
-        return launch_few_as<2, 5, XF32, F32>(p, pm, q, splits, device, stream);
+        return launch_few_as<2, 5, XF32, F32, false>(p, pm, q, splits, device, stream);
     if (q.R <= 4)
-        return launch_few_as<4, 4, XF32, F32>(p, pm, q, splits, device, stream);
-    return launch_few_as<8, 4, XF32, F32>(p, pm, q, splits, device, stream);
+        return launch_few_as<4, 4, XF32, F32, false>(p, pm, q, splits, device, stream);
+    return launch_few_as<8, 4, XF32, F32, false>(p, pm, q, splits, device, stream);
+}
+
+// Few rows on at least twice as many experts, few of which are then shared: a row's tiles read its expert's weights on their own.
+// Measured (us, GPU time of a call here / by the parts' kernel and mxfp4_group_kernel), rows x K x N on 64 experts, no expert
+// shared: 1x7168x2048 5.4 / 13.6, 4x2048x1032 5.1 / 7.9, 8x7168x2048 12.8 / 16.6, 16x7168x2048 22.1 / 26.7, 16x2048x7168 26.1 / 25.6;
+// 16 rows of eight experts 14.5 / 18.1 and 19.5 / 16.1; all 16 of one expert 13.4 / 15.2 and 17.5 / 8.9 at worst (a Python call takes
+// 22 for two launches and a workspace, 13 for one).  More rows gain nothing, and lose where they share.
+bool few_expert_rows(int64_t rows, int num_groups)
+{
+    return rows <= kFewExpertRows && 2 * rows <= num_groups;
+}
+
+template <bool XF32, bool F32>
+mxfp8_status_t launch_few_experts(const GemmParams &p, const PartsParams &q, const void *p_codes, int device, cudaStream_t stream)
+{
+    CUtensorMap pm;
+    mxfp8_status_t st;
+    if ((st = code_map(&pm, p_codes, p.num_groups * p.P, q.pitch, kGemmRows)) != MXFP8_OK)
+        return st;
+    return launch_few_as<2, 5, XF32, F32, true>(p, pm, q, few_splits(q.R * p.p_tiles, p.k_iters, kFewSms), device, stream);
 }
 
 template <bool GROUPED>
@@ -648,7 +670,7 @@ mxfp8_status_t mxfp4_linear(const void *x, int x_type, int64_t M, int64_t K, int
 
 size_t mxfp4_linear_grouped_workspace_bytes(int64_t total_rows, int64_t K, int num_groups)
 {
-    if (total_rows <= 0 || K <= 0 || num_groups < 1 || total_rows >= kMaxDim / kParts)
+    if (total_rows <= 0 || K <= 0 || num_groups < 1 || total_rows >= kMaxDim / kParts || few_expert_rows(total_rows, num_groups))
         return 0;
     return static_cast<size_t>(total_rows) * kParts * mxfp4_row_bytes(K) + mxfp4_grouped_scale_bytes(total_rows * kParts, K, num_groups);
 }
@@ -665,10 +687,12 @@ mxfp8_status_t mxfp4_linear_grouped(const void *x, int x_type, int64_t T, int64_
         return MXFP8_ERR_SHAPE;
     if (num_groups < 1 || num_groups > MXFP8_MAX_GROUPS || offsets == nullptr)
         return MXFP8_ERR_GROUPS;
-    if (total_rows > 0 && N > 0 && K > 0 && workspace == nullptr)
+    const bool few = few_expert_rows(total_rows, num_groups);
+    if (total_rows > 0 && N > 0 && K > 0 && workspace == nullptr && !few)
         return MXFP8_ERR_WORKSPACE;
     GemmParams p;
-    if ((st = gemm_params(&p, q.out, q.scale, total_rows * kParts, b_codes, b_scale, N, K, out, out_type, N)) != MXFP8_OK)
+    // (few rows have no operand in memory: the weights stand for it in the checks)
+    if ((st = gemm_params(&p, few ? b_codes : q.out, few ? b_codes : q.scale, total_rows * kParts, b_codes, b_scale, N, K, out, out_type, N)) != MXFP8_OK)
         return st;
     const int64_t bound = (total_rows * kParts / 128 + num_groups) * static_cast<int64_t>(p.p_tiles);
     if (bound >= kMaxDim - (int64_t{1} << 20) || num_groups * N >= kMaxDim)
@@ -693,6 +717,12 @@ mxfp8_status_t mxfp4_linear_grouped(const void *x, int x_type, int64_t T, int64_
     q.offsets = p.offsets = offsets;
     q.num_groups = p.num_groups = num_groups;
     q.err_flag = err_flag;  // the products have nothing to add to what the parts' kernel reports
+    if (few) {
+        p.err_flag = err_flag;
+        if (x_type == MXFP4_F32)
+            return out_type == MXFP4_F32 ? launch_few_experts<true, true>(p, q, b_codes, device, stream) : launch_few_experts<true, false>(p, q, b_codes, device, stream);
+        return out_type == MXFP4_F32 ? launch_few_experts<false, true>(p, q, b_codes, device, stream) : launch_few_experts<false, false>(p, q, b_codes, device, stream);
+    }
     if ((st = launch_parts<true>(q, x_type, total_rows * q.chunks, device, stream)) != MXFP8_OK)
         return st;
     return launch_experts<kParts>(p, q.out, b_codes, K, out_type, device, stream);

@@ -6,6 +6,9 @@
 // its share of K; against a kernel of its own that writes the parts, a launch, its gap and the workspace fall away.
 // 1x8192x28672 in 20.9 us (6.0 TB/s), 1x4096x4096 in 5.1.  Bound by the weights' bytes, or the start and end of the CTAs; more rows
 // by the splitting, whose four warps issue too little (few_rows() in mxfp4.cu has the limit).
+//
+// Experts: a tile is 128 columns of one row, whose expert the CTA finds in the offsets, which it checks itself.  Rows that share an
+// expert read its weights again, through L2 (few_expert_rows() has the limit).
 #pragma once
 
 #include "mxfp4_parts.cuh"
@@ -16,16 +19,17 @@ namespace mxfp8 {
 constexpr int kFewRows = 8;
 
 // MROWS: rows of x that the stages hold (2, 4 or 8).
-template <int MROWS, int STAGES, bool XF32, bool F32>
+template <int MROWS, int STAGES, bool XF32, bool F32, bool GROUPED>
 __global__ void __launch_bounds__(kGemmThreads, 2)
-    mxfp4_few_kernel(const __grid_constant__ CUtensorMap p_map, const GemmParams p, const void *x, int64_t ldx, int64_t K, int rows, int splits)
+    mxfp4_few_kernel(const __grid_constant__ CUtensorMap p_map, const GemmParams p, const PartsParams x, int splits)
 {
     using S = SplitShape<MROWS * kParts, STAGES>;
     extern __shared__ unsigned char gemm_smem[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full, drain;
     __shared__ uint32_t tmem_slot;
+    __shared__ int expert;
 
-    const int pairs = (rows + 1) / 2;
+    const int rows = GROUPED ? 1 : static_cast<int>(x.R), pairs = (rows + 1) / 2;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const uint32_t base = (smem_u32(gemm_smem) + 1023u) & ~1023u;
@@ -38,6 +42,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
         }
         mbar_init(smem_u32(&acc_full), 1);
         mbar_init(smem_u32(&drain), 1);
+        expert = -1;
         fence_mbar_init();
     }
     if (warp == 2)
@@ -48,10 +53,39 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
     const uint32_t tmem = tmem_slot;
     pdl_wait_and_release();
 
-    const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
+    const int rank = static_cast<int>(blockIdx.x) % splits;
+    int tile = static_cast<int>(blockIdx.x) / splits, p_row = 0;
+    int64_t from = 0, to = 0;  // x's first row, the output's
+    bool live = true, idle = false;  // live: `from` is a row of x; idle: nothing to add up (a cluster's CTAs agree)
+    const uint8_t *ps = p.p_scale;
+    if constexpr (GROUPED) {
+        to = tile / p.p_tiles;
+        tile -= static_cast<int>(to) * p.p_tiles;
+        int bad = tid == 0 && p.offsets[0] != 0;
+        for (int g = tid; g < p.num_groups; g += kGemmThreads) {
+            const int64_t a = p.offsets[g], b = p.offsets[g + 1];
+            bad |= a < 0 || b < a || b > x.R;
+            if (a <= to && to < b)
+                expert = g;  // (of bad offsets perhaps one of several: it is not used)
+        }
+        bad = __syncthreads_or(bad);
+        from = x.rows != nullptr ? x.rows[to] : to;
+        idle = bad || expert < 0;
+        // a row of no expert is one that a plan marks as such, or lost
+        live = from >= 0 && from < x.T;
+        if (blockIdx.x % (p.p_tiles * splits) == 0 && tid == 0 && p.err_flag != nullptr && (bad || (expert < 0 ? x.rows == nullptr || from >= 0 : !live)))
+            atomicOr(p.err_flag, 1);
+        if (!bad && expert < 0 && rank == 0 && tid < kGemmRows && tile * int64_t{kGemmRows} + tid < p.P)
+            store_out<F32>(p.out, to * p.ldo + tile * int64_t{kGemmRows} + tid, 0u);
+        if (!idle) {
+            p_row = static_cast<int>(expert * p.P);
+            ps += static_cast<int64_t>(expert) * p.p_planes * p.kc * 512;
+        }
+    }
     const int64_t p0 = static_cast<int64_t>(tile) * kGemmRows;
+    ps += static_cast<int64_t>(tile) * p.kc * 512;
     const int k0 = static_cast<int>(static_cast<int64_t>(p.k_iters) * rank / splits);
-    const int k1 = static_cast<int>(static_cast<int64_t>(p.k_iters) * (rank + 1) / splits);
+    const int k1 = idle ? k0 : static_cast<int>(static_cast<int64_t>(p.k_iters) * (rank + 1) / splits);
     const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
     int slot = 0;
     uint32_t phase = 0;
@@ -65,7 +99,6 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
 
     if (warp == 0 || warp == 3) {
         // ---- producers of the weights: codes (warp 0), scales (warp 3) ----
-        const uint8_t *ps = p.p_scale + static_cast<int64_t>(tile) * p.kc * 512;
         int issued = 0;
         for (int k = k0; k < k1; ++k) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_cycles(empty0 + 8 * slot, phase ^ 1, kGemmWait));
@@ -75,7 +108,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
             if (elect_one()) {
                 if (warp == 0) {
                     mbar_arrive_expect_tx(bar, S::kPBytes);
-                    tma_load_2d_shared(dp, &p_map, bar, k * 128, static_cast<int>(p0));
+                    tma_load_2d_shared(dp, &p_map, bar, k * 128, p_row + static_cast<int>(p0));
                 } else {
                     const uint32_t sb = 512u * min(2, p.kc - 2 * k);
                     mbar_arrive_expect_tx(bar, sb);
@@ -147,8 +180,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 next[i] = Piece{};
-                if (m0 + i < rows && t < tasks && c < K) {  // K is a multiple of 8
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(x) + ((m0 + i) * ldx + c) * (XF32 ? 4 : 2));
+                if (m0 + i < rows && t < tasks && c < x.K && live) {  // K is a multiple of 8
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(x.x) + ((from + m0 + i) * x.ldx + c) * (XF32 ? 4 : 2));
                     next[i].lo = src[0];
                     if constexpr (XF32)
                         next[i].hi = src[1];
@@ -183,7 +216,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
                     }
                 }
                 if (m0 + i < rows)
-                    split_parts(v, true, [&](int j, uint32_t q, uint32_t scales) {
+                    split_parts(v, live, [&](int j, uint32_t q, uint32_t scales) {
                         *reinterpret_cast<uint32_t *>(codes + i * 1024 + j * 128 + (((lane >> 2) ^ j) << 4)) = q;
                         if ((lane & 15) == 0)
                             *reinterpret_cast<uint32_t *>(scale + (8 * i + j) * 16) = scales;
@@ -195,15 +228,16 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
                 mbar_arrive(full0 + 8 * s);
         }
         // ---- this CTA's sums: to the output, or to shared memory for the cluster (every stage has been consumed) ----
-        ok = epilogue_all(ok && mbar_wait_cycles(smem_u32(&acc_full), 0, kGemmWait));
-        if (ok) {
+        if (!idle)
+            ok = epilogue_all(ok && mbar_wait_cycles(smem_u32(&acc_full), 0, kGemmWait));
+        if (ok && !idle) {
             tc_fence_after();
             const int valid = rows * kParts;
             for (int q = 0; q < valid; q += 32) {
                 uint32_t v[32];
                 tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + q, v);
                 if (splits == 1) {
-                    store_parts<F32, kParts>(p, v, quarter, lane, q, valid - q, p0);
+                    store_parts<F32, kParts>(p, v, quarter, lane, to * kParts + q, valid - q, p0);
                 } else {
                     float *part = reinterpret_cast<float *>(smem) + q / kParts * kGemmRows + quarter * 32 + lane;
 #pragma unroll
@@ -225,7 +259,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
     __syncthreads();
     if (warp == 2)
         tmem_dealloc(tmem, S::kColumns);
-    if (splits > 1) {
+    if (splits > 1 && !idle) {
         cluster_sync();
         for (int i = rank * kGemmThreads + tid; i < rows * (kGemmRows / 4); i += splits * kGemmThreads) {
             const int row = i / (kGemmRows / 4), col = i % (kGemmRows / 4) * 4;
@@ -239,7 +273,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (p0 + col + j < p.P)
-                    store_out<F32>(p.out, int64_t{row} * p.ldo + p0 + col + j, __float_as_uint(s[j]));
+                    store_out<F32>(p.out, (to + row) * p.ldo + p0 + col + j, __float_as_uint(s[j]));
         }
         cluster_sync();  // the peers have read this CTA's sums
     }

@@ -454,9 +454,10 @@ def linear_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, w: MXFP4Matrix,
         raise ValueError(f"x has {K} columns, w has {w.cols}")
     R, dev, lib_ = T if rows is None else rows.numel(), x.device, _lib()
     out = torch.empty((R, w.rows), dtype=out_dtype, device=dev)
-    workspace = torch.empty((lib_.mxfp4_linear_grouped_workspace_bytes(R, K, groups),), dtype=torch.uint8, device=dev)
+    nbytes = lib_.mxfp4_linear_grouped_workspace_bytes(R, K, groups)
+    workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
     st = lib_.mxfp4_linear_grouped(x.data_ptr(), kind, T, K, ld, _addr(rows), R, groups, offsets.data_ptr(), wc, wsc, w.rows,
-                                   out.data_ptr(), out_kind, _addr(err_flag), workspace.data_ptr(), _stream_of(dev))
+                                   out.data_ptr(), out_kind, _addr(err_flag), _addr(workspace), _stream_of(dev))
     if st:
         raise MXFP8Error(st, "mxfp4_linear_grouped")
     return out

@@ -108,6 +108,15 @@ def test_linear_grouped_statuses(cuda_lib):
     assert g(off=A + 4) == ALIGN and g(rows=A + 2) == ALIGN and g(err=A + 1) == ALIGN
 
 
+def test_few_rows_on_many_experts_need_no_workspace(cuda_lib):
+    g = linear_grouped
+    assert mx.mxfp4_linear_grouped_workspace_bytes(16, 40, 32) == 0 and mx.mxfp4_linear_grouped_workspace_bytes(16, 40, 31) > 0
+    assert mx.mxfp4_linear_grouped_workspace_bytes(17, 40, 512) > 0
+    assert g(R=4, G=8, ws=None) == DEVICE and g(R=5, G=8, ws=None) == WORKSPACE
+    assert g(R=4, G=8, ws=None, T=0, x=None) == DEVICE  # no tokens: rows of no expert, or of NaN
+    assert g(R=4, G=8, ws=None, x=None) == NULL and g(R=4, G=8, ws=None, b=None) == NULL
+
+
 def test_linear_workspaces(cuda_lib):
     assert mx.mxfp4_linear_workspace_bytes(9, 40, 40) == 72 * 32 + mx.mxfp4_scale_bytes(72, 40)
     assert mx.mxfp4_linear_grouped_workspace_bytes(3, 40, 2) == 24 * 32 + mx.mxfp4_grouped_scale_bytes(24, 40, 2)

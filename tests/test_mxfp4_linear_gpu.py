@@ -195,3 +195,117 @@ def test_experts_dropped_choices_and_bad_indices():
         assert mx.mxfp4_linear_grouped(x.cuda(), 0, 10, K, K, rows.cuda(), R, G, torch.tensor(bad).cuda(), w.codes, w.scales, N, out, 1,
                                        err, ws) == 0
         assert int(err) == 1 and bool((out == 9).all()), bad
+
+
+# Few rows on many experts, each in a tile of its own: row counts per expert, the rest of 40 experts without any.
+WEIGHTS = {}
+
+
+def few_experts(G, N, K):
+    """4-bit weights of G experts, and a function that gives the values of one."""
+    if (G, N, K) not in WEIGHTS:
+        w = torch.randn(G, N, K, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(BF16)
+        parts = [mx.quantize_mxfp4(v).row for v in w]
+        WEIGHTS[G, N, K] = (mx.MXFP4Matrix(torch.stack([p.codes for p in parts]), torch.stack([p.scales for p in parts]), N, K), w, {})
+    m, w, known = WEIGHTS[G, N, K]
+
+    def values(g):
+        if g not in known:
+            known[g] = ref.cast(w[g].cpu())
+        return known[g]
+    return m, values
+
+
+FEW = [{0: 1}, {39: 2}, {3: 1, 4: 1, 20: 1, 39: 1}, {7: 16}, {0: 5, 1: 1, 38: 3}, {e: 1 for e in range(1, 33, 2)}]
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("N,K", [(1, 8), (40, 72), (264, 520), (129, 4104), (1032, 2048), (2568, 264)])
+@pytest.mark.parametrize("few", FEW)
+def test_few_rows_on_many_experts(few, N, K, dtype, out_dtype):
+    sizes = [few.get(e, 0) for e in range(40)]
+    assert mx.mxfp4_linear_grouped_workspace_bytes(sum(sizes), K, 40) == 0
+    R, T = sum(sizes), 3
+    x, off = draw(T, K, dtype, 1), torch.tensor([0] + sizes).cumsum(0)
+    rows = torch.randint(0, T, (R,), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    w, values = few_experts(40, N, K)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mx.linear_mxfp4_grouped(x.cuda(), off.cuda(), w, rows=rows.cuda(), out_dtype=out_dtype, err_flag=err)
+    wide = torch.full((R, K + 24), float("nan"), dtype=dtype)
+    wide[:, :K] = x[rows.long()]
+    ordered = mx.linear_mxfp4_grouped(wide.cuda()[:, :K], off.cuda(), w, out_dtype=out_dtype, err_flag=err)
+    assert int(err) == 0 and mx.mxfp8_device_fault_word() == 0
+    assert torch.equal(got, ordered)
+    for g in few:
+        s = slice(int(off[g]), int(off[g + 1]))
+        want, tol = bound(x[rows[s].long()], values(g), out_dtype == BF16)
+        assert bool(((got[s].cpu().double() - want).abs() <= tol).all()), g
+
+
+def test_few_rows_dropped_and_bad():
+    G, N, K, R, T = 64, 200, 1096, 12, 5
+    x, (w, values) = draw(T, K, BF16, 4).cuda(), few_experts(G, N, K)
+    sizes = [0] * G
+    sizes[2], sizes[33], sizes[63] = 1, 4, 3
+    off = torch.tensor([0] + sizes).cumsum(0).cuda()
+    rows = torch.tensor([4, 0, 1, 2, 2, 3, 4, 0, -1, -1, -1, -1], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(off, rows, x=x):
+        out = torch.full((R + 2, N), 9.0, device="cuda")  # a guard behind the rows
+        st = mx.mxfp4_linear_grouped(x, 0, x.shape[0], K, K, rows, R, G, off, w.codes, w.scales, N, out, 1, err, None)
+        assert st == 0 and bool((out[R:] == 9).all()) and mx.mxfp8_device_fault_word() == 0
+        return out[:R]
+    good = run(off, rows)
+    assert int(err) == 0 and bool((good[8:] == 0).all())
+    for g, s in ((2, slice(0, 1)), (33, slice(1, 5)), (63, slice(5, 8))):
+        want, tol = bound(x[rows[s].long()].cpu(), values(g), False)
+        assert bool(((good[s].cpu().double() - want).abs() <= tol).all()), g
+    lost = rows.clone()
+    lost[9] = 2  # a row of no expert that is not marked
+    assert torch.equal(run(off, lost), good) and int(err) == 1
+    err.zero_()
+    wrong = rows.clone()
+    wrong[1], wrong[6] = T, -1
+    got = run(off, wrong)
+    keep = torch.ones(R, dtype=torch.bool)
+    keep[[1, 6]] = False
+    assert int(err) == 1 and bool(torch.isnan(got[[1, 6]]).all()) and torch.equal(got[keep], good[keep])
+    for at, value in ((0, 1), (10, -1), (40, 2), (64, R + 1), (64, 1 << 62)):
+        err.zero_()
+        bad = off.clone()
+        bad[at] = value
+        assert bool((run(bad, rows) == 9).all()) and int(err) == 1, (at, value)
+    err.zero_()
+    bad_x = x.clone()
+    bad_x[3, 77], bad_x[1, 5] = float("nan"), float("inf")
+    got = run(off, rows, bad_x)
+    assert bool(torch.isnan(got[[2, 5]]).all()) and int(err) == 0
+    keep = torch.ones(R, dtype=torch.bool)
+    keep[[2, 5]] = False
+    assert torch.equal(got[keep], good[keep])
+    none = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    zero = mx.linear_mxfp4_grouped(x[:0], torch.zeros(G + 1, dtype=torch.int64, device="cuda"), w, rows=none, out_dtype=F32, err_flag=err)
+    assert zero.shape == (R, N) and bool((zero == 0).all()) and int(err) == 0
+
+
+def test_few_rows_repeat_and_follow_a_graph():
+    G, N, K = 32, 520, 2048
+    x, (w, _) = draw(8, K, BF16, 6).cuda(), few_experts(G, N, K)
+    off = torch.zeros(G + 1, dtype=torch.int64, device="cuda")
+    off[5:] = 3
+    off[20:] = 8
+    first = mx.linear_mxfp4_grouped(x, off, w, out_dtype=F32)
+    for _ in range(5):
+        assert torch.equal(mx.linear_mxfp4_grouped(x, off, w, out_dtype=F32), first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mx.linear_mxfp4_grouped(x, off, w, out_dtype=F32)
+    moved = torch.zeros_like(off)
+    moved[9:] = 8
+    want = mx.linear_mxfp4_grouped(x, moved, w, out_dtype=F32)
+    graph.replay()
+    assert torch.equal(out, first)
+    off.copy_(moved)
+    graph.replay()
+    assert torch.equal(out, want) and not torch.equal(out, first)
