@@ -36,6 +36,15 @@ mxfp8_status_t code_map(CUtensorMap *map, const void *codes, int64_t rows, int64
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The same codes without a swizzle, in boxes that are only read before the first row: zeros.
+mxfp8_status_t zeros_map(CUtensorMap *map, const void *codes, int64_t rows, int64_t cols, int box_rows)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 // Experts' codes [groups, rows, cols]: an expert's rows end in zeros, not in the next expert's.
 mxfp8_status_t weight_map(CUtensorMap *map, const void *codes, int64_t groups, int64_t rows, int64_t cols)
 {
@@ -65,7 +74,7 @@ mxfp8_status_t gradient_map(CUtensorMap *map, void *out, int64_t groups, int64_t
 }
 
 struct Maps {
-    CUtensorMap p, q, q_part, p_scale, q_scale, out;
+    CUtensorMap p, q, q_part, p_scale, q_scale, out, zeros, zero_row;
 };
 
 template <int MODE, bool F32>
@@ -79,7 +88,7 @@ mxfp8_status_t launch_pair(const Product8Params &p, const Maps &m, int64_t tiles
         return st;
     const int64_t pairs = tiles < ctas / 2 ? tiles : ctas / 2;
     return launch_serialized(mxfp8_pair_kernel<MODE, F32>, dim3(static_cast<unsigned>(2 * pairs)), kP8Threads<MODE>, smem, 2, stream, m.p, m.q, m.q_part,
-                             m.p_scale, m.q_scale, m.out, p);
+                             m.p_scale, m.q_scale, m.out, m.zeros, m.zero_row, p);
 }
 
 mxfp8_status_t zero(void *out, int64_t bytes, cudaStream_t stream)
@@ -176,6 +185,7 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
     if (wgrad) {
         if ((st = code_map(&m.p, a, total_rows, N, 128)) != MXFP8_OK || (st = code_map(&m.q, b, total_rows, K, 128)) != MXFP8_OK ||
             (st = scale_map(&m.p_scale, a_scale, a_tile_rows, 1, 1)) != MXFP8_OK || (st = scale_map(&m.q_scale, b_scale, b_tile_rows, 1, 1)) != MXFP8_OK ||
+            (st = zeros_map(&m.zeros, a, total_rows, N, kZeroRows)) != MXFP8_OK || (st = zeros_map(&m.zero_row, a, total_rows, N, 1)) != MXFP8_OK ||
             (st = gradient_map(&m.out, out, num_groups, N, K, f32)) != MXFP8_OK)
             return st;
         m.q_part = m.q;
@@ -184,7 +194,7 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
             (st = code_map(&m.q_part, a, total_rows, sum, 32)) != MXFP8_OK || (st = scale_map(&m.p_scale, b_scale, b_tile_rows, kc, 1)) != MXFP8_OK ||
             (st = scale_map(&m.q_scale, a_scale, a_tile_rows, kc, 2)) != MXFP8_OK)
             return st;
-        m.out = m.q;
+        m.out = m.zeros = m.zero_row = m.q;
     }
     switch (product) {
     case MXFP8_FORWARD:

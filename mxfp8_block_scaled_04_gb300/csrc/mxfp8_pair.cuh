@@ -13,8 +13,11 @@
 // columns, whose two accumulators share nothing, were slower throughout (8192x8192x8192 312 -> 356 us): operand loads.
 //
 // A weight gradient's last stage may hold rows of the next expert.  Steps past the expert's last 32 rows are not issued;
-// where the rows are no multiple of 32 each CTA's warp 2 zeroes the rest of the last step in shared memory (its own
-// barrier says that the copy has landed) before the MMA warp sees the stage.
+// where the rows are no multiple of 32 each CTA's warp 2 zeroes the rest of the last step in shared memory before the MMA warp
+// sees the stage: copies from before the codes' first row, which read zeros, once its own barrier says that the codes have
+// landed.  Like the codes they signal the first CTA's barrier, which expects them in the codes' place, so that nothing but
+// copies orders them before the MMAs that the first CTA issues for both.  (Generic stores need a release and an acquire at
+// cluster scope for that: 64 experts of 1024 rows on average, fp32 out, 1130 us against 970.)
 //
 // Measured: 8192x8192x8192 312 us (3.5 PFLOP/s; the bf16 rate measured with cuBLAS twice over is 3.8), 64 experts of 1024 rows on
 // average, 7168 -> 2048: forward 598 us, input gradient 632, weight gradient 944 to fp32 (3.76 GB: 5.7 TB/s were 660 at
@@ -38,6 +41,16 @@ constexpr int kP8Scales = 3 * 512;            // P's tile of this CTA, Q's two t
 constexpr int kP8Epi = (kP8Stages * (kP8Stage + kP8Scales) + 1023) / 1024 * 1024;  // the epilogue's buffers from here on
 constexpr int kP8Smem = kP8Epi + 1024;
 constexpr int kP8Acc1 = 224, kP8ScaleCol = 480;  // TMEM columns, as in mxfp4_pair.cuh
+
+// The boxes of zeros that cover `rows` (1 to 31) rows: of 8 rows, the last one back over rows that are zero already, or of one.
+constexpr int kZeroRows = 8;
+struct ZeroBoxes {
+    int rows, count;  // of a box; boxes
+};
+__device__ __forceinline__ ZeroBoxes zero_boxes(int rows)
+{
+    return rows >= kZeroRows ? ZeroBoxes{kZeroRows, (rows + kZeroRows - 1) / kZeroRows} : ZeroBoxes{1, rows};
+}
 
 // A weight gradient's tile has few stages and many bytes to write: eight epilogue warps, with a buffer of 32 rows x 128
 // bytes each (four warps with two each, 64 experts of 2048 x 7168, bf16 out: two rows each 352 against 527 us, 1024 rows
@@ -152,16 +165,12 @@ __device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d, uint64_t a, uint64_
                  : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
     mxfp8_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap q_part_map, const __grid_constant__ CUtensorMap ps_map,
-                      const __grid_constant__ CUtensorMap qs_map, const __grid_constant__ CUtensorMap out_map, const Product8Params p)
+                      const __grid_constant__ CUtensorMap qs_map, const __grid_constant__ CUtensorMap out_map,
+                      const __grid_constant__ CUtensorMap zeros_map, const __grid_constant__ CUtensorMap zero_row_map, const Product8Params p)
 {
     constexpr bool kTails = MODE == kWeightGrad;
     constexpr bool kPMn = MODE != kForward, kQMn = MODE == kWeightGrad;
@@ -182,8 +191,12 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
         prefetch_tensormap(&ps_map);
         prefetch_tensormap(&qs_map);
         prefetch_tensormap(&out_map);
+        if (kTails) {
+            prefetch_tensormap(&zeros_map);
+            prefetch_tensormap(&zero_row_map);
+        }
         for (int s = 0; s < kP8Stages; ++s) {
-            mbar_init(smem_u32(&full[s]), kTails ? 3 : 1);  // the expectation; a zeroed stage's two CTAs
+            mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
         }
@@ -247,9 +260,12 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
                     const uint32_t dp = base + slot * kP8Stage;
                     if (warp == 0) {
                         if (rank == 0) {
-                            mbar_arrive_expect_tx(full0 + 8 * slot, 2 * (kP8Scales + (zeroed ? 0 : code_bytes)));
-                            if (kTails && !zeroed)
-                                mbar_arrive_many(full0 + 8 * slot, 2);
+                            uint32_t bytes = code_bytes;
+                            if (zeroed) {  // the rows behind the expert's last, of both operands, once the codes have landed
+                                const ZeroBoxes z = zero_boxes(32 - c.tail);
+                                bytes = 2 * z.count * z.rows * 128;
+                            }
+                            mbar_arrive_expect_tx(full0 + 8 * slot, 2 * (kP8Scales + bytes));
                         }
                         if (zeroed)
                             mbar_arrive_expect_tx(landed0 + 8 * slot, code_bytes);
@@ -311,16 +327,14 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
                     break;
                 }
                 phases ^= 1u << s;
-                const int last = (c.steps - 1) % 4 * 32;  // first row of the last step within the stage
-                unsigned char *stage = gemm_smem + (base - smem_u32(gemm_smem)) + s * kP8Stage;
-                for (int i = (last + c.tail) * 8 + lane; i < (last + 32) * 8; i += 32) {  // whole rows: the swizzle stays inside
-                    *reinterpret_cast<uint4 *>(stage + i * 16) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(stage + kP8Codes + i * 16) = make_uint4(0, 0, 0, 0);
+                const int rows = 32 - c.tail, end = (c.steps - 1) % 4 * 32 + 32;  // the last step's, within the stage
+                const ZeroBoxes z = zero_boxes(rows);
+                if ((lane & 15) < z.count) {  // lanes from 0 on: P's boxes, from 16 on: Q's.  Whole rows: the swizzle stays inside
+                    const int at = min(end - rows + (lane & 15) * z.rows, end - z.rows);
+                    const uint32_t dst = base + s * kP8Stage + (lane >> 4) * kP8Codes + at * 128;
+                    tma_load_2d_pair(dst, z.rows == 1 ? &zero_row_map : &zeros_map, lead_full + 8 * s, 0, -z.rows);
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_peer(lead_full + 8 * s);
             }
             slot = (slot + c.k_iters) % kP8Stages;
         }

@@ -160,9 +160,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
             return false;
     }
 }
-// Arrive on a barrier of either CTA.  What these arrivals order is not generic memory (accumulator reads that have
-// completed; zeros already handed to the async proxy), so the default scope does: with .release.cluster an arrival took
-// 1000 to 3000 cycles, and a wait with .acquire.cluster 360 where the phase was already complete.
+// Arrive on a barrier of either CTA.  What these arrivals order is not generic memory but accumulator reads that have
+// completed, so the default scope does: with .release.cluster an arrival took 1000 to 3000 cycles, and a wait with
+// .acquire.cluster 360 where the phase was already complete.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t mapped)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");

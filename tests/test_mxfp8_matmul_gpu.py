@@ -106,3 +106,24 @@ def test_each_position_counts():
 def test_sums_keep_fp32():
     """Norm-wise error of long sums of random signs: far below one rounding to 2^-14 per step."""
     assert Layer([4096, 100], 256, 4096).check(F32) < 2e-6
+
+
+def test_ragged_rows_stay_out_of_their_neighbours():
+    """An expert's last stage holds the next one's rows, 2^20 times as large or as small: exact sums of small integers show one that
+    is added.  Both CTAs of a pair zero such rows; repeats take other interleavings."""
+    g = torch.Generator().manual_seed(9)
+    sizes = [1 + (37 * i) % 131 for i in range(60)]
+    off = torch.tensor([0] + sizes).cumsum(0).tolist()
+    R, N, K = off[-1], 528, 784
+    x, dy = (torch.randint(-4, 5, (R, c), generator=g).double() for c in (K, N))
+    for e in range(1, 60, 2):
+        x[off[e]:off[e + 1]] *= 2.0 ** 20
+    qx, qd = cast(x.to(BF16), off, "e4m3"), cast(dy.to(BF16), off, "e5m2")
+    offsets = torch.tensor(off).cuda()
+    first = mx.matmul_mxfp8_grouped_wgrad(qd, qx, offsets)
+    for e in range(60):
+        s = slice(off[e], off[e + 1])
+        assert torch.equal(first[e].cpu().double(), dy[s].t() @ x[s]), e
+    for _ in range(30):
+        assert torch.equal(mx.matmul_mxfp8_grouped_wgrad(qd, qx, offsets), first)
+    assert mx.mxfp8_device_fault_word() == 0
