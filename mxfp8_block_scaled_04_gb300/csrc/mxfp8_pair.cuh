@@ -414,8 +414,12 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8Acc1;
             const int row = c.p_at + static_cast<int>(rank) * 128 + quarter * 32;
             const int start = buf == 0 ? kP8Tile - kCols : 0;  // the columns that the accumulators share first
-            if (part == 1 && lane == 0)  // its share of the tile before is read, and none of this tile's is in the shared columns
-                mbar_arrive_peer(lead_empty);
+            if (part == 1) {  // its share of the tile before is read, and none of this tile's is in the shared columns
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_peer(lead_empty);
+            }
             for (int i = part; i < kP8Tile / kCols; i += 2) {
                 const int q = (start + kCols * i) & (kP8Tile - 1);
                 const bool live = q < c.valid && row < p.P;

@@ -34,3 +34,11 @@ def test_no_arrival_stands_for_stores(name):
     text = source(name)
     for m in re.finditer(r"mbar_arrive_peer\(", text):
         assert not any("fence_proxy_async" in s for s in statements_before(text, m.start(), 3)), text[m.start() - 200:m.end() + 40]
+
+
+@pytest.mark.parametrize("name", PAIRS)
+def test_arrivals_follow_the_accumulators_reads(name):
+    """Every arrival that frees accumulators comes behind the fence that orders this thread's reads of them."""
+    text = source(name)
+    for m in re.finditer(r"mbar_arrive_peer\(", text):
+        assert "tc_fence_before()" in statements_before(text, m.start(), 3), text[m.start() - 200:m.end() + 40]
