@@ -41,7 +41,7 @@ FALLBACK_HBM_GBS = 6800.0
 # Every source the library is built from, the CUDA sources and the headers with the launch code and the ABI: a
 # committed ncu traffic figure is only reported while these are unchanged since it was taken.
 KERNEL_SOURCES = [f"mxfp8_block_scaled_04_gb300/csrc/{f}"
-                  for f in ("api.cu", "block_norm.cu", "block_norm.cuh", "dact.cuh", "dbias_reduce.cuh", "dgated.cuh", "groups.cuh",
+                  for f in ("api.cu", "block_norm.cu", "block_norm.cuh", "dact.cuh", "dbias_reduce.cuh", "dgated.cuh", "empty_sum.cuh", "groups.cuh",
                             "moe.cu", "moe.cuh", "mxfp4.cu", "mxfp4_cast.cuh", "mxfp4_few.cuh", "mxfp4_gemm.cuh", "mxfp4_pair.cuh", "mxfp4_parts.cuh",
                             "mxfp4_split.cuh", "mxfp8_matmul.cu", "mxfp8_pair.cuh", "ptx.cuh", "quantize.cuh", "tcgen05.cuh")]
 HEADERS = ["include/block_norm.h", "include/moe.h", "include/mxfp8_matmul.h", "include/mxfp4.h", "include/mxfp8.h", "mxfp8_block_scaled_04_gb300/csrc/host.h"]

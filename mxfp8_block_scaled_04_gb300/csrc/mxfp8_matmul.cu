@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "../../include/mxfp8_matmul.h"
+#include "empty_sum.cuh"
 #include "host.h"
 #include "mxfp8_pair.cuh"
 
@@ -91,15 +92,6 @@ mxfp8_status_t launch_pair(const Product8Params &p, const Maps &m, int64_t tiles
                              m.p_scale, m.q_scale, m.out, m.zeros, m.zero_row, p);
 }
 
-mxfp8_status_t zero(void *out, int64_t bytes, cudaStream_t stream)
-{
-    if (cudaMemsetAsync(out, 0, static_cast<size_t>(bytes), stream) != cudaSuccess) {
-        cudaGetLastError();
-        return MXFP8_ERR_LAUNCH;
-    }
-    return MXFP8_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -146,12 +138,18 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
                             static_cast<const void *>(err_flag)})
         if (!pointer_on_device(ptr, device))
             return MXFP8_ERR_DEVICE;
-    if (empty)
-        return MXFP8_OK;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    const int size = out_type == MXFP4_F32 ? 4 : 2;
-    if (sum == 0)
-        return zero(out, out_rows * cols * size, stream);
+    if (empty || sum == 0) {
+        EmptySumParams e{};
+        e.offsets = offsets;
+        e.num_groups = num_groups;
+        e.total = total_rows;
+        e.out = out;
+        e.count = out_rows * cols;
+        e.cols = cols;
+        e.err_flag = err_flag;
+        return launch_empty_sum(e, out_type == MXFP4_F32, stream);
+    }
     Product8Params p{};
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;

@@ -1,0 +1,93 @@
+"""Experts' products whose sum or output is empty keep the contract of the others: bad offsets write nothing and are told, rows of no
+expert become zeros and are told, good offsets give zeros.  All results are exact."""
+import pytest
+import torch
+
+import mxfp8_block_scaled_04_gb300 as mx
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
+GOOD, SHORT = [0, 4, 4, 10], [0, 4, 4, 7]
+BAD = [[0, 7, 5, 10], [1, 4, 4, 10], [0, 4, 4, 11], [0, -1, 4, 10], [0, 4, 4, 1 << 62], [-3, 0, 4, 10]]
+NONE = [0, 0, 0, 0]
+BAD_NONE = [[0, 0, 0, 1], [0, 3, 0, 0], [1, 1, 1, 1], [-1, 0, 0, 0], [0, 0, -2, 0]]
+
+
+def flag():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def outputs(call, shape, dtype):
+    """call(out, err_flag) on a guarded output: (rows, flag); without a flag the rows are the same."""
+    seen = []
+    for err in (flag(), None):
+        n = 1
+        for s in shape:
+            n *= s
+        buffer = torch.full((n + 64,), 9.0, dtype=dtype, device="cuda")
+        assert call(buffer[32:], err) == 0
+        assert bool((buffer[:32] == 9).all()) and bool((buffer[n + 32:] == 9).all())
+        seen.append(buffer[32:n + 32].view(shape))
+        told = int(err) if err is not None else told
+    assert torch.equal(seen[0].nan_to_num(5), seen[1].nan_to_num(5))
+    assert mx.mxfp8_device_fault_word() == 0
+    return seen[0], told
+
+
+# ---- MXFP8 ---------------------------------------------------------------------------------------------
+
+def product8(kind, R, N, K, off, dtype):
+    codes, plane = torch.zeros(4096, dtype=U8, device="cuda"), torch.zeros(4096, dtype=U8, device="cuda")
+    shape = {0: (R, N), 1: (R, K), 2: (len(off) - 1, N, K)}[kind]
+    offsets = torch.tensor(off, device="cuda")
+    return outputs(lambda out, err: mx.mxfp8_matmul_grouped(kind, codes, plane, plane.numel(), 0, codes, plane, plane.numel(), 0, R, N, K, len(off) - 1,
+                                                            offsets, out, 0 if dtype is BF16 else 1, err), shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,N,K", [(0, 48, 0), (1, 0, 48)])
+def test_mxfp8_rows_of_an_empty_sum(kind, N, K, dtype):
+    out, told = product8(kind, 10, N, K, GOOD, dtype)
+    assert bool((out == 0).all()) and told == 0
+    out, told = product8(kind, 10, N, K, SHORT, dtype)
+    assert bool((out == 0).all()) and told == 1
+    for bad in BAD:
+        out, told = product8(kind, 10, N, K, bad, dtype)
+        assert bool((out == 9).all()) and told == 1, bad
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,K", [(16, 16), (48, 1040)])
+def test_mxfp8_weight_gradient_of_no_rows(N, K, dtype):
+    out, told = product8(2, 0, N, K, NONE, dtype)
+    assert bool((out == 0).all()) and told == 0
+    out, told = product8(2, 0, N, K, [0] * 513, dtype)
+    assert bool((out == 0).all()) and told == 0
+    for bad in BAD_NONE + [[0] * 512 + [1], [0] * 300 + [1] + [0] * 212]:
+        out, told = product8(2, 0, N, K, bad, dtype)
+        assert bool((out == 9).all()) and told == 1, bad
+
+
+def test_mxfp8_empty_outputs():
+    for kind, N, K in ((0, 32, 64), (1, 32, 64)):  # no rows
+        assert product8(kind, 0, N, K, NONE, F32)[1] == 0
+        for bad in BAD_NONE:
+            assert product8(kind, 0, N, K, bad, F32)[1] == 1, (kind, bad)
+    for kind, N, K in ((0, 0, 64), (1, 64, 0), (2, 0, 64), (2, 64, 0), (0, 0, 0), (1, 0, 0), (2, 0, 0)):  # no columns
+        assert product8(kind, 10, N, K, GOOD, F32)[1] == 0 and product8(kind, 10, N, K, SHORT, F32)[1] == 1
+        for bad in BAD:
+            assert product8(kind, 10, N, K, bad, F32)[1] == 1, (kind, bad)
+
+
+def test_mxfp8_wrappers_tell_of_bad_offsets():
+    E, N, K = 3, 32, 64
+    empty, plane = (lambda cols: torch.empty(0, cols, dtype=U8, device="cuda")), torch.zeros(512, dtype=U8, device="cuda")
+    x, dy = (mx.MXFP8Tensor(empty(c), plane, empty(c), plane, None) for c in (K, N))
+    w = mx.quantize_grouped(torch.ones(E * N, K, dtype=BF16, device="cuda"), (torch.arange(E + 1) * N).cuda(), swizzled=True)
+    for off, told in ((NONE, 0), ([0, 0, 2, 2], 1)):
+        for call in (lambda o, e: mx.matmul_mxfp8_grouped(x, o, w, err_flag=e), lambda o, e: mx.matmul_mxfp8_grouped_dgrad(dy, o, w, err_flag=e),
+                     lambda o, e: mx.matmul_mxfp8_grouped_wgrad(dy, x, o, err_flag=e)):
+            err = flag()
+            call(torch.tensor(off, device="cuda"), err)
+            assert int(err) == told
