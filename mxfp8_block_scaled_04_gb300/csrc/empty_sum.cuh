@@ -23,6 +23,12 @@ struct EmptySumParams {
     int *err_flag;
 };
 
+// A product's output [total, cols].
+inline EmptySumParams empty_sum(const int64_t *offsets, int num_groups, int64_t total, const int32_t *rows, int64_t T, void *out, int64_t cols, int *err_flag)
+{
+    return {offsets, num_groups, total, rows, T, out, total * cols, cols, err_flag};
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kEmptySumThreads) empty_sum_kernel(const EmptySumParams p)
 {

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "../../include/mxfp4.h"
+#include "empty_sum.cuh"
 #include "host.h"
 #include "mxfp4_cast.cuh"
 #include "mxfp4_few.cuh"
@@ -611,11 +612,9 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
                             static_cast<const void *>(err_flag)})
         if (!pointer_on_device(ptr, device))
             return MXFP8_ERR_DEVICE;
-    if (total_rows == 0 || N == 0)
-        return MXFP8_OK;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    if (K == 0)
-        return zero_rows(out, total_rows, N, N, out_type, stream);
+    if (total_rows == 0 || N == 0 || K == 0)
+        return launch_empty_sum(empty_sum(offsets, num_groups, total_rows, nullptr, 0, out, N, err_flag), out_type == MXFP4_F32, stream);
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     p.offsets = offsets;
@@ -706,11 +705,9 @@ mxfp8_status_t mxfp4_linear_grouped(const void *x, int x_type, int64_t T, int64_
                             static_cast<const void *>(err_flag), static_cast<const void *>(workspace)})
         if (!pointer_on_device(ptr, device))
             return MXFP8_ERR_DEVICE;
-    if (total_rows == 0 || N == 0)
-        return MXFP8_OK;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    if (K == 0)
-        return zero_rows(out, total_rows, N, N, out_type, stream);
+    if (total_rows == 0 || N == 0 || K == 0)
+        return launch_empty_sum(empty_sum(offsets, num_groups, total_rows, rows, T, out, N, err_flag), out_type == MXFP4_F32, stream);
     if ((p.fault = fault_word_address(device)) == nullptr)
         return MXFP8_ERR_DEVICE;
     q.rows = rows;

@@ -91,3 +91,71 @@ def test_mxfp8_wrappers_tell_of_bad_offsets():
             err = flag()
             call(torch.tensor(off, device="cuda"), err)
             assert int(err) == told
+
+
+# ---- MXFP4 ---------------------------------------------------------------------------------------------
+
+def product4(R, N, K, off, dtype):
+    codes, plane = torch.zeros(4096, dtype=U8, device="cuda"), torch.zeros(4096, dtype=U8, device="cuda")
+    offsets = torch.tensor(off, device="cuda")
+    return outputs(lambda out, err: mx.mxfp4_matmul_grouped(codes, plane, R, len(off) - 1, offsets, codes, plane, N, K, out, 0 if dtype is BF16 else 1, err),
+                   (R, N), dtype)
+
+
+def linear4(R, N, K, off, dtype, rows=None, T=10, workspace=True):
+    x = torch.ones(T, max(K, 8), dtype=dtype, device="cuda")
+    codes, plane = torch.zeros(1 << 16, dtype=U8, device="cuda"), torch.zeros(1 << 16, dtype=U8, device="cuda")
+    offsets = torch.tensor(off, device="cuda")
+    rows = None if rows is None else torch.tensor(rows, dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 16, dtype=U8, device="cuda") if workspace else None
+    kind = 0 if dtype is BF16 else 1
+    return outputs(lambda out, err: mx.mxfp4_linear_grouped(x, kind, T, K, max(K, 8), rows, R, len(off) - 1, offsets, codes, plane, N, out, kind, err, ws),
+                   (R, N), dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [1, 40, 513])
+def test_mxfp4_rows_of_an_empty_sum(N, dtype):
+    for call in (product4, linear4):
+        out, told = call(10, N, 0, GOOD, dtype)
+        assert bool((out == 0).all()) and told == 0
+        out, told = call(10, N, 0, SHORT, dtype)
+        assert bool((out == 0).all()) and told == 1
+        for bad in BAD:
+            out, told = call(10, N, 0, bad, dtype)
+            assert bool((out == 9).all()) and told == 1, bad
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("groups", [3, 40])  # few rows on many experts take a kernel of their own
+def test_uncast_rows_of_an_empty_sum_follow_their_indices(groups, dtype):
+    grow = lambda off: off + [off[-1]] * (groups - 3)  # noqa: E731
+    rows = [0, 1, 2, 3, 2, 1, 0, -1, -1, -1]
+    out, told = linear4(10, 40, 0, grow(SHORT), dtype, rows, T=4, workspace=groups == 3)
+    assert bool((out == 0).all()) and told == 0  # a plan marks the rows of no expert
+    rows[8] = 2
+    out, told = linear4(10, 40, 0, grow(SHORT), dtype, rows, T=4, workspace=groups == 3)
+    assert bool((out == 0).all()) and told == 1  # a lost one
+    rows[8], rows[1], rows[5] = -1, 4, -1
+    out, told = linear4(10, 40, 0, grow(SHORT), dtype, rows, T=4, workspace=groups == 3)
+    lost = torch.zeros(10, dtype=torch.bool, device="cuda")
+    lost[[1, 5]] = True  # rows that x does not have
+    assert bool(out[lost].isnan().all()) and bool((out[~lost] == 0).all()) and told == 1
+    for bad in BAD:
+        out, told = linear4(10, 40, 0, grow(bad), dtype, rows, T=4, workspace=groups == 3)
+        assert bool((out == 9).all()) and told == 1, bad
+
+
+def test_mxfp4_empty_outputs():
+    for K in (0, 64):
+        for call in (product4, linear4):
+            assert call(0, 40, K, NONE, F32)[1] == 0
+            for bad in BAD_NONE:
+                assert call(0, 40, K, bad, F32)[1] == 1, bad
+            assert call(10, 0, K, GOOD, F32)[1] == 0 and call(10, 0, K, SHORT, F32)[1] == 1
+            for bad in BAD:
+                assert call(10, 0, K, bad, F32)[1] == 1, bad
+        marked = [0, 1, 2, 3, 2, 1, 0, -1, -1, -1]
+        assert linear4(10, 0, K, SHORT, F32, marked, T=4)[1] == 0
+        assert linear4(10, 0, K, SHORT, F32, marked[:9] + [1], T=4)[1] == 1
+        assert linear4(10, 0, K, SHORT, F32, [7] + marked[1:], T=4)[1] == 1
