@@ -226,14 +226,19 @@ mxfp8_status_t block_norm_backward(const block_norm_config_t *cfg, int64_t T, in
         if (!pointer_on_device(ptr, device))
             return MXFP8_ERR_DEVICE;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    if (H == 0)
-        return MXFP8_OK;
+    auto zero = [&](float *out, int64_t n) {
+        if (out == nullptr || n == 0 || cudaMemsetAsync(out, 0, static_cast<size_t>(n) * sizeof(float), stream) == cudaSuccess)
+            return MXFP8_OK;
+        cudaGetLastError();
+        return MXFP8_ERR_LAUNCH;
+    };
+    const bool per_token = cfg->gate_kind == BLOCK_GATE_TOKEN;
+    if (H == 0)  // sums over no columns
+        return zero(per_token ? dgate : nullptr, T);
     if (T == 0) {  // sums over no rows
-        for (float *out : {dpre, dpost, cfg->gate_kind == BLOCK_GATE_CHANNEL ? dgate : nullptr})
-            if (out != nullptr && cudaMemsetAsync(out, 0, static_cast<size_t>(H) * sizeof(float), stream) != cudaSuccess) {
-                cudaGetLastError();
-                return MXFP8_ERR_LAUNCH;
-            }
+        for (float *out : {dpre, dpost, per_token ? nullptr : dgate})
+            if ((st = zero(out, H)) != MXFP8_OK)
+                return st;
         return MXFP8_OK;
     }
     NormParams p = params(cfg, T, H);

@@ -276,3 +276,15 @@ def test_no_rows():
     z = torch.empty(4, 0, dtype=BF16, device="cuda")
     assert mx.block_norm(z, z, torch.empty(0, device="cuda")).x.shape == (4, 0)
     assert math.prod(mx.block_norm_backward(z, z, z, z, torch.empty(0, device="cuda")).h.shape) == 0
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_a_gate_per_token_of_rows_without_columns(T):
+    """Sums over nothing are zeros."""
+    z, w = torch.empty(T, 0, dtype=BF16, device="cuda"), torch.empty(0, device="cuda")
+    gate = torch.ones(T, 1, device="cuda")
+    torch.full((T, 1), 7.0, device="cuda")  # what the gradient's memory may hold
+    assert bool((mx.block_norm_backward(z, z, z, z, w, w, gate).gate == 0).all())
+    cfg, out = mx.BlockNormConfig(0, 0, 2, 1.0, EPS, None, None, gate.data_ptr()), torch.full((T + 2,), 9.0, device="cuda")
+    assert mx.block_norm_backward_c(cfg, T, 0, None, 0, None, 0, None, 0, None, 0, None, None, None, None, out[1:T + 1], None) == 0
+    assert bool((out[1:T + 1] == 0).all()) and bool((out[[0, -1]] == 9).all())
