@@ -288,3 +288,44 @@ def test_a_gate_per_token_of_rows_without_columns(T):
     cfg, out = mx.BlockNormConfig(0, 0, 2, 1.0, EPS, None, None, gate.data_ptr()), torch.full((T + 2,), 9.0, device="cuda")
     assert mx.block_norm_backward_c(cfg, T, 0, None, 0, None, 0, None, 0, None, 0, None, None, None, None, out[1:T + 1], None) == 0
     assert bool((out[1:T + 1] == 0).all()) and bool((out[[0, -1]] == 9).all())
+
+
+# Layouts of the gradients that the options meet: two vectors per thread with the weights kept in shared memory, a row shared by
+# two CTAs with an odd split and with whole ones.
+@pytest.mark.parametrize("yt,ht", TYPES)
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("kind", ["none", "channel", "token"])
+@pytest.mark.parametrize("T,H", [(61, 4800), (331, 5000), (37, 8200), (170, 8208), (9, 16384)])
+def test_backward_options_of_long_rows(T, H, kind, post, yt, ht):
+    for gh, gx in ((True, True), (True, False), (False, True)):
+        check_backward(T, H, yt, ht, post, kind, 0.25, gh, gx)
+    assert mx.mxfp8_device_fault_word() == 0
+
+
+@pytest.mark.parametrize("yt,ht", TYPES)
+@pytest.mark.parametrize("T,H", [(61, 4800), (170, 8208), (9, 16384)])
+def test_forward_options_of_long_rows(T, H, yt, ht):
+    for post in (True, False):
+        for kind in ("none", "channel", "token"):
+            check_forward(T, H, yt, ht, post, kind, -0.5)
+    assert mx.mxfp8_device_fault_word() == 0
+
+
+@pytest.mark.parametrize("T,H", [(40, 520), (200, 4800), (170, 8208)])
+def test_outputs_of_long_rows_alone(T, H):
+    """Each output wanted alone is what it is among the others, without the inputs that it does not need."""
+    y, h, dh, dx = draw(T, H, BF16, 1), draw(T, H, F32, 2), draw(T, H, F32, 3), draw(T, H, BF16, 4)
+    w1, w2 = vec(H, 5), vec(H, 6)
+    names = ("dh", "dy", "dpre", "dpost", "dgate")
+    ws = torch.empty(mx.block_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+    for kind, number in (("channel", 1), ("token", 2), ("none", 0)):
+        for post in (w1, None):
+            gate = gate_of(kind, T, H)
+            cfg = mx.BlockNormConfig(0, 1, number, 0.5, EPS, w2.data_ptr(), None if post is None else post.data_ptr(), None if gate is None else gate.data_ptr())
+            whole = dict(zip(names, (lambda g: (g.h, g.y, g.pre_weight, g.post_weight, g.gate))(mx.block_norm_backward(dh, dx, y, h, w2, post, gate, 0.5))))
+            for alone in (n for n in names if whole[n] is not None):
+                out = {n: torch.full_like(whole[n], 9.0) if n == alone else None for n in names}
+                needs_y = alone == "dgate" or (post is not None and alone in ("dy", "dpost"))
+                assert mx.block_norm_backward_c(cfg, T, H, dh, H, dx, H, y if needs_y else None, H, h, H, *(out[n] for n in names), ws) == 0
+                assert torch.equal(out[alone], whole[alone]), (kind, alone)
+    assert mx.mxfp8_device_fault_word() == 0

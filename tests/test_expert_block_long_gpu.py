@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import mxfp8_ref as ref
+import test_block_norm_gpu as norms
 import mxfp8_block_scaled_04_gb300 as mx
 from mxfp8_block_scaled_04_gb300 import norm
 
@@ -201,3 +202,33 @@ def test_stream_in_place(T, H, dtype):
     x = torch.empty(T, H, dtype=BF16, device="cuda")
     assert norm.block_norm_c(cfg, T, H, y, H, h, H, h, x) == 0
     assert ctypes.sizeof(cfg) > 0 and torch.equal(h, want.h) and torch.equal(x, want.x)
+
+
+@pytest.mark.parametrize("T,H,kind", [(270000, 8192, "token"), (132000, 16384, "token"), (132000, 16384, "channel")])
+def test_norm_gradients_past_2_to_31_elements(T, H, kind):
+    """Those of y, of the gate and of the weight behind the block, by the formulas and bounds of the norms' own tests."""
+    y, h, dh, dx = (randn(T, H, seed=s) for s in range(4))
+    w1, w2 = 1 + 0.3 * randn(H, seed=5).float(), 1 + 0.3 * randn(H, seed=6).float()
+    gate = 0.4 + 0.1 * (randn(T, 1, seed=7) if kind == "token" else randn(H, seed=7)).float()
+    g = mx.block_norm_backward(dh, dx, y, h, w2, w1, gate, 0.7)
+    assert mx.mxfp8_device_fault_word() == 0
+    rows = torch.tensor(some(T)).cuda()
+    part = gate[rows] if kind == "token" else gate
+    want, mags = norms.formulas(dh[rows], dx[rows], y[rows], h[rows], w2, w1, part, 0.7, 1e-6)
+    for name, got in (("y", g.y), ("h", g.h)):
+        tol = 2.0 ** -17 * mags[name]
+        norms.inside(got[rows], want[name], tol + 2.0 ** -8 * (want[name].abs() + tol), name)
+    if kind == "token":
+        norms.inside(g.gate.view(-1)[rows], want["gate"], 128 * 2.0 ** -23 * mags["gate"], "gate")
+    sums = {n: [torch.zeros(H, dtype=torch.float64, device="cuda") for _ in range(2)] for n in ("pre", "post", "gate")}
+    for a in range(0, T, 4096):
+        s = slice(a, a + 4096)
+        want, mags = norms.formulas(dh[s], dx[s], y[s], h[s], w2, w1, gate[s] if kind == "token" else gate, 0.7, 1e-6)
+        for n, (total, most) in sums.items():
+            if n != "gate" or kind == "channel":
+                total += want[n]
+                most += mags[n]
+    path = T / 76 + 38 + 8 + 64  # additions of a sum over tokens, and its terms' own roundings
+    for n, got in (("pre", g.pre_weight), ("post", g.post_weight), ("gate", g.gate)):
+        if n != "gate" or kind == "channel":
+            norms.inside(got, sums[n][0], (path + 64) * 2.0 ** -23 * sums[n][1], n)
