@@ -113,10 +113,9 @@ mxfp8_status_t launch_types(NormParams p, int element_bytes, int device, cudaStr
     };
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
-    if (shared && v == 2)
-        return keep ? run(Two{}, std::true_type{}, Two{}) : run(Two{}, std::false_type{}, Two{});
+    static_assert(kNormShare / 2 >= 8 * kNormThreads, "half of a shared row is two vectors per thread");
     if (shared)
-        return run(One{}, std::false_type{}, Two{});
+        return keep ? run(Two{}, std::true_type{}, Two{}) : run(Two{}, std::false_type{}, Two{});
     if (v == 1)
         return run(One{}, std::false_type{}, One{});
     return keep ? run(Two{}, std::true_type{}, One{}) : run(Two{}, std::false_type{}, One{});
