@@ -125,8 +125,11 @@ mxfp8_status_t mxfp4_matmul_grouped(const void *a_codes, const void *a_scale, in
 /*
  * Products of rows that are not cast with 4-bit weights (serving: weights in 4 bits, tokens as they are):
  * out [M, N] = x [M, K] * B [N, K]^T, sums in fp32, rounded once to out_type.  x enters as a sum of eight 4-bit rows per row,
- * which differs from x, per block of 32, by at most 2^-22 of the block's largest magnitude (or 2^-126), so that the
- * result is that of the unquantized rows to fp32 accuracy.  A NaN or an infinity in a row of x makes that output row NaN.
+ * 24-bit fixed point under each block's scale: an element differs from x by at most 2^-22 of the largest magnitude in its block of
+ * 32 (or 2^-126).  Where a block's magnitudes are alike that is fp32 accuracy; an element 2^-15 of its block's largest keeps about
+ * 8 bits, one below 2^-23 hardly any.  What the parts add up to on the way is at most 7/3 of sum |x| |B|: where that passes fp32's range
+ * the result may be an infinity or NaN though x and the result do not.  A NaN or an infinity in a row of x makes that output row
+ * NaN.
  *
  *   x            device, x_type, 16-byte aligned; K and ldx multiples of 8, ldx >= K; M < 2^28.
  *   b_codes, b_scale, out, out_type, ldo   as for mxfp4_matmul.  (A block of B with scale 255 makes its output column NaN.)

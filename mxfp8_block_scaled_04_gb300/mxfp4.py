@@ -405,8 +405,12 @@ def matmul_mxfp4_grouped(a: MXFP4Matrix, offsets: torch.Tensor, b: MXFP4Matrix, 
 def linear_mxfp4(x: torch.Tensor, w: MXFP4Matrix, out_dtype: torch.dtype = torch.bfloat16,
                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """x [M, K] (CUDA bf16 or fp32, not cast; K a multiple of 8, rows contiguous) times 4-bit weights w [N, K] transposed:
-    [M, N] in ``out_dtype``, or into ``out`` (rows contiguous).  To fp32 accuracy the product of the unquantized rows; for
-    few rows, as a serving step has (for many, cast them and use ``matmul_mxfp4``)."""
+    [M, N] in ``out_dtype``, or into ``out`` (rows contiguous).  For few rows, as a serving step has (for many, cast them and use
+    ``matmul_mxfp4``).
+
+    x enters as 24-bit fixed point under the scale of each block of 32 columns: an element is off by at most 2^-22 of its block's
+    largest magnitude, which is fp32 accuracy where a block's magnitudes are alike and less for elements far below an outlier.
+    A NaN or an infinity in a row of x makes that output row NaN, and results may overflow from 3/7 of fp32's range on."""
     if stream is not None:
         with _on(stream):
             return linear_mxfp4(x, w, out_dtype, out)

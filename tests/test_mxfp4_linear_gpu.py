@@ -309,3 +309,28 @@ def test_few_rows_repeat_and_follow_a_graph():
     off.copy_(moved)
     graph.replay()
     assert torch.equal(out, want) and not torch.equal(out, first)
+
+
+def test_the_largest_values():
+    """What the parts add up to on the way is at most 7/3 of sum |x| |w|: below the end of fp32's range results are as accurate as
+    anywhere, in one element and in sums that end far below their terms."""
+    v = torch.arange(0x7E00, 0x7F80, dtype=torch.int32).to(torch.int16).view(BF16)  # from 2^125 on
+    v = torch.cat((v, -v))
+    x = torch.zeros(v.numel(), 64, dtype=BF16)
+    x[:, 5] = v
+    x[:, 6] = v / 2
+    x[:, 40] = -v
+    weight = torch.zeros(40, 64, dtype=BF16)
+    weight[0, 5], weight[1, 6] = 1.0, 1.0
+    weight[2, 5] = weight[2, 40] = 0.5  # the halves cancel
+    weight[3, 5] = 0.25
+    weight[39] = 0.0078125
+    w, wv = mx.quantize_mxfp4(weight.cuda()).row, ref.cast(weight)
+    for M in (2, 20, v.numel()):  # in the product's own kernel, by parts of a kernel before it, in pairs of CTAs
+        for dtype in (BF16, F32):
+            got = mx.linear_mxfp4(x[-M:].to(dtype).cuda(), w, F32).cpu().double()
+            want, tol = bound(x[-M:], wv, False)
+            inside = 7 / 3 * (x[-M:].double().abs() @ wv.double().abs().t()) < 2.0 ** 128
+            assert bool(inside[:, [3, 39]].all()) and (M < v.numel() or bool(inside.any(0).all()))
+            assert bool(((got - want).abs() <= tol)[inside].all()), (M, dtype)
+    assert mx.mxfp8_device_fault_word() == 0
