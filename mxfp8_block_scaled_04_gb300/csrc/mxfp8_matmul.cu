@@ -55,10 +55,11 @@ mxfp8_status_t weight_map(CUtensorMap *map, const void *codes, int64_t groups, i
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// A scale plane as tile_rows rows of kc tiles of 512 bytes, in boxes of one tile x box_rows tile rows.
+// A scale plane as tile_rows rows of kc tiles of 512 bytes, in boxes of one tile x box_rows tile rows.  (A map has a row at least;
+// of a plane without one the kernel reads none.)
 mxfp8_status_t scale_map(CUtensorMap *map, const void *scale, int64_t tile_rows, int64_t kc, int box_rows)
 {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kc) * 128, static_cast<cuuint64_t>(tile_rows)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kc) * 128, static_cast<cuuint64_t>(tile_rows < 1 ? 1 : tile_rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kc) * 512};
     const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, scale, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
@@ -174,8 +175,6 @@ mxfp8_status_t mxfp8_matmul_grouped(int product, const void *a, const void *a_sc
     p.formats = (static_cast<uint32_t>(p_fmt) << 7) | (static_cast<uint32_t>(q_fmt) << 10);
     const int64_t unit = wgrad ? 512 : kc * 512;
     const int64_t a_tile_rows = static_cast<int64_t>(a_scale_bytes) / unit, b_tile_rows = static_cast<int64_t>(b_scale_bytes) / unit;
-    if (a_tile_rows < 1 || b_tile_rows < 1)
-        return MXFP8_ERR_WORKSPACE;
     p.p_tile_rows = wgrad ? a_tile_rows : b_tile_rows;
     p.q_tile_rows = wgrad ? b_tile_rows : a_tile_rows;
     const bool f32 = out_type == MXFP4_F32;

@@ -159,3 +159,21 @@ def test_mxfp4_empty_outputs():
         assert linear4(10, 0, K, SHORT, F32, marked, T=4)[1] == 0
         assert linear4(10, 0, K, SHORT, F32, marked[:9] + [1], T=4)[1] == 1
         assert linear4(10, 0, K, SHORT, F32, [7] + marked[1:], T=4)[1] == 1
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("plane_bytes", [0, 1, 511, 512])
+def test_mxfp8_rows_of_no_expert_need_no_planes(plane_bytes, dtype):
+    """Offsets that give no expert a row need none of the ragged planes' bytes; others need more than there are."""
+    R, N, K = 10, 48, 80
+    codes, plane = torch.full((4096,), 0x7F, dtype=U8, device="cuda"), torch.full((4096,), 127, dtype=U8, device="cuda")
+    kind_of = 0 if dtype is BF16 else 1
+    for kind, shape in ((0, (R, N)), (1, (R, K)), (2, (3, N, K))):
+        w = plane.numel() if kind != 2 else plane_bytes
+        for off, value in (([0, 0, 0, 0], 0), ([0, 0, 4, 4], 9), ([0, 0, 0, -1], 9)):
+            if plane_bytes == 512 and off[2] == 4:
+                continue  # one tile is there
+            offsets = torch.tensor(off, device="cuda")
+            out, told = outputs(lambda out, err: mx.mxfp8_matmul_grouped(kind, codes, plane, plane_bytes, 0, codes, plane, w, 0, R, N, K, 3, offsets, out, kind_of,
+                                                                         err), shape, dtype)
+            assert bool((out == value).all()) and told == 1, (kind, off)
