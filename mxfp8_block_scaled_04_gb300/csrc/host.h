@@ -62,7 +62,9 @@ struct KernelSetup {
 
 // Launch with programmatic stream serialisation (and, with cluster > 1, in thread-block clusters of that
 // many consecutive blocks).  Only kernels whose threads all wait (griddepcontrol.wait) before their first
-// global access are launched this way.
+// global access are launched this way.  The exception: a products' kernel behind mxfp4_parts_kernel reads weights, their scales
+// and offsets before it waits.  That holds because the parts' kernel is the launch just before it, writes none of these, and
+// waits before it lets the next one start, so that whatever wrote them has ended; nothing may be launched between the two.
 template <typename... Params, typename... Args>
 mxfp8_status_t launch_serialized(void (*kern)(Params...), dim3 grid, unsigned block, size_t smem, int cluster,
                                  cudaStream_t stream, Args &&...args)

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kPartsThreads<GROUPED>) mxfp4_parts_kernel(con
 {
     constexpr int kThreads = kPartsThreads<GROUPED>;
     __shared__ GroupTable<GROUPED> groups;
-    pdl_wait_and_release();
+    pdl_wait_and_release();  // in this order: the products' kernel reads weights and offsets as soon as it is let start
     const int tid = threadIdx.x, lane = tid & 31;
     // A unit's elements are loaded before the one before it is split, the first ones before the table of groups is made.
     struct Unit {

@@ -78,8 +78,9 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
 // Programmatic dependent launch.  The library's kernels are launched so that the
 // next kernel on the stream may start while this one drains: each lets its
 // successor launch at once, and waits, before its first global memory access,
-// until the kernel before it has finished and its writes are visible.  Without
-// the launch attribute both are no-ops.
+// until the kernel before it has finished and its writes are visible (the one
+// exception stands at launch_serialized).  Without the launch attribute both are
+// no-ops.
 __device__ __forceinline__ void pdl_wait_and_release()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
