@@ -12,7 +12,7 @@
 //
 // Measured (8192x7168, y bf16, both weights, a gate per channel): forward 76 us with a bf16 stream (6.1 TB/s), 115 with fp32;
 // gradients 123 (5.7 TB/s) and 181.  4000x16384: 95 and 174.  Bound by HBM; by the chain of loads, reductions and stores for few
-// rows (16x7168 4.7 and 9.5 us, launches included) and by issue for short ones (16000x1024 gradients 50 us, 3.9 TB/s).
+// rows (16x7168 4.7 and 9.5 us, launches included) and by issue for short ones (16000x1024 gradients 45 us, 4.4 TB/s).
 #pragma once
 
 #include <cstdint>
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_backward_kernel(const
 }
 
 // The CTAs' sums, in order: a warp takes 32 columns of every W-th CTA's; the W warps' are added in order.  W is 8, or 32 for the
-// many CTAs of short rows (16000x1024, 1064 CTAs: gradients 50 -> 44.5 us; for 152 and fewer 8 are as fast or faster).
+// many CTAs of short rows (16000x1024, 1064 CTAs: gradients 50 -> 45 us; for 152 and fewer 8 are as fast or faster).
 constexpr int kNormReduceFew = 256, kNormReduceMany = 1024, kNormReduceCtas = 256;
 __global__ void __launch_bounds__(kNormReduceMany) block_norm_reduce_kernel(const NormParams p, int ctas)
 {

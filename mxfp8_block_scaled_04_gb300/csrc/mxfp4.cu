@@ -314,7 +314,9 @@ mxfp8_status_t launch_few(const GemmParams &p, const PartsParams &q, const void 
 // Measured (us, GPU time of a call here / by the parts' kernel and mxfp4_group_kernel), rows x K x N on 64 experts, no expert
 // shared: 1x7168x2048 5.4 / 13.6, 4x2048x1032 5.1 / 7.9, 8x7168x2048 12.8 / 16.6, 16x7168x2048 22.1 / 26.7, 16x2048x7168 26.1 / 25.6;
 // 16 rows of eight experts 14.5 / 18.1 and 19.5 / 16.1; all 16 of one expert 13.4 / 15.2 and 17.5 / 8.9 at worst (a Python call takes
-// 22 for two launches and a workspace, 13 for one).  More rows gain nothing, and lose where they share.
+// 22 for two launches and a workspace, 13 for one).  More rows gain where the experts are narrow, and lose where they are wide and
+// shared: 24 rows of 2048x1032 6.4 / 11.3, 64 12.2 / 17.4; 32 of 7168x2048 42.0 / 49.1; 24 of 2048x7168 36.9 / 35.7, shared by two 29.3 /
+// 22.3, 64 of them 67.9 / 45.4.  The rule reads rows and experts alone and stops where both kinds are served.
 bool few_expert_rows(int64_t rows, int num_groups)
 {
     return rows <= kFewExpertRows && 2 * rows <= num_groups;

@@ -20,11 +20,11 @@
 // cluster scope for that: 64 experts of 1024 rows on average, fp32 out, 1130 us against 970.)
 //
 // Measured: 8192x8192x8192 312 us (3.5 PFLOP/s; the bf16 rate measured with cuBLAS twice over is 3.8), 64 experts of 1024 rows on
-// average, 7168 -> 2048: forward 598 us, input gradient 632, weight gradient 944 to fp32 (3.76 GB: 5.7 TB/s were 660 at
-// HBM's rate) and 719 to bf16; two rows per expert 153, 146, 596 and 352.  Many rows: bound by the MMAs under the power limit (tensor
-// pipe active 72% of the forward's cycles at 1.77 GHz), the ragged last tile of each expert and, for the weight gradient, the
-// path between SMs and L2, where a stage's loads take 3600 to 4200 cycles while tiles are stored.  Few: the weights' bytes
-// (6.3 TB/s), or the gradient's.
+// average, 7168 -> 2048: forward 598 us, input gradient 632, weight gradient 970 to fp32 (912 where every expert has 1024; the 3.76 GB
+// that it writes take 553 at the copy rate) and 755 to bf16 (697); two rows per expert 153, 146, 607 and 354.  Many rows: bound by the
+// MMAs under the power limit (tensor pipe active 73% of the forward's cycles), the ragged last tile of each expert and, for the
+// weight gradient, most likely the path from the SMs to L2 (requests in close to 60% of its cycles, DRAM 4.1 TB/s, tensor pipe 41%):
+// a stage's loads take 3600 to 4200 cycles while tiles are stored.  Few: the weights' bytes (6.3 TB/s), or the gradient's.
 #pragma once
 
 #include "mxfp4_gemm.cuh"
