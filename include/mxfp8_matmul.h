@@ -9,7 +9,8 @@
  *     input gradient    dx [R, K] = dy W_g      dy's rows and W's columns    (blocks of 32 along N)
  *     weight gradient   dW_g [N, K] = dy_g^T x_g   dy's and x's columns      (blocks of 32 rows of the expert)
  * W is the cast of its [E * N, K] rows in E groups of N rows.  Products of codes and scales are exact, sums fp32, rounded
- * once to the output's type.  Formats may differ between the operands (MXFP8_E4M3, MXFP8_E5M2).
+ * once to the output's type.  Sums to fp32 are made in pieces (2048 rows of a weight gradient, 8192 elements of the other two)
+ * that are added in order: the tensor core truncates its sums.  Formats may differ between the operands (MXFP8_E4M3, MXFP8_E5M2).
  */
 #ifndef MXFP8_MATMUL_GB300_H
 #define MXFP8_MATMUL_GB300_H

@@ -137,10 +137,11 @@ __device__ __forceinline__ bool epilogue_all(bool ok)
     return r != 0;
 }
 
-// Rows q0 .. q0 + 31 (of which `rows` are written) of 128 columns from col0; quarter: the warp's 32 lanes.
-template <bool F32>
+// Rows q0 .. q0 + 31 (of which `rows` are written) of 128 columns from col0; quarter: the warp's 32 lanes.  ADDS (fp32, vectors):
+// where `add`, to what the same call has stored there before, each thread its own elements.
+template <bool F32, bool ADDS = false>
 __device__ __forceinline__ void store_chunk(const GemmParams &p, const uint32_t (&v)[32], unsigned char *buffer, int quarter, int lane,
-                                            int64_t row0, int rows, int64_t col0)
+                                            int64_t row0, int rows, int64_t col0, bool add = false)
 {
     constexpr int kSize = F32 ? 4 : 2;
     if (!p.vec_out) {
@@ -170,9 +171,16 @@ __device__ __forceinline__ void store_chunk(const GemmParams &p, const uint32_t 
     unsigned char *out = static_cast<unsigned char *>(p.out) + ((row0 + r0) * p.ldo + col0) * kSize + vec * 16;
 #pragma unroll
     for (int i = 0; i < kEpiRows / kPerPass; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(buffer + (r0 + i * kPerPass) * kRowBytes + vec * 16);
-        if (live && r0 + i * kPerPass < rows)
-            *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(i) * kPerPass * p.ldo * kSize) = q;
+        uint4 q = *reinterpret_cast<const uint4 *>(buffer + (r0 + i * kPerPass) * kRowBytes + vec * 16);
+        if (live && r0 + i * kPerPass < rows) {
+            uint4 *to = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(i) * kPerPass * p.ldo * kSize);
+            if (ADDS && add) {
+                const float4 b = *reinterpret_cast<const float4 *>(to), s = *reinterpret_cast<const float4 *>(&q);
+                *reinterpret_cast<float4 *>(to) = make_float4(b.x + s.x, b.y + s.y, b.z + s.z, b.w + s.w);
+            } else {
+                *to = q;
+            }
+        }
     }
 }
 

@@ -19,6 +19,15 @@
 // copies orders them before the MMAs that the first CTA issues for both.  (Generic stores need a release and an acquire at
 // cluster scope for that: 64 experts of 1024 rows on average, fp32 out, 1130 us against 970.)
 //
+// The tensor core truncates its fp32 sums (one rounds them): an error toward zero that grows with their length, and faster where
+// tokens differ in scale.  To fp32 a sum is made in pieces of kP8Piece stages, each in a fresh accumulator, added in order: of
+// 2048 rows for the weight gradient, in the epilogue's registers (an epilogue warp keeps its columns through a tile), of 8192
+// elements for the other two, in the output.  Norm-wise error against 64 bits of a weight gradient of 2048, 8192 and 65536
+// rows: normal values 0.7e-7, 0.9e-7, 1.3e-7 (in one piece 0.7e-7, 3.0e-7, 45e-7; a plain fp32 product 0.4e-7, 0.6e-7, 1.2e-7); rows
+// scaled by exp of a normal value 3.1e-7, 3.5e-7, 4.2e-7 (in one piece 3.1e-7, 20e-7, 244e-7).  8192x8192x8192 to fp32 333 -> 359 us, 8
+// experts of 8192 rows 538 -> 576, of up to 2048 rows as before; pieces added in the output took 548 and 970.  To bf16 the
+// truncation is far below the rounding, and a sum is one piece.
+//
 // Measured: 8192x8192x8192 312 us (3.5 PFLOP/s; the bf16 rate measured with cuBLAS twice over is 3.8), 64 experts of 1024 rows on
 // average, 7168 -> 2048: forward 598 us, input gradient 632, weight gradient 970 to fp32 (912 where every expert has 1024; the 3.76 GB
 // that it writes take 553 at the copy rate) and 755 to bf16 (697); two rows per expert 153, 146, 607 and 354.  Many rows: bound by the
@@ -41,6 +50,15 @@ constexpr int kP8Scales = 3 * 512;            // P's tile of this CTA, Q's two t
 constexpr int kP8Epi = (kP8Stages * (kP8Stage + kP8Scales) + 1023) / 1024 * 1024;  // the epilogue's buffers from here on
 constexpr int kP8Smem = kP8Epi + 1024;
 constexpr int kP8Acc1 = 224, kP8ScaleCol = 480;  // TMEM columns, as in mxfp4_pair.cuh
+
+// Stages of a piece of a sum to fp32.
+template <int MODE>
+constexpr int kP8Piece = MODE == kWeightGrad ? 16 : 64;
+template <int MODE, bool F32>
+__device__ __forceinline__ int sum_pieces(int k_iters)
+{
+    return F32 && k_iters > kP8Piece<MODE> ? (k_iters + kP8Piece<MODE> - 1) / kP8Piece<MODE> : 1;
+}
 
 // The boxes of zeros that cover `rows` (1 to 31) rows: of 8 rows, the last one back over rows that are zero already, or of one.
 constexpr int kZeroRows = 8;
@@ -239,6 +257,14 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
         }
     };
 
+    // the next piece of a tile's sum, or the next tile
+    auto next_piece = [&](const Tile8 &c, int &piece, int &n_tile) {
+        if (++piece == sum_pieces<MODE, F32>(c.k_iters)) {
+            piece = 0;
+            ++n_tile;
+        }
+    };
+
     if (warp == 0 || warp == 3) {
         // ---- producers of this CTA's operands: codes (warp 0), scales (warp 3); they signal the first CTA's barriers ----
         const uint32_t lead_full = map_to_rank(full0, 0), own_landed = map_to_rank(landed0, rank);
@@ -346,19 +372,21 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
         const uint64_t q_desc = kQMn ? desc_mn128(base + kP8Codes) : desc_sw128(base + kP8Codes);
         const uint64_t s_desc = desc_scales(scales);
         const uint32_t formats = p.formats | (kPMn ? 1u << 15 : 0u) | (kQMn ? 1u << 16 : 0u);
-        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles && ok; ++n_tile) {
+        int piece = 0, k0 = 0;  // of the tile's sum, and its first stage
+        for (int n_tile = 0, acc = 0, t; (t = tile_of(n_tile)) < num_tiles && ok; ++acc) {  // acc: accumulators so far
             const Tile8 c = tile8<MODE>(t, p, groups);
             const int n = (c.valid + 31) & ~31;  // halves of whole 16-row groups
-            const int buf = n_tile & 1;
+            const int buf = acc & 1;
             const uint32_t d = tmem + buf * kP8Acc1;
-            if (n_tile >= 1)  // the columns shared with the tile before are read, and all of the one before that
-                ok = mbar_wait_cycles(smem_u32(&acc_empty), (n_tile - 1) & 1, kGemmWait);
+            if (acc >= 1)  // the columns shared with the accumulator before are read, and all of the one before that
+                ok = mbar_wait_cycles(smem_u32(&acc_empty), (acc - 1) & 1, kGemmWait);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            for (int k = 0; k < c.k_iters; ++k) {
+            const int k1 = sum_pieces<MODE, F32>(c.k_iters) > 1 ? min(c.k_iters, k0 + kP8Piece<MODE>) : c.k_iters;
+            for (int k = k0; k < k1; ++k) {
                 ok = mbar_wait_cycles(full0 + 8 * slot, phase, kGemmWait);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
@@ -375,7 +403,7 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < left)
-                            tc_mma_mxf8_pair(d, pd + j * kPStep, qd + j * kQStep, mxf8_idesc(formats, kP8Tile, n, j), sp, sq, k > 0 || j > 0);
+                            tc_mma_mxf8_pair(d, pd + j * kPStep, qd + j * kQStep, mxf8_idesc(formats, kP8Tile, n, j), sp, sq, k > k0 || j > 0);
                     tc_commit_pair(empty0 + 8 * slot);
                 }
                 __syncwarp();
@@ -386,6 +414,8 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
             if (elect_one())
                 tc_commit_pair(smem_u32(&acc_full[buf]));
             __syncwarp();
+            next_piece(c, piece, n_tile);
+            k0 = piece * kP8Piece<MODE>;
         }
         if (!ok) {
             if (elect_one()) {
@@ -397,15 +427,17 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
         }
     } else if (kTails && warp >= 4) {
         // ---- epilogue of this CTA's 128 rows of an expert's gradient: a warp has 32 rows, a thread one ----
-        constexpr int kCols = F32 ? 32 : 64;  // 128 bytes of a row
+        constexpr int kCols = F32 ? 32 : 64, kChunks = kP8Tile / kCols;  // 128 bytes of a row
         // (two warps to 32 rows, a chunk of 128 bytes of each in turn)
         const int quarter = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lead_empty = map_to_rank(smem_u32(&acc_empty), 0);
         unsigned char *buffer = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Epi + (warp - 4) * 4096;
-        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
+        float sum[F32 ? kChunks / 2 : 1][32];  // of the pieces before
+        int piece = 0;
+        for (int n_tile = 0, acc = 0, t; (t = tile_of(n_tile)) < num_tiles; ++acc) {
             const Tile8 c = tile8<MODE>(t, p, groups);
-            const int buf = n_tile & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+            const int buf = acc & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cycles(smem_u32(&acc_full[buf]), (acc >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
@@ -413,15 +445,18 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
             tc_fence_after();
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kP8Acc1;
             const int row = c.p_at + static_cast<int>(rank) * 128 + quarter * 32;
-            const int start = buf == 0 ? kP8Tile - kCols : 0;  // the columns that the accumulators share first
-            if (part == 1) {  // its share of the tile before is read, and none of this tile's is in the shared columns
+            // The columns that the accumulators share are the last chunk of buffer 0 and the first of buffer 1.  The warp that has them
+            // frees them after its first chunk; the other one's share of the accumulator before is read.
+            const bool shares = part == (buf ^ 1), more = piece + 1 < sum_pieces<MODE, F32>(c.k_iters);
+            if (!shares) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_peer(lead_empty);
             }
-            for (int i = part; i < kP8Tile / kCols; i += 2) {
-                const int q = (start + kCols * i) & (kP8Tile - 1);
+#pragma unroll(F32 ? kChunks / 2 : 1)
+            for (int i = 0; i < kChunks / 2; ++i) {
+                const int q = kCols * (part == 0 ? 2 * i : (kChunks - 1 + 2 * i) % kChunks);
                 const bool live = q < c.valid && row < p.P;
                 uint32_t v[kCols];
                 if (live) {
@@ -429,7 +464,7 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
                     for (int h = 0; h < kCols / 32; ++h)
                         tmem_load32(d + q + 32 * h, *reinterpret_cast<uint32_t (*)[32]>(&v[32 * h]));
                 }
-                if (i == 0) {
+                if (i == 0 && shares) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
@@ -437,6 +472,19 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
                 }
                 if (!live)
                     continue;
+                if constexpr (F32) {
+                    if (piece > 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(sum[i][j] + __uint_as_float(v[j]));
+                    }
+                    if (more) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sum[i][j] = __uint_as_float(v[j]);
+                        continue;
+                    }
+                }
                 if (lane == 0)
                     bulk_store_wait<0>();
                 __syncwarp();
@@ -459,6 +507,7 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
                 if (lane == 0)
                     tma_store_3d(&out_map, smem_u32(buffer), c.q_at + q, row, c.group);
             }
+            next_piece(c, piece, n_tile);
         }
         if (lane == 0)
             bulk_store_wait<0>();
@@ -470,10 +519,11 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
         unsigned char *stage_out = gemm_smem + (base - smem_u32(gemm_smem)) + kP8Epi;
         int chunk = 0;
         clear_rows_from<F32>(p, no_expert, quarter * 32 + lane);
-        for (int n_tile = 0, t; (t = tile_of(n_tile)) < num_tiles; ++n_tile) {
+        int piece = 0;
+        for (int n_tile = 0, acc = 0, t; (t = tile_of(n_tile)) < num_tiles; ++acc) {
             const Tile8 c = tile8<MODE>(t, p, groups);
-            const int buf = n_tile & 1;
-            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (n_tile >> 1) & 1, kGemmWait))) {
+            const int buf = acc & 1;
+            if (!epilogue_all(mbar_wait_cycles(smem_u32(&acc_full[buf]), (acc >> 1) & 1, kGemmWait))) {
                 if (lane == 0)
                     atomicOr(p.fault, 1u);
                 break;
@@ -493,9 +543,10 @@ __global__ void __launch_bounds__(kP8Threads<MODE>, 1)
                         mbar_arrive_peer(lead_empty);
                 }
                 if (q < c.valid)
-                    store_chunk<F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.out_row + q, c.valid - q,
-                                 c.p_at + rank * 128);
+                    store_chunk<F32, F32>(p, v, stage_out + (chunk++ & 1) * (kEpiBytes<F32> / 2), quarter, lane, c.out_row + q, c.valid - q,
+                                          c.p_at + rank * 128, piece > 0);
             }
+            next_piece(c, piece, n_tile);
         }
     }
     tc_fence_before();

@@ -127,3 +127,66 @@ def test_ragged_rows_stay_out_of_their_neighbours():
     for _ in range(30):
         assert torch.equal(mx.matmul_mxfp8_grouped_wgrad(qd, qx, offsets), first)
     assert mx.mxfp8_device_fault_word() == 0
+
+
+def in_pieces(total, piece):
+    """(start, end) of the pieces that a sum to fp32 is made in."""
+    return [(a, min(a + piece, total)) for a in range(0, total, piece)]
+
+
+def added(parts):
+    s = parts[0]
+    for t in parts[1:]:
+        s = s + t
+    return s
+
+
+@pytest.mark.parametrize("N,K", [(16, 16), (272, 528), (2064, 1040)])
+def test_long_weight_gradients_are_sums_of_pieces(N, K):
+    """To fp32 a sum over more than 2048 rows is the sum of its pieces, bit for bit, whatever the other experts have."""
+    sizes = [9011, 5, 0, 4096, 2048, 2049, 40, 6000]
+    off = torch.tensor([0] + sizes).cumsum(0).tolist()
+    R = off[-1]
+    x, dy = draw(R, K, 1), draw(R, N, 2)
+    whole = mx.matmul_mxfp8_grouped_wgrad(cast(dy, off, "e5m2"), cast(x, off, "e4m3"), torch.tensor(off).cuda())
+    cuts = [(e, off[e] + a, off[e] + b) for e in range(len(sizes)) for a, b in in_pieces(sizes[e], 2048)]
+    ends = [0] + [b for _, _, b in cuts]  # a piece starts at a whole number of blocks: the same casts
+    parts = mx.matmul_mxfp8_grouped_wgrad(cast(dy, ends, "e5m2"), cast(x, ends, "e4m3"), torch.tensor(ends).cuda())
+    for e, n in enumerate(sizes):
+        mine = [parts[i] for i, c in enumerate(cuts) if c[0] == e]
+        assert torch.equal(whole[e], added(mine) if n else torch.zeros_like(whole[e])), e
+    again = mx.matmul_mxfp8_grouped_wgrad(cast(dy, off, "e5m2"), cast(x, off, "e4m3"), torch.tensor(off).cuda())
+    assert torch.equal(again, whole) and mx.mxfp8_device_fault_word() == 0
+
+
+@pytest.mark.parametrize("sizes", [[40], [300, 0, 1, 257]])
+def test_long_products_are_sums_of_pieces(sizes):
+    """Forward over K and input gradient over N to fp32: of pieces of 8192."""
+    off = torch.tensor([0] + sizes).cumsum(0).tolist()
+    E, R, L, C = len(sizes), off[-1], 2 * 8192 + 3616, 272
+    offsets = torch.tensor(off).cuda()
+
+    def ends(n):
+        return [n * e for e in range(E + 1)]
+    x, w = draw(R, L, 3), draw(E * C, L, 4, 0.2)
+    y = mx.matmul_mxfp8_grouped(cast(x, off, "e4m3"), offsets, cast(w, ends(C), "e4m3"), F32)
+    parts = [mx.matmul_mxfp8_grouped(cast(x[:, a:b].contiguous(), off, "e4m3"), offsets, cast(w[:, a:b].contiguous(), ends(C), "e4m3"), F32)
+             for a, b in in_pieces(L, 8192)]
+    assert torch.equal(y, added(parts))
+    dy, w = draw(R, L, 5), draw(E * L, C, 6, 0.2)
+    dx = mx.matmul_mxfp8_grouped_dgrad(cast(dy, off, "e5m2"), offsets, cast(w, ends(L), "e4m3"), F32)
+    parts = []
+    for a, b in in_pieces(L, 8192):
+        rows = w.view(E, L, C)[:, a:b].reshape(E * (b - a), C).contiguous()
+        parts.append(mx.matmul_mxfp8_grouped_dgrad(cast(dy[:, a:b].contiguous(), off, "e5m2"), offsets, cast(rows, ends(b - a), "e4m3"), F32))
+    assert torch.equal(dx, added(parts)) and mx.mxfp8_device_fault_word() == 0
+
+
+def test_long_weight_gradients_keep_fp32():
+    """65536 rows of very different scale: norm-wise within 1e-6 of the 64-bit product.  The truncation of a step is at most 2^-23 of the
+    partial sum; 64 steps of a piece reach 2^-17 of it at worst, and the partial sums of random signs, far below the sum of the
+    magnitudes, leave a twentieth of that (one sum of 2048 steps was 2.4e-5 off)."""
+    layer = Layer([65536], 48, 80)
+    got = mx.matmul_mxfp8_grouped_wgrad(layer.dy, layer.x, layer.offsets)[0].cpu().double()
+    want = layer.cols("dy")[0].t() @ layer.cols("x")[0]
+    assert float((got - want).norm() / want.norm()) < 1e-6
